@@ -15,11 +15,15 @@ Entry points (same names as the C ABI):
   fp8_quant_gemm_fused(x, qw, s_ch)        -> y bf16 [M,N]  (optionally qa, s_tok)
   fp8_gemm_scaled_fp8out(qa, s_tok, qw, s_ch) -> (q_out uint8 [M,N], s_out fp32 [M])  (optionally y32)
   fp8_gemm_grouped_scaled(qa, s_tok, row_token, expert_offsets, qw, s_ch) -> y bf16 [R,N]
+  fp8_kv_append_rope_paged(k, v, positions, cos_sin, scales, slot_mapping, cache, q=q) -> q_out  rotate + FP8 append
+  fp8_attn_decode_paged(q, cache, block_table, seq_lens, scales, block_size)  -> out  one new token per sequence
+  fp8_attn_prefill_paged(q, cu_q, cache, block_table, seq_lens, scales, block_size) -> out  several new tokens
   fp8_workspace_bytes(M, N, K) (fused call), fp8_gemm_workspace_bytes(M, N, K),
   fp8_fp8out_workspace_bytes(M, N, K), fp8_grouped_workspace_bytes(T, R, E, N, K)
   fp8_status_string(code)
 """
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -37,7 +41,9 @@ EXPORTS = ("fp8_quantize_per_token", "fp8_quantize_static", "fp8_quantize_per_to
            "fp8_gemm_grouped_scaled", "fp8_workspace_bytes", "fp8_gemm_workspace_bytes", "fp8_fp8out_workspace_bytes",
            "fp8_grouped_workspace_bytes", "fp8_quantize_mx", "fp8_gemm_mx", "fp8_mx_workspace_bytes",
            "fp8_kv_channel_scales", "fp8_kv_scales_workspace_bytes",
-           "fp8_kv_quantize_paged", "fp8_kv_dequantize_paged", "fp8_stream_read", "fp8_quant_gemm_fused_noalloc",
+           "fp8_kv_quantize_paged", "fp8_kv_dequantize_paged", "fp8_kv_append_rope_paged", "fp8_attn_decode_paged",
+           "fp8_attn_prefill_paged", "fp8_attn_decode_workspace_bytes", "fp8_attn_prefill_workspace_bytes",
+           "fp8_stream_read", "fp8_quant_gemm_fused_noalloc",
            "fp8_status_string")
 
 _lib = None
@@ -97,6 +103,20 @@ def lib():
         L.fp8_kv_quantize_paged.argtypes = [vp, st, i64, i64, i64, vp, st, vp, vp, i64, vp]
         L.fp8_kv_dequantize_paged.restype = st
         L.fp8_kv_dequantize_paged.argtypes = [vp, i64, vp, i64, i64, vp, st, vp, st, i64, vp]
+        f32, i32 = ctypes.c_float, ctypes.c_int32
+        L.fp8_kv_append_rope_paged.restype = st
+        L.fp8_kv_append_rope_paged.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, st, i64, i64, i64, i64, vp, vp, i64,
+                                               i64, i32, vp, st, vp, vp, i64, vp]
+        L.fp8_attn_decode_workspace_bytes.restype = sz
+        L.fp8_attn_decode_workspace_bytes.argtypes = [i64] * 7
+        L.fp8_attn_decode_paged.restype = st
+        L.fp8_attn_decode_paged.argtypes = [vp, i64, st, vp, i64, i64, vp, st, vp, i64, i64, vp, i64, i64, i64, i64,
+                                            i64, f32, f32, vp, i64, vp, i64, vp, vp, sz, vp]
+        L.fp8_attn_prefill_workspace_bytes.restype = sz
+        L.fp8_attn_prefill_workspace_bytes.argtypes = [i64] * 9
+        L.fp8_attn_prefill_paged.restype = st
+        L.fp8_attn_prefill_paged.argtypes = [vp, i64, st, vp, i64, vp, i64, i64, vp, st, vp, i64, i64, vp, i64, i64,
+                                             i64, i64, i64, i64, i32, vp, f32, f32, vp, i64, vp, i64, vp, vp, sz, vp]
         L.fp8_quant_gemm_fused_noalloc.restype = st
         L.fp8_quant_gemm_fused_noalloc.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, i64, i64, vp, vp, vp]
         L.fp8_stream_read.restype = st
@@ -430,6 +450,193 @@ def fp8_kv_dequantize_paged(cache, slot_mapping, scales, fmt="e5m2", out=None, o
            lib().fp8_kv_dequantize_paged(_ptr(cache), num_slots, _ptr(slot_mapping), T, C, _ptr(scales),
                                          _kv_fmt(fmt), _ptr(out), odt, ldo, _stream(stream)))
     return out
+
+
+def _on_stream(fn):
+    """Runs fn with the first argument's device current and, when a stream is
+    given, with that stream current: what fn allocates (outputs, workspace)
+    then belongs to the stream that uses it, so the allocator cannot hand it to
+    other work while the call still runs."""
+
+    @functools.wraps(fn)
+    def call(t, *args, stream=None, **kwargs):
+        torch = _torch()
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{fn.__name__}: expected CUDA tensors")
+        if stream is not None:
+            if stream.device != t.device:
+                raise ValueError(f"stream: on {stream.device}, expected {t.device}")
+            with torch.cuda.stream(stream):
+                return fn(t, *args, **kwargs)
+        if t.device.index != torch.cuda.current_device():
+            with torch.cuda.device(t.device):
+                return fn(t, *args, **kwargs)
+        return fn(t, *args, **kwargs)
+
+    return call
+
+
+def _heads(t, name, device=None, dtype=None):
+    """[T, H, D] with the heads of a row adjacent -> (T, H, D, row stride, dtype code)."""
+    code = _kv_dtype(t, name, device)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected a 3-D tensor [tokens, heads, head_dim]")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if n and h and d and ((d > 1 and s2 != 1) or (h > 1 and s1 != d)):
+        raise ValueError(f"{name}: expected the heads of a token adjacent (strides [*, head_dim, 1])")
+    return n, h, d, (s0 if n > 1 else h * d), code
+
+
+@_on_stream
+def fp8_kv_append_rope_paged(k, v, positions, cos_sin, scales, slot_mapping, cache, fmt="e5m2", q=None, q_out=None,
+                             interleaved=False):
+    """Rotate k [T, Hkv, D] (and q [T, Hq, D]) by positions int32 [T] with the table
+    cos_sin fp32 [P, rot_dim] (cosines, then sines) and write k and v as FP8 codes
+    of value / scales [2 * Hkv * D] into the rows slot_mapping int32 [T] of the
+    uint8 cache [num_slots, 2 * Hkv * D]; returns the rotated q (q_out, which may
+    be q itself), or None without q.  stream: the stream to run on."""
+    torch = _torch()
+    dev = k.device
+    T, Hkv, D, ldk, dt = _heads(k, "k")
+    if _heads(v, "v", dev, k.dtype)[:3] != (T, Hkv, D):
+        raise ValueError("v: expected k's shape")
+    ldv = v.stride(0) if T > 1 else Hkv * D
+    Hq = ldq = ldqo = 0
+    if q is not None:
+        Tq, Hq, Dq, ldq, _ = _heads(q, "q", dev, k.dtype)
+        if (Tq, Dq) != (T, D):
+            raise ValueError("q: expected shape [T, Hq, D] with k's T and D")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+        if _heads(q_out, "q_out", dev, k.dtype)[:3] != (T, Hq, D):
+            raise ValueError("q_out: expected q's shape")
+        ldqo = q_out.stride(0) if T > 1 else Hq * D
+    elif q_out is not None:
+        raise ValueError("q_out: given without q")
+    _on_device(cos_sin, torch.float32, "cos_sin", dev)
+    if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin: expected a contiguous fp32 tensor [P, rot_dim]")
+    _vec(positions, torch.int32, "positions", T, dev)
+    _vec(slot_mapping, torch.int32, "slot_mapping", T, dev)
+    _vec(scales, torch.float32, "scales", 2 * Hkv * D, dev)
+    _kv_cache(cache, 2 * Hkv * D, dev)
+    _check("fp8_kv_append_rope_paged",
+           lib().fp8_kv_append_rope_paged(_ptr(q), ldq, _ptr(q_out), ldqo, _ptr(k), ldk, _ptr(v), ldv, dt, T, Hq, Hkv,
+                                          D, _ptr(positions), _ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1],
+                                          int(bool(interleaved)), _ptr(scales), _kv_fmt(fmt), _ptr(slot_mapping),
+                                          _ptr(cache), cache.shape[0], _stream(None)))
+    return q_out
+
+
+def _attn_args(q, cache, block_table, seq_lens, scales, block_size, sm_scale, alibi_slopes, out, lse):
+    """The checks both attention calls share -> (rows, B, Hq, Hkv, D, blocks, ldq, ldo, ld_table, dtype code, sm_scale, out)."""
+    torch = _torch()
+    dev = q.device
+    rows, Hq, D, ldq, dt = _heads(q, "q")
+    _kv_cache(cache, None, dev)
+    slots, C = cache.shape
+    if block_size < 1 or slots % block_size:
+        raise ValueError("cache: expected [num_blocks * block_size, 2 * Hkv * D]")
+    if D == 0 or C == 0 or C % (2 * D):
+        raise ValueError("cache: rows are not 2 * Hkv * D codes of q's D")
+    Hkv = C // (2 * D)
+    _on_device(block_table, torch.int32, "block_table", dev)
+    if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table: expected a 2-D row-major int32 tensor [B, max_blocks]")
+    B, width = block_table.shape
+    _vec(seq_lens, torch.int32, "seq_lens", B, dev)
+    _vec(scales, torch.float32, "scales", C, dev)
+    if alibi_slopes is not None:
+        _vec(alibi_slopes, torch.float32, "alibi_slopes", Hq, dev)
+    if out is None:
+        out = torch.empty((rows, Hq, D), dtype=q.dtype, device=dev)
+    if _heads(out, "out", dev, q.dtype)[:3] != (rows, Hq, D):
+        raise ValueError("out: expected q's shape")
+    if lse is not None:
+        _dense(lse, torch.float32, "lse", (rows, Hq), dev)
+    ldo = out.stride(0) if rows > 1 else Hq * D
+    ld_table = block_table.stride(0) if B > 1 else width
+    scale = D ** -0.5 if sm_scale is None else float(sm_scale)
+    return rows, B, width, Hq, Hkv, D, slots // block_size, ldq, ldo, ld_table, dt, scale, out
+
+
+@_on_stream
+def fp8_attn_decode_paged(q, cache, block_table, seq_lens, scales, block_size, fmt="e5m2", max_len=None, sm_scale=None,
+                          softcap=0.0, alibi_slopes=None, window=0, out=None, lse=None, ws=None):
+    """Attention of one new token per sequence, q [B, Hq, D], over its seq_lens int32
+    [B] cached tokens (the new one's among them) in the pages block_table int32
+    [B, max_blocks] of the uint8 cache [num_blocks * block_size, 2 * Hkv * D] with
+    channel scales fp32 [2 * Hkv * D] -> out [B, Hq, D] in q's type.
+
+    max_len: the longest sequence's length when the host knows it (plans the
+    launch; by default the block table's width).  sm_scale: D ** -0.5 by default.
+    softcap, alibi_slopes fp32 [Hq], window: 0 / None for off.  lse: fp32 [B, Hq]
+    that receives the log-sum-exp.  ws: uint8 workspace of at least
+    fp8_attn_decode_workspace_bytes(...) bytes, allocated when not given.
+    stream: the stream to run on."""
+    (rows, B, width, Hq, Hkv, D, blocks, ldq, ldo, ld_table, dt, scale, out) = _attn_args(
+        q, cache, block_table, seq_lens, scales, block_size, sm_scale, alibi_slopes, out, lse)
+    if rows != B:
+        raise ValueError("q: expected one row per sequence of block_table")
+    max_len = int(max_len or 0)
+    need = int(lib().fp8_attn_decode_workspace_bytes(B, Hq, Hkv, D, block_size, width, max_len)) if ws is None else 0
+    if need and need != SIZE_MAX:
+        ws = _torch().empty(need, dtype=_torch().uint8, device=q.device)
+    elif ws is not None:
+        ws = _workspace(ws, 0, "fp8_attn_decode_paged", q.device)
+    _check("fp8_attn_decode_paged",
+           lib().fp8_attn_decode_paged(_ptr(q), ldq, dt, _ptr(cache), blocks, block_size, _ptr(scales), _kv_fmt(fmt),
+                                       _ptr(block_table), ld_table, width, _ptr(seq_lens), B, Hq, Hkv, D, max_len,
+                                       scale, softcap, _ptr(alibi_slopes), window, _ptr(out), ldo, _ptr(lse),
+                                       _ptr(ws), _nbytes(ws), _stream(None)))
+    return out
+
+
+@_on_stream
+def fp8_attn_prefill_paged(q, cu_q, cache, block_table, seq_lens, scales, block_size, fmt="e5m2", max_q=None,
+                           max_len=None, causal=True, prefix_lens=None, sm_scale=None, softcap=0.0, alibi_slopes=None,
+                           window=0, out=None, lse=None, ws=None):
+    """Attention of several new tokens per sequence -- a prompt, a chunk of one, drafted
+    tokens -- over the cache: rows cu_q[b] .. cu_q[b + 1] (int32 [B + 1]) of q
+    [T, Hq, D] are sequence b's newest tokens, the last of seq_lens[b] cached ones
+    -> out [T, Hq, D] in q's type.  Causal (each token sees its own and earlier
+    keys, and the first prefix_lens[b] int32 [B] of them in any case), or every key
+    of the sequence when causal is false.  Rows no sequence owns are left as they
+    were (uninitialised when out is allocated here).  max_q: the most new tokens of
+    one sequence when the host knows it.  The other arguments as for
+    fp8_attn_decode_paged."""
+    torch = _torch()
+    (T, B, width, Hq, Hkv, D, blocks, ldq, ldo, ld_table, dt, scale, out) = _attn_args(
+        q, cache, block_table, seq_lens, scales, block_size, sm_scale, alibi_slopes, out, lse)
+    _vec(cu_q, torch.int32, "cu_q", B + 1, q.device)
+    if prefix_lens is not None:
+        _vec(prefix_lens, torch.int32, "prefix_lens", B, q.device)
+    max_q, max_len = int(max_q or 0), int(max_len or 0)
+    need = int(lib().fp8_attn_prefill_workspace_bytes(T, B, Hq, Hkv, D, block_size, width, max_q, max_len)) if ws is None else 0
+    if need and need != SIZE_MAX:
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif ws is not None:
+        ws = _workspace(ws, 0, "fp8_attn_prefill_paged", q.device)
+    _check("fp8_attn_prefill_paged",
+           lib().fp8_attn_prefill_paged(_ptr(q), ldq, dt, _ptr(cu_q), T, _ptr(cache), blocks, block_size, _ptr(scales),
+                                        _kv_fmt(fmt), _ptr(block_table), ld_table, width, _ptr(seq_lens), B, Hq, Hkv,
+                                        D, max_q, max_len, int(bool(causal)), _ptr(prefix_lens), scale, softcap,
+                                        _ptr(alibi_slopes), window, _ptr(out), ldo, _ptr(lse), _ptr(ws), _nbytes(ws),
+                                        _stream(None)))
+    return out
+
+
+def fp8_attn_decode_workspace_bytes(B, Hq, Hkv, D, block_size, max_blocks, max_len=0):
+    """Workspace bytes of fp8_attn_decode_paged."""
+    return int(lib().fp8_attn_decode_workspace_bytes(B, Hq, Hkv, D, block_size, max_blocks, max_len))
+
+
+def fp8_attn_prefill_workspace_bytes(T, B, Hq, Hkv, D, block_size, max_blocks, max_q=0, max_len=0):
+    """Workspace bytes of fp8_attn_prefill_paged."""
+    return int(lib().fp8_attn_prefill_workspace_bytes(T, B, Hq, Hkv, D, block_size, max_blocks, max_q, max_len))
 
 
 def fp8_gemm_scaled(qa, s_tok, qw, s_ch, y=None, ws=None, stream=None):

@@ -8,7 +8,9 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstdint>
 
 #include "kernels.hpp"
@@ -106,6 +108,69 @@ fp8_status_t kv_row_type(fp8_kv_dtype_t t, int64_t C, int64_t* eb) {
 }
 
 fp8_status_t from_hip(hipError_t e) { return e == hipSuccess ? FP8_OK : FP8_ERR_DEVICE; }
+
+// Attention extents: positions, rows and row-head pairs are 32-bit in the kernels.
+constexpr int64_t kMaxAttn = int64_t(1) << 30;
+
+fp8_status_t check_attn_dims(int64_t rows, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size,
+                             int64_t max_blocks, int64_t max_q, int64_t max_len) {
+    if (rows < 0 || B < 0 || Hq < 0 || Hkv < 0 || D < 0 || max_blocks < 0 || max_q < 0 || max_len < 0)
+        return FP8_ERR_INVALID_ARGUMENT;
+    if (block_size < 1 || Hkv < 1 || Hq % Hkv != 0) return FP8_ERR_INVALID_ARGUMENT;
+    if (D != 64 && D != 128 && D != 256) return FP8_ERR_UNSUPPORTED;
+    if (rows > kMaxAttn || B > kMaxAttn || Hq > kMaxAttn / D || block_size > kMaxAttn || max_blocks > kMaxAttn)
+        return FP8_ERR_UNSUPPORTED;
+    if (block_size * max_blocks > kMaxAttn || rows * Hq > kMaxAttn || B * Hq > kMaxAttn / 16) return FP8_ERR_UNSUPPORTED;
+    return FP8_OK;
+}
+
+// Launch hints: unknown (0) or past what the buffers hold is taken as the most
+// they hold.  A wrong hint changes no result.
+int64_t hint(int64_t v, int64_t most) { return v > 0 ? std::min(v, most) : most; }
+
+size_t attn_ws(int64_t rows, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size, int64_t max_blocks,
+               int64_t max_q, int64_t max_len) {
+    return round_up(fp8k::attn_paged_ws_bytes(B, rows, Hq, Hkv, D, max_q, hint(max_len, block_size * max_blocks)),
+                    kAlign);
+}
+
+// Both attention entry points; cu_q null: one new row per sequence.
+fp8_status_t attn(fp8k::PagedAttn p, fp8_kv_dtype_t dtype, fp8_kv_format_t fmt, int64_t rows, int64_t B, int64_t Hq,
+                  int64_t Hkv, int64_t D, int64_t block_size, int64_t max_blocks, int64_t max_q, int64_t max_len,
+                  int64_t window, float sm_scale, void* ws, size_t ws_bytes, hipStream_t stream) {
+    FP8_TRY(check_attn_dims(rows, B, Hq, Hkv, D, block_size, max_blocks, max_q, max_len));
+    FP8_TRY(check_kv_format(fmt));
+    const int64_t eb = kv_elem_bytes(dtype);
+    if (eb == 0) return FP8_ERR_INVALID_ARGUMENT;
+    if (!std::isfinite(sm_scale) || !std::isfinite(p.softcap) || p.softcap < 0 || window < 0 || p.num_blocks < 0)
+        return FP8_ERR_INVALID_ARGUMENT;
+    if (p.num_blocks > kMaxDim / block_size) return FP8_ERR_UNSUPPORTED;
+    const bool some = rows > 0 && B > 0 && Hq > 0;
+    FP8_TRY(check_matrix(p.q, rows, Hq * D, p.ldq, eb));
+    FP8_TRY(check_matrix(p.out, rows, Hq * D, p.ldo, eb));
+    FP8_TRY(check_matrix(p.cache, p.num_blocks * block_size, 2 * Hkv * D, 2 * Hkv * D, 1, true));
+    if (some) {
+        FP8_TRY(check_vector(p.scales, 2 * Hkv * D));
+        if (p.seq_lens == nullptr || (max_blocks > 0 && p.block_table == nullptr)) return FP8_ERR_INVALID_ARGUMENT;
+        if (max_blocks > 0 && p.ld_table < max_blocks) return FP8_ERR_INVALID_ARGUMENT;
+        const uintptr_t words = reinterpret_cast<uintptr_t>(p.seq_lens) | reinterpret_cast<uintptr_t>(p.block_table) |
+                                reinterpret_cast<uintptr_t>(p.cu_q) | reinterpret_cast<uintptr_t>(p.prefix) |
+                                reinterpret_cast<uintptr_t>(p.alibi) | reinterpret_cast<uintptr_t>(p.lse);
+        if ((words & 3u) != 0) return FP8_ERR_UNSUPPORTED;
+    }
+    const size_t need = attn_ws(rows, B, Hq, Hkv, D, block_size, max_blocks, max_q, max_len);
+    if (ws_bytes < need) return FP8_ERR_WORKSPACE;
+    if (need > 0 && ws == nullptr) return FP8_ERR_INVALID_ARGUMENT;
+    if (need > 0 && !aligned16(ws)) return FP8_ERR_UNSUPPORTED;
+    if (!some) return FP8_OK;
+    p.scale = sm_scale * 1.44269504088896341f;  // scores in powers of two
+    p.B = (int)B, p.rows = (int)rows, p.Hq = (int)Hq, p.Hkv = (int)Hkv;
+    p.block = (int)block_size, p.max_blocks = (int)max_blocks;
+    p.window = (int)std::min(window, kMaxAttn);  // no key is further back
+    p.dtype = (int)dtype;
+    return from_hip(fp8k::launch_attn_paged(p, (int)D, (int)fmt, max_q, hint(max_len, block_size * max_blocks), ws,
+                                            stream));
+}
 
 // Bytes the GEMM path itself needs for an M x N x K problem: the skinny
 // kernel's fp32 split-k partial sums when it splits k, else none.
@@ -327,6 +392,87 @@ fp8_status_t fp8_kv_dequantize_paged(const uint8_t* cache, int64_t num_slots, co
     if (T == 0 || C == 0) return FP8_OK;
     return from_hip(fp8k::launch_kv_dequantize_paged(cache, num_slots, slot_mapping, T, C, scales, (int)fmt, out,
                                                      (int)out_dtype, ldo, stream));
+}
+
+fp8_status_t fp8_kv_append_rope_paged(const void* q, int64_t ldq, void* q_out, int64_t ldqo, const void* k,
+                                      int64_t ldk, const void* v, int64_t ldv, fp8_kv_dtype_t dtype, int64_t T,
+                                      int64_t Hq, int64_t Hkv, int64_t D, const int32_t* positions,
+                                      const float* cos_sin, int64_t P, int64_t rot_dim, int32_t interleaved,
+                                      const float* scales, fp8_kv_format_t fmt, const int32_t* slot_mapping,
+                                      uint8_t* cache, int64_t num_slots, hipStream_t stream) {
+    if (T < 0 || Hq < 0 || Hkv < 0 || D < 0 || P < 0 || rot_dim < 0 || num_slots < 0) return FP8_ERR_INVALID_ARGUMENT;
+    if (T > kMaxDim || D > kMaxDim || P > kMaxDim || num_slots > kMaxDim) return FP8_ERR_UNSUPPORTED;
+    if (D % 16 != 0 || D == 0 || rot_dim % 16 != 0 || rot_dim == 0) return FP8_ERR_UNSUPPORTED;
+    if (rot_dim > D) return FP8_ERR_INVALID_ARGUMENT;
+    if (Hq > kMaxDim / D || Hkv > kMaxDim / (2 * D) || (Hq + 2 * Hkv) * D > kMaxDim - 4096) return FP8_ERR_UNSUPPORTED;
+    FP8_TRY(check_kv_format(fmt));
+    const int64_t eb = kv_elem_bytes(dtype);
+    if (eb == 0) return FP8_ERR_INVALID_ARGUMENT;
+    FP8_TRY(check_matrix(q, T, Hq * D, ldq, eb));
+    FP8_TRY(check_matrix(q_out, T, Hq * D, ldqo, eb));
+    FP8_TRY(check_matrix(k, T, Hkv * D, ldk, eb));
+    FP8_TRY(check_matrix(v, T, Hkv * D, ldv, eb));
+    FP8_TRY(check_matrix(cos_sin, T > 0 ? P : 0, rot_dim, rot_dim, 4));
+    FP8_TRY(check_vector(scales, T > 0 ? 2 * Hkv * D : 0));
+    FP8_TRY(check_matrix(cache, num_slots, 2 * Hkv * D, 2 * Hkv * D, 1, true));
+    if (T > 0 && (positions == nullptr || (Hkv > 0 && slot_mapping == nullptr))) return FP8_ERR_INVALID_ARGUMENT;
+    if (((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slot_mapping)) & 3u) != 0)
+        return FP8_ERR_UNSUPPORTED;
+    if (T == 0 || P == 0 || Hq + Hkv == 0) return FP8_OK;
+    fp8k::KvAppend p;
+    p.q = q, p.k = k, p.v = v, p.q_out = q_out;
+    p.ldq = ldq, p.ldk = ldk, p.ldv = ldv, p.ldqo = ldqo;
+    p.positions = positions, p.cos_sin = cos_sin, p.scales = scales, p.slot = slot_mapping;
+    p.cache = cache, p.num_slots = num_slots;
+    p.T = (int)T, p.Hq = (int)Hq, p.Hkv = (int)Hkv, p.D = (int)D, p.rot = (int)rot_dim, p.P = (int)P;
+    p.tokens_per_block = 1;
+    return from_hip(fp8k::launch_kv_append_rope(p, (int)dtype, (int)fmt, interleaved != 0, stream));
+}
+
+size_t fp8_attn_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size,
+                                       int64_t max_blocks, int64_t max_len) {
+    if (check_attn_dims(B, B, Hq, Hkv, D, block_size, max_blocks, 1, max_len) != FP8_OK) return SIZE_MAX;
+    return attn_ws(B, B, Hq, Hkv, D, block_size, max_blocks, 1, max_len);
+}
+
+fp8_status_t fp8_attn_decode_paged(const void* q, int64_t ldq, fp8_kv_dtype_t dtype, const uint8_t* cache,
+                                   int64_t num_blocks, int64_t block_size, const float* scales, fp8_kv_format_t fmt,
+                                   const int32_t* block_table, int64_t ld_table, int64_t max_blocks,
+                                   const int32_t* seq_lens, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                   int64_t max_len, float sm_scale, float softcap, const float* alibi_slopes,
+                                   int64_t window, void* out, int64_t ldo, float* lse, void* ws, size_t ws_bytes,
+                                   hipStream_t stream) {
+    fp8k::PagedAttn p = {};
+    p.q = q, p.ldq = ldq, p.out = out, p.ldo = ldo, p.lse = lse;
+    p.cache = cache, p.num_blocks = num_blocks, p.scales = scales;
+    p.block_table = block_table, p.ld_table = ld_table, p.seq_lens = seq_lens;
+    p.softcap = softcap, p.alibi = alibi_slopes, p.causal = 1;
+    return attn(p, dtype, fmt, B, B, Hq, Hkv, D, block_size, max_blocks, 1, max_len, window, sm_scale, ws, ws_bytes,
+                stream);
+}
+
+size_t fp8_attn_prefill_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size,
+                                        int64_t max_blocks, int64_t max_q, int64_t max_len) {
+    if (check_attn_dims(T, B, Hq, Hkv, D, block_size, max_blocks, max_q, max_len) != FP8_OK) return SIZE_MAX;
+    return attn_ws(T, B, Hq, Hkv, D, block_size, max_blocks, hint(max_q, T), max_len);
+}
+
+fp8_status_t fp8_attn_prefill_paged(const void* q, int64_t ldq, fp8_kv_dtype_t dtype, const int32_t* cu_q, int64_t T,
+                                    const uint8_t* cache, int64_t num_blocks, int64_t block_size, const float* scales,
+                                    fp8_kv_format_t fmt, const int32_t* block_table, int64_t ld_table,
+                                    int64_t max_blocks, const int32_t* seq_lens, int64_t B, int64_t Hq, int64_t Hkv,
+                                    int64_t D, int64_t max_q, int64_t max_len, int32_t causal,
+                                    const int32_t* prefix_lens, float sm_scale, float softcap,
+                                    const float* alibi_slopes, int64_t window, void* out, int64_t ldo, float* lse,
+                                    void* ws, size_t ws_bytes, hipStream_t stream) {
+    if (T > 0 && B > 0 && cu_q == nullptr) return FP8_ERR_INVALID_ARGUMENT;
+    fp8k::PagedAttn p = {};
+    p.q = q, p.ldq = ldq, p.out = out, p.ldo = ldo, p.lse = lse, p.cu_q = cu_q;
+    p.cache = cache, p.num_blocks = num_blocks, p.scales = scales;
+    p.block_table = block_table, p.ld_table = ld_table, p.seq_lens = seq_lens, p.prefix = prefix_lens;
+    p.softcap = softcap, p.alibi = alibi_slopes, p.causal = causal != 0;
+    return attn(p, dtype, fmt, T, B, Hq, Hkv, D, block_size, max_blocks, max_q < 0 ? max_q : hint(max_q, std::max<int64_t>(T, 0)), max_len, window,
+                sm_scale, ws, ws_bytes, stream);
 }
 
 fp8_status_t fp8_gemm_scaled(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw,

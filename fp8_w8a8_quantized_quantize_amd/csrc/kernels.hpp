@@ -50,6 +50,51 @@ hipError_t launch_kv_dequantize_paged(const uint8_t* cache, int64_t num_slots, c
                                       int64_t C, const float* scales, int fmt, void* out, int out_dtype, int64_t ldo,
                                       hipStream_t stream);
 
+// Append with rotation (kv_append.hip): strides in elements, rows 16-byte
+// aligned, D and rot multiples of 16, q may be null with Hq == 0.
+// tokens_per_block is the launcher's.
+struct KvAppend {
+    const void *q, *k, *v;
+    void* q_out;
+    int64_t ldq, ldk, ldv, ldqo;
+    const int32_t* positions;
+    const float* cos_sin;
+    const float* scales;
+    const int32_t* slot;
+    uint8_t* cache;
+    int64_t num_slots;
+    int T, Hq, Hkv, D, rot, P, tokens_per_block;
+};
+hipError_t launch_kv_append_rope(const KvAppend& p, int dtype, int fmt, bool interleaved, hipStream_t stream);
+
+// Attention over the paged cache (attn_paged.hip).  Sequence b owns q rows
+// [cu_q[b], cu_q[b + 1]) (row b when cu_q is null) of `rows` rows in all;
+// its key j lies in cache row block_table[b][j / block] * block + j % block.
+// scale2: the score scale times log2(e); softcap 0, window 0, alibi null and
+// prefix null turn those off.
+struct PagedAttn {
+    const void* q;
+    void* out;
+    float* lse;  // [rows, Hq], may be null
+    int64_t ldq, ldo;
+    const int32_t* cu_q;
+    const uint8_t* cache;
+    int64_t num_blocks;
+    const float* scales;
+    const int32_t* block_table;
+    int64_t ld_table;
+    const int32_t* seq_lens;
+    const int32_t* prefix;
+    const float* alibi;
+    float scale, softcap;
+    int B, rows, Hq, Hkv, block, max_blocks, window, causal, dtype;
+};
+// max_q and max_len plan the launch; longer rows and sequences are still
+// computed whole.  ws: attn_paged_ws_bytes bytes, 16-byte aligned.
+size_t attn_paged_ws_bytes(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_len);
+hipError_t launch_attn_paged(const PagedAttn& p, int D, int fmt, int64_t max_q, int64_t max_len, void* ws,
+                             hipStream_t stream);
+
 // The dense GEMM launchers write BF16 y, or, when y32 is not null, the fp32
 // value acc * (s_tok * s_ch) before rounding to y32 (same row stride ldy).
 

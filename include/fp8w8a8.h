@@ -351,6 +351,104 @@ fp8_status_t fp8_kv_dequantize_paged(const uint8_t* cache, int64_t num_slots, co
                                      fp8_kv_dtype_t out_dtype, int64_t ldo, hipStream_t stream);
 
 /*
+ * Append to the paged FP8 KV cache with the rotary position embedding applied
+ * on the way (cache format as above): rotates the queries and keys of T tokens
+ * by their positions and writes the keys and values as FP8 codes, in one pass.
+ *   turn(x): for each pair (a, b) of the first rot_dim elements of a head and
+ *     its cosine c and sine s from row positions[t] of cos_sin,
+ *     a' = fl32(fl32(a c) - fl32(b s)),  b' = fl32(fl32(b c) + fl32(a s));
+ *     pair i is elements (i, i + rot_dim / 2), or (2 i, 2 i + 1) when
+ *     interleaved != 0; elements from rot_dim on stay as they are;
+ *   q_out[t, h]             = round(turn(q[t, h]))            to q's type, RNE
+ *   cache[slot, h D + d]            = enc_fmt(fl32(turn(k[t, h])[d] / s))
+ *   cache[slot, (Hkv + h) D + d]    = enc_fmt(fl32(v[t, h][d] / s)),
+ *     slot = slot_mapping[t], s = max(scales[channel], 1e-12f)
+ * so a cache row is 2 Hkv D channels, K heads first: the codes are those of
+ * fp8_kv_quantize_paged on the rotated row.
+ * q, k, v, q_out: dtype elements [T, heads, D], heads adjacent (element stride
+ * D), row strides ldq, ldk, ldv, ldqo elements, rows 16-byte aligned (slices
+ * of one QKV projection output qualify).  q_out may be q itself (same pointer
+ * and stride), else they must not overlap; q and q_out may be NULL with
+ * Hq == 0, k and v with Hkv == 0.  cos_sin: fp32 [P, rot_dim], rot_dim / 2
+ * cosines then rot_dim / 2 sines, 16-byte aligned.  A token whose slot is
+ * outside [0, num_slots) (padding carries -1) writes no cache row; one whose
+ * position is outside [0, P) writes nothing at all, q_out included.  Two
+ * tokens naming the same slot race.  D and rot_dim are multiples of 16,
+ * 16 <= rot_dim <= D.  No workspace.
+ */
+fp8_status_t fp8_kv_append_rope_paged(const void* q, int64_t ldq, void* q_out, int64_t ldqo, const void* k,
+                                      int64_t ldk, const void* v, int64_t ldv, fp8_kv_dtype_t dtype, int64_t T,
+                                      int64_t Hq, int64_t Hkv, int64_t D, const int32_t* positions,
+                                      const float* cos_sin, int64_t P, int64_t rot_dim, int32_t interleaved,
+                                      const float* scales, fp8_kv_format_t fmt, const int32_t* slot_mapping,
+                                      uint8_t* cache, int64_t num_slots, hipStream_t stream);
+
+/*
+ * Attention over the paged FP8 KV cache (FP32 softmax beside FP8 K and V:
+ * DeepSeek V4 950 page, §2.3; paged FP8 blocks and the online softmax over
+ * them: 512K-context page, §3.3).  Sequence b has seq_lens[b] keys; key j is
+ * cache row block_table[b, j / block_size] * block_size + j % block_size, a
+ * row as fp8_kv_append_rope_paged lays it out.  With k, v the decoded values
+ * fl32(dec(code) * max(scale, 1e-12f)) of KV head h / (Hq / Hkv):
+ *   score(q, j) = cap(sm_scale * sum_d q[d] k_j[d]) + slope_h * (j - pos)
+ *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(score_j - max_j score_j)
+ *   lse = log(sum_j exp(score_j))
+ * over the keys the query sees; cap(x) = softcap * tanh(x / softcap) when
+ * softcap > 0, else x; slope_h = alibi_slopes[h] (fp32 [Hq]) or 0 when NULL.
+ *   decode:  one query per sequence, the newest token: pos = seq_lens[b] - 1,
+ *            keys j <= pos;
+ *   prefill: sequence b's new tokens are rows [cu_q[b], cu_q[b + 1]) of q
+ *            (cu_q int32 [B + 1], device); row i of n is at
+ *            pos = seq_lens[b] - n + i and sees keys j <= pos, and those below
+ *            prefix_lens[b] (int32 [B], or NULL), when causal != 0; every key
+ *            of the sequence otherwise.
+ * window > 0 hides keys with pos - j >= window.  The new tokens' own keys and
+ * values are in the cache already (append first).  A query that sees no key
+ * (an empty sequence, more new tokens than keys) gives a row of +0 and
+ * lse -inf.  The softmax, its sums and the products accumulate in fp32; out is
+ * rounded once, RNE, to q's type.
+ * q, out: dtype elements [rows, Hq, D], heads adjacent, row strides ldq, ldo,
+ * rows 16-byte aligned; lse fp32 [rows, Hq] or NULL; out does not overlap q.
+ * cache: u8 [num_blocks * block_size, 2 Hkv D]; scales fp32 [2 Hkv D];
+ * block_table int32 [B, max_blocks], row stride ld_table.  D is 64, 128 or
+ * 256 and Hq a multiple of Hkv; any block_size >= 1.
+ * max_q and max_len plan the launch: bounds of the new rows and of the length
+ * of one sequence, 0 for not known.  They may be wrong: longer sequences are
+ * still computed whole, only slower.
+ * The device arrays are not validated: lengths are taken within
+ * [0, max_blocks * block_size], rows within [0, T); a page number outside
+ * [0, num_blocks) hides its keys.  Rows of q that no sequence owns are left as
+ * they were in out and lse.  Codes no query sees (stale rows of a page, NaN
+ * codes among them) do not matter; within a sequence inputs are assumed finite.
+ * ws: at least the matching *_workspace_bytes of the same arguments, 16-byte
+ * aligned (key shares of long sequences; may be NULL when that is 0; contents
+ * on entry do not matter).  Results do not depend on timing: shares are joined
+ * in a fixed order.
+ */
+fp8_status_t fp8_attn_decode_paged(const void* q, int64_t ldq, fp8_kv_dtype_t dtype, const uint8_t* cache,
+                                   int64_t num_blocks, int64_t block_size, const float* scales, fp8_kv_format_t fmt,
+                                   const int32_t* block_table, int64_t ld_table, int64_t max_blocks,
+                                   const int32_t* seq_lens, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                   int64_t max_len, float sm_scale, float softcap, const float* alibi_slopes,
+                                   int64_t window, void* out, int64_t ldo, float* lse, void* ws, size_t ws_bytes,
+                                   hipStream_t stream);
+
+fp8_status_t fp8_attn_prefill_paged(const void* q, int64_t ldq, fp8_kv_dtype_t dtype, const int32_t* cu_q, int64_t T,
+                                    const uint8_t* cache, int64_t num_blocks, int64_t block_size, const float* scales,
+                                    fp8_kv_format_t fmt, const int32_t* block_table, int64_t ld_table,
+                                    int64_t max_blocks, const int32_t* seq_lens, int64_t B, int64_t Hq, int64_t Hkv,
+                                    int64_t D, int64_t max_q, int64_t max_len, int32_t causal,
+                                    const int32_t* prefix_lens, float sm_scale, float softcap,
+                                    const float* alibi_slopes, int64_t window, void* out, int64_t ldo, float* lse,
+                                    void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes of the two calls (host only; SIZE_MAX for sizes they refuse). */
+size_t fp8_attn_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size,
+                                       int64_t max_blocks, int64_t max_len);
+size_t fp8_attn_prefill_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size,
+                                        int64_t max_blocks, int64_t max_q, int64_t max_len);
+
+/*
  * HBM read ceiling (a measurement utility beside the layer, not part of it):
  * reads the `bytes` bytes at p once with plain 16-byte vector loads
  * (nontemporal loads when `nontemporal` != 0) from about `workgroups`
