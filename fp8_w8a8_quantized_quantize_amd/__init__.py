@@ -47,6 +47,7 @@ EXPORTS = ("fp8_quantize_per_token", "fp8_quantize_static", "fp8_quantize_per_to
            "fp8_status_string")
 
 _lib = None
+_torch_module = None
 
 
 class Fp8Error(RuntimeError):
@@ -137,8 +138,11 @@ def _check(fn, code):
 
 
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream):
@@ -452,6 +456,10 @@ def fp8_kv_dequantize_paged(cache, slot_mapping, scales, fmt="e5m2", out=None, o
     return out
 
 
+# The attention calls are a few microseconds of GPU work at small sizes, so
+# their argument checks take a tensor's facts once and only spell out what is
+# wrong (through the checks above) when something is.
+
 def _on_stream(fn):
     """Runs fn with the first argument's device current and, when a stream is
     given, with that stream current: what fn allocates (outputs, workspace)
@@ -468,7 +476,7 @@ def _on_stream(fn):
                 raise ValueError(f"stream: on {stream.device}, expected {t.device}")
             with torch.cuda.stream(stream):
                 return fn(t, *args, **kwargs)
-        if t.device.index != torch.cuda.current_device():
+        if t.get_device() != torch.cuda.current_device():
             with torch.cuda.device(t.device):
                 return fn(t, *args, **kwargs)
         return fn(t, *args, **kwargs)
@@ -476,18 +484,47 @@ def _on_stream(fn):
     return call
 
 
-def _heads(t, name, device=None, dtype=None):
-    """[T, H, D] with the heads of a row adjacent -> (T, H, D, row stride, dtype code)."""
-    code = _kv_dtype(t, name, device)
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+def _raw_stream(di):
+    """The current stream of device number di, as a pointer."""
+    get = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+    return get(di) if get is not None else _torch().cuda.current_stream(di).cuda_stream
+
+
+def _heads(t, name, di=None, dtype=None):
+    """[T, H, D] with the heads of a row adjacent, on device number di and of
+    dtype when given -> (T, H, D, row stride, address)."""
+    if dtype is None or not isinstance(t, _torch().Tensor) or t.dtype is not dtype or t.get_device() != di:
+        _kv_dtype(t, name)
+        if dtype is not None and t.dtype is not dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+        if di is not None and t.get_device() != di:
+            raise ValueError(f"{name}: on {t.device}, expected device {di}")
     if t.dim() != 3:
         raise ValueError(f"{name}: expected a 3-D tensor [tokens, heads, head_dim]")
     n, h, d = t.shape
     s0, s1, s2 = t.stride()
-    if n and h and d and ((d > 1 and s2 != 1) or (h > 1 and s1 != d)):
+    if (s2 != 1 and d > 1 or s1 != d and h > 1) and n and h and d:
         raise ValueError(f"{name}: expected the heads of a token adjacent (strides [*, head_dim, 1])")
-    return n, h, d, (s0 if n > 1 else h * d), code
+    return n, h, d, (s0 if n > 1 else h * d), t.data_ptr()
+
+
+def _flat(t, dtype, name, n, di):
+    """Address of a contiguous tensor of n elements on device number di."""
+    if isinstance(t, _torch().Tensor) and t.dtype is dtype and t.get_device() == di and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
+    _vec(t, dtype, name, n)
+    raise ValueError(f"{name}: on {t.device}, expected device {di}")
+
+
+def _paged_cache(cache, di):
+    """(slots, channels, address) of a uint8 cache [num_slots, channels]."""
+    torch = _torch()
+    if not (isinstance(cache, torch.Tensor) and cache.dtype is torch.uint8 and cache.get_device() == di and cache.dim() == 2
+            and cache.is_contiguous()):
+        _kv_cache(cache)
+        raise ValueError(f"cache: on {cache.device}, expected device {di}")
+    slots, C = cache.shape
+    return slots, C, cache.data_ptr()
 
 
 @_on_stream
@@ -499,68 +536,88 @@ def fp8_kv_append_rope_paged(k, v, positions, cos_sin, scales, slot_mapping, cac
     uint8 cache [num_slots, 2 * Hkv * D]; returns the rotated q (q_out, which may
     be q itself), or None without q.  stream: the stream to run on."""
     torch = _torch()
-    dev = k.device
-    T, Hkv, D, ldk, dt = _heads(k, "k")
-    if _heads(v, "v", dev, k.dtype)[:3] != (T, Hkv, D):
+    dt = _kv_dtype(k, "k")
+    dtype, di = k.dtype, k.get_device()
+    T, Hkv, D, ldk, kp = _heads(k, "k", di, dtype)
+    Tv, Hv, Dv, ldv, vp = _heads(v, "v", di, dtype)
+    if (Tv, Hv, Dv) != (T, Hkv, D):
         raise ValueError("v: expected k's shape")
-    ldv = v.stride(0) if T > 1 else Hkv * D
-    Hq = ldq = ldqo = 0
+    Hq = ldq = ldqo = qp = qop = 0
     if q is not None:
-        Tq, Hq, Dq, ldq, _ = _heads(q, "q", dev, k.dtype)
+        Tq, Hq, Dq, ldq, qp = _heads(q, "q", di, dtype)
         if (Tq, Dq) != (T, D):
             raise ValueError("q: expected shape [T, Hq, D] with k's T and D")
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
-        if _heads(q_out, "q_out", dev, k.dtype)[:3] != (T, Hq, D):
+            q_out = q.new_empty((T, Hq, D))
+        To, Ho, Do, ldqo, qop = _heads(q_out, "q_out", di, dtype)
+        if (To, Ho, Do) != (T, Hq, D):
             raise ValueError("q_out: expected q's shape")
-        ldqo = q_out.stride(0) if T > 1 else Hq * D
     elif q_out is not None:
         raise ValueError("q_out: given without q")
-    _on_device(cos_sin, torch.float32, "cos_sin", dev)
-    if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-        raise ValueError("cos_sin: expected a contiguous fp32 tensor [P, rot_dim]")
-    _vec(positions, torch.int32, "positions", T, dev)
-    _vec(slot_mapping, torch.int32, "slot_mapping", T, dev)
-    _vec(scales, torch.float32, "scales", 2 * Hkv * D, dev)
-    _kv_cache(cache, 2 * Hkv * D, dev)
+    C = 2 * Hkv * D
+    if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+        raise TypeError("cos_sin: expected a contiguous float32 CUDA tensor [P, rot_dim]")
+    P, rot = cos_sin.shape
+    slots, cols, cp = _paged_cache(cache, di)
+    if cols != C:
+        raise TypeError("cache: expected a contiguous uint8 CUDA tensor [num_slots, 2 * Hkv * D]")
+    i32, f32 = torch.int32, torch.float32
     _check("fp8_kv_append_rope_paged",
-           lib().fp8_kv_append_rope_paged(_ptr(q), ldq, _ptr(q_out), ldqo, _ptr(k), ldk, _ptr(v), ldv, dt, T, Hq, Hkv,
-                                          D, _ptr(positions), _ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1],
-                                          int(bool(interleaved)), _ptr(scales), _kv_fmt(fmt), _ptr(slot_mapping),
-                                          _ptr(cache), cache.shape[0], _stream(None)))
+           lib().fp8_kv_append_rope_paged(qp, ldq, qop, ldqo, kp, ldk, vp, ldv, dt, T, Hq, Hkv, D,
+                                          _flat(positions, i32, "positions", T, di),
+                                          _flat(cos_sin, f32, "cos_sin", P * rot, di), P, rot,
+                                          1 if interleaved else 0, _flat(scales, f32, "scales", C, di), _kv_fmt(fmt),
+                                          _flat(slot_mapping, i32, "slot_mapping", T, di), cp, slots, _raw_stream(di)))
     return q_out
 
 
-def _attn_args(q, cache, block_table, seq_lens, scales, block_size, sm_scale, alibi_slopes, out, lse):
-    """The checks both attention calls share -> (rows, B, Hq, Hkv, D, blocks, ldq, ldo, ld_table, dtype code, sm_scale, out)."""
+def _attn_args(q, cache, block_table, seq_lens, scales, block_size, alibi_slopes, out, lse):
+    """What both attention calls check -> (rows, B, table width, Hq, Hkv, D, blocks, ldq, ldo, ld_table, out, and the
+    addresses of q, cache, scales, block_table, seq_lens, alibi_slopes, out, lse)."""
     torch = _torch()
-    dev = q.device
-    rows, Hq, D, ldq, dt = _heads(q, "q")
-    _kv_cache(cache, None, dev)
-    slots, C = cache.shape
+    dtype, di = q.dtype, q.get_device()
+    rows, Hq, D, ldq, qp = _heads(q, "q", di, dtype)
+    slots, C, cp = _paged_cache(cache, di)
     if block_size < 1 or slots % block_size:
         raise ValueError("cache: expected [num_blocks * block_size, 2 * Hkv * D]")
     if D == 0 or C == 0 or C % (2 * D):
         raise ValueError("cache: rows are not 2 * Hkv * D codes of q's D")
-    Hkv = C // (2 * D)
-    _on_device(block_table, torch.int32, "block_table", dev)
-    if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype is not torch.int32 or block_table.get_device() != di:
+        _on_device(block_table, torch.int32, "block_table", q.device)
+    if block_table.dim() != 2:
         raise ValueError("block_table: expected a 2-D row-major int32 tensor [B, max_blocks]")
     B, width = block_table.shape
-    _vec(seq_lens, torch.int32, "seq_lens", B, dev)
-    _vec(scales, torch.float32, "scales", C, dev)
-    if alibi_slopes is not None:
-        _vec(alibi_slopes, torch.float32, "alibi_slopes", Hq, dev)
+    ld_table, one = block_table.stride()
+    if one != 1 and width > 1:
+        raise ValueError("block_table: expected a 2-D row-major int32 tensor [B, max_blocks]")
+    f32 = torch.float32
+    sp, lp = _flat(scales, f32, "scales", C, di), _flat(seq_lens, torch.int32, "seq_lens", B, di)
+    ap = 0 if alibi_slopes is None else _flat(alibi_slopes, f32, "alibi_slopes", Hq, di)
     if out is None:
-        out = torch.empty((rows, Hq, D), dtype=q.dtype, device=dev)
-    if _heads(out, "out", dev, q.dtype)[:3] != (rows, Hq, D):
+        out = q.new_empty((rows, Hq, D))
+    ro, ho, do, ldo, op = _heads(out, "out", di, dtype)
+    if (ro, ho, do) != (rows, Hq, D):
         raise ValueError("out: expected q's shape")
+    ep = 0
     if lse is not None:
-        _dense(lse, torch.float32, "lse", (rows, Hq), dev)
-    ldo = out.stride(0) if rows > 1 else Hq * D
-    ld_table = block_table.stride(0) if B > 1 else width
-    scale = D ** -0.5 if sm_scale is None else float(sm_scale)
-    return rows, B, width, Hq, Hkv, D, slots // block_size, ldq, ldo, ld_table, dt, scale, out
+        _dense(lse, f32, "lse", (rows, Hq), q.device)
+        ep = lse.data_ptr()
+    return (rows, B, width, Hq, C // (2 * D), D, slots // block_size, ldq, ldo, ld_table if B > 1 else width, out,
+            qp, cp, sp, block_table.data_ptr(), lp, ap, op, ep)
+
+
+def _attn_ws(ws, need, device):
+    """(workspace kept alive over the call, its address, its bytes)."""
+    torch = _torch()
+    if ws is None:
+        if need == 0 or need == SIZE_MAX:   # sizes the library refuses: the call says so
+            return None, 0, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _on_device(ws, torch.uint8, "ws", device)
+        if not ws.is_contiguous():
+            raise ValueError("ws: expected a contiguous uint8 tensor")
+    return ws, ws.data_ptr(), ws.numel()
 
 
 @_on_stream
@@ -577,21 +634,17 @@ def fp8_attn_decode_paged(q, cache, block_table, seq_lens, scales, block_size, f
     that receives the log-sum-exp.  ws: uint8 workspace of at least
     fp8_attn_decode_workspace_bytes(...) bytes, allocated when not given.
     stream: the stream to run on."""
-    (rows, B, width, Hq, Hkv, D, blocks, ldq, ldo, ld_table, dt, scale, out) = _attn_args(
-        q, cache, block_table, seq_lens, scales, block_size, sm_scale, alibi_slopes, out, lse)
+    dt = _kv_dtype(q, "q")
+    (rows, B, width, Hq, Hkv, D, blocks, ldq, ldo, ld_table, out, qp, cp, sp, tp, lp, ap, op, ep) = _attn_args(
+        q, cache, block_table, seq_lens, scales, block_size, alibi_slopes, out, lse)
     if rows != B:
         raise ValueError("q: expected one row per sequence of block_table")
-    max_len = int(max_len or 0)
-    need = int(lib().fp8_attn_decode_workspace_bytes(B, Hq, Hkv, D, block_size, width, max_len)) if ws is None else 0
-    if need and need != SIZE_MAX:
-        ws = _torch().empty(need, dtype=_torch().uint8, device=q.device)
-    elif ws is not None:
-        ws = _workspace(ws, 0, "fp8_attn_decode_paged", q.device)
+    max_len = max_len or 0
+    ws, wp, wn = _attn_ws(ws, fp8_attn_decode_workspace_bytes(B, Hq, Hkv, D, block_size, width, max_len), q.device)
     _check("fp8_attn_decode_paged",
-           lib().fp8_attn_decode_paged(_ptr(q), ldq, dt, _ptr(cache), blocks, block_size, _ptr(scales), _kv_fmt(fmt),
-                                       _ptr(block_table), ld_table, width, _ptr(seq_lens), B, Hq, Hkv, D, max_len,
-                                       scale, softcap, _ptr(alibi_slopes), window, _ptr(out), ldo, _ptr(lse),
-                                       _ptr(ws), _nbytes(ws), _stream(None)))
+           lib().fp8_attn_decode_paged(qp, ldq, dt, cp, blocks, block_size, sp, _kv_fmt(fmt), tp, ld_table, width, lp, B,
+                                       Hq, Hkv, D, max_len, D ** -0.5 if sm_scale is None else sm_scale, softcap, ap,
+                                       window, op, ldo, ep, wp, wn, _raw_stream(q.get_device())))
     return out
 
 
@@ -608,32 +661,30 @@ def fp8_attn_prefill_paged(q, cu_q, cache, block_table, seq_lens, scales, block_
     were (uninitialised when out is allocated here).  max_q: the most new tokens of
     one sequence when the host knows it.  The other arguments as for
     fp8_attn_decode_paged."""
-    torch = _torch()
-    (T, B, width, Hq, Hkv, D, blocks, ldq, ldo, ld_table, dt, scale, out) = _attn_args(
-        q, cache, block_table, seq_lens, scales, block_size, sm_scale, alibi_slopes, out, lse)
-    _vec(cu_q, torch.int32, "cu_q", B + 1, q.device)
-    if prefix_lens is not None:
-        _vec(prefix_lens, torch.int32, "prefix_lens", B, q.device)
-    max_q, max_len = int(max_q or 0), int(max_len or 0)
-    need = int(lib().fp8_attn_prefill_workspace_bytes(T, B, Hq, Hkv, D, block_size, width, max_q, max_len)) if ws is None else 0
-    if need and need != SIZE_MAX:
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif ws is not None:
-        ws = _workspace(ws, 0, "fp8_attn_prefill_paged", q.device)
+    dt = _kv_dtype(q, "q")
+    (T, B, width, Hq, Hkv, D, blocks, ldq, ldo, ld_table, out, qp, cp, sp, tp, lp, ap, op, ep) = _attn_args(
+        q, cache, block_table, seq_lens, scales, block_size, alibi_slopes, out, lse)
+    i32, di = _torch().int32, q.get_device()
+    cup = _flat(cu_q, i32, "cu_q", B + 1, di)
+    pp = 0 if prefix_lens is None else _flat(prefix_lens, i32, "prefix_lens", B, di)
+    max_q, max_len = max_q or 0, max_len or 0
+    ws, wp, wn = _attn_ws(ws, fp8_attn_prefill_workspace_bytes(T, B, Hq, Hkv, D, block_size, width, max_q, max_len),
+                          q.device)
     _check("fp8_attn_prefill_paged",
-           lib().fp8_attn_prefill_paged(_ptr(q), ldq, dt, _ptr(cu_q), T, _ptr(cache), blocks, block_size, _ptr(scales),
-                                        _kv_fmt(fmt), _ptr(block_table), ld_table, width, _ptr(seq_lens), B, Hq, Hkv,
-                                        D, max_q, max_len, int(bool(causal)), _ptr(prefix_lens), scale, softcap,
-                                        _ptr(alibi_slopes), window, _ptr(out), ldo, _ptr(lse), _ptr(ws), _nbytes(ws),
-                                        _stream(None)))
+           lib().fp8_attn_prefill_paged(qp, ldq, dt, cup, T, cp, blocks, block_size, sp, _kv_fmt(fmt), tp, ld_table,
+                                        width, lp, B, Hq, Hkv, D, max_q, max_len, 1 if causal else 0, pp,
+                                        D ** -0.5 if sm_scale is None else sm_scale, softcap, ap, window, op, ldo, ep,
+                                        wp, wn, _raw_stream(di)))
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def fp8_attn_decode_workspace_bytes(B, Hq, Hkv, D, block_size, max_blocks, max_len=0):
     """Workspace bytes of fp8_attn_decode_paged."""
     return int(lib().fp8_attn_decode_workspace_bytes(B, Hq, Hkv, D, block_size, max_blocks, max_len))
 
 
+@functools.lru_cache(maxsize=1024)
 def fp8_attn_prefill_workspace_bytes(T, B, Hq, Hkv, D, block_size, max_blocks, max_q=0, max_len=0):
     """Workspace bytes of fp8_attn_prefill_paged."""
     return int(lib().fp8_attn_prefill_workspace_bytes(T, B, Hq, Hkv, D, block_size, max_blocks, max_q, max_len))

@@ -118,7 +118,7 @@ fp8_status_t check_attn_dims(int64_t rows, int64_t B, int64_t Hq, int64_t Hkv, i
         return FP8_ERR_INVALID_ARGUMENT;
     if (block_size < 1 || Hkv < 1 || Hq % Hkv != 0) return FP8_ERR_INVALID_ARGUMENT;
     if (D != 64 && D != 128 && D != 256) return FP8_ERR_UNSUPPORTED;
-    if (rows > kMaxAttn || B > kMaxAttn || Hq > kMaxAttn / D || block_size > kMaxAttn || max_blocks > kMaxAttn)
+    if (Hkv > 65535 || rows > kMaxAttn || B > kMaxAttn || Hq > kMaxAttn / D || block_size > kMaxAttn || max_blocks > kMaxAttn)
         return FP8_ERR_UNSUPPORTED;
     if (block_size * max_blocks > kMaxAttn || rows * Hq > kMaxAttn || B * Hq > kMaxAttn / 16) return FP8_ERR_UNSUPPORTED;
     return FP8_OK;
@@ -130,8 +130,8 @@ int64_t hint(int64_t v, int64_t most) { return v > 0 ? std::min(v, most) : most;
 
 size_t attn_ws(int64_t rows, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size, int64_t max_blocks,
                int64_t max_q, int64_t max_len) {
-    return round_up(fp8k::attn_paged_ws_bytes(B, rows, Hq, Hkv, D, max_q, hint(max_len, block_size * max_blocks)),
-                    kAlign);
+    const int64_t all_len = block_size * max_blocks;
+    return round_up(fp8k::attn_paged_ws_bytes(B, rows, Hq, Hkv, D, max_q, hint(max_len, all_len), all_len), kAlign);
 }
 
 // Both attention entry points; cu_q null: one new row per sequence.
@@ -164,6 +164,10 @@ fp8_status_t attn(fp8k::PagedAttn p, fp8_kv_dtype_t dtype, fp8_kv_format_t fmt, 
     if (need > 0 && !aligned16(ws)) return FP8_ERR_UNSUPPORTED;
     if (!some) return FP8_OK;
     p.scale = sm_scale * 1.44269504088896341f;  // scores in powers of two
+    // The kernels may read (never use) one page number and one cache row: there is one of each, even in an empty table
+    // or pool.
+    if (max_blocks == 0) p.block_table = p.seq_lens, p.ld_table = 0;
+    if (p.num_blocks == 0) p.cache = reinterpret_cast<const uint8_t*>(p.scales);
     p.B = (int)B, p.rows = (int)rows, p.Hq = (int)Hq, p.Hkv = (int)Hkv;
     p.block = (int)block_size, p.max_blocks = (int)max_blocks;
     p.window = (int)std::min(window, kMaxAttn);  // no key is further back

@@ -19,21 +19,40 @@
 // matrix cores take 64 with both terms.  Scores, maxima, sums and outputs are
 // fp32.
 //
-// One pass with running maximum and sum.  Scores are formed transposed,
-// S^T = K Q^T, so that a lane's four results belong to one column: its maximum,
-// sum and rescale need no lane but the three others of that column, and its p
+// One pass with a running reference m and sum.  m is the maximum of the first
+// tile's scores and moves only when a score passes it by 2^5 (p stays below
+// 2^15 in fp16 and the result does not depend on m), so most tiles need no
+// other lane.  Scores are formed transposed, S^T = K Q^T, so that a lane's four
+// results belong to one column: its reference, sum and rescale need no lane but
+// the three others of that column, and its p
 // are, as they stand, the operand of O^T = V^T P^T.  The k index of that second
 // product may be any order as long as both operands share it: slot (g, e) of a
 // 32-key tile is key 16 (e / 4) + 4 g + e % 4, the keys whose scores the lane
 // group g holds.  Its V operand wants, per lane, one channel of 8 keys: a lane
-// loads D / 16 channels of its 8 keys and turns bytes around in registers
+// reads D / 16 channels of its 8 keys and turns bytes around in registers
 // (v_perm_b32; for E5M2, a cut-off fp16, the same instruction decodes).
 //
-// Split.  A workgroup is one KV head of one sequence and a share of its keys;
-// its four waves take 32-key tiles in turn and are joined in LDS.  Shares
-// beyond one per sequence go to the workspace and a second kernel joins them in
-// a fixed order.  No wave waits for another workgroup.
+// The codes come through LDS: whole rows by DMA (16 bytes a lane, D / 16
+// adjacent lanes a row), two tiles in flight per wave, each wave its own ring
+// and its own waits.  Read straight into the operand's registers, a key's row
+// is touched by lanes 16 apart: every lane is a request of its own, and with
+// about 70 of them outstanding per CU the kernel stood at 4.4 TB/s whatever it
+// computed (131072 tokens x 8 heads of 128: 72 us with the arithmetic taken out).
+// In LDS the 16-byte units of row r sit at u ^ swizzle(r), so that neither the
+// 16 rows of a K operand nor the row pieces of V meet in a bank.
+//
+// Split.  A workgroup's four waves are `hw` neighbouring KV heads (4, 2 or 1)
+// times 4 / hw key interleaves; a round is a 32-key tile for each of them, and
+// waves of one head are joined in LDS.  An item -- hw heads of one sequence and
+// column tile -- is a run of rounds.  Either every workgroup takes whole items,
+// or the runs of all items, laid end to end, are cut into one equal share per
+// workgroup, whatever the lengths are: every workgroup adds up the rounds of
+// all sequences (a scan) and finds its own share.  A share's first and last
+// item may be part of one; those parts go to the workspace, and a second kernel
+// joins them, in order, into the rows that were cut.  No wave waits for another
+// workgroup.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_common.hpp"
 
@@ -49,16 +68,29 @@ constexpr int kWaves = 4;      // waves of a workgroup
 constexpr int kCols = 16;      // query columns of a tile
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.44269504088896341f;
-constexpr float kPShift = 14.0f;  // p is held as p * 2^14
+constexpr float kPShift = 10.0f;  // p is held as p * 2^10
+constexpr float kSlack = 5.0f;    // and may pass 1 by 2^5, before its reference is moved
 
 struct StreamArgs {
     PagedAttn p;
     int group;         // query heads per KV head
-    int col_tiles;     // column tiles a KV head is planned for
-    int splits;        // key shares per (sequence, column tile)
-    int chunk;         // keys of a share per round, a multiple of kTile * kWaves
-    float* part_o;     // [splits][rows][Hq][D]
-    float2* part_ml;   // [splits][rows][Hq]: running maximum (log2), sum
+    int hw;            // KV heads of a workgroup
+    int col_tiles;     // whole items: column tiles a KV head is planned for
+    int log_shares;    // equal shares: their number's logarithm, -1 for whole items
+    int min_share;     // and their fewest rounds
+    float* part_o;     // [2 shares][hw][kCols][D]: parts of rows, a share's first and last
+    float2* part_ml;   // [2 shares][hw][kCols]: reference (log2), sum
+    int* starts;       // [B + 1]: cost before every sequence, cost of all
+    int spread;        // the join's thread groups per output row
+    int join_rows;     // and the new rows of a sequence it takes at a time
+    uint32_t magic;    // key / block = key * magic >> shift for keys below 2^31
+    int shift;
+
+    __device__ __forceinline__ int page(int key) const { return (int)(((uint64_t)(uint32_t)key * magic) >> shift); }
+    __device__ __forceinline__ int round_keys() const { return kTile * kWaves / hw; }
+    __device__ __forceinline__ int share_of(int total) const {
+        return max((total + (1 << log_shares) - 1) >> log_shares, min_share);
+    }
 };
 
 // A sequence's new rows and length, held inside the buffers whatever the
@@ -97,7 +129,91 @@ __device__ __forceinline__ void tile_keys(const PagedAttn& p, const Seq& s, int 
     int unused;
     visible(p, s, prefix, first, lo, unused);
     visible(p, s, prefix, last, unused, hi);
+    hi = max(hi, 0);
     lo = min(lo, hi);
+}
+
+// The keys any row of a sequence sees start at `base`, whole tiles of them; its
+// items' rounds, and the items of it (column tiles x head groups).
+struct Run {
+    int base, rounds, items;
+};
+
+__device__ __forceinline__ Run run_of(const StreamArgs& a, const Seq& s, int prefix) {
+    int lo, hi, unused;
+    visible(a.p, s, prefix, 0, lo, unused);
+    visible(a.p, s, prefix, s.nq - 1, unused, hi);
+    Run r;
+    // without a window every sequence starts at key 0
+    r.base = a.p.window > 0 ? min(lo, max(hi, 0)) / kTile * kTile : 0;
+    r.rounds = s.nq > 0 && hi > r.base ? (hi - r.base + a.round_keys() - 1) / a.round_keys() : 0;
+    r.items = r.rounds > 0 ? (s.nq * a.group + kCols - 1) / kCols * (a.p.Hkv / a.hw) : 0;
+    return r;
+}
+
+// Cost of an item's start (page and length look-ups, the first tiles' latency,
+// the join of its waves) in rounds: measured about 6 us against 1.5 us a round.
+constexpr int kItemCost = 4;
+
+// The sequence in which this workgroup's share starts, the cost before that
+// sequence, and the cost of all: thread i scans sequence i, 256 at a time.
+// Workgroup 0 leaves the starts for the join.
+struct Found {
+    int b, before, total;
+};
+
+__device__ __forceinline__ Found find_share(const StreamArgs& a, int* lds) {
+    const PagedAttn& p = a.p;
+    constexpr int kThreads = kWaves * kWave;
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    auto cost = [&](int b) {
+        const Run r = run_of(a, sequence(p, b), p.prefix ? p.prefix[b] : 0);
+        return (r.rounds + kItemCost) * r.items;
+    };
+    if (p.B == 1) {
+        const int total = cost(0);
+        if (blockIdx.x == 0 && tid == 0) a.starts[0] = 0, a.starts[1] = total;
+        return Found{0, 0, total};
+    }
+    int* const wave_sum = lds;       // [2][kWaves], by turns
+    int* const found = lds + 2 * kWaves;
+    int total = 0, before = 0, mine = 0, turn = 0;
+    const bool once = p.B <= kThreads;
+    for (int pass = 0; pass < 2; ++pass) {
+        const int share = a.share_of(total);
+        const int64_t start = (int64_t)blockIdx.x * share;  // of the second pass
+        int run = 0;
+        for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+            const int b = b0 + tid;
+            if (pass == 0 || !once) {
+                mine = b < p.B ? cost(b) : 0;
+                int sum = mine;
+#pragma unroll
+                for (int by = 1; by < kWave; by <<= 1) {
+                    const int v = __shfl_up(sum, by, kWave);
+                    if (lane >= by) sum += v;
+                }
+                int* const sums = wave_sum + turn * kWaves;
+                turn ^= 1;
+                if (lane == kWave - 1) sums[wave] = sum;
+                __syncthreads();
+                before = run + sum - mine;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) {
+                    if (w < wave) before += sums[w];
+                    run += sums[w];
+                }
+            }
+            if (pass == 1 && b < p.B) {
+                if (start >= before && start < before + mine) found[0] = b, found[1] = before;
+                if (blockIdx.x == 0) a.starts[b] = before;
+            }
+        }
+        if (pass == 0) total = run;
+    }
+    if (blockIdx.x == 0 && tid == 0) a.starts[p.B] = total;
+    __syncthreads();
+    return Found{found[0], found[1], total};  // nothing is found past the end: the caller looks at total
 }
 
 // Two codes (bytes j of even and odd) -> packed fp16, exact.
@@ -127,23 +243,30 @@ __device__ __forceinline__ v8h row_f16(uint32_t lo, uint32_t hi) {
     return __builtin_bit_cast(v8h, r);
 }
 
-// 8 consecutive elements of a query row as fp32.
-__device__ __forceinline__ void load_q8(const PagedAttn& p, int64_t e, float (&x)[8]) {
+// 8 consecutive elements of a query row, as they are and as fp32.
+__device__ __forceinline__ void load_q8(const PagedAttn& p, int64_t e, v4u (&raw)[2]) {
     if (p.dtype == kKvF32) {
-        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + e);
-        const float4 a = f[0], b = f[1];
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+        const v4u* f = reinterpret_cast<const v4u*>(static_cast<const float*>(p.q) + e);
+        raw[0] = f[0];
+        raw[1] = f[1];
     } else {
-        const v4u w = *reinterpret_cast<const v4u*>(static_cast<const uint16_t*>(p.q) + e);
+        raw[0] = *reinterpret_cast<const v4u*>(static_cast<const uint16_t*>(p.q) + e);
+        raw[1] = raw[0];
+    }
+}
+
+__device__ __forceinline__ void unpack_q8(const PagedAttn& p, const v4u (&raw)[2], float (&x)[8]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (p.dtype == kKvBF16) {
-                x[2 * i] = __uint_as_float(w[i] << 16);
-                x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            } else {
-                x[2 * i] = half_to_float(w[i] & 0xFFFFu);
-                x[2 * i + 1] = half_to_float(w[i] >> 16);
-            }
+    for (int i = 0; i < 4; ++i) {
+        if (p.dtype == kKvF32) {
+            x[i] = __uint_as_float(raw[0][i]);
+            x[4 + i] = __uint_as_float(raw[1][i]);
+        } else if (p.dtype == kKvBF16) {
+            x[2 * i] = __uint_as_float(raw[0][i] << 16);
+            x[2 * i + 1] = __uint_as_float(raw[0][i] & 0xFFFF0000u);
+        } else {
+            x[2 * i] = half_to_float(raw[0][i] & 0xFFFFu);
+            x[2 * i + 1] = half_to_float(raw[0][i] >> 16);
         }
     }
 }
@@ -159,14 +282,28 @@ __device__ __forceinline__ void store_o4(const PagedAttn& p, int64_t e, const fl
     }
 }
 
+// v of the lane 16 (32) away: gfx950's row and half swaps, no trip through LDS.
+__device__ __forceinline__ float swap16(float v) {
+    const uint32_t u = __float_as_uint(v);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return __uint_as_float((threadIdx.x & 16) ? r[0] : r[1]);
+}
+
+__device__ __forceinline__ float swap32(float v) {
+    const uint32_t u = __float_as_uint(v);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+// Over the four lanes of a column (16 and 32 apart).
 __device__ __forceinline__ float max_over_groups(float v) {
-    v = fmaxf(v, __shfl_xor(v, 16, kWave));
-    return fmaxf(v, __shfl_xor(v, 32, kWave));
+    v = fmaxf(v, swap16(v));
+    return fmaxf(v, swap32(v));
 }
 
 __device__ __forceinline__ float sum_over_groups(float v) {
-    v += __shfl_xor(v, 16, kWave);
-    return v + __shfl_xor(v, 32, kWave);
+    v += swap16(v);
+    return v + swap32(v);
 }
 
 // cap * tanh(x / cap) in fp32: 1 - 2 / (exp(2 x / cap) + 1), whose absolute
@@ -188,39 +325,112 @@ __device__ __forceinline__ void write_row(const PagedAttn& p, int64_t row, int h
     if (p.lse && d == 0) p.lse[row * p.Hq + h] = L == 0.0f ? -INFINITY : kLn2 * (M - kPShift + __builtin_amdgcn_logf(L));
 }
 
-// Codes of one 32-key tile as a wave holds them.
 template <int D>
-struct Codes {
-    v4u k[2][D / 64];   // K: keys 16 t + lane % 16, channels 64 i + 16 g ..
-    uint32_t v[8][D / 64];  // V: keys of slot (g, e), channels lane % 16 * D / 16 ..
+__device__ __forceinline__ int swizzle(int row) {
+    if constexpr (D == 64) return ((row >> 1) ^ (row >> 3)) & 3;
+    if constexpr (D == 128) return (row ^ (row >> 3)) & 7;
+    return row & 15;
+}
+
+__device__ __forceinline__ void compiler_fence() { asm volatile("" ::: "memory"); }
+
+// 16 bytes per lane into LDS: lane i's land at lds + 16 i (lds is wave-uniform).
+__device__ __forceinline__ void dma16(const uint8_t* src, uint8_t* lds) {
+    __builtin_amdgcn_global_load_lds(src, lds, 16, 0, 0);
+}
+
+// LDS of a workgroup: every wave's ring of two tiles (K rows, then V rows), the
+// rows' cache slots and page numbers, and the waves' maxima and sums; the ring is free again
+// when the waves' outputs are joined in it.
+template <int D>
+struct StreamLds {
+    static constexpr int kStages = D == 64 ? 4 : 2;
+    static constexpr int kRing = kStages * 2 * kTile * D;  // bytes of a wave
+    static constexpr int kSlots = kWaves * kRing;
+    static constexpr int kPages = kSlots + kWaves * kTile * 4;
+    static constexpr int kMl = kPages + kWaves * kStages * kWave * 4;
+    static constexpr int kBytes = kMl + kWaves * kCols * 8;
 };
 
-template <int D, int FMT>
+extern __shared__ __attribute__((aligned(1024))) uint8_t attn_smem[];
+
+__device__ __forceinline__ uint32_t word(uint32_t v, int) { return v; }
+__device__ __forceinline__ uint32_t word(const v2u& v, int i) { return v[i]; }
+__device__ __forceinline__ uint32_t word(const v4u& v, int i) { return v[i]; }
+
+// BIAS: the score cap and the distance bias are compiled in.
+template <int D, int FMT, bool BIAS>
 __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(StreamArgs a) {
     const PagedAttn& p = a.p;
-    constexpr int kParts = D == 256 ? 2 : 1;  // rounds of the waves' join (34 KB of LDS)
-    constexpr int kI = 4 / kParts;
-    constexpr int NJ = D / 32;  // matrix instructions along the channels of K
-    constexpr int VB = D / 16;  // V channels of a lane
-    __shared__ int slots_lds[kWaves][kTile];
-    __shared__ float2 ml_lds[kWaves][kCols];
-    __shared__ float o_lds[kWaves][kCols][D / kParts + 4];
+    constexpr int NJ = D / 32;           // matrix instructions along the channels of K
+    constexpr int VB = D / 16;           // V channels of a lane
+    constexpr int UR = D / 16;           // 16-byte units of a row
+    constexpr int RI = kWave / UR;       // rows of one DMA instruction
+    constexpr int NI = kTile / RI;       // DMA instructions of a tile's K, and of its V
+    using Lds = StreamLds<D>;
+    constexpr int S = Lds::kStages;
+    constexpr int kTileBytes = 2 * kTile * D;
+    constexpr int kOutRow = D + 4;       // floats of a joined row, padded off the banks
+    static_assert(kCols * kOutRow * 4 <= Lds::kRing, "a wave's outputs fit its ring");
 
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+    uint8_t* const ring = attn_smem + wave * Lds::kRing;
+    int* const slots = reinterpret_cast<int*>(attn_smem + Lds::kSlots) + wave * kTile;
+    int* const pages = reinterpret_cast<int*>(attn_smem + Lds::kPages) + wave * S * kWave;
+    float2* const ml = reinterpret_cast<float2*>(attn_smem + Lds::kMl);
     const int n = lane % 16, g = lane / 16;
-    int id = blockIdx.x;
-    const int hk = id % p.Hkv;
-    id /= p.Hkv;
-    const int ct0 = id % a.col_tiles;
-    id /= a.col_tiles;
-    const int split = id % a.splits;
-    const int b = id / a.splits;
-    const Seq seq = sequence(p, b);
-    const int prefix = p.prefix ? p.prefix[b] : 0;
-    const int64_t C = 2 * (int64_t)p.Hkv * D;
-    const int32_t* table = p.block_table + (int64_t)b * p.ld_table;
+    const int head_groups = p.Hkv / a.hw;
+    const uint32_t C = 2u * p.Hkv * D;
+    const int last_page = max(p.max_blocks - 1, 0);
 
-    for (int ct = ct0; ct * kCols < seq.nq * a.group; ct += a.col_tiles) {
+    // the first item: a whole one, or where this workgroup's share starts
+    int b = blockIdx.x, ct = 0, hg = 0, at_item = 0;  // at_item: cost of the item before this share
+    int left = 0;  // cost left of the share
+    if (a.log_shares >= 0) {
+        const Found f = find_share(a, reinterpret_cast<int*>(attn_smem));
+        const int share = a.share_of(f.total);
+        const int64_t start = (int64_t)blockIdx.x * share;
+        left = (int)min((int64_t)share, f.total - start);
+        if (left <= 0) return;
+        b = __builtin_amdgcn_readfirstlane(f.b);
+        const Run r = run_of(a, sequence(p, b), p.prefix ? p.prefix[b] : 0);
+        const int at = (int)start - f.before, item = at / (r.rounds + kItemCost);
+        at_item = __builtin_amdgcn_readfirstlane(at - item * (r.rounds + kItemCost));
+        ct = __builtin_amdgcn_readfirstlane(item / head_groups);
+        hg = __builtin_amdgcn_readfirstlane(item - ct * head_groups);
+        __syncthreads();
+    } else {
+        ct = blockIdx.z;
+        hg = blockIdx.y;
+    }
+
+    while (b < p.B) {
+        const Seq seq = sequence(p, b);
+        const int prefix = p.prefix ? p.prefix[b] : 0;
+        const Run run = run_of(a, seq, prefix);
+        int r0 = 0, r1 = run.rounds;  // its rounds that are this workgroup's
+        bool mine = true;
+        if (a.log_shares < 0) {
+            if (ct * kCols >= seq.nq * a.group) break;
+        } else {
+            if (run.items == 0 || ct * kCols >= seq.nq * a.group) {
+                ct = hg = 0, ++b;  // the next sequence
+                continue;
+            }
+            const int taken = min(left, run.rounds + kItemCost - at_item);
+            r0 = max(at_item - kItemCost, 0);
+            r1 = max(at_item + taken - kItemCost, 0);
+            mine = r1 > r0;  // else the share ends in the item's start, which the next one then pays for
+            left -= taken;
+            at_item = 0;
+        }
+        // where the result goes: the rows, or the share's first or last part
+        const int part = r0 == 0 && r1 == run.rounds ? -1 : 2 * (int)blockIdx.x + (r0 == 0);
+        const int hk0 = hg * a.hw, hk = hk0 + wave % a.hw;
+        const int32_t* table = p.block_table + (int64_t)b * p.ld_table;
+
+        if (!mine) break;
+
         // this lane's column
         const int col = ct * kCols + n;
         const bool has_col = col < seq.nq * a.group;
@@ -231,21 +441,91 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
         visible(p, seq, prefix, qi, lo, hi);
         if (!has_col) hi = 0;
         tile_keys(p, seq, prefix, a.group, ct, tlo, thi);
-        const int base = tlo / kTile * kTile;
-        const int chunk_tiles = a.chunk / (kTile * kWaves);  // tiles a wave takes of one chunk
 
-        // q times the key scales, as two fp16 terms
+        const float slope = p.alibi ? p.alibi[head] * kLog2e : 0.0f;
+        const int pos = seq.len - seq.nq + qi;
+        const float cap_in = p.softcap > 0.0f ? 2.0f * kLog2e / p.softcap : 0.0f;
+
+        float m = -INFINITY, l = 0.0f;
+        v4f o[VB];
+#pragma unroll
+        for (int j = 0; j < VB; ++j) o[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+
+        // this wave's tiles: keys k0 + stride i and on, up to `end`
+        const int stride = a.round_keys();
+        const int k0 = run.base + r0 * stride + wave / a.hw * kTile;
+        const int end = (int)min((int64_t)thi, (int64_t)run.base + (int64_t)r1 * stride);
+
+        // Page numbers of keys key0 + lane % 32, by DMA into LDS: as a load into a register the compiler would wait for
+        // it, and with it for the row DMA issued after it.  The index does not wait for the sequence's length: it is
+        // held inside the table, and rows_of drops what lies outside the visible keys of these rounds.
+        auto fetch_pages = [&](int i) {
+            __builtin_amdgcn_global_load_lds(table + min(a.page(k0 + i * stride + lane % kTile), last_page),
+                                             pages + i % S * kWave, 4, 0, 0);
+        };
+        // cache rows of the tile's keys into LDS, 0 for none; returns the mask of those that are there
+        auto rows_of = [&](int i) {
+            const int key = k0 + i * stride + lane % kTile, page = pages[i % S * kWave + lane];
+            const bool ok = key >= tlo && key < end && page >= 0 && page < p.num_blocks;
+            if (lane < kTile) slots[lane] = ok ? (page - a.page(key)) * p.block + key : 0;
+            __builtin_amdgcn_wave_barrier();  // read below by this wave's other lanes; a wave's LDS accesses are in order
+            return (uint32_t)__ballot(ok);
+        };
+        const uint8_t* const kbase = p.cache + hk * D;
+        auto fetch = [&](int i) {
+            uint8_t* const tile = ring + i % S * kTileBytes;
+            uint32_t row[NI];
+#pragma unroll
+            for (int j = 0; j < NI; ++j) row[j] = slots[RI * j + lane / UR];
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+                const int r = RI * j + lane / UR;
+                const uint8_t* src = kbase + (uint64_t)row[j] * C + ((lane % UR) ^ swizzle<D>(r)) * 16;
+                dma16(src, tile + j * 1024);
+                dma16(src + p.Hkv * D, tile + kTile * D + j * 1024);
+            }
+        };
+        // The ring holds S tiles.  Step i issues the rows of tile i + S - 1, and before them the page numbers of tile
+        // i + 2 S - 1: once tile i has landed, so have the page numbers that the next step needs, and one counter wait
+        // that leaves S - 1 tiles in flight covers both.
+        uint32_t masks[S];
+        auto fill = [&]() {
+#pragma unroll
+            for (int i = 0; i < S - 1; ++i) {
+                masks[i] = rows_of(i);
+                compiler_fence();
+                fetch_pages(i + S);
+                fetch(i);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < S; ++i) fetch_pages(i);
+        // the query and its scales, on their way while the pages are
+        v4u raw[NJ][2];
+        float4 ks[NJ][2];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int e0 = 64 * (j / 2) + 16 * g + 8 * (j % 2);
+            load_q8(p, row * p.ldq + (int64_t)head * D + e0, raw[j]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) ks[j][i] = *reinterpret_cast<const float4*>(p.scales + hk * D + e0 + 4 * i);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        fill();
+
+        // meanwhile: q times the key scales, as two fp16 terms
         v8h qh[NJ], ql[NJ];
         float c;  // score (log2 units, or natural ones under a cap) per unit of the product
         {
             float x[NJ][8], top = 0.0f;
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-                const int e0 = 64 * (j / 2) + 16 * g + 8 * (j % 2);
-                load_q8(p, row * p.ldq + (int64_t)head * D + e0, x[j]);
+                unpack_q8(p, raw[j], x[j]);
+                const float s[8] = {ks[j][0].x, ks[j][0].y, ks[j][0].z, ks[j][0].w,
+                                    ks[j][1].x, ks[j][1].y, ks[j][1].z, ks[j][1].w};
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    x[j][e] *= fmaxf(p.scales[hk * D + e0 + e], kScaleFloor);
+                    x[j][e] *= fmaxf(s[e], kScaleFloor);
                     top = fmaxf(top, fabsf(x[j][e]));
                 }
             }
@@ -261,78 +541,51 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
                 }
             c = __builtin_amdgcn_ldexpf(p.scale, -shift);
         }
-        const float slope = p.alibi ? p.alibi[head] * kLog2e : 0.0f;
-        const int pos = seq.len - seq.nq + qi;
-        const float cap_in = p.softcap > 0.0f ? 2.0f * kLog2e / p.softcap : 0.0f;
         if (p.softcap > 0.0f) c *= kLn2;  // the cap takes the natural score
 
-        float m = -INFINITY, l = 0.0f;
-        v4f o[VB];
+        auto step = [&](const uint8_t* tile, int key0, uint32_t mask) {
+            // Both reads are typed vector loads: read as bytes they might alias the DMA's writes, and the compiler
+            // would wait for the next tile's here.
+            v4u kw[2][D / 64];
 #pragma unroll
-        for (int j = 0; j < VB; ++j) o[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-
-        // this wave's tiles: number i of it is tile chunk_tiles * kWaves * c + kWaves * (i % chunk_tiles) + wave of
-        // chunk c = split + splits * (i / chunk_tiles)
-        int in_chunk = 0, first = base + (split * chunk_tiles * kWaves + wave) * kTile;
-        const int64_t next_chunk = (int64_t)a.splits * chunk_tiles * kWaves * kTile - (int64_t)chunk_tiles * kWaves * kTile;
-        auto advance = [&](int key) {
-            int64_t k = (int64_t)key + kWaves * kTile;
-            if (++in_chunk == chunk_tiles) {
-                in_chunk = 0;
-                k += next_chunk;
-            }
-            return (int)min(k, (int64_t)0x7FFFFF00);
-        };
-        // page of key key0 + lane % 32, -1 outside the visible keys
-        auto page_of = [&](int key0) {
-            const int key = key0 + lane % kTile;
-            return key >= tlo && key < thi ? table[key / p.block] : -1;
-        };
-        // cache rows of the tile's keys into LDS, -1 for none; returns their mask
-        auto rows_of = [&](int key0, int page) {
-            const int key = key0 + lane % kTile;
-            const bool ok = page >= 0 && page < p.num_blocks;
-            const int r = ok ? page * p.block + key % p.block : -1;
-            if (lane < kTile) slots_lds[wave][lane] = r;
-            __builtin_amdgcn_wave_barrier();  // read below by this wave's other lanes; a wave's LDS accesses are in order
-            return (uint32_t)__ballot(ok);
-        };
-        auto fetch = [&](Codes<D>& w) {
-            const uint8_t* kbase = p.cache + hk * D + 16 * g;
-            const uint8_t* vbase = p.cache + (int64_t)(p.Hkv + hk) * D + n * VB;
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int64_t at = (int64_t)max(slots_lds[wave][16 * t + n], 0) * C;
-#pragma unroll
-                for (int i = 0; i < D / 64; ++i) w.k[t][i] = *reinterpret_cast<const v4u*>(kbase + at + 64 * i);
-            }
+                for (int i = 0; i < D / 64; ++i) {
+                    const int r = 16 * t + n;
+                    kw[t][i] = *reinterpret_cast<const v4u*>(tile + r * D + ((4 * i + g) ^ swizzle<D>(r)) * 16);
+                }
+            typedef typename std::conditional<D == 64, uint32_t, typename std::conditional<D == 128, v2u, v4u>::type>::type vrow;
+            vrow v[8];  // the V codes of this lane's 8 keys, channels n * VB ..
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int64_t at = (int64_t)max(slots_lds[wave][16 * (e / 4) + 4 * g + e % 4], 0) * C;
-                __builtin_memcpy(w.v[e], __builtin_assume_aligned(vbase + at, VB), VB);
+                const int r = 16 * (e / 4) + 4 * g + e % 4;
+                v[e] = *reinterpret_cast<const vrow*>(tile + kTile * D + r * D + ((n * VB / 16) ^ swizzle<D>(r)) * 16 +
+                                                      n * VB % 16);
             }
-        };
-        auto step = [&](Codes<D>& w, int key0, uint32_t mask) {
             float s[2][4];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+                v4f acc = {0.0f, 0.0f, 0.0f, 0.0f}, rest = acc;
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    const v8h k = row_f16<FMT>(w.k[t][j / 2][2 * (j % 2)], w.k[t][j / 2][2 * (j % 2) + 1]);
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qh[j], acc, 0, 0, 0);
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, ql[j], acc, 0, 0, 0);
+                for (int i = 0; i < D / 64; ++i) {
+                    const v4u w = kw[t][i];
+#pragma unroll
+                    for (int j = 2 * i; j < 2 * i + 2; ++j) {
+                        const v8h k = row_f16<FMT>(w[2 * (j % 2)], w[2 * (j % 2) + 1]);
+                        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qh[j], acc, 0, 0, 0);
+                        rest = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, ql[j], rest, 0, 0, 0);
+                    }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[t][i] = acc[i] * c;
+                for (int i = 0; i < 4; ++i) s[t][i] = (acc[i] + rest[i]) * c;
             }
-            if (p.softcap > 0.0f) {
+            if constexpr (BIAS) {
+                if (p.softcap > 0.0f) {
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                    for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s[t][i] = kLog2e * soft_cap(s[t][i], p.softcap, cap_in);
-            }
-            if (p.alibi) {
+                        for (int i = 0; i < 4; ++i) s[t][i] = kLog2e * soft_cap(s[t][i], p.softcap, cap_in);
+                }
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -348,17 +601,13 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
                         const bool see = ((mask >> j) & 1u) && key0 + j >= lo && key0 + j < hi;
                         s[t][i] = see ? s[t][i] : -INFINITY;
                         // a code behind the sequence may be anything, NaN too: 0 * NaN must not reach the sum
-                        if (!((mask >> j) & 1u)) {
-#pragma unroll
-                            for (int q = 0; q < D / 64; ++q) w.v[4 * t + i][q] = 0u;
-                        }
+                        v[4 * t + i] = ((mask >> j) & 1u) ? v[4 * t + i] : vrow(0u);
                     }
             }
             float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
                               fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-            top = max_over_groups(top);
-            if (__any(top > m)) {
-                const float up = fmaxf(top, m);
+            if (__any(top > m + kSlack)) {
+                const float up = fmaxf(max_over_groups(top), m);
                 const float f = up == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - up);
                 m = up;
                 l *= f;
@@ -369,7 +618,7 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
             v8h ph, pl;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                // the shift is added last: m - kPShift would round for scores past 2^24 and p pass fp16's range
+                // the shift is added last: m - kPShift would round for large scores and p pass fp16's range
                 const float x = __builtin_amdgcn_exp2f((s[e / 4][e % 4] - mm) + kPShift);
                 l += x;
                 ph[e] = (_Float16)x;
@@ -379,141 +628,139 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
             for (int j = 0; j < VB; ++j) {
                 v4u r;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) r[i] = pair_f16<FMT>(w.v[2 * i][j / 4], w.v[2 * i + 1][j / 4], j % 4);
-                const v8h v = __builtin_bit_cast(v8h, r);
-                o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, ph, o[j], 0, 0, 0);
-                o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pl, o[j], 0, 0, 0);
+                for (int i = 0; i < 4; ++i) r[i] = pair_f16<FMT>(word(v[2 * i], j / 4), word(v[2 * i + 1], j / 4), j % 4);
+                const v8h vt = __builtin_bit_cast(v8h, r);
+                o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vt, ph, o[j], 0, 0, 0);
+                o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vt, pl, o[j], 0, 0, 0);
             }
         };
 
-        // Two tiles' codes are in flight: while one is used the next is on its way, and the page numbers of the
-        // one after that.
-        Codes<D> w[2];
-        int k0 = first;
-        if (k0 < thi) {
-            uint32_t mask0 = rows_of(k0, page_of(k0));
-            fetch(w[0]);
-            int k1 = advance(k0);
-            int page = page_of(k1);
-            while (true) {
-                uint32_t mask1 = rows_of(k1, page);
-                int k2 = 0;
-                if (k1 < thi) {
-                    fetch(w[1]);
-                    k2 = advance(k1);
-                    page = page_of(k2);
-                }
-                step(w[0], k0, mask0);
-                if (k1 >= thi) break;
-                mask0 = rows_of(k2, page);
-                if (k2 < thi) {
-                    fetch(w[0]);
-                    k0 = k2;
-                    const int k3 = advance(k2);
-                    page = page_of(k3);
-                    step(w[1], k1, mask1);
-                    k1 = k3;
-                } else {
-                    step(w[1], k1, mask1);
-                    break;
-                }
-            }
+        for (int i = 0; k0 + i * stride < end; ++i) {
+            masks[S - 1] = rows_of(i + S - 1);
+            compiler_fence();
+            fetch_pages(i + 2 * S - 1);
+            fetch(i + S - 1);  // past the last tile: row 0, unused
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 1) * (2 * NI + 1)) : "memory");
+            step(ring + i % S * kTileBytes, k0 + i * stride, masks[0]);
+            compiler_fence();
+#pragma unroll
+            for (int j = 0; j < S - 1; ++j) masks[j] = masks[j + 1];
         }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing lands in the ring any more
         l = sum_over_groups(l);
 
-        // The waves' results joined in wave order, the channels in kParts rounds.
-        if (g == 0) ml_lds[wave][n] = make_float2(m, l);
+        // the waves of a head joined in wave order
+        if (g == 0) ml[wave * kCols + n] = make_float2(m, l);
+        float* const outs = reinterpret_cast<float*>(ring);
 #pragma unroll
-        for (int part = 0; part < kParts; ++part) {
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < kI; ++i)
-#pragma unroll
-                for (int j = 0; j < VB; j += 4)
-                    *reinterpret_cast<float4*>(&o_lds[wave][n][(kI * g + i) * VB + j]) =
-                        make_float4(o[j][kI * part + i], o[j + 1][kI * part + i], o[j + 2][kI * part + i],
-                                    o[j + 3][kI * part + i]);
-            __syncthreads();
-            for (int x = threadIdx.x; x < kCols * D / kParts / 4; x += kWaves * kWave) {
-                const int cc = x / (D / kParts / 4), y = x % (D / kParts / 4) * 4;
-                const int ccol = ct * kCols + cc;
-                if (ccol >= seq.nq * a.group) continue;
-                const int d = y / (kI * VB) * (4 * VB) + part * kI * VB + y % (kI * VB);
-                float M = -INFINITY, L = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w) M = fmaxf(M, ml_lds[w][cc].x);
-                float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w) {
-                    const float f = ml_lds[w][cc].x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml_lds[w][cc].x - M);
-                    const float4 v = *reinterpret_cast<const float4*>(&o_lds[w][cc][y]);
-                    L += f * ml_lds[w][cc].y;
-                    r = make_float4(r.x + f * v.x, r.y + f * v.y, r.z + f * v.z, r.w + f * v.w);
-                }
-                const int i = ccol / a.group, h = hk * a.group + ccol % a.group;
-                const int64_t orow = seq.row0 + i;
-                if (a.splits > 1) {
-                    const int64_t at = ((int64_t)split * p.rows + orow) * p.Hq + h;
-                    if (d == 0) a.part_ml[at] = make_float2(M, L);
-                    *reinterpret_cast<float4*>(a.part_o + at * D + d) = r;
-                } else {
-                    write_row(p, orow, h, a.group, D, d, M, L, r);
-                }
+            for (int j = 0; j < VB; j += 4)
+                *reinterpret_cast<float4*>(outs + n * kOutRow + (4 * g + i) * VB + j) =
+                    make_float4(o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]);
+        __syncthreads();
+        for (int x = threadIdx.x; x < a.hw * kCols * D / 4; x += kWaves * kWave) {
+            const int d = x % (D / 4) * 4, cc = x / (D / 4) % kCols, hs = x / (D / 4 * kCols);
+            const int ccol = ct * kCols + cc;
+            if (ccol >= seq.nq * a.group) continue;
+            float M = -INFINITY, L = 0.0f;
+            for (int w = hs; w < kWaves; w += a.hw) M = fmaxf(M, ml[w * kCols + cc].x);
+            float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int w = hs; w < kWaves; w += a.hw) {
+                const float2 y = ml[w * kCols + cc];
+                const float f = y.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(y.x - M);
+                const float4 v = *reinterpret_cast<const float4*>(attn_smem + w * Lds::kRing + (cc * kOutRow + d) * 4);
+                L += f * y.y;
+                r = make_float4(r.x + f * v.x, r.y + f * v.y, r.z + f * v.z, r.w + f * v.w);
             }
-            __syncthreads();
+            const int i = ccol / a.group, h = (hk0 + hs) * a.group + ccol % a.group;
+            const int64_t orow = seq.row0 + i;
+            if (part >= 0) {
+                const int64_t at = ((int64_t)part * a.hw + hs) * kCols + cc;
+                if (d == 0) a.part_ml[at] = make_float2(M, L);
+                *reinterpret_cast<float4*>(a.part_o + at * D + d) = r;
+            } else {
+                write_row(p, orow, h, a.group, D, d, M, L, r);
+            }
+        }
+        __syncthreads();
+
+        // the next item
+        if (a.log_shares < 0) {
+            ct += a.col_tiles;
+        } else {
+            if (left <= 0) break;
+            if (++hg == head_groups) hg = 0, ++ct;
         }
     }
 }
 
-// Joins the key shares of every output row, in share order: four waves take
-// shares in turn, then their sums meet in LDS.
+// Joins the key shares of the output rows.  A group of D / 4 threads adds up a
+// row's weighted shares, four channels a thread, every `spread`-th of them when
+// several groups of the workgroup take one row; LDS joins those in order.
 template <int D>
 __global__ __launch_bounds__(kWaves* kWave) void attn_join(StreamArgs a) {
     const PagedAttn& p = a.p;
-    constexpr int V = D / kWave;  // channels of a lane
-    __shared__ float sums[kWaves][D];
-    __shared__ float weight[kWaves];
-    const int h = blockIdx.x % p.Hq;
-    const int by = blockIdx.x / p.Hq;
-    const int b = by % p.B, i0 = by / p.B;
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-    const Seq seq = sequence(p, b);
-    const int prefix = p.prefix ? p.prefix[b] : 0;
-    const int per_pass = gridDim.x / (p.Hq * p.B);
-    for (int i = i0; i < seq.nq; i += per_pass) {
-        // the shares that have keys, as the first kernel dealt them out
-        int lo, hi;
-        tile_keys(p, seq, prefix, a.group, (i * a.group + h % a.group) / kCols, lo, hi);
-        const int keys = max(0, hi - lo / kTile * kTile);
-        const int shares = (int)min((int64_t)a.splits, ((int64_t)keys + a.chunk - 1) / a.chunk);
-        const int64_t at = (int64_t)(seq.row0 + i) * p.Hq + h;
-        const int64_t stride = (int64_t)p.rows * p.Hq;
-        float M = -INFINITY;
-        for (int s = lane; s < shares; s += kWave) M = fmaxf(M, a.part_ml[s * stride + at].x);
-        M = wave_max(M);
-        float L = 0.0f, r[V];
+    constexpr int kThreads = kWaves * kWave;
+    constexpr int kLanes = D / 4;                // threads of a group
+    constexpr int kGroups = kThreads / kLanes;
+    __shared__ float4 sums[kThreads];
+    __shared__ float lsum[kGroups];
+    const int tid = threadIdx.x, d4 = tid % kLanes, grp = tid / kLanes, part = grp % a.spread;
+    const int64_t heads = (int64_t)blockIdx.x * (kGroups / a.spread) + grp / a.spread;  // row of the launch: (i0, b, h)
+    const int h = (int)(heads % p.Hq), b = (int)(heads / p.Hq % p.B);
+    const int i0 = (int)(heads / p.Hq / p.B);
+    const bool live = i0 < a.join_rows;
+    Seq seq = {0, 0, 0};
+    if (live) seq = sequence(p, b);
+    const int prefix = live && p.prefix ? p.prefix[b] : 0;
+    // Every thread goes through as many rounds as the longest sequence of its workgroup: the barriers are for all.
+    for (int i = i0; __syncthreads_or(i < seq.nq); i += a.join_rows) {
+        float M = -INFINITY, L = 0.0f;
+        float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        int shares = 0;
+        bool cut = false;  // else the first kernel has written the row
+        if (i < seq.nq) {
+            // the shares that its item was cut into, as the first kernel dealt them out
+            const Run run = run_of(a, seq, prefix);
+            const int col = i * a.group + h % a.group, hk = h / a.group;
+            const int at = a.starts[b] + (col / kCols * (p.Hkv / a.hw) + hk / a.hw) * (run.rounds + kItemCost) + kItemCost;
+            const int share = a.share_of(a.starts[p.B]);
+            const int first = at / share;
+            shares = run.rounds == 0 ? 0 : (at + run.rounds - 1) / share - first + 1;
+            cut = shares != 1;
+            if (cut) {
+                // the item's first round is in its first share
+                const auto slot = [&](int s) {
+                    return ((2 * (first + s) + (s == 0)) * a.hw + hk % a.hw) * kCols + col % kCols;
+                };
+                for (int s = d4; s < shares; s += kLanes) M = fmaxf(M, a.part_ml[slot(s)].x);
 #pragma unroll
-        for (int v = 0; v < V; ++v) r[v] = 0.0f;
-        for (int s = wave; s < shares; s += kWaves) {
-            const float2 ml = a.part_ml[s * stride + at];
-            const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - M);
-            L += f * ml.y;
-#pragma unroll
-            for (int v = 0; v < V; ++v) r[v] += f * a.part_o[(s * stride + at) * D + lane * V + v];
+                for (int off = kLanes / 2; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, kLanes));
+#pragma unroll 8
+                for (int s = part; s < shares; s += a.spread) {
+                    const int x = slot(s);
+                    const float2 y = a.part_ml[x];
+                    const float4 v = *reinterpret_cast<const float4*>(a.part_o + (int64_t)x * D + 4 * d4);
+                    const float f = y.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(y.x - M);
+                    L += f * y.y;
+                    r = make_float4(r.x + f * v.x, r.y + f * v.y, r.z + f * v.z, r.w + f * v.w);
+                }
+            }
         }
-#pragma unroll
-        for (int v = 0; v < V; ++v) sums[wave][lane * V + v] = r[v];
-        if (lane == 0) weight[wave] = L;
-        __syncthreads();
-        static_assert(kWaves == 4, "four sums");
-        L = weight[0] + weight[1] + weight[2] + weight[3];
-        if (threadIdx.x < D / 4) {
-            const int d = 4 * threadIdx.x;
-            float y[4];
-#pragma unroll
-            for (int v = 0; v < 4; ++v) y[v] = (sums[0][d + v] + sums[1][d + v]) + (sums[2][d + v] + sums[3][d + v]);
-            write_row(p, seq.row0 + i, h, a.group, D, d, M, L, make_float4(y[0], y[1], y[2], y[3]));
+        if (a.spread > 1) {
+            sums[tid] = r;
+            if (d4 == 0) lsum[grp] = L;
+            __syncthreads();
+            if (part == 0) {
+                for (int k = 1; k < a.spread; ++k) {
+                    const float4 v = sums[tid + k * kLanes];
+                    r = make_float4(r.x + v.x, r.y + v.y, r.z + v.z, r.w + v.w);
+                    L += lsum[grp + k];
+                }
+            }
         }
-        __syncthreads();
+        if (part == 0 && cut) write_row(p, seq.row0 + i, h, a.group, D, 4 * d4, M, L, r);
     }
 }
 
@@ -523,62 +770,103 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int64_t kMaxGrid = 1 << 26;
 
 struct StreamPlan {
-    int64_t col_tiles, splits, chunk;
+    int hw, log_shares, min_share;
+    int64_t col_tiles;
 };
 
-// Key shares: enough workgroups to fill the card (two of four waves on each
-// of 256 CUs), none with fewer than 256 keys.
-StreamPlan stream_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t max_q, int64_t max_len) {
-    constexpr int64_t kTarget = 1024, kMinKeys = 256, kRound = kTile * kWaves;
+StreamPlan stream_plan(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_len,
+                       int64_t all_len) {
     StreamPlan s;
-    s.col_tiles = std::max<int64_t>(1, ceil_div(std::max<int64_t>(max_q, 1) * (Hq / Hkv), kCols));
-    s.col_tiles = std::max<int64_t>(1, std::min(s.col_tiles, kMaxGrid / std::max<int64_t>(1, B * Hkv)));
-    const int64_t units = std::max<int64_t>(1, B * Hkv * s.col_tiles);
-    s.splits = std::min(ceil_div(kTarget, units), std::max<int64_t>(1, max_len / kMinKeys));
-    s.chunk = std::max<int64_t>(kRound, ceil_div(ceil_div(max_len, s.splits), kRound) * kRound);
-    s.splits = std::max<int64_t>(1, std::min(s.splits, ceil_div(max_len, s.chunk)));
+    B = std::max<int64_t>(B, 1);
+    s.col_tiles = ceil_div(std::max<int64_t>(max_q, 1) * (Hq / Hkv), kCols);
+    s.col_tiles = std::max<int64_t>(1, std::min<int64_t>({s.col_tiles, kMaxGrid / (B * Hkv), 65535}));
+    const int most = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
+    const int log_shares = D == 256 ? 8 : 9;
+    const int64_t fill = int64_t(1) << log_shares;
+    s.hw = most;
+    s.log_shares = -1;
+    s.min_share = 2;
+    if (max_len <= 1024) {
+        while (s.hw > 1 && B * (Hkv / s.hw) * s.col_tiles < fill) s.hw /= 2;
+        if (max_len <= 640 || B * (Hkv / s.hw) * s.col_tiles >= fill) return s;
+    }
+    // costs of all sequences are added up in 32 bits
+    const int64_t cost = (ceil_div(all_len, kTile) + kItemCost) * (rows * (Hq / Hkv) / kCols + B) * Hkv;
+    if (cost >= (int64_t(1) << 30)) return s;
+    s.hw = most;
+    const int64_t items = B * (Hkv / most) * s.col_tiles;
+    if (items < 32 || items * max_len * most / (kTile * kWaves) < 16 * fill) s.hw = 1;
+    s.log_shares = log_shares;
     return s;
 }
 
+template <int D, int FMT, bool BIAS>
+hipError_t launch_stream(const StreamArgs& a, hipStream_t stream) {
+    constexpr int lds = StreamLds<D>::kBytes;
+    const dim3 grid = a.log_shares >= 0 ? dim3(1u << a.log_shares)
+                                        : dim3((unsigned)a.p.B, (unsigned)(a.p.Hkv / a.hw), (unsigned)a.col_tiles);
+    if constexpr (lds > 64 * 1024) {
+        const hipError_t e = FP8K_SET_LDS((attn_stream<D, FMT, BIAS>), lds);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((attn_stream<D, FMT, BIAS>), grid, dim3(kWaves * kWave), lds, stream, a);
+    return hipGetLastError();
+}
+
 template <int D>
-hipError_t launch(const StreamArgs& a, int fmt, unsigned grid, int64_t max_q, hipStream_t stream) {
-    if (fmt == kKvE5M2)
-        hipLaunchKernelGGL((attn_stream<D, kKvE5M2>), dim3(grid), dim3(kWaves * kWave), 0, stream, a);
-    else
-        hipLaunchKernelGGL((attn_stream<D, kKvE4M3>), dim3(grid), dim3(kWaves * kWave), 0, stream, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.splits == 1) return e;
+hipError_t launch(StreamArgs a, int fmt, int64_t max_q, hipStream_t stream) {
+    const bool bias = a.p.softcap > 0.0f || a.p.alibi != nullptr;
+    hipError_t e = fmt == kKvE5M2 ? (bias ? launch_stream<D, kKvE5M2, true>(a, stream)
+                                          : launch_stream<D, kKvE5M2, false>(a, stream))
+                                  : (bias ? launch_stream<D, kKvE4M3, true>(a, stream)
+                                          : launch_stream<D, kKvE4M3, false>(a, stream));
+    if (e != hipSuccess || a.log_shares < 0) return e;
     const int64_t heads = (int64_t)a.p.B * a.p.Hq;
-    const int64_t per_head = std::max<int64_t>(1, std::min(max_q, kMaxGrid / heads));
-    hipLaunchKernelGGL((attn_join<D>), dim3((unsigned)(heads * per_head)), dim3(kWaves * kWave), 0, stream, a);
+    a.join_rows = (int)std::max<int64_t>(1, std::min(max_q, kMaxGrid / heads));
+    constexpr int kGroups = kWaves * kWave / (D / 4);
+    a.spread = 1;
+    while (a.spread < kGroups && heads * a.join_rows * a.spread < 2048) a.spread *= 2;
+    const int64_t per_block = kGroups / a.spread;
+    const unsigned grid = (unsigned)ceil_div(heads * a.join_rows, per_block);
+    hipLaunchKernelGGL((attn_join<D>), dim3(grid), dim3(kWaves * kWave), 0, stream, a);
     return hipGetLastError();
 }
 
 }  // namespace
 
-size_t attn_paged_ws_bytes(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q,
-                           int64_t max_len) {
-    const StreamPlan s = stream_plan(B, Hq, Hkv, max_q, max_len);
-    return s.splits > 1 ? (size_t)(s.splits * rows * Hq) * ((size_t)D * 4 + 8) : 0;
+size_t attn_paged_ws_bytes(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_len,
+                           int64_t all_len) {
+    const StreamPlan s = stream_plan(B, rows, Hq, Hkv, D, max_q, max_len, all_len);
+    if (B == 0 || rows == 0 || s.log_shares < 0) return 0;
+    const size_t parts = (size_t)2 << s.log_shares;
+    return parts * s.hw * kCols * ((size_t)D * 4 + 8) + ((size_t)B + 1) * 4;
 }
 
 hipError_t launch_attn_paged(const PagedAttn& p, int D, int fmt, int64_t max_q, int64_t max_len, void* ws,
                              hipStream_t stream) {
-    const StreamPlan s = stream_plan(p.B, p.Hq, p.Hkv, max_q, max_len);
-    StreamArgs a;
+    const StreamPlan s = stream_plan(p.B, p.rows, p.Hq, p.Hkv, D, max_q, max_len, (int64_t)p.max_blocks * p.block);
+    StreamArgs a = {};
     a.p = p;
     a.group = p.Hq / p.Hkv;
+    a.hw = s.hw;
     a.col_tiles = (int)s.col_tiles;
-    a.splits = (int)s.splits;
-    a.chunk = (int)s.chunk;
-    a.part_o = static_cast<float*>(ws);
-    a.part_ml = reinterpret_cast<float2*>(static_cast<float*>(ws) + s.splits * p.rows * p.Hq * D);
-    const unsigned grid = (unsigned)((int64_t)p.B * p.Hkv * s.col_tiles * s.splits);
+    a.log_shares = s.log_shares;
+    a.min_share = s.min_share;
+    if (s.log_shares >= 0) {
+        const size_t cols = ((size_t)2 << s.log_shares) * s.hw * kCols;
+        a.part_o = static_cast<float*>(ws);
+        a.part_ml = reinterpret_cast<float2*>(a.part_o + cols * D);
+        a.starts = reinterpret_cast<int*>(a.part_ml + cols);
+    }
+    // magic = ceil(2^shift / block), shift = 31 + ceil(log2(block)), is off by e < 1, which adds key e / 2^shift < 1 / block
+    a.shift = 31;
+    while ((int64_t(1) << (a.shift - 31)) < p.block) ++a.shift;
+    a.magic = (uint32_t)(((uint64_t(1) << a.shift) + p.block - 1) / p.block);
     const int64_t q = std::max<int64_t>(1, max_q);
     switch (D) {
-        case 64: return launch<64>(a, fmt, grid, q, stream);
-        case 128: return launch<128>(a, fmt, grid, q, stream);
-        default: return launch<256>(a, fmt, grid, q, stream);
+        case 64: return launch<64>(a, fmt, q, stream);
+        case 128: return launch<128>(a, fmt, q, stream);
+        default: return launch<256>(a, fmt, q, stream);
     }
 }
 

@@ -71,7 +71,8 @@ hipError_t launch_kv_append_rope(const KvAppend& p, int dtype, int fmt, bool int
 // [cu_q[b], cu_q[b + 1]) (row b when cu_q is null) of `rows` rows in all;
 // its key j lies in cache row block_table[b][j / block] * block + j % block.
 // scale2: the score scale times log2(e); softcap 0, window 0, alibi null and
-// prefix null turn those off.
+// prefix null turn those off.  block_table holds one entry and
+// cache one row at least.
 struct PagedAttn {
     const void* q;
     void* out;
@@ -90,8 +91,10 @@ struct PagedAttn {
     int B, rows, Hq, Hkv, block, max_blocks, window, causal, dtype;
 };
 // max_q and max_len plan the launch; longer rows and sequences are still
-// computed whole.  ws: attn_paged_ws_bytes bytes, 16-byte aligned.
-size_t attn_paged_ws_bytes(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_len);
+// computed whole.  ws: attn_paged_ws_bytes bytes (all_len = max_blocks * block),
+// 16-byte aligned.
+size_t attn_paged_ws_bytes(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_len,
+                           int64_t all_len);
 hipError_t launch_attn_paged(const PagedAttn& p, int D, int fmt, int64_t max_q, int64_t max_len, void* ws,
                              hipStream_t stream);
 

@@ -411,7 +411,8 @@ fp8_status_t fp8_kv_append_rope_paged(const void* q, int64_t ldq, void* q_out, i
  * rows 16-byte aligned; lse fp32 [rows, Hq] or NULL; out does not overlap q.
  * cache: u8 [num_blocks * block_size, 2 Hkv D]; scales fp32 [2 Hkv D];
  * block_table int32 [B, max_blocks], row stride ld_table.  D is 64, 128 or
- * 256 and Hq a multiple of Hkv; any block_size >= 1.
+ * 256 and Hq a multiple of Hkv, Hkv <= 65535; any block_size >= 1; positions,
+ * rows * Hq and block_size * max_blocks up to 2^30.
  * max_q and max_len plan the launch: bounds of the new rows and of the length
  * of one sequence, 0 for not known.  They may be wrong: longer sequences are
  * still computed whole, only slower.
