@@ -43,11 +43,12 @@
 //
 // Split.  A workgroup's four waves are `hw` neighbouring KV heads (4, 2 or 1)
 // times 4 / hw key interleaves; a round is a 32-key tile for each of them, and
-// waves of one head are joined in LDS.  An item -- hw heads of one sequence and
-// column tile -- is a run of rounds.  Either every workgroup takes whole items,
-// or the runs of all items, laid end to end, are cut into one equal share per
-// workgroup, whatever the lengths are: every workgroup adds up the rounds of
-// all sequences (a scan) and finds its own share.  A share's first and last
+// waves of one head are joined in LDS.  An item -- one sequence and column tile
+// -- is a run of rounds.  Either a workgroup takes whole items, or the runs of
+// all items, laid end to end, are cut into equal shares, whatever the lengths
+// are: every workgroup adds up the rounds of all sequences (a scan) and finds
+// its own share.  Workgroups of the same share and neighbouring heads are
+// neighbours in the grid: together they read whole cache rows.  A share's first and last
 // item may be part of one; those parts go to the workspace, and a second kernel
 // joins them, in order, into the rows that were cut.  No wave waits for another
 // workgroup.
@@ -76,10 +77,10 @@ struct StreamArgs {
     int group;         // query heads per KV head
     int hw;            // KV heads of a workgroup
     int col_tiles;     // whole items: column tiles a KV head is planned for
-    int log_shares;    // equal shares: their number's logarithm, -1 for whole items
-    int min_share;     // and their fewest rounds
-    float* part_o;     // [2 shares][hw][kCols][D]: parts of rows, a share's first and last
-    float2* part_ml;   // [2 shares][hw][kCols]: reference (log2), sum
+    int shares;        // equal shares: their number for every head group, 0 for whole items
+    int min_share;     // and their least cost
+    float* part_o;     // [workgroups][2][hw][kCols][D]: parts of rows, a share's first and last
+    float2* part_ml;   // [workgroups][2][hw][kCols]: reference (log2), sum
     int* starts;       // [B + 1]: cost before every sequence, cost of all
     int spread;        // the join's thread groups per output row
     int join_rows;     // and the new rows of a sequence it takes at a time
@@ -88,9 +89,8 @@ struct StreamArgs {
 
     __device__ __forceinline__ int page(int key) const { return (int)(((uint64_t)(uint32_t)key * magic) >> shift); }
     __device__ __forceinline__ int round_keys() const { return kTile * kWaves / hw; }
-    __device__ __forceinline__ int share_of(int total) const {
-        return max((total + (1 << log_shares) - 1) >> log_shares, min_share);
-    }
+    __device__ __forceinline__ int head_groups() const { return p.Hkv / hw; }
+    __device__ __forceinline__ int share_of(int total) const { return max((total + shares - 1) / shares, min_share); }
 };
 
 // A sequence's new rows and length, held inside the buffers whatever the
@@ -134,7 +134,7 @@ __device__ __forceinline__ void tile_keys(const PagedAttn& p, const Seq& s, int 
 }
 
 // The keys any row of a sequence sees start at `base`, whole tiles of them; its
-// items' rounds, and the items of it (column tiles x head groups).
+// items' rounds, and its items (column tiles).
 struct Run {
     int base, rounds, items;
 };
@@ -147,7 +147,7 @@ __device__ __forceinline__ Run run_of(const StreamArgs& a, const Seq& s, int pre
     // without a window every sequence starts at key 0
     r.base = a.p.window > 0 ? min(lo, max(hi, 0)) / kTile * kTile : 0;
     r.rounds = s.nq > 0 && hi > r.base ? (hi - r.base + a.round_keys() - 1) / a.round_keys() : 0;
-    r.items = r.rounds > 0 ? (s.nq * a.group + kCols - 1) / kCols * (a.p.Hkv / a.hw) : 0;
+    r.items = r.rounds > 0 ? (s.nq * a.group + kCols - 1) / kCols : 0;
     return r;
 }
 
@@ -181,7 +181,7 @@ __device__ __forceinline__ Found find_share(const StreamArgs& a, int* lds) {
     const bool once = p.B <= kThreads;
     for (int pass = 0; pass < 2; ++pass) {
         const int share = a.share_of(total);
-        const int64_t start = (int64_t)blockIdx.x * share;  // of the second pass
+        const int64_t start = (int64_t)(blockIdx.x / a.head_groups()) * share;  // of the second pass
         int run = 0;
         for (int b0 = 0; b0 < p.B; b0 += kThreads) {
             const int b = b0 + tid;
@@ -379,29 +379,29 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
     int* const pages = reinterpret_cast<int*>(attn_smem + Lds::kPages) + wave * S * kWave;
     float2* const ml = reinterpret_cast<float2*>(attn_smem + Lds::kMl);
     const int n = lane % 16, g = lane / 16;
-    const int head_groups = p.Hkv / a.hw;
     const uint32_t C = 2u * p.Hkv * D;
     const int last_page = max(p.max_blocks - 1, 0);
 
     // the first item: a whole one, or where this workgroup's share starts
-    int b = blockIdx.x, ct = 0, hg = 0, at_item = 0;  // at_item: cost of the item before this share
-    int left = 0;  // cost left of the share
-    if (a.log_shares >= 0) {
+    int b = 0, ct = 0, hg = 0, at_item = 0;  // at_item: cost of the item before this share
+    int left = 0;                            // cost left of the share
+    if (a.shares > 0) {
         const Found f = find_share(a, reinterpret_cast<int*>(attn_smem));
-        const int share = a.share_of(f.total);
-        const int64_t start = (int64_t)blockIdx.x * share;
+        const int share = a.share_of(f.total), nth = blockIdx.x / a.head_groups();
+        const int64_t start = (int64_t)nth * share;
         left = (int)min((int64_t)share, f.total - start);
         if (left <= 0) return;
+        hg = blockIdx.x - nth * a.head_groups();
         b = __builtin_amdgcn_readfirstlane(f.b);
         const Run r = run_of(a, sequence(p, b), p.prefix ? p.prefix[b] : 0);
-        const int at = (int)start - f.before, item = at / (r.rounds + kItemCost);
-        at_item = __builtin_amdgcn_readfirstlane(at - item * (r.rounds + kItemCost));
-        ct = __builtin_amdgcn_readfirstlane(item / head_groups);
-        hg = __builtin_amdgcn_readfirstlane(item - ct * head_groups);
+        const int at = (int)start - f.before;
+        ct = __builtin_amdgcn_readfirstlane(at / (r.rounds + kItemCost));
+        at_item = __builtin_amdgcn_readfirstlane(at - ct * (r.rounds + kItemCost));
         __syncthreads();
     } else {
-        ct = blockIdx.z;
-        hg = blockIdx.y;
+        hg = blockIdx.x % a.head_groups();
+        b = blockIdx.x / a.head_groups();
+        ct = blockIdx.y;
     }
 
     while (b < p.B) {
@@ -410,11 +410,11 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
         const Run run = run_of(a, seq, prefix);
         int r0 = 0, r1 = run.rounds;  // its rounds that are this workgroup's
         bool mine = true;
-        if (a.log_shares < 0) {
+        if (a.shares == 0) {
             if (ct * kCols >= seq.nq * a.group) break;
         } else {
             if (run.items == 0 || ct * kCols >= seq.nq * a.group) {
-                ct = hg = 0, ++b;  // the next sequence
+                ct = 0, ++b;  // the next sequence
                 continue;
             }
             const int taken = min(left, run.rounds + kItemCost - at_item);
@@ -686,11 +686,11 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
         __syncthreads();
 
         // the next item
-        if (a.log_shares < 0) {
+        if (a.shares == 0) {
             ct += a.col_tiles;
         } else {
             if (left <= 0) break;
-            if (++hg == head_groups) hg = 0, ++ct;
+            ++ct;
         }
     }
 }
@@ -724,7 +724,7 @@ __global__ __launch_bounds__(kWaves* kWave) void attn_join(StreamArgs a) {
             // the shares that its item was cut into, as the first kernel dealt them out
             const Run run = run_of(a, seq, prefix);
             const int col = i * a.group + h % a.group, hk = h / a.group;
-            const int at = a.starts[b] + (col / kCols * (p.Hkv / a.hw) + hk / a.hw) * (run.rounds + kItemCost) + kItemCost;
+            const int at = a.starts[b] + col / kCols * (run.rounds + kItemCost) + kItemCost;
             const int share = a.share_of(a.starts[p.B]);
             const int first = at / share;
             shares = run.rounds == 0 ? 0 : (at + run.rounds - 1) / share - first + 1;
@@ -732,7 +732,8 @@ __global__ __launch_bounds__(kWaves* kWave) void attn_join(StreamArgs a) {
             if (cut) {
                 // the item's first round is in its first share
                 const auto slot = [&](int s) {
-                    return ((2 * (first + s) + (s == 0)) * a.hw + hk % a.hw) * kCols + col % kCols;
+                    const int group = (first + s) * a.head_groups() + hk / a.hw;
+                    return ((2 * group + (s == 0)) * a.hw + hk % a.hw) * kCols + col % kCols;
                 };
                 for (int s = d4; s < shares; s += kLanes) M = fmaxf(M, a.part_ml[slot(s)].x);
 #pragma unroll
@@ -770,7 +771,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int64_t kMaxGrid = 1 << 26;
 
 struct StreamPlan {
-    int hw, log_shares, min_share;
+    int hw, shares, min_share;
     int64_t col_tiles;
 };
 
@@ -781,30 +782,29 @@ StreamPlan stream_plan(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t
     s.col_tiles = ceil_div(std::max<int64_t>(max_q, 1) * (Hq / Hkv), kCols);
     s.col_tiles = std::max<int64_t>(1, std::min<int64_t>({s.col_tiles, kMaxGrid / (B * Hkv), 65535}));
     const int most = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
-    const int log_shares = D == 256 ? 8 : 9;
-    const int64_t fill = int64_t(1) << log_shares;
+    const int64_t fill = D == 256 ? 256 : 512;  // workgroups that are resident at once
     s.hw = most;
-    s.log_shares = -1;
+    s.shares = 0;
     s.min_share = 2;
     if (max_len <= 1024) {
         while (s.hw > 1 && B * (Hkv / s.hw) * s.col_tiles < fill) s.hw /= 2;
         if (max_len <= 640 || B * (Hkv / s.hw) * s.col_tiles >= fill) return s;
     }
     // costs of all sequences are added up in 32 bits
-    const int64_t cost = (ceil_div(all_len, kTile) + kItemCost) * (rows * (Hq / Hkv) / kCols + B) * Hkv;
+    const int64_t cost = (ceil_div(all_len, kTile) + kItemCost) * (rows * (Hq / Hkv) / kCols + B);
     if (cost >= (int64_t(1) << 30)) return s;
     s.hw = most;
     const int64_t items = B * (Hkv / most) * s.col_tiles;
     if (items < 32 || items * max_len * most / (kTile * kWaves) < 16 * fill) s.hw = 1;
-    s.log_shares = log_shares;
+    s.shares = (int)std::max<int64_t>(1, fill / (Hkv / s.hw));
     return s;
 }
 
 template <int D, int FMT, bool BIAS>
 hipError_t launch_stream(const StreamArgs& a, hipStream_t stream) {
     constexpr int lds = StreamLds<D>::kBytes;
-    const dim3 grid = a.log_shares >= 0 ? dim3(1u << a.log_shares)
-                                        : dim3((unsigned)a.p.B, (unsigned)(a.p.Hkv / a.hw), (unsigned)a.col_tiles);
+    const unsigned groups = a.p.Hkv / a.hw;
+    const dim3 grid = a.shares > 0 ? dim3(a.shares * groups) : dim3(a.p.B * groups, (unsigned)a.col_tiles);
     if constexpr (lds > 64 * 1024) {
         const hipError_t e = FP8K_SET_LDS((attn_stream<D, FMT, BIAS>), lds);
         if (e != hipSuccess) return e;
@@ -820,7 +820,7 @@ hipError_t launch(StreamArgs a, int fmt, int64_t max_q, hipStream_t stream) {
                                           : launch_stream<D, kKvE5M2, false>(a, stream))
                                   : (bias ? launch_stream<D, kKvE4M3, true>(a, stream)
                                           : launch_stream<D, kKvE4M3, false>(a, stream));
-    if (e != hipSuccess || a.log_shares < 0) return e;
+    if (e != hipSuccess || a.shares == 0) return e;
     const int64_t heads = (int64_t)a.p.B * a.p.Hq;
     a.join_rows = (int)std::max<int64_t>(1, std::min(max_q, kMaxGrid / heads));
     constexpr int kGroups = kWaves * kWave / (D / 4);
@@ -837,9 +837,8 @@ hipError_t launch(StreamArgs a, int fmt, int64_t max_q, hipStream_t stream) {
 size_t attn_paged_ws_bytes(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_len,
                            int64_t all_len) {
     const StreamPlan s = stream_plan(B, rows, Hq, Hkv, D, max_q, max_len, all_len);
-    if (B == 0 || rows == 0 || s.log_shares < 0) return 0;
-    const size_t parts = (size_t)2 << s.log_shares;
-    return parts * s.hw * kCols * ((size_t)D * 4 + 8) + ((size_t)B + 1) * 4;
+    if (B == 0 || rows == 0 || s.shares == 0) return 0;
+    return (size_t)s.shares * Hkv * 2 * kCols * ((size_t)D * 4 + 8) + ((size_t)B + 1) * 4;
 }
 
 hipError_t launch_attn_paged(const PagedAttn& p, int D, int fmt, int64_t max_q, int64_t max_len, void* ws,
@@ -850,10 +849,10 @@ hipError_t launch_attn_paged(const PagedAttn& p, int D, int fmt, int64_t max_q, 
     a.group = p.Hq / p.Hkv;
     a.hw = s.hw;
     a.col_tiles = (int)s.col_tiles;
-    a.log_shares = s.log_shares;
+    a.shares = s.shares;
     a.min_share = s.min_share;
-    if (s.log_shares >= 0) {
-        const size_t cols = ((size_t)2 << s.log_shares) * s.hw * kCols;
+    if (s.shares > 0) {
+        const size_t cols = (size_t)s.shares * p.Hkv * 2 * kCols;
         a.part_o = static_cast<float*>(ws);
         a.part_ml = reinterpret_cast<float2*>(a.part_o + cols * D);
         a.starts = reinterpret_cast<int*>(a.part_ml + cols);
