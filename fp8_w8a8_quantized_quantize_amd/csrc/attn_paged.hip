@@ -11,26 +11,26 @@
 //     out_c = vs_c * sum_j p_j code(v_j)_c / sum_j p_j,  p_j = exp(s_j - max s)
 // so the codes go into the matrix instruction as they are: every E4M3 and E5M2
 // value is exact in fp16, the key scales move to the query and the value scales
-// to the output.  q_c ks_c and p_j are not exact in fp16; each is fed as two
-// fp16 terms, high part and rest (22 bits), scaled by a power of two first so
-// that neither part underflows where it matters (q per column to 2^15, p to
-// 2^14).  The second term costs a second matrix instruction, which is free
-// here: a CU needs about 12 bytes of codes a cycle to keep up with HBM and the
-// matrix cores take 64 with both terms.  Scores, maxima, sums and outputs are
-// fp32.
+// to the output.  q_c ks_c and p_j are rounded to fp16 (2^-11 of half a step),
+// scaled by a power of two first so that nothing underflows that matters (q per
+// column to 2^15, p to 2^8): an eighth of the rounding that bf16 outputs get at
+// the end.  For fp16 and fp32 outputs, where it would show, each is fed as two
+// fp16 terms, high part and rest (2^-22), at the cost of a second matrix
+// instruction.  Scores, references, sums and outputs are fp32; the sum of p is
+// a product with ones, so numerator and denominator see the same p.
 //
-// One pass with a running reference m and sum.  m is the maximum of the first
-// tile's scores and moves only when a score passes it by 2^5 (p stays below
-// 2^15 in fp16 and the result does not depend on m), so most tiles need no
-// other lane.  Scores are formed transposed, S^T = K Q^T, so that a lane's four
-// results belong to one column: its reference, sum and rescale need no lane but
-// the three others of that column, and its p
-// are, as they stand, the operand of O^T = V^T P^T.  The k index of that second
-// product may be any order as long as both operands share it: slot (g, e) of a
-// 32-key tile is key 16 (e / 4) + 4 g + e % 4, the keys whose scores the lane
-// group g holds.  Its V operand wants, per lane, one channel of 8 keys: a lane
-// reads D / 16 channels of its 8 keys and turns bytes around in registers
-// (v_perm_b32; for E5M2, a cut-off fp16, the same instruction decodes).
+// One pass with a running reference m.  m is 2^8 below the largest score of the
+// first tile and moves only when a score passes it by 2^12 (p stays below 2^13
+// in fp16, and the result does not depend on m beyond rounding), so most tiles
+// need no other lane.  Scores are formed transposed, S^T = K Q^T, so that a
+// lane's four results belong to one column: its reference and rescale need no
+// lane but the three others of that column, and its p are, as they stand, the
+// operand of O^T = V^T P^T.  The k index of that second product may be any
+// order as long as both operands share it: slot (g, e) of a 32-key tile is key
+// 16 (e / 4) + 4 g + e % 4, the keys whose scores the lane group g holds.  Its
+// V operand wants, per lane, one channel of 8 keys: a lane reads D / 16
+// channels of its 8 keys and turns bytes around in registers (v_perm_b32; for
+// E5M2, a cut-off fp16, the same instruction decodes).
 //
 // The codes come through LDS: whole rows by DMA (16 bytes a lane, D / 16
 // adjacent lanes a row), two tiles in flight per wave, each wave its own ring
@@ -67,15 +67,31 @@ typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 constexpr int kTile = 32;      // keys per step of a wave
 constexpr int kWaves = 4;      // waves of a workgroup
 constexpr int kCols = 16;      // query columns of a tile
+constexpr int kLogRound = 7;   // of kTile * kWaves
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.44269504088896341f;
-constexpr float kPShift = 10.0f;  // p is held as p * 2^10
-constexpr float kSlack = 5.0f;    // and may pass 1 by 2^5, before its reference is moved
+constexpr float kPShift = 8.0f;   // a new reference leaves the largest p at 2^8,
+constexpr float kPLimit = 12.0f;  // and stays until one passes 2^12
+constexpr float kNoRef = -3.0e38f;
+
+// n / d for 0 <= n < 2^31 by a product: magic = ceil(2^shift / d) with shift =
+// 31 + ceil(log2(d)) is off by e < 1, which adds n e / 2^shift < 1 / d.
+struct FastDiv {
+    uint32_t magic;
+    int shift;
+
+    FastDiv(int64_t d = 1) : shift(31) {
+        while ((int64_t(1) << (shift - 31)) < d) ++shift;
+        magic = (uint32_t)(((uint64_t(1) << shift) + d - 1) / d);
+    }
+    __device__ __forceinline__ int of(int n) const { return (int)(((uint64_t)(uint32_t)n * magic) >> shift); }
+};
 
 struct StreamArgs {
     PagedAttn p;
     int group;         // query heads per KV head
-    int hw;            // KV heads of a workgroup
+    int hw, log_hw;    // KV heads of a workgroup
+    int head_groups;   // workgroups that share a sequence's rows
     int col_tiles;     // whole items: column tiles a KV head is planned for
     int shares;        // equal shares: their number for every head group, 0 for whole items
     int min_share;     // and their least cost
@@ -84,12 +100,10 @@ struct StreamArgs {
     int* starts;       // [B + 1]: cost before every sequence, cost of all
     int spread;        // the join's thread groups per output row
     int join_rows;     // and the new rows of a sequence it takes at a time
-    uint32_t magic;    // key / block = key * magic >> shift for keys below 2^31
-    int shift;
+    FastDiv by_block, by_group, by_head_groups;
 
-    __device__ __forceinline__ int page(int key) const { return (int)(((uint64_t)(uint32_t)key * magic) >> shift); }
-    __device__ __forceinline__ int round_keys() const { return kTile * kWaves / hw; }
-    __device__ __forceinline__ int head_groups() const { return p.Hkv / hw; }
+    __device__ __forceinline__ int page(int key) const { return by_block.of(key); }
+    __device__ __forceinline__ int round_keys() const { return (kTile * kWaves) >> log_hw; }
     __device__ __forceinline__ int share_of(int total) const { return max((total + shares - 1) / shares, min_share); }
 };
 
@@ -122,13 +136,12 @@ __device__ __forceinline__ void visible(const PagedAttn& p, const Seq& s, int pr
 }
 
 // Keys [lo, hi) that some column of tile ct sees.
-__device__ __forceinline__ void tile_keys(const PagedAttn& p, const Seq& s, int prefix, int group, int ct, int& lo,
-                                          int& hi) {
-    const int first = ct * kCols / group;
-    const int last = min(s.nq * group - 1, ct * kCols + kCols - 1) / group;
+__device__ __forceinline__ void tile_keys(const StreamArgs& a, const Seq& s, int prefix, int ct, int& lo, int& hi) {
+    const int first = a.by_group.of(ct * kCols);
+    const int last = a.by_group.of(min(s.nq * a.group - 1, ct * kCols + kCols - 1));
     int unused;
-    visible(p, s, prefix, first, lo, unused);
-    visible(p, s, prefix, last, unused, hi);
+    visible(a.p, s, prefix, first, lo, unused);
+    visible(a.p, s, prefix, last, unused, hi);
     hi = max(hi, 0);
     lo = min(lo, hi);
 }
@@ -146,7 +159,7 @@ __device__ __forceinline__ Run run_of(const StreamArgs& a, const Seq& s, int pre
     Run r;
     // without a window every sequence starts at key 0
     r.base = a.p.window > 0 ? min(lo, max(hi, 0)) / kTile * kTile : 0;
-    r.rounds = s.nq > 0 && hi > r.base ? (hi - r.base + a.round_keys() - 1) / a.round_keys() : 0;
+    r.rounds = s.nq > 0 && hi > r.base ? (hi - r.base + a.round_keys() - 1) >> (kLogRound - a.log_hw) : 0;
     r.items = r.rounds > 0 ? (s.nq * a.group + kCols - 1) / kCols : 0;
     return r;
 }
@@ -181,7 +194,7 @@ __device__ __forceinline__ Found find_share(const StreamArgs& a, int* lds) {
     const bool once = p.B <= kThreads;
     for (int pass = 0; pass < 2; ++pass) {
         const int share = a.share_of(total);
-        const int64_t start = (int64_t)(blockIdx.x / a.head_groups()) * share;  // of the second pass
+        const int64_t start = (int64_t)(a.by_head_groups.of(blockIdx.x)) * share;  // of the second pass
         int run = 0;
         for (int b0 = 0; b0 < p.B; b0 += kThreads) {
             const int b = b0 + tid;
@@ -301,11 +314,6 @@ __device__ __forceinline__ float max_over_groups(float v) {
     return fmaxf(v, swap32(v));
 }
 
-__device__ __forceinline__ float sum_over_groups(float v) {
-    v += swap16(v);
-    return v + swap32(v);
-}
-
 // cap * tanh(x / cap) in fp32: 1 - 2 / (exp(2 x / cap) + 1), whose absolute
 // error is that of a few roundings at the cap's magnitude.
 __device__ __forceinline__ float soft_cap(float x, float cap, float two_log2e_over_cap) {
@@ -313,16 +321,16 @@ __device__ __forceinline__ float soft_cap(float x, float cap, float two_log2e_ov
     return cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(e + 1.0f));
 }
 
-// Four channels of an output row from its sum r of p_j code(v_j), maximum M
+// Four channels of an output row from its sum r of p_j code(v_j), reference M
 // and sum L of p_j; an empty row (L == 0) is zeros, its log-sum-exp -inf.
-__device__ __forceinline__ void write_row(const PagedAttn& p, int64_t row, int h, int group, int D, int d, float M,
+__device__ __forceinline__ void write_row(const PagedAttn& p, int64_t row, int h, int hk, int D, int d, float M,
                                           float L, const float4& r) {
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    const float4 sc = *reinterpret_cast<const float4*>(p.scales + (int64_t)(p.Hkv + h / group) * D + d);
+    const float4 sc = *reinterpret_cast<const float4*>(p.scales + (int64_t)(p.Hkv + hk) * D + d);
     store_o4(p, row * p.ldo + (int64_t)h * D + d,
              make_float4(r.x * inv * fmaxf(sc.x, kScaleFloor), r.y * inv * fmaxf(sc.y, kScaleFloor),
                          r.z * inv * fmaxf(sc.z, kScaleFloor), r.w * inv * fmaxf(sc.w, kScaleFloor)));
-    if (p.lse && d == 0) p.lse[row * p.Hq + h] = L == 0.0f ? -INFINITY : kLn2 * (M - kPShift + __builtin_amdgcn_logf(L));
+    if (p.lse && d == 0) p.lse[row * p.Hq + h] = L == 0.0f ? -INFINITY : kLn2 * (M + __builtin_amdgcn_logf(L));
 }
 
 template <int D>
@@ -340,14 +348,14 @@ __device__ __forceinline__ void dma16(const uint8_t* src, uint8_t* lds) {
 }
 
 // LDS of a workgroup: every wave's ring of two tiles (K rows, then V rows), the
-// rows' cache slots and page numbers, and the waves' maxima and sums; the ring is free again
+// rows' cache offsets and page numbers, and the waves' references and sums; the ring is free again
 // when the waves' outputs are joined in it.
 template <int D>
 struct StreamLds {
     static constexpr int kStages = D == 64 ? 4 : 2;
     static constexpr int kRing = kStages * 2 * kTile * D;  // bytes of a wave
-    static constexpr int kSlots = kWaves * kRing;
-    static constexpr int kPages = kSlots + kWaves * kTile * 4;
+    static constexpr int kRows = kWaves * kRing;
+    static constexpr int kPages = kRows + kWaves * kTile * 8;
     static constexpr int kMl = kPages + kWaves * kStages * kWave * 4;
     static constexpr int kBytes = kMl + kWaves * kCols * 8;
 };
@@ -358,8 +366,9 @@ __device__ __forceinline__ uint32_t word(uint32_t v, int) { return v; }
 __device__ __forceinline__ uint32_t word(const v2u& v, int i) { return v[i]; }
 __device__ __forceinline__ uint32_t word(const v4u& v, int i) { return v[i]; }
 
-// BIAS: the score cap and the distance bias are compiled in.
-template <int D, int FMT, bool BIAS>
+// BIAS: the score cap and the distance bias are compiled in.  TERMS: fp16 terms
+// of the scaled query and of p.
+template <int D, int FMT, bool BIAS, int TERMS>
 __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(StreamArgs a) {
     const PagedAttn& p = a.p;
     constexpr int NJ = D / 32;           // matrix instructions along the channels of K
@@ -375,7 +384,7 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
     uint8_t* const ring = attn_smem + wave * Lds::kRing;
-    int* const slots = reinterpret_cast<int*>(attn_smem + Lds::kSlots) + wave * kTile;
+    uint64_t* const rows = reinterpret_cast<uint64_t*>(attn_smem + Lds::kRows) + wave * kTile;
     int* const pages = reinterpret_cast<int*>(attn_smem + Lds::kPages) + wave * S * kWave;
     float2* const ml = reinterpret_cast<float2*>(attn_smem + Lds::kMl);
     const int n = lane % 16, g = lane / 16;
@@ -387,11 +396,11 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
     int left = 0;                            // cost left of the share
     if (a.shares > 0) {
         const Found f = find_share(a, reinterpret_cast<int*>(attn_smem));
-        const int share = a.share_of(f.total), nth = blockIdx.x / a.head_groups();
+        const int share = a.share_of(f.total), nth = a.by_head_groups.of(blockIdx.x);
         const int64_t start = (int64_t)nth * share;
         left = (int)min((int64_t)share, f.total - start);
         if (left <= 0) return;
-        hg = blockIdx.x - nth * a.head_groups();
+        hg = blockIdx.x - nth * a.head_groups;
         b = __builtin_amdgcn_readfirstlane(f.b);
         const Run r = run_of(a, sequence(p, b), p.prefix ? p.prefix[b] : 0);
         const int at = (int)start - f.before;
@@ -399,8 +408,8 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
         at_item = __builtin_amdgcn_readfirstlane(at - ct * (r.rounds + kItemCost));
         __syncthreads();
     } else {
-        hg = blockIdx.x % a.head_groups();
-        b = blockIdx.x / a.head_groups();
+        b = a.by_head_groups.of(blockIdx.x);
+        hg = blockIdx.x - b * a.head_groups;
         ct = blockIdx.y;
     }
 
@@ -426,7 +435,7 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
         }
         // where the result goes: the rows, or the share's first or last part
         const int part = r0 == 0 && r1 == run.rounds ? -1 : 2 * (int)blockIdx.x + (r0 == 0);
-        const int hk0 = hg * a.hw, hk = hk0 + wave % a.hw;
+        const int hk0 = hg * a.hw, hk = hk0 + (wave & (a.hw - 1));
         const int32_t* table = p.block_table + (int64_t)b * p.ld_table;
 
         if (!mine) break;
@@ -434,26 +443,27 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
         // this lane's column
         const int col = ct * kCols + n;
         const bool has_col = col < seq.nq * a.group;
-        const int qi = has_col ? col / a.group : 0;
+        const int qi = has_col ? a.by_group.of(col) : 0;
         const int head = hk * a.group + (has_col ? col - qi * a.group : 0);
         const int64_t row = seq.row0 + qi;
         int lo, hi, tlo, thi;
         visible(p, seq, prefix, qi, lo, hi);
         if (!has_col) hi = 0;
-        tile_keys(p, seq, prefix, a.group, ct, tlo, thi);
+        tile_keys(a, seq, prefix, ct, tlo, thi);
 
         const float slope = p.alibi ? p.alibi[head] * kLog2e : 0.0f;
         const int pos = seq.len - seq.nq + qi;
         const float cap_in = p.softcap > 0.0f ? 2.0f * kLog2e / p.softcap : 0.0f;
 
-        float m = -INFINITY, l = 0.0f;
-        v4f o[VB];
+        float m = kNoRef;
+        v4f o[VB], l = {0.0f, 0.0f, 0.0f, 0.0f};  // the sum of p, four times over
 #pragma unroll
-        for (int j = 0; j < VB; ++j) o[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < VB; ++j) o[j] = l;
+        const v8h ones = {1, 1, 1, 1, 1, 1, 1, 1};
 
         // this wave's tiles: keys k0 + stride i and on, up to `end`
         const int stride = a.round_keys();
-        const int k0 = run.base + r0 * stride + wave / a.hw * kTile;
+        const int k0 = run.base + r0 * stride + (wave >> a.log_hw) * kTile;
         const int end = (int)min((int64_t)thi, (int64_t)run.base + (int64_t)r1 * stride);
 
         // Page numbers of keys key0 + lane % 32, by DMA into LDS: as a load into a register the compiler would wait for
@@ -463,24 +473,25 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
             __builtin_amdgcn_global_load_lds(table + min(a.page(k0 + i * stride + lane % kTile), last_page),
                                              pages + i % S * kWave, 4, 0, 0);
         };
-        // cache rows of the tile's keys into LDS, 0 for none; returns the mask of those that are there
+        // byte offsets of the tile's cache rows into LDS, 0 for none; returns the mask of those that are there
         auto rows_of = [&](int i) {
             const int key = k0 + i * stride + lane % kTile, page = pages[i % S * kWave + lane];
             const bool ok = key >= tlo && key < end && page >= 0 && page < p.num_blocks;
-            if (lane < kTile) slots[lane] = ok ? (page - a.page(key)) * p.block + key : 0;
+            const uint32_t row = ok ? (page - a.page(key)) * p.block + key : 0;
+            if (lane < kTile) rows[lane] = (uint64_t)row * C;
             __builtin_amdgcn_wave_barrier();  // read below by this wave's other lanes; a wave's LDS accesses are in order
             return (uint32_t)__ballot(ok);
         };
         const uint8_t* const kbase = p.cache + hk * D;
         auto fetch = [&](int i) {
             uint8_t* const tile = ring + i % S * kTileBytes;
-            uint32_t row[NI];
+            uint64_t row[NI];
 #pragma unroll
-            for (int j = 0; j < NI; ++j) row[j] = slots[RI * j + lane / UR];
+            for (int j = 0; j < NI; ++j) row[j] = rows[RI * j + lane / UR];
 #pragma unroll
             for (int j = 0; j < NI; ++j) {
                 const int r = RI * j + lane / UR;
-                const uint8_t* src = kbase + (uint64_t)row[j] * C + ((lane % UR) ^ swizzle<D>(r)) * 16;
+                const uint8_t* src = kbase + row[j] + ((lane % UR) ^ swizzle<D>(r)) * 16;
                 dma16(src, tile + j * 1024);
                 dma16(src + p.Hkv * D, tile + kTile * D + j * 1024);
             }
@@ -513,8 +524,8 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         fill();
 
-        // meanwhile: q times the key scales, as two fp16 terms
-        v8h qh[NJ], ql[NJ];
+        // meanwhile: q times the key scales, in fp16 terms
+        v8h qt[TERMS][NJ];
         float c;  // score (log2 units, or natural ones under a cap) per unit of the product
         {
             float x[NJ][8], top = 0.0f;
@@ -536,8 +547,8 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float y = __builtin_amdgcn_ldexpf(x[j][e], shift);
-                    qh[j][e] = (_Float16)y;
-                    ql[j][e] = (_Float16)(y - (float)qh[j][e]);
+                    qt[0][j][e] = (_Float16)y;
+                    if constexpr (TERMS == 2) qt[1][j][e] = (_Float16)(y - (float)qt[0][j][e]);
                 }
             c = __builtin_amdgcn_ldexpf(p.scale, -shift);
         }
@@ -562,7 +573,7 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
                 v[e] = *reinterpret_cast<const vrow*>(tile + kTile * D + r * D + ((n * VB / 16) ^ swizzle<D>(r)) * 16 +
                                                       n * VB % 16);
             }
-            float s[2][4];
+            v4f s[2];  // products; under BIAS scores
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 v4f acc = {0.0f, 0.0f, 0.0f, 0.0f}, rest = acc;
@@ -572,58 +583,68 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
 #pragma unroll
                     for (int j = 2 * i; j < 2 * i + 2; ++j) {
                         const v8h k = row_f16<FMT>(w[2 * (j % 2)], w[2 * (j % 2) + 1]);
-                        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qh[j], acc, 0, 0, 0);
-                        rest = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, ql[j], rest, 0, 0, 0);
+                        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qt[0][j], acc, 0, 0, 0);
+                        if constexpr (TERMS == 2) rest = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qt[1][j], rest, 0, 0, 0);
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[t][i] = (acc[i] + rest[i]) * c;
+                s[t] = TERMS == 2 ? acc + rest : acc;
             }
             if constexpr (BIAS) {
-                if (p.softcap > 0.0f) {
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) s[t][i] = kLog2e * soft_cap(s[t][i], p.softcap, cap_in);
-                }
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[t][i] += slope * (float)(key0 + 16 * t + 4 * g + i - pos);
-            }
-            const bool whole = mask == 0xFFFFFFFFu && !__any(key0 < lo || key0 + kTile > hi);
-            if (!whole) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int j = 16 * t + 4 * g + i;
-                        const bool see = ((mask >> j) & 1u) && key0 + j >= lo && key0 + j < hi;
-                        s[t][i] = see ? s[t][i] : -INFINITY;
-                        // a code behind the sequence may be anything, NaN too: 0 * NaN must not reach the sum
-                        v[4 * t + i] = ((mask >> j) & 1u) ? v[4 * t + i] : vrow(0u);
+                        float x = s[t][i] * c;
+                        if (p.softcap > 0.0f) x = kLog2e * soft_cap(x, p.softcap, cap_in);
+                        s[t][i] = x + slope * (float)(key0 + 16 * t + 4 * g + i - pos);
                     }
             }
-            float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                              fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-            if (__any(top > m + kSlack)) {
-                const float up = fmaxf(max_over_groups(top), m);
-                const float f = up == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - up);
-                m = up;
+            const bool whole = mask == 0xFFFFFFFFu && !__any(key0 < lo || key0 + kTile > hi);
+            float x[8];  // scores above the reference
+            auto above = [&]() {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    x[e] = BIAS ? s[e / 4][e % 4] - m : __builtin_fmaf(s[e / 4][e % 4], c, -m);
+            };
+            auto hide = [&]() {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int j = 16 * (e / 4) + 4 * g + e % 4;
+                    const bool see = ((mask >> j) & 1u) && key0 + j >= lo && key0 + j < hi;
+                    x[e] = see ? x[e] : -INFINITY;
+                    // a code behind the sequence may be anything, NaN too: 0 * NaN must not reach the sum
+                    v[e] = ((mask >> j) & 1u) ? v[e] : vrow(0u);
+                }
+            };
+            above();
+            if (!whole) hide();
+            float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+            if (__any(top > kPLimit)) {
+                // move the references of the columns that need it, kPShift below the largest score; scores past 2^24 are
+                // themselves too coarse for the shift, and one of them takes all the weight
+                const float old = m;
+                m = 0.0f;
+                above();
+                if (!whole) hide();
+                top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+                top = max_over_groups(top);
+                m = top > old + kPLimit ? (fabsf(top) < 16777216.0f ? top - kPShift : top) : old;
+                const float f = __builtin_amdgcn_exp2f(old - m);
                 l *= f;
 #pragma unroll
                 for (int j = 0; j < VB; ++j) o[j] *= f;
+                above();
+                if (!whole) hide();
             }
-            const float mm = m == -INFINITY ? 0.0f : m;
             v8h ph, pl;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                // the shift is added last: m - kPShift would round for large scores and p pass fp16's range
-                const float x = __builtin_amdgcn_exp2f((s[e / 4][e % 4] - mm) + kPShift);
-                l += x;
-                ph[e] = (_Float16)x;
-                pl[e] = (_Float16)(x - (float)ph[e]);
+                const float y = __builtin_amdgcn_exp2f(x[e]);
+                ph[e] = (_Float16)y;
+                if constexpr (TERMS == 2) pl[e] = (_Float16)(y - (float)ph[e]);
             }
+            l = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, ph, l, 0, 0, 0);
+            if constexpr (TERMS == 2) l = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pl, l, 0, 0, 0);
 #pragma unroll
             for (int j = 0; j < VB; ++j) {
                 v4u r;
@@ -631,7 +652,7 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
                 for (int i = 0; i < 4; ++i) r[i] = pair_f16<FMT>(word(v[2 * i], j / 4), word(v[2 * i + 1], j / 4), j % 4);
                 const v8h vt = __builtin_bit_cast(v8h, r);
                 o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vt, ph, o[j], 0, 0, 0);
-                o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vt, pl, o[j], 0, 0, 0);
+                if constexpr (TERMS == 2) o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vt, pl, o[j], 0, 0, 0);
             }
         };
 
@@ -647,10 +668,8 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
             for (int j = 0; j < S - 1; ++j) masks[j] = masks[j + 1];
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing lands in the ring any more
-        l = sum_over_groups(l);
-
         // the waves of a head joined in wave order
-        if (g == 0) ml[wave * kCols + n] = make_float2(m, l);
+        if (g == 0) ml[wave * kCols + n] = make_float2(m, l[0]);
         float* const outs = reinterpret_cast<float*>(ring);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -663,24 +682,24 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
             const int d = x % (D / 4) * 4, cc = x / (D / 4) % kCols, hs = x / (D / 4 * kCols);
             const int ccol = ct * kCols + cc;
             if (ccol >= seq.nq * a.group) continue;
-            float M = -INFINITY, L = 0.0f;
+            float M = kNoRef, L = 0.0f;
             for (int w = hs; w < kWaves; w += a.hw) M = fmaxf(M, ml[w * kCols + cc].x);
             float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             for (int w = hs; w < kWaves; w += a.hw) {
                 const float2 y = ml[w * kCols + cc];
-                const float f = y.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(y.x - M);
+                const float f = __builtin_amdgcn_exp2f(y.x - M);
                 const float4 v = *reinterpret_cast<const float4*>(attn_smem + w * Lds::kRing + (cc * kOutRow + d) * 4);
                 L += f * y.y;
                 r = make_float4(r.x + f * v.x, r.y + f * v.y, r.z + f * v.z, r.w + f * v.w);
             }
-            const int i = ccol / a.group, h = (hk0 + hs) * a.group + ccol % a.group;
+            const int i = a.by_group.of(ccol), h = (hk0 + hs) * a.group + ccol - i * a.group;
             const int64_t orow = seq.row0 + i;
             if (part >= 0) {
                 const int64_t at = ((int64_t)part * a.hw + hs) * kCols + cc;
                 if (d == 0) a.part_ml[at] = make_float2(M, L);
                 *reinterpret_cast<float4*>(a.part_o + at * D + d) = r;
             } else {
-                write_row(p, orow, h, a.group, D, d, M, L, r);
+                write_row(p, orow, h, hk0 + hs, D, d, M, L, r);
             }
         }
         __syncthreads();
@@ -704,64 +723,79 @@ __global__ __launch_bounds__(kWaves* kWave) void attn_join(StreamArgs a) {
     constexpr int kThreads = kWaves * kWave;
     constexpr int kLanes = D / 4;                // threads of a group
     constexpr int kGroups = kThreads / kLanes;
+    constexpr int kBatch = 8;
     __shared__ float4 sums[kThreads];
-    __shared__ float lsum[kGroups];
+    __shared__ float2 group_ml[kGroups];
     const int tid = threadIdx.x, d4 = tid % kLanes, grp = tid / kLanes, part = grp % a.spread;
-    const int64_t heads = (int64_t)blockIdx.x * (kGroups / a.spread) + grp / a.spread;  // row of the launch: (i0, b, h)
-    const int h = (int)(heads % p.Hq), b = (int)(heads / p.Hq % p.B);
-    const int i0 = (int)(heads / p.Hq / p.B);
+    const uint32_t nth = blockIdx.x * (kGroups / a.spread) + grp / a.spread;  // row of the launch: (i0, b, h)
+    const uint32_t rest = nth / p.Hq;
+    const int h = (int)(nth - rest * p.Hq), i0 = (int)(rest / p.B), b = (int)(rest - i0 * p.B);
+    const int hk = a.by_group.of(h);
     const bool live = i0 < a.join_rows;
     Seq seq = {0, 0, 0};
     if (live) seq = sequence(p, b);
     const int prefix = live && p.prefix ? p.prefix[b] : 0;
     // Every thread goes through as many rounds as the longest sequence of its workgroup: the barriers are for all.
     for (int i = i0; __syncthreads_or(i < seq.nq); i += a.join_rows) {
-        float M = -INFINITY, L = 0.0f;
+        float M = kNoRef, L = 0.0f;
         float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         int shares = 0;
         bool cut = false;  // else the first kernel has written the row
         if (i < seq.nq) {
             // the shares that its item was cut into, as the first kernel dealt them out
             const Run run = run_of(a, seq, prefix);
-            const int col = i * a.group + h % a.group, hk = h / a.group;
+            const int col = i * a.group + h - hk * a.group;
             const int at = a.starts[b] + col / kCols * (run.rounds + kItemCost) + kItemCost;
             const int share = a.share_of(a.starts[p.B]);
             const int first = at / share;
             shares = run.rounds == 0 ? 0 : (at + run.rounds - 1) / share - first + 1;
             cut = shares != 1;
             if (cut) {
-                // the item's first round is in its first share
-                const auto slot = [&](int s) {
-                    const int group = (first + s) * a.head_groups() + hk / a.hw;
-                    return ((2 * group + (s == 0)) * a.hw + hk % a.hw) * kCols + col % kCols;
-                };
-                for (int s = d4; s < shares; s += kLanes) M = fmaxf(M, a.part_ml[slot(s)].x);
+                // the item's first round is in its first share; kBatch shares at a time, so that their loads travel together
+                for (int s0 = part; s0 < shares; s0 += kBatch * a.spread) {
+                    float2 y[kBatch];
+                    float4 v[kBatch];
+                    float top = M;
 #pragma unroll
-                for (int off = kLanes / 2; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, kLanes));
-#pragma unroll 8
-                for (int s = part; s < shares; s += a.spread) {
-                    const int x = slot(s);
-                    const float2 y = a.part_ml[x];
-                    const float4 v = *reinterpret_cast<const float4*>(a.part_o + (int64_t)x * D + 4 * d4);
-                    const float f = y.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(y.x - M);
-                    L += f * y.y;
-                    r = make_float4(r.x + f * v.x, r.y + f * v.y, r.z + f * v.z, r.w + f * v.w);
+                    for (int k = 0; k < kBatch; ++k) {
+                        const int s = min(s0 + k * a.spread, shares - 1);
+                        const int group = (first + s) * a.head_groups + (hk >> a.log_hw);
+                        const int x = ((2 * group + (s == 0)) * a.hw + (hk & (a.hw - 1))) * kCols + col % kCols;
+                        y[k] = a.part_ml[x];
+                        v[k] = *reinterpret_cast<const float4*>(a.part_o + (int64_t)x * D + 4 * d4);
+                        if (s0 + k * a.spread >= shares) y[k].x = kNoRef;
+                        top = fmaxf(top, y[k].x);
+                    }
+                    const float g = __builtin_amdgcn_exp2f(M - top);
+                    M = top;
+                    L *= g;
+                    r = make_float4(r.x * g, r.y * g, r.z * g, r.w * g);
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        if (s0 + k * a.spread >= shares) break;
+                        const float f = __builtin_amdgcn_exp2f(y[k].x - M);
+                        L += f * y[k].y;
+                        r = make_float4(r.x + f * v[k].x, r.y + f * v[k].y, r.z + f * v[k].z, r.w + f * v[k].w);
+                    }
                 }
             }
         }
         if (a.spread > 1) {
             sums[tid] = r;
-            if (d4 == 0) lsum[grp] = L;
+            if (d4 == 0) group_ml[grp] = make_float2(M, L);
             __syncthreads();
             if (part == 0) {
                 for (int k = 1; k < a.spread; ++k) {
                     const float4 v = sums[tid + k * kLanes];
-                    r = make_float4(r.x + v.x, r.y + v.y, r.z + v.z, r.w + v.w);
-                    L += lsum[grp + k];
+                    const float2 y = group_ml[grp + k];
+                    const float top = fmaxf(M, y.x), f = __builtin_amdgcn_exp2f(M - top), g = __builtin_amdgcn_exp2f(y.x - top);
+                    M = top;
+                    L = L * f + y.y * g;
+                    r = make_float4(r.x * f + v.x * g, r.y * f + v.y * g, r.z * f + v.z * g, r.w * f + v.w * g);
                 }
             }
         }
-        if (part == 0 && cut) write_row(p, seq.row0 + i, h, a.group, D, 4 * d4, M, L, r);
+        if (part == 0 && cut) write_row(p, seq.row0 + i, h, hk, D, 4 * d4, M, L, r);
     }
 }
 
@@ -800,26 +834,29 @@ StreamPlan stream_plan(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t
     return s;
 }
 
-template <int D, int FMT, bool BIAS>
+template <int D, int FMT, bool BIAS, int TERMS>
 hipError_t launch_stream(const StreamArgs& a, hipStream_t stream) {
     constexpr int lds = StreamLds<D>::kBytes;
-    const unsigned groups = a.p.Hkv / a.hw;
+    const unsigned groups = a.head_groups;
     const dim3 grid = a.shares > 0 ? dim3(a.shares * groups) : dim3(a.p.B * groups, (unsigned)a.col_tiles);
     if constexpr (lds > 64 * 1024) {
-        const hipError_t e = FP8K_SET_LDS((attn_stream<D, FMT, BIAS>), lds);
+        const hipError_t e = FP8K_SET_LDS((attn_stream<D, FMT, BIAS, TERMS>), lds);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((attn_stream<D, FMT, BIAS>), grid, dim3(kWaves * kWave), lds, stream, a);
+    hipLaunchKernelGGL((attn_stream<D, FMT, BIAS, TERMS>), grid, dim3(kWaves * kWave), lds, stream, a);
     return hipGetLastError();
 }
 
 template <int D>
 hipError_t launch(StreamArgs a, int fmt, int64_t max_q, hipStream_t stream) {
-    const bool bias = a.p.softcap > 0.0f || a.p.alibi != nullptr;
-    hipError_t e = fmt == kKvE5M2 ? (bias ? launch_stream<D, kKvE5M2, true>(a, stream)
-                                          : launch_stream<D, kKvE5M2, false>(a, stream))
-                                  : (bias ? launch_stream<D, kKvE4M3, true>(a, stream)
-                                          : launch_stream<D, kKvE4M3, false>(a, stream));
+    const bool bias = a.p.softcap > 0.0f || a.p.alibi != nullptr, one = a.p.dtype == kKvBF16;
+    hipError_t e;
+    if (fmt == kKvE5M2)
+        e = bias ? (one ? launch_stream<D, kKvE5M2, true, 1>(a, stream) : launch_stream<D, kKvE5M2, true, 2>(a, stream))
+                 : (one ? launch_stream<D, kKvE5M2, false, 1>(a, stream) : launch_stream<D, kKvE5M2, false, 2>(a, stream));
+    else
+        e = bias ? (one ? launch_stream<D, kKvE4M3, true, 1>(a, stream) : launch_stream<D, kKvE4M3, true, 2>(a, stream))
+                 : (one ? launch_stream<D, kKvE4M3, false, 1>(a, stream) : launch_stream<D, kKvE4M3, false, 2>(a, stream));
     if (e != hipSuccess || a.shares == 0) return e;
     const int64_t heads = (int64_t)a.p.B * a.p.Hq;
     a.join_rows = (int)std::max<int64_t>(1, std::min(max_q, kMaxGrid / heads));
@@ -857,10 +894,11 @@ hipError_t launch_attn_paged(const PagedAttn& p, int D, int fmt, int64_t max_q, 
         a.part_ml = reinterpret_cast<float2*>(a.part_o + cols * D);
         a.starts = reinterpret_cast<int*>(a.part_ml + cols);
     }
-    // magic = ceil(2^shift / block), shift = 31 + ceil(log2(block)), is off by e < 1, which adds key e / 2^shift < 1 / block
-    a.shift = 31;
-    while ((int64_t(1) << (a.shift - 31)) < p.block) ++a.shift;
-    a.magic = (uint32_t)(((uint64_t(1) << a.shift) + p.block - 1) / p.block);
+    a.log_hw = s.hw == 4 ? 2 : s.hw == 2 ? 1 : 0;
+    a.head_groups = p.Hkv / s.hw;
+    a.by_block = FastDiv(p.block);
+    a.by_group = FastDiv(a.group);
+    a.by_head_groups = FastDiv(a.head_groups);
     const int64_t q = std::max<int64_t>(1, max_q);
     switch (D) {
         case 64: return launch<64>(a, fmt, q, stream);

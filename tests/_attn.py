@@ -41,14 +41,16 @@ def make(lens, Hq, Hkv, D, block, fmt, dtype, seed, new=None, extra_pages=3, wid
 def reference(s, causal=True, softcap=0.0, alibi=None, window=0, prefix=None, sm_scale=None):
     """(out, lse, tol) in float64.  tol: how far out may be off, elementwise, for an output of q's type.
 
-    The operator's own arithmetic, against the exact value: q times the key scale and p each go through two fp16
-    terms (22 bits: relative 2^-22 each), a score is a sum of D products in fp32 (at most (D + 8) roundings of
-    2^-24 of sum |q k|, twice for the two terms), its exponential is good to 2^-22 plus the rounding of its argument
+    The operator's own arithmetic, against the exact value: q times the key scale and p each go through one fp16 term
+    where the output is bf16 (off by half a step, 2^-11 relative) and two where it is fp16 or fp32 (2^-22), `term`
+    below, a score is a sum of D products in fp32 (at most (D + 8) roundings of 2^-24 of sum |q k|, twice for the two
+    terms), its exponential is good to 2^-22 plus the rounding of its argument
     (2^-23 of |score| in base 2, under 2^-22 of the natural one), the cap and the bias add roundings of their own
     magnitude (2^-20 of the cap: 1 - 2 / (e + 1) and two approximations of 1 ulp; 2^-23 of the bias).  With ds the sum
     of those, p is off by the factor 1 +- ds, numerator and denominator both, so out by 2 ds * A with
     A = sum p |v| / sum p; the fp32 sums over n keys add n 2^-24 A at the most, and the value scale and the
     division 2^-22 A.  Then one rounding to the type.  s["lse_tol"] receives the same for lse."""
+    term = 2.0 ** -11 if s["q"].dtype == torch.bfloat16 else 2.0 ** -22
     q, D, Hq, Hkv, block = s["q"].double(), s["D"], s["Hq"], s["Hkv"], s["block"]
     G = Hq // Hkv
     scale = D ** -0.5 if sm_scale is None else sm_scale
@@ -81,7 +83,7 @@ def reference(s, causal=True, softcap=0.0, alibi=None, window=0, prefix=None, sm
             x = q[r0:r1, h]
             w = x @ k.T * scale
             mag = x.abs() @ k.abs().T * abs(scale)
-            ds = mag * (2.0 ** -21 + 2 * (D + 8) * 2.0 ** -24)
+            ds = mag * (term + 2.0 ** -22 + 2 * (D + 8) * 2.0 ** -24)
             if softcap:
                 w = softcap * torch.tanh(w / softcap)
                 ds = ds + softcap * 2.0 ** -20
@@ -89,7 +91,7 @@ def reference(s, causal=True, softcap=0.0, alibi=None, window=0, prefix=None, sm
                 bias = float(alibi[h]) * (j[None, :] - pos)
                 w = w + bias
                 ds = ds + bias.abs() * 2.0 ** -23
-            ds = ds + w.abs() * 2.0 ** -22 + 2.0 ** -21
+            ds = ds + w.abs() * 2.0 ** -22 + term + 2.0 ** -21
             w = torch.where(see, w, -math.inf)
             any_ = see.any(1)
             m = torch.where(any_, w.max(1).values, 0.0)[:, None]
