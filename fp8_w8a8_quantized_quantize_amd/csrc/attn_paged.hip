@@ -98,9 +98,9 @@ struct StreamArgs {
     float* part_o;     // [workgroups][2][hw][kCols][D]: parts of rows, a share's first and last
     float2* part_ml;   // [workgroups][2][hw][kCols]: reference (log2), sum
     int* starts;       // [B + 1]: cost before every sequence, cost of all
-    int spread;        // the join's thread groups per output row
+    int spread, log_spread;  // the join's thread groups per output row
     int join_rows;     // and the new rows of a sequence it takes at a time
-    FastDiv by_block, by_group, by_head_groups;
+    FastDiv by_block, by_group, by_head_groups, by_heads, by_batch;
 
     __device__ __forceinline__ int page(int key) const { return by_block.of(key); }
     __device__ __forceinline__ int round_keys() const { return (kTile * kWaves) >> log_hw; }
@@ -168,6 +168,17 @@ __device__ __forceinline__ Run run_of(const StreamArgs& a, const Seq& s, int pre
 // the join of its waves) in rounds: measured about 6 us against 1.5 us a round.
 constexpr int kItemCost = 4;
 
+// Inclusive sums over the lanes of a wave.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);   // row_shr:2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);   // row_shr:4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);   // row_shr:8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
+    return v;
+}
+
 // The sequence in which this workgroup's share starts, the cost before that
 // sequence, and the cost of all: thread i scans sequence i, 256 at a time.
 // Workgroup 0 leaves the starts for the join.
@@ -188,6 +199,19 @@ __device__ __forceinline__ Found find_share(const StreamArgs& a, int* lds) {
         if (blockIdx.x == 0 && tid == 0) a.starts[0] = 0, a.starts[1] = total;
         return Found{0, 0, total};
     }
+    if (p.B <= kWave) {
+        // every wave for itself
+        const int mine = lane < p.B ? cost(lane) : 0, upto = wave_scan(mine);
+        const int total = __builtin_amdgcn_readlane(upto, kWave - 1);
+        const int64_t start = (int64_t)a.by_head_groups.of(blockIdx.x) * a.share_of(total);
+        const uint64_t past = __ballot(upto > start);
+        if (blockIdx.x == 0 && wave == 0) {
+            if (lane < p.B) a.starts[lane] = upto - mine;
+            if (lane == 0) a.starts[p.B] = total;
+        }
+        const int b = past ? __builtin_ctzll(past) : 0;
+        return Found{b, __builtin_amdgcn_readlane(upto - mine, b), total};
+    }
     int* const wave_sum = lds;       // [2][kWaves], by turns
     int* const found = lds + 2 * kWaves;
     int total = 0, before = 0, mine = 0, turn = 0;
@@ -200,12 +224,7 @@ __device__ __forceinline__ Found find_share(const StreamArgs& a, int* lds) {
             const int b = b0 + tid;
             if (pass == 0 || !once) {
                 mine = b < p.B ? cost(b) : 0;
-                int sum = mine;
-#pragma unroll
-                for (int by = 1; by < kWave; by <<= 1) {
-                    const int v = __shfl_up(sum, by, kWave);
-                    if (lane >= by) sum += v;
-                }
+                const int sum = wave_scan(mine);
                 int* const sums = wave_sum + turn * kWaves;
                 turn ^= 1;
                 if (lane == kWave - 1) sums[wave] = sum;
@@ -257,8 +276,9 @@ __device__ __forceinline__ v8h row_f16(uint32_t lo, uint32_t hi) {
 }
 
 // 8 consecutive elements of a query row, as they are and as fp32.
+template <int TERMS>  // 1: bf16, 2: fp16 or fp32
 __device__ __forceinline__ void load_q8(const PagedAttn& p, int64_t e, v4u (&raw)[2]) {
-    if (p.dtype == kKvF32) {
+    if (TERMS == 2 && p.dtype == kKvF32) {
         const v4u* f = reinterpret_cast<const v4u*>(static_cast<const float*>(p.q) + e);
         raw[0] = f[0];
         raw[1] = f[1];
@@ -268,15 +288,16 @@ __device__ __forceinline__ void load_q8(const PagedAttn& p, int64_t e, v4u (&raw
     }
 }
 
+template <int TERMS>
 __device__ __forceinline__ void unpack_q8(const PagedAttn& p, const v4u (&raw)[2], float (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (p.dtype == kKvF32) {
-            x[i] = __uint_as_float(raw[0][i]);
-            x[4 + i] = __uint_as_float(raw[1][i]);
-        } else if (p.dtype == kKvBF16) {
+        if (TERMS == 1) {
             x[2 * i] = __uint_as_float(raw[0][i] << 16);
             x[2 * i + 1] = __uint_as_float(raw[0][i] & 0xFFFF0000u);
+        } else if (p.dtype == kKvF32) {
+            x[i] = __uint_as_float(raw[0][i]);
+            x[4 + i] = __uint_as_float(raw[1][i]);
         } else {
             x[2 * i] = half_to_float(raw[0][i] & 0xFFFFu);
             x[2 * i + 1] = half_to_float(raw[0][i] >> 16);
@@ -517,7 +538,7 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const int e0 = 64 * (j / 2) + 16 * g + 8 * (j % 2);
-            load_q8(p, row * p.ldq + (int64_t)head * D + e0, raw[j]);
+            load_q8<TERMS>(p, row * p.ldq + (int64_t)head * D + e0, raw[j]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) ks[j][i] = *reinterpret_cast<const float4*>(p.scales + hk * D + e0 + 4 * i);
         }
@@ -531,7 +552,7 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
             float x[NJ][8], top = 0.0f;
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-                unpack_q8(p, raw[j], x[j]);
+                unpack_q8<TERMS>(p, raw[j], x[j]);
                 const float s[8] = {ks[j][0].x, ks[j][0].y, ks[j][0].z, ks[j][0].w,
                                     ks[j][1].x, ks[j][1].y, ks[j][1].z, ks[j][1].w};
 #pragma unroll
@@ -610,10 +631,10 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int j = 16 * (e / 4) + 4 * g + e % 4;
-                    const bool see = ((mask >> j) & 1u) && key0 + j >= lo && key0 + j < hi;
-                    x[e] = see ? x[e] : -INFINITY;
+                    const bool there = (mask >> j) & 1u;
+                    x[e] = (there & (key0 + j >= lo) & (key0 + j < hi)) ? x[e] : -INFINITY;
                     // a code behind the sequence may be anything, NaN too: 0 * NaN must not reach the sum
-                    v[e] = ((mask >> j) & 1u) ? v[e] : vrow(0u);
+                    v[e] &= there ? ~0u : 0u;
                 }
             };
             above();
@@ -668,6 +689,32 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
             for (int j = 0; j < S - 1; ++j) masks[j] = masks[j + 1];
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing lands in the ring any more
+        if (a.hw == kWaves) {
+            // a wave has its head to itself: results go from its registers
+            if (has_col) {
+                const int64_t at = part >= 0 ? ((int64_t)part * a.hw + wave) * kCols + n : 0;
+                if (part >= 0 && g == 0) a.part_ml[at] = make_float2(m, l[0]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < VB; j += 4) {
+                        const int d = (4 * g + i) * VB + j;
+                        const float4 r = make_float4(o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]);
+                        if (part >= 0)
+                            *reinterpret_cast<float4*>(a.part_o + at * D + d) = r;
+                        else
+                            write_row(p, row, head, hk, D, d, m, l[0], r);
+                    }
+            }
+            if (a.shares == 0) {
+                ct += a.col_tiles;
+            } else {
+                if (left <= 0) break;
+                ++ct;
+            }
+            continue;
+        }
+
         // the waves of a head joined in wave order
         if (g == 0) ml[wave * kCols + n] = make_float2(m, l[0]);
         float* const outs = reinterpret_cast<float*>(ring);
@@ -726,10 +773,10 @@ __global__ __launch_bounds__(kWaves* kWave) void attn_join(StreamArgs a) {
     constexpr int kBatch = 8;
     __shared__ float4 sums[kThreads];
     __shared__ float2 group_ml[kGroups];
-    const int tid = threadIdx.x, d4 = tid % kLanes, grp = tid / kLanes, part = grp % a.spread;
-    const uint32_t nth = blockIdx.x * (kGroups / a.spread) + grp / a.spread;  // row of the launch: (i0, b, h)
-    const uint32_t rest = nth / p.Hq;
-    const int h = (int)(nth - rest * p.Hq), i0 = (int)(rest / p.B), b = (int)(rest - i0 * p.B);
+    const int tid = threadIdx.x, d4 = tid % kLanes, grp = tid / kLanes, part = grp & (a.spread - 1);
+    const int nth = blockIdx.x * (kGroups >> a.log_spread) + (grp >> a.log_spread);  // row of the launch: (i0, b, h)
+    const int rest = a.by_heads.of(nth), i0 = a.by_batch.of(rest);
+    const int h = nth - rest * p.Hq, b = rest - i0 * p.B;
     const int hk = a.by_group.of(h);
     const bool live = i0 < a.join_rows;
     Seq seq = {0, 0, 0};
@@ -861,8 +908,8 @@ hipError_t launch(StreamArgs a, int fmt, int64_t max_q, hipStream_t stream) {
     const int64_t heads = (int64_t)a.p.B * a.p.Hq;
     a.join_rows = (int)std::max<int64_t>(1, std::min(max_q, kMaxGrid / heads));
     constexpr int kGroups = kWaves * kWave / (D / 4);
-    a.spread = 1;
-    while (a.spread < kGroups && heads * a.join_rows * a.spread < 2048) a.spread *= 2;
+    a.spread = 1, a.log_spread = 0;
+    while (a.spread < kGroups && heads * a.join_rows * a.spread < 2048) a.spread *= 2, ++a.log_spread;
     const int64_t per_block = kGroups / a.spread;
     const unsigned grid = (unsigned)ceil_div(heads * a.join_rows, per_block);
     hipLaunchKernelGGL((attn_join<D>), dim3(grid), dim3(kWaves * kWave), 0, stream, a);
@@ -898,6 +945,8 @@ hipError_t launch_attn_paged(const PagedAttn& p, int D, int fmt, int64_t max_q, 
     a.head_groups = p.Hkv / s.hw;
     a.by_block = FastDiv(p.block);
     a.by_group = FastDiv(a.group);
+    a.by_heads = FastDiv(p.Hq);
+    a.by_batch = FastDiv(p.B);
     a.by_head_groups = FastDiv(a.head_groups);
     const int64_t q = std::max<int64_t>(1, max_q);
     switch (D) {
