@@ -128,8 +128,12 @@ fp8_status_t check_attn_dims(int64_t rows, int64_t B, int64_t Hq, int64_t Hkv, i
 // they hold.  A wrong hint changes no result.
 int64_t hint(int64_t v, int64_t most) { return v > 0 ? std::min(v, most) : most; }
 
+// Whether the tiled kernel takes a call: from 64 query rows per KV head on.
+bool attn_tiled(int64_t Hq, int64_t Hkv, int64_t max_q) { return max_q > 1 && max_q * (Hq / Hkv) > 64; }
+
 size_t attn_ws(int64_t rows, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size, int64_t max_blocks,
                int64_t max_q, int64_t max_len) {
+    if (attn_tiled(Hq, Hkv, max_q)) return 0;
     const int64_t all_len = block_size * max_blocks;
     return round_up(fp8k::attn_paged_ws_bytes(B, rows, Hq, Hkv, D, max_q, hint(max_len, all_len), all_len), kAlign);
 }
@@ -172,6 +176,7 @@ fp8_status_t attn(fp8k::PagedAttn p, fp8_kv_dtype_t dtype, fp8_kv_format_t fmt, 
     p.block = (int)block_size, p.max_blocks = (int)max_blocks;
     p.window = (int)std::min(window, kMaxAttn);  // no key is further back
     p.dtype = (int)dtype;
+    if (attn_tiled(Hq, Hkv, max_q)) return from_hip(fp8k::launch_attn_tiled(p, (int)D, (int)fmt, max_q, stream));
     return from_hip(fp8k::launch_attn_paged(p, (int)D, (int)fmt, max_q, hint(max_len, block_size * max_blocks), ws,
                                             stream));
 }

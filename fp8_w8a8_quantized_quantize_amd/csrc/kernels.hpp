@@ -90,6 +90,8 @@ struct PagedAttn {
     float scale, softcap;
     int B, rows, Hq, Hkv, block, max_blocks, window, causal, dtype;
 };
+// The streaming form (attn_paged.hip), for few rows per sequence, and the tiled
+// one (attn_prefill.hip), for many.
 // max_q and max_len plan the launch; longer rows and sequences are still
 // computed whole.  ws: attn_paged_ws_bytes bytes (all_len = max_blocks * block),
 // 16-byte aligned.
@@ -97,6 +99,7 @@ size_t attn_paged_ws_bytes(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int
                            int64_t all_len);
 hipError_t launch_attn_paged(const PagedAttn& p, int D, int fmt, int64_t max_q, int64_t max_len, void* ws,
                              hipStream_t stream);
+hipError_t launch_attn_tiled(const PagedAttn& p, int D, int fmt, int64_t max_q, hipStream_t stream);
 
 // The dense GEMM launchers write BF16 y, or, when y32 is not null, the fp32
 // value acc * (s_tok * s_ch) before rounding to y32 (same row stride ldy).
