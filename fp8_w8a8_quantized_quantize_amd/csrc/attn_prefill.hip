@@ -8,20 +8,23 @@
 //
 // Tile.  The columns are a KV head's query rows, token times group, so one pass
 // over the keys serves all query heads of the group.  A workgroup of four waves
-// takes 128 NC columns, 32 NC a wave, and walks over 64-key tiles that all its
-// waves share in LDS: K as fp16 rows, V as fp16 transposed, eight keys of a
-// channel in 16 bytes in the order in which a lane holds its p.  Codes become
-// fp16 once per workgroup, on the way into LDS.  NC = 2 halves the LDS bytes per
-// matrix instruction (64 columns a wave: each 1 KB operand read feeds two
-// 32x32x16 instructions of 32 cycles; four waves then need 64 of the 128 bytes
-// a cycle that LDS gives); it takes the registers of one wave per SIMD, so the
-// overlap of softmax and matrix work is inside the wave: scores of tile i + 1
-// are formed while the softmax of tile i runs.
+// takes 128 columns, 32 a wave, and walks over 64-key tiles that all its waves
+// share in LDS: K as fp16 rows, V as fp16 transposed, eight keys of a channel in
+// 16 bytes in the order in which a lane holds its p.  Codes become fp16 once per
+// workgroup, on the way into LDS.  D = 128 takes 231 registers and 72 KB of LDS,
+// two workgroups a CU: the softmax of one wave runs beside the matrix work of
+// the other on its SIMD.  64 columns a wave (half the LDS reads per matrix
+// instruction, one wave per SIMD) spilled and took 3.7 ms where this takes 1.2
+// (8192 tokens, 64 / 8 heads of 128, bf16), and so did forming the next tile's
+// scores during the softmax (2.3 ms).
 //
-// One barrier per tile: step i writes V of tile i and K of tile i + 1 into the
-// buffers last read in steps i - 2 and i - 1, loads K of tile i + 2 and V of
-// tile i + 1 into registers, and after the barrier forms S(i + 1) = Q K(i + 1),
-// p of tile i, and adds p V(i).
+// Bound: matrix cores 42 %, vector unit 50 % of the cycles (240 instructions per
+// 32 columns x 64 keys, 32 of them exponentials, beside 32 matrix instructions
+// of 32 cycles), LDS 55 %; what is lost is waves of a SIMD wanting the same unit.
+//
+// One barrier per tile: step t writes K and V of tile t into the buffers last
+// read in step t - 2, starts the loads of tile t + 1 into registers, and computes
+// after the barrier.
 #include <algorithm>
 
 #include "attn_common.hpp"
@@ -35,50 +38,50 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 constexpr int kWavesT = 4;
 constexpr int kThreadsT = kWavesT * kWave;
 constexpr int kKeys = 64;  // keys of a tile
+constexpr int kTileCols = kWavesT * 32;  // query columns of a workgroup
 
 struct TileArgs {
     PagedAttn p;
     int group;
     int col_tiles;  // planned per KV head; further ones are taken in turn
-    FastDiv by_block, by_group, by_kv_heads;
+    FastDiv by_block, by_group, by_kv_heads, by_batch;
 };
 
-template <int D, int TERMS>
-constexpr int col_groups() {
-    return TERMS == 1 && D <= 128 ? 2 : 1;
-}
-
-template <int D, int TERMS>
-constexpr int tile_cols() {
-    return kWavesT * 32 * col_groups<D, TERMS>();
-}
-
-// LDS: two K tiles, two V tiles, cache offsets of 16 rows per wave for three
-// tiles, and which keys of two tiles are there.
+// LDS rows are padded by 16 bytes, so that the operand reads (32 neighbouring
+// rows) spread over the banks; V is written for every D / 32-nd channel at once,
+// so its 16-byte units also sit at unit ^ (channel / 16 % 8).
+// LDS: two K tiles, two V tiles, cache offsets of 16 rows per wave for two
+// tiles, and which keys of four tiles are there.
 template <int D>
 struct TileLds {
-    static constexpr int kK = kKeys * D * 2;
-    static constexpr int kV = 2 * kK;
-    static constexpr int kRows = 4 * kK;
-    static constexpr int kMask = kRows + 3 * kKeys * 8;
-    static constexpr int kBytes = kMask + 2 * kWavesT * 4;
+    static constexpr int kKRow = 2 * D + 16, kVRow = 2 * kKeys + 16;  // bytes; padded off the banks
+    static constexpr int kKTile = kKeys * kKRow, kVTile = D * kVRow;
+    static constexpr int kV = 2 * kKTile;
+    static constexpr int kRows = kV + 2 * kVTile;
+    static constexpr int kMask = kRows + 2 * kKeys * 8;
+    static constexpr int kBytes = kMask + 4 * kWavesT * 4;
 };
 
 extern __shared__ __attribute__((aligned(1024))) uint8_t tile_smem[];
 
-// Place of the 16-byte units of a K row (2 D bytes) and of a V channel (128
-// bytes) such that neighbouring rows' units lie in different banks.
-template <int D>
-__device__ __forceinline__ int swz_k(int key) {
-    return D == 64 ? (key ^ (key >> 3)) & 7 : key & 15;
+// Scheduling hint for N operand reads from LDS with M matrix instructions each:
+// the first AHEAD reads at once, then a read per M instructions, so that an LDS
+// round trip (about 150 cycles with eight waves reading) passes behind AHEAD
+// instructions of 32 cycles.
+template <int N, int M, int AHEAD>
+__device__ __forceinline__ void reads_ahead() {
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+    for (int i = 0; i < N - AHEAD; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, M, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, M * AHEAD, 0);
 }
-__device__ __forceinline__ int swz_v(int d) { return (d ^ (d >> 3)) & 7; }
 
 template <int D, int FMT, bool BIAS, int TERMS>
-__global__ __launch_bounds__(kThreadsT, 1) void attn_tile(TileArgs a) {
+__global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArgs a) {
     const PagedAttn& p = a.p;
-    constexpr int NC = col_groups<D, TERMS>();
-    constexpr int COLS = tile_cols<D, TERMS>();
     constexpr int NK = D / 16;  // matrix instructions along the channels of K
     constexpr int DB = D / 32;  // 32-channel blocks of the output
     constexpr int VB = D / 32;  // V channels a thread stages
@@ -88,49 +91,42 @@ __global__ __launch_bounds__(kThreadsT, 1) void attn_tile(TileArgs a) {
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int c = lane % 32, h = lane / 32;
-    const int nth = a.by_kv_heads.of(blockIdx.x), hk = blockIdx.x - nth * p.Hkv;
-    const int b = blockIdx.y;
+    // KV heads vary fastest (with 8 of them an XCD keeps to one head's keys), then sequences; every sequence's last column
+    // tiles, which see the most keys, come first.
+    const int rest = a.by_kv_heads.of(blockIdx.x), hk = blockIdx.x - rest * p.Hkv;
+    const int nth = a.by_batch.of(rest), b = rest - nth * p.B;
     const Seq seq = sequence(p, b);
     const int prefix = p.prefix ? p.prefix[b] : 0;
     const int cols = seq.nq * a.group;
     const uint32_t C = 2u * p.Hkv * D;
     const int32_t* table = p.block_table + (int64_t)b * p.ld_table;
     const int last_page = max(p.max_blocks - 1, 0);
-    uint64_t* const rows = reinterpret_cast<uint64_t*>(tile_smem + Lds::kRows) + wave * 16;  // [tile % 3][4 waves][16]
-    uint32_t* const there = reinterpret_cast<uint32_t*>(tile_smem + Lds::kMask);             // [tile % 2][4 waves]
+    uint64_t* const rows = reinterpret_cast<uint64_t*>(tile_smem + Lds::kRows) + wave * 16;  // [tile % 2][4 waves][16]
+    uint32_t* const there = reinterpret_cast<uint32_t*>(tile_smem + Lds::kMask);             // [tile % 4][4 waves]
 
-    // the last column tiles see the most keys: they go first
-    for (int ct = a.col_tiles - 1 - nth + (cols > a.col_tiles * COLS ? (cols - 1) / (a.col_tiles * COLS) * a.col_tiles : 0);
-         ct >= 0; ct -= a.col_tiles) {
-        if (ct * COLS >= cols) continue;
-        // this lane's columns
-        int lo[NC], hi[NC], pos[NC], head[NC];
-        int64_t row[NC];
-        bool has[NC];
-        float slope[NC];
-#pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            const int col = ct * COLS + (wave * NC + n) * 32 + c;
-            has[n] = col < cols;
-            const int qi = has[n] ? a.by_group.of(col) : 0;
-            head[n] = hk * a.group + (has[n] ? col - qi * a.group : 0);
-            row[n] = seq.row0 + qi;
-            pos[n] = seq.len - seq.nq + qi;
-            visible(p, seq, prefix, qi, lo[n], hi[n]);
-            if (!has[n]) lo[n] = 0x7FFFFFFF, hi[n] = 0;
-            slope[n] = p.alibi ? p.alibi[head[n]] * kLog2e : 0.0f;
-        }
+    const int rounds = cols > 0 ? (cols - 1) / (a.col_tiles * kTileCols) : 0;  // more than planned: taken in turn
+    for (int ct = rounds * a.col_tiles + a.col_tiles - 1 - nth; ct >= 0; ct -= a.col_tiles) {
+        if (ct * kTileCols >= cols) continue;
+        // this lane's column
+        const int col = ct * kTileCols + wave * 32 + c;
+        const bool has = col < cols;
+        const int qi = has ? a.by_group.of(col) : 0;
+        const int head = hk * a.group + (has ? col - qi * a.group : 0);
+        const int64_t row = seq.row0 + qi;
+        const int pos = seq.len - seq.nq + qi;
+        const float slope = p.alibi ? p.alibi[head] * kLog2e : 0.0f;
+        int lo, hi;
+        visible(p, seq, prefix, qi, lo, hi);
+        if (!has) lo = 0x7FFFFFFF, hi = 0;
         // the keys any column of the workgroup sees, and of this wave
         int tlo, thi, unused;
-        visible(p, seq, prefix, a.by_group.of(ct * COLS), tlo, unused);
-        visible(p, seq, prefix, a.by_group.of(min(cols - 1, ct * COLS + COLS - 1)), unused, thi);
+        visible(p, seq, prefix, a.by_group.of(ct * kTileCols), tlo, unused);
+        visible(p, seq, prefix, a.by_group.of(min(cols - 1, ct * kTileCols + kTileCols - 1)), unused, thi);
         thi = max(thi, 0);
         tlo = min(tlo, thi);
         const int base = p.window > 0 ? tlo / kKeys * kKeys : 0;
         const int tiles = thi > base ? (thi - base + kKeys - 1) / kKeys : 0;
-        int wlo = lo[0], whi = hi[0];
-#pragma unroll
-        for (int n = 1; n < NC; ++n) wlo = min(wlo, lo[n]), whi = max(whi, hi[n]);
+        int wlo = lo, whi = hi;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
             wlo = min(wlo, __shfl_xor(wlo, off, kWave));
@@ -140,54 +136,45 @@ __global__ __launch_bounds__(kThreadsT, 1) void attn_tile(TileArgs a) {
         whi = __builtin_amdgcn_readfirstlane(whi);
 
         // q times the key scales, in fp16 terms
-        v8h qt[TERMS][NC][NK];
-        float cs[NC];
+        v8h qt[TERMS][NK];
+        float cs;
+        {
+            float x[NK][8], top = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            v4u raw[NK][2];
-            float top = 0.0f;
-#pragma unroll
-            for (int s = 0; s < NK; ++s)
-                load_q8<TERMS>(p, row[n] * p.ldq + (int64_t)head[n] * D + 16 * s + 8 * h, raw[s]);
-            float x[NK][8];
-#pragma unroll
-            for (int s = 0; s < NK; ++s) {
-                unpack_q8<TERMS>(p, raw[s], x[s]);
-                const float4* ks = reinterpret_cast<const float4*>(p.scales + hk * D + 16 * s + 8 * h);
+            for (int st = 0; st < NK; ++st) {
+                v4u raw[2];
+                load_q8<TERMS>(p, row * p.ldq + (int64_t)head * D + 16 * st + 8 * h, raw);
+                unpack_q8<TERMS>(p, raw, x[st]);
+                const float4* ks = reinterpret_cast<const float4*>(p.scales + hk * D + 16 * st + 8 * h);
                 const float4 k0 = ks[0], k1 = ks[1];
                 const float k[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    x[s][e] *= fmaxf(k[e], kScaleFloor);
-                    top = fmaxf(top, fabsf(x[s][e]));
+                    x[st][e] *= fmaxf(k[e], kScaleFloor);
+                    top = fmaxf(top, fabsf(x[st][e]));
                 }
             }
             top = fmaxf(top, swap32(top));
             const int shift = 15 - __builtin_amdgcn_frexp_expf(top);
 #pragma unroll
-            for (int s = 0; s < NK; ++s)
+            for (int st = 0; st < NK; ++st)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float y = __builtin_amdgcn_ldexpf(x[s][e], shift);
-                    qt[0][n][s][e] = (_Float16)y;
-                    if constexpr (TERMS == 2) qt[TERMS - 1][n][s][e] = (_Float16)(y - (float)qt[0][n][s][e]);
+                    const float y = __builtin_amdgcn_ldexpf(x[st][e], shift);
+                    qt[0][st][e] = (_Float16)y;
+                    if constexpr (TERMS == 2) qt[TERMS - 1][st][e] = (_Float16)(y - (float)qt[0][st][e]);
                 }
-            cs[n] = __builtin_amdgcn_ldexpf(p.scale, -shift);
-            if (p.softcap > 0.0f) cs[n] *= kLn2;  // the cap takes the natural score
+            cs = __builtin_amdgcn_ldexpf(p.scale, -shift);
         }
+        if (p.softcap > 0.0f) cs *= kLn2;  // the cap takes the natural score
         const float cap_in = p.softcap > 0.0f ? 2.0f * kLog2e / p.softcap : 0.0f;
 
-        float m[NC], l[NC];
-        v16f o[NC][DB];
+        float m = 0.0f, l = 0.0f, limit = kNoRef;
+        v16f o[DB];
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            m[n] = kNoRef;
-            l[n] = 0.0f;
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[n][d][i] = 0.0f;
-        }
+            for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
 
         // ---- staging.  A wave stages keys 16 wave .. + 15 of a tile: K, a quarter row per thread; V, the eight keys of
         // two lane groups, VB channels per thread.
@@ -197,16 +184,16 @@ __global__ __launch_bounds__(kThreadsT, 1) void attn_tile(TileArgs a) {
             const int key = base + t * kKeys + 16 * wave + lane % 16;
             const bool ok = key >= tlo && key < thi && page >= 0 && page < p.num_blocks;
             const uint32_t r = ok ? (page - a.by_block.of(key)) * p.block + key : 0;
-            if (lane < 16) rows[t % 3 * kKeys + lane] = (uint64_t)r * C;
+            if (lane < 16) rows[t % 2 * kKeys + lane] = (uint64_t)r * C;
             const uint32_t mask = (uint32_t)__ballot(ok) & 0xFFFFu;
-            if (lane == 0) there[t % 2 * kWavesT + wave] = mask;
+            if (lane == 0) there[t % 4 * kWavesT + wave] = mask;
             __builtin_amdgcn_wave_barrier();
             return mask;
         };
         v4u kreg[D / 64];
         vpiece vreg[8];
         auto load_k = [&](int t) {
-            const uint8_t* src = p.cache + rows[t % 3 * kKeys + lane / 4] + hk * D + lane % 4 * (D / 4);
+            const uint8_t* src = p.cache + rows[t % 2 * kKeys + lane / 4] + hk * D + lane % 4 * (D / 4);
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) kreg[i] = *reinterpret_cast<const v4u*>(src + 16 * i);
         };
@@ -214,16 +201,16 @@ __global__ __launch_bounds__(kThreadsT, 1) void attn_tile(TileArgs a) {
             const uint8_t* src = p.cache + (int64_t)(p.Hkv + hk) * D + c * VB;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                vreg[e] = *reinterpret_cast<const vpiece*>(src + rows[t % 3 * kKeys + 8 * (e / 4) + 4 * h + e % 4]);
+                vreg[e] = *reinterpret_cast<const vpiece*>(src + rows[t % 2 * kKeys + 8 * (e / 4) + 4 * h + e % 4]);
         };
         auto store_k = [&](int t) {
-            uint8_t* dst = tile_smem + t % 2 * Lds::kK + (16 * wave + lane / 4) * 2 * D;
+            uint8_t* dst = tile_smem + t % 2 * Lds::kKTile + (16 * wave + lane / 4) * Lds::kKRow;
 #pragma unroll
             for (int i = 0; i < D / 64; ++i)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int unit = (lane % 4 * (D / 64) + i) * 2 + k;
-                    *reinterpret_cast<v8h*>(dst + (unit ^ swz_k<D>(16 * wave + lane / 4)) * 16) =
+                    *reinterpret_cast<v8h*>(dst + unit * 16) =
                         row_f16<FMT>(kreg[i][2 * k], kreg[i][2 * k + 1]);
                 }
         };
@@ -234,7 +221,7 @@ __global__ __launch_bounds__(kThreadsT, 1) void attn_tile(TileArgs a) {
                 return vreg[e];
         };
         auto store_v = [&](int t, uint32_t mask) {
-            uint8_t* const dst = tile_smem + Lds::kV + t % 2 * Lds::kK;
+            uint8_t* const dst = tile_smem + Lds::kV + t % 2 * Lds::kVTile;
             if (mask != 0xFFFFu) {
                 // a code behind the sequence may be anything, NaN too: 0 * NaN must not reach the sum
 #pragma unroll
@@ -247,112 +234,94 @@ __global__ __launch_bounds__(kThreadsT, 1) void attn_tile(TileArgs a) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) r[i] = pair_f16<FMT>(vword(2 * i, j / 4), vword(2 * i + 1, j / 4), j % 4);
                 const int d = c * VB + j;
-                *reinterpret_cast<v4u*>(dst + d * 128 + ((2 * wave + h) ^ swz_v(d)) * 16) = r;
+                *reinterpret_cast<v4u*>(dst + d * Lds::kVRow + ((2 * wave + h) ^ (d / 16 % 8)) * 16) = r;
             }
         };
-        v16f s[NC][2];
+        v16f s[2];
         auto scores = [&](int t) {
-            const uint8_t* src = tile_smem + t % 2 * Lds::kK;
+            const uint8_t* src = tile_smem + t % 2 * Lds::kKTile + c * Lds::kKRow + h * 16;
 #pragma unroll
-            for (int n = 0; n < NC; ++n)
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) s[n][kb][i] = 0.0f;
+            for (int j = 0; j < 32; ++j) s[j / 16][j % 16] = 0.0f;
 #pragma unroll
             for (int st = 0; st < NK; ++st)
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) {
-                    const int key = 32 * kb + c;
-                    const v8h k = *reinterpret_cast<const v8h*>(src + key * 2 * D + ((2 * st + h) ^ swz_k<D>(key)) * 16);
+                    const v8h k = *reinterpret_cast<const v8h*>(src + 32 * kb * Lds::kKRow + 32 * st);
 #pragma unroll
-                    for (int n = 0; n < NC; ++n)
-#pragma unroll
-                        for (int x = 0; x < TERMS; ++x)
-                            s[n][kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, qt[x][n][st], s[n][kb], 0, 0, 0);
+                    for (int x = 0; x < TERMS; ++x) s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, qt[x][st], s[kb], 0, 0, 0);
                 }
+            reads_ahead<2 * NK, TERMS, 4>();
         };
-        // p of tile t from its scores z
-        v8h ph[TERMS][NC][4];
-        auto softmax = [&](int t, v16f (&z)[NC][2], uint64_t mask) {
+        // key of a lane's score j, less 4 h
+        auto key_of = [](int j) { return 32 * (j / 16) + 8 * (j % 16 / 4) + j % 4; };
+        // Scores of tile t above the reference, in place.
+        auto above = [&](int t, uint64_t mask) {
             const int key0 = base + t * kKeys;
+            if constexpr (BIAS) {
+                if (p.softcap > 0.0f) {
 #pragma unroll
-            for (int n = 0; n < NC; ++n) {
-                if constexpr (BIAS) {
-#pragma unroll
-                    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float x = z[n][kb][i] * cs[n];
-                            if (p.softcap > 0.0f) x = kLog2e * soft_cap(x, p.softcap, cap_in);
-                            z[n][kb][i] = x + slope[n] * (float)(key0 + 32 * kb + 8 * (i / 4) + 4 * h + i % 4 - pos[n]);
-                        }
+                    for (int j = 0; j < 32; ++j) s[j / 16][j % 16] = kLog2e * soft_cap(s[j / 16][j % 16] * cs, p.softcap, cap_in);
                 }
-                const bool whole = mask == ~0ull && !__any(key0 < lo[n] || key0 + kKeys > hi[n]);
-                if (!whole) {
+                const float by = p.softcap > 0.0f ? 1.0f : cs, dist = (float)(key0 + 4 * h - pos);
 #pragma unroll
-                    for (int kb = 0; kb < 2; ++kb)
+                for (int j = 0; j < 32; ++j)
+                    s[j / 16][j % 16] = __builtin_fmaf(slope, dist + (float)key_of(j), __builtin_fmaf(s[j / 16][j % 16], by, -m));
+            } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int j = 32 * kb + 8 * (i / 4) + 4 * h + i % 4;
-                            const bool see = ((mask >> j) & 1u) & (key0 + j >= lo[n]) & (key0 + j < hi[n]);
-                            // below every reference: exp2 gives 0 (the scale's sign would turn an infinity round)
-                            z[n][kb][i] = see ? z[n][kb][i] : __uint_as_float(0x7FC00000u);
-                        }
+                for (int j = 0; j < 32; ++j) s[j / 16][j % 16] = __builtin_fmaf(s[j / 16][j % 16], cs, -m);
+            }
+            if (mask != ~0ull || __any(key0 < lo || key0 + kKeys > hi)) {
+                const uint64_t mine = mask >> (4 * h);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const int key = key0 + 4 * h + key_of(j);
+                    const bool see = ((mine >> key_of(j)) & 1u) & (key >= lo) & (key < hi);
+                    s[j / 16][j % 16] = see ? s[j / 16][j % 16] : -INFINITY;
                 }
-                auto above = [&](int kb, int i) {
-                    const float x = BIAS ? z[n][kb][i] - m[n] : __builtin_fmaf(z[n][kb][i], cs[n], -m[n]);
-                    return whole ? x : z[n][kb][i] == z[n][kb][i] ? x : -INFINITY;
-                };
-                float top = -INFINITY;
+            }
+            float top = s[0][0];
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
+            for (int j = 1; j < 32; ++j) top = fmaxf(top, s[j / 16][j % 16]);
+            if (__any(top > limit)) {
+                // Move the references of the columns that need it, kPShift below the largest score (scores past 2^24 are
+                // themselves too coarse for the shift).  A column without a reference has m = 0 and no sum yet.
+                top = fmaxf(top, swap32(top));
+                const bool move = top > limit;
+                const float by = move ? (fabsf(top + m) < 16777216.0f ? top - kPShift : top) : 0.0f;
+                const float f = limit == kPLimit ? __builtin_amdgcn_exp2f(-by) : 1.0f;
+                m += by;
+                limit = move ? kPLimit : limit;
+                l *= f;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) top = fmaxf(top, above(kb, i));
-                if (__any(top > kPLimit)) {
-                    // move the references of the columns that need it, as in the streaming form
-                    const float old = m[n];
-                    m[n] = 0.0f;
-                    top = -INFINITY;
+                for (int d = 0; d < DB; ++d) o[d] *= f;
 #pragma unroll
-                    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) top = fmaxf(top, above(kb, i));
-                    top = fmaxf(top, swap32(top));
-                    m[n] = top > old + kPLimit ? (fabsf(top) < 16777216.0f ? top - kPShift : top) : old;
-                    const float f = __builtin_amdgcn_exp2f(old - m[n]);
-                    l[n] *= f;
-#pragma unroll
-                    for (int d = 0; d < DB; ++d) o[n][d] *= f;
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float y = __builtin_amdgcn_exp2f(above(u / 2, 8 * (u % 2) + e));
-                        l[n] += y;
-                        ph[0][n][u][e] = (_Float16)y;
-                        if constexpr (TERMS == 2) ph[TERMS - 1][n][u][e] = (_Float16)(y - (float)ph[0][n][u][e]);
-                    }
+                for (int j = 0; j < 32; ++j) s[j / 16][j % 16] -= by;
             }
         };
+        // p and its product with V, 16 keys at a time
         auto product = [&](int t) {
-            const uint8_t* src = tile_smem + Lds::kV + t % 2 * Lds::kK;
+            const uint8_t* src = tile_smem + Lds::kV + t % 2 * Lds::kVTile + c * Lds::kVRow + (h ^ (c / 16)) * 16;
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 4; ++u) {
+                v8h ph[TERMS];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float y = __builtin_amdgcn_exp2f(s[u / 2][8 * (u % 2) + e]);
+                    l += y;
+                    ph[0][e] = (_Float16)y;
+                    if constexpr (TERMS == 2) ph[TERMS - 1][e] = (_Float16)(y - (float)ph[0][e]);
+                }
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
-                    const int d = 32 * db + c;
-                    const v8h v = *reinterpret_cast<const v8h*>(src + d * 128 + ((2 * u + h) ^ swz_v(d)) * 16);
+                    const v8h v = *reinterpret_cast<const v8h*>(src + 32 * db * Lds::kVRow + 32 * (u ^ (db % 4)));
 #pragma unroll
-                    for (int n = 0; n < NC; ++n)
-#pragma unroll
-                        for (int x = 0; x < TERMS; ++x)
-                            o[n][db] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, ph[x][n][u], o[n][db], 0, 0, 0);
+                    for (int x = 0; x < TERMS; ++x) o[db] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, ph[x], o[db], 0, 0, 0);
                 }
+            }
+            reads_ahead<4 * DB, TERMS, 4>();
         };
         auto mask_of = [&](int t) {
-            const uint32_t* w = there + t % 2 * kWavesT;
+            const uint32_t* w = there + t % 4 * kWavesT;
             const uint32_t lo32 = w[0] | (w[1] << 16), hi32 = w[2] | (w[3] << 16);
             return ((uint64_t)__builtin_amdgcn_readfirstlane(hi32) << 32) | (uint32_t)__builtin_amdgcn_readfirstlane(lo32);
         };
@@ -363,48 +332,31 @@ __global__ __launch_bounds__(kThreadsT, 1) void attn_tile(TileArgs a) {
             int page = page_of(1);
             load_k(0);
             load_v(0);
-            store_k(0);
-            uint32_t m1 = rows_of(1, page);
-            page = page_of(2);
-            load_k(1);
-            __syncthreads();
-            uint64_t mask = mask_of(0);
-            if (sees(0)) scores(0);
             for (int t = 0; t < tiles; ++t) {
+                store_k(t);
                 store_v(t, m0);
-                store_k(t + 1);
-                const uint32_t m2 = rows_of(t + 2, page);
-                page = page_of(t + 3);
-                load_k(t + 2);
+                m0 = rows_of(t + 1, page);
+                page = page_of(t + 2);
+                load_k(t + 1);
                 load_v(t + 1);
                 __syncthreads();
-                const bool now = sees(t);
-                v16f z[NC][2];
-#pragma unroll
-                for (int n = 0; n < NC; ++n) z[n][0] = s[n][0], z[n][1] = s[n][1];
-                const uint64_t next_mask = mask_of(t + 1);
-                if (t + 1 < tiles && sees(t + 1)) scores(t + 1);
-                if (now) {
-                    softmax(t, z, mask);
+                if (sees(t)) {
+                    scores(t);
+                    above(t, mask_of(t));
                     product(t);
                 }
-                mask = next_mask;
-                m0 = m1, m1 = m2;
             }
         }
 
         // ---- results
+        l += swap32(l);
+        if (has) {
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            const float L = l[n] + swap32(l[n]);
-            if (has[n]) {
+            for (int db = 0; db < DB; ++db)
 #pragma unroll
-                for (int db = 0; db < DB; ++db)
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-                        write_row(p, row[n], head[n], hk, D, 32 * db + 2 * i + 4 * h, m[n], L,
-                                  make_float4(o[n][db][i], o[n][db][i + 1], o[n][db][i + 2], o[n][db][i + 3]));
-            }
+                for (int i = 0; i < 16; i += 4)
+                    write_row(p, row, head, hk, D, 32 * db + 2 * i + 4 * h, m, l,
+                              make_float4(o[db][i], o[db][i + 1], o[db][i + 2], o[db][i + 3]));
         }
         __syncthreads();
     }
@@ -423,9 +375,9 @@ hipError_t launch_tile(const TileArgs& a, dim3 grid, hipStream_t stream) {
 
 template <int D, int TERMS>
 hipError_t launch(TileArgs a, int fmt, int64_t max_q, hipStream_t stream) {
-    const int64_t tiles = (max_q * a.group + tile_cols<D, TERMS>() - 1) / tile_cols<D, TERMS>();
-    a.col_tiles = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, (int64_t(1) << 30) / a.p.Hkv));
-    const dim3 grid((unsigned)(a.col_tiles * a.p.Hkv), (unsigned)a.p.B);
+    const int64_t tiles = (max_q * a.group + kTileCols - 1) / kTileCols, per_tile = (int64_t)a.p.B * a.p.Hkv;
+    a.col_tiles = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, (int64_t(1) << 30) / per_tile));
+    const dim3 grid((unsigned)(a.col_tiles * per_tile));
     const bool bias = a.p.softcap > 0.0f || a.p.alibi != nullptr;
     if (fmt == kKvE5M2)
         return bias ? launch_tile<D, kKvE5M2, true, TERMS>(a, grid, stream) : launch_tile<D, kKvE5M2, false, TERMS>(a, grid, stream);
@@ -441,6 +393,7 @@ hipError_t launch_attn_tiled(const PagedAttn& p, int D, int fmt, int64_t max_q, 
     a.by_block = FastDiv(p.block);
     a.by_group = FastDiv(a.group);
     a.by_kv_heads = FastDiv(p.Hkv);
+    a.by_batch = FastDiv(p.B);
     const bool one = p.dtype == kKvBF16;
     switch (D) {
         case 64: return one ? launch<64, 1>(a, fmt, max_q, stream) : launch<64, 2>(a, fmt, max_q, stream);
