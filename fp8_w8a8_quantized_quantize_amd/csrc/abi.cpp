@@ -128,14 +128,35 @@ fp8_status_t check_attn_dims(int64_t rows, int64_t B, int64_t Hq, int64_t Hkv, i
 // they hold.  A wrong hint changes no result.
 int64_t hint(int64_t v, int64_t most) { return v > 0 ? std::min(v, most) : most; }
 
-// Whether the tiled kernel takes a call: from 64 query rows per KV head on.
-bool attn_tiled(int64_t Hq, int64_t Hkv, int64_t max_q) { return max_q > 1 && max_q * (Hq / Hkv) > 64; }
+// Whether the tiled kernel takes a call, by the query rows of a sequence that
+// share a KV head.  The streaming kernel walks over the keys once per 16 of
+// them, the tiled one once per 128, but has its products wait on LDS.
+// Streaming / tiled, us, 64 / 8 heads of 128, bf16, 16384 keys:
+//     rows            24          32          64          128         512
+//     1 sequence      22.6/23.4   21.4/21.4   25.6/26.1   35.6/35.1   89/59
+//     8 sequences     100/84      99/66       116/85      196/110     616/348
+//     32 sequences    265/288     246/229     412/294     823/386     3922/1452
+// Two-term products (fp16 and fp32) fill the tiled kernel's matrix cores twice,
+// and D = 256 leaves it one workgroup a CU; two sequences, 16384 keys:
+//     rows                    24          64          256
+//     fp16, D = 128           39/55       53/58       131/100
+//     bf16, D = 256 (32/8)    39/73 (12)  50/66 (32)  116/80 (128)
+bool attn_tiled(int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, bool two_terms) {
+    const int64_t columns = max_q * (Hq / Hkv);
+    return two_terms || D == 256 ? columns > 64 : columns >= 32;
+}
 
+// The same for every type, which the queries are not told.
 size_t attn_ws(int64_t rows, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size, int64_t max_blocks,
                int64_t max_q, int64_t max_len) {
-    if (attn_tiled(Hq, Hkv, max_q)) return 0;
     const int64_t all_len = block_size * max_blocks;
-    return round_up(fp8k::attn_paged_ws_bytes(B, rows, Hq, Hkv, D, max_q, hint(max_len, all_len), all_len), kAlign);
+    max_len = hint(max_len, all_len);
+    if (B == 0 || rows == 0) return 0;
+    const bool one = attn_tiled(Hq, Hkv, D, max_q, false), two = attn_tiled(Hq, Hkv, D, max_q, true);
+    size_t need = 0;
+    if (one || two) need = fp8k::attn_tiled_ws_bytes(B, rows, Hq, Hkv, D, max_q, max_len);
+    if (!one || !two) need = std::max(need, fp8k::attn_paged_ws_bytes(B, rows, Hq, Hkv, D, max_q, max_len, all_len));
+    return round_up(need, kAlign);
 }
 
 // Both attention entry points; cu_q null: one new row per sequence.
@@ -176,9 +197,9 @@ fp8_status_t attn(fp8k::PagedAttn p, fp8_kv_dtype_t dtype, fp8_kv_format_t fmt, 
     p.block = (int)block_size, p.max_blocks = (int)max_blocks;
     p.window = (int)std::min(window, kMaxAttn);  // no key is further back
     p.dtype = (int)dtype;
-    if (attn_tiled(Hq, Hkv, max_q)) return from_hip(fp8k::launch_attn_tiled(p, (int)D, (int)fmt, max_q, stream));
-    return from_hip(fp8k::launch_attn_paged(p, (int)D, (int)fmt, max_q, hint(max_len, block_size * max_blocks), ws,
-                                            stream));
+    max_len = hint(max_len, block_size * max_blocks);
+    return from_hip(attn_tiled(Hq, Hkv, D, max_q, dtype != FP8_KV_BF16) ? fp8k::launch_attn_tiled(p, (int)D, (int)fmt, max_q, max_len, ws, stream)
+                                               : fp8k::launch_attn_paged(p, (int)D, (int)fmt, max_q, max_len, ws, stream));
 }
 
 // Bytes the GEMM path itself needs for an M x N x K problem: the skinny

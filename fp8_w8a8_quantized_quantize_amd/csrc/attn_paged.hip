@@ -76,6 +76,7 @@ struct StreamArgs {
     float* part_o;     // [workgroups][2][hw][kCols][D]: parts of rows, a share's first and last
     float2* part_ml;   // [workgroups][2][hw][kCols]: reference (log2), sum
     int* starts;       // [B + 1]: cost before every sequence, cost of all
+    int splits;        // the join alone: parts of every row, laid out [rows][Hq][splits], 0 for cut rows as above
     int spread, log_spread;  // the join's thread groups per output row
     int join_rows;     // and the new rows of a sequence it takes at a time
     FastDiv by_block, by_group, by_head_groups, by_heads, by_batch;
@@ -633,13 +634,17 @@ __global__ __launch_bounds__(kWaves* kWave) void attn_join(StreamArgs a) {
         int shares = 0;
         bool cut = false;  // else the first kernel has written the row
         if (i < seq.nq) {
-            // the shares that its item was cut into, as the first kernel dealt them out
-            const Run run = run_of(a, seq, prefix);
             const int col = i * a.group + h - hk * a.group;
-            const int at = a.starts[b] + col / kCols * (run.rounds + kItemCost) + kItemCost;
-            const int share = a.share_of(a.starts[p.B]);
-            const int first = at / share;
-            shares = run.rounds == 0 ? 0 : (at + run.rounds - 1) / share - first + 1;
+            int first = 0;
+            shares = a.splits;
+            if (a.splits == 0) {
+                // the shares that its item was cut into, as the first kernel dealt them out
+                const Run run = run_of(a, seq, prefix);
+                const int at = a.starts[b] + col / kCols * (run.rounds + kItemCost) + kItemCost;
+                const int share = a.share_of(a.starts[p.B]);
+                first = at / share;
+                shares = run.rounds == 0 ? 0 : (at + run.rounds - 1) / share - first + 1;
+            }
             cut = shares != 1;
             if (cut) {
                 // the item's first round is in its first share; kBatch shares at a time, so that their loads travel together
@@ -651,9 +656,10 @@ __global__ __launch_bounds__(kWaves* kWave) void attn_join(StreamArgs a) {
                     for (int k = 0; k < kBatch; ++k) {
                         const int s = min(s0 + k * a.spread, shares - 1);
                         const int group = (first + s) * a.head_groups + (hk >> a.log_hw);
-                        const int x = ((2 * group + (s == 0)) * a.hw + (hk & (a.hw - 1))) * kCols + col % kCols;
+                        const int64_t x = a.splits > 0 ? ((int64_t)(seq.row0 + i) * p.Hq + h) * a.splits + s
+                                                       : ((2 * group + (s == 0)) * a.hw + (hk & (a.hw - 1))) * kCols + col % kCols;
                         y[k] = a.part_ml[x];
-                        v[k] = *reinterpret_cast<const float4*>(a.part_o + (int64_t)x * D + 4 * d4);
+                        v[k] = *reinterpret_cast<const float4*>(a.part_o + x * D + 4 * d4);
                         if (s0 + k * a.spread >= shares) y[k].x = kNoRef;
                         top = fmaxf(top, y[k].x);
                     }
@@ -739,16 +745,7 @@ hipError_t launch_stream(const StreamArgs& a, hipStream_t stream) {
 }
 
 template <int D>
-hipError_t launch(StreamArgs a, int fmt, int64_t max_q, hipStream_t stream) {
-    const bool bias = a.p.softcap > 0.0f || a.p.alibi != nullptr, one = a.p.dtype == kKvBF16;
-    hipError_t e;
-    if (fmt == kKvE5M2)
-        e = bias ? (one ? launch_stream<D, kKvE5M2, true, 1>(a, stream) : launch_stream<D, kKvE5M2, true, 2>(a, stream))
-                 : (one ? launch_stream<D, kKvE5M2, false, 1>(a, stream) : launch_stream<D, kKvE5M2, false, 2>(a, stream));
-    else
-        e = bias ? (one ? launch_stream<D, kKvE4M3, true, 1>(a, stream) : launch_stream<D, kKvE4M3, true, 2>(a, stream))
-                 : (one ? launch_stream<D, kKvE4M3, false, 1>(a, stream) : launch_stream<D, kKvE4M3, false, 2>(a, stream));
-    if (e != hipSuccess || a.shares == 0) return e;
+hipError_t launch_join(StreamArgs a, int64_t max_q, hipStream_t stream) {
     const int64_t heads = (int64_t)a.p.B * a.p.Hq;
     a.join_rows = (int)std::max<int64_t>(1, std::min(max_q, kMaxGrid / heads));
     constexpr int kGroups = kWaves * kWave / (D / 4);
@@ -760,6 +757,20 @@ hipError_t launch(StreamArgs a, int fmt, int64_t max_q, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <int D>
+hipError_t launch(const StreamArgs& a, int fmt, int64_t max_q, hipStream_t stream) {
+    const bool bias = a.p.softcap > 0.0f || a.p.alibi != nullptr, one = a.p.dtype == kKvBF16;
+    hipError_t e;
+    if (fmt == kKvE5M2)
+        e = bias ? (one ? launch_stream<D, kKvE5M2, true, 1>(a, stream) : launch_stream<D, kKvE5M2, true, 2>(a, stream))
+                 : (one ? launch_stream<D, kKvE5M2, false, 1>(a, stream) : launch_stream<D, kKvE5M2, false, 2>(a, stream));
+    else
+        e = bias ? (one ? launch_stream<D, kKvE4M3, true, 1>(a, stream) : launch_stream<D, kKvE4M3, true, 2>(a, stream))
+                 : (one ? launch_stream<D, kKvE4M3, false, 1>(a, stream) : launch_stream<D, kKvE4M3, false, 2>(a, stream));
+    if (e != hipSuccess || a.shares == 0) return e;
+    return launch_join<D>(a, max_q, stream);
+}
+
 }  // namespace
 
 size_t attn_paged_ws_bytes(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_len,
@@ -767,6 +778,24 @@ size_t attn_paged_ws_bytes(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int
     const StreamPlan s = stream_plan(B, rows, Hq, Hkv, D, max_q, max_len, all_len);
     if (B == 0 || rows == 0 || s.shares == 0) return 0;
     return (size_t)s.shares * Hkv * 2 * kCols * ((size_t)D * 4 + 8) + ((size_t)B + 1) * 4;
+}
+
+hipError_t launch_attn_join(const PagedAttn& p, int D, int splits, float* part_o, float2* part_ml, int64_t max_q,
+                            hipStream_t stream) {
+    StreamArgs a = {};
+    a.p = p;
+    a.group = p.Hq / p.Hkv;
+    a.splits = splits;
+    a.part_o = part_o;
+    a.part_ml = part_ml;
+    a.by_group = FastDiv(a.group);
+    a.by_heads = FastDiv(p.Hq);
+    a.by_batch = FastDiv(p.B);
+    switch (D) {
+        case 64: return launch_join<64>(a, max_q, stream);
+        case 128: return launch_join<128>(a, max_q, stream);
+        default: return launch_join<256>(a, max_q, stream);
+    }
 }
 
 hipError_t launch_attn_paged(const PagedAttn& p, int D, int fmt, int64_t max_q, int64_t max_len, void* ws,

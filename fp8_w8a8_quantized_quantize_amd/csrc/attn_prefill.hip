@@ -25,6 +25,10 @@
 // One barrier per tile: step t writes K and V of tile t into the buffers last
 // read in step t - 2, starts the loads of tile t + 1 into registers, and computes
 // after the barrier.
+//
+// Where column tiles are few, several workgroups share a tile's keys: each
+// leaves its unscaled fp32 sums, its reference and its sum of p in the
+// workspace, and the streaming form's join adds them in their order.
 #include <algorithm>
 
 #include "attn_common.hpp"
@@ -44,7 +48,10 @@ struct TileArgs {
     PagedAttn p;
     int group;
     int col_tiles;  // planned per KV head; further ones are taken in turn
-    FastDiv by_block, by_group, by_kv_heads, by_batch;
+    int splits;     // workgroups that share a column tile's keys
+    float* part_o;    // [rows][Hq][splits][D], with splits > 1
+    float2* part_ml;  // [rows][Hq][splits]: reference (log2), sum
+    FastDiv by_block, by_group, by_kv_heads, by_batch, by_splits;
 };
 
 // LDS rows are padded by 16 bytes, so that the operand reads (32 neighbouring
@@ -94,7 +101,8 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
     // KV heads vary fastest (with 8 of them an XCD keeps to one head's keys), then sequences; every sequence's last column
     // tiles, which see the most keys, come first.
     const int rest = a.by_kv_heads.of(blockIdx.x), hk = blockIdx.x - rest * p.Hkv;
-    const int nth = a.by_batch.of(rest), b = rest - nth * p.B;
+    const int tile_split = a.by_batch.of(rest), b = rest - tile_split * p.B;
+    const int nth = a.by_splits.of(tile_split), split = tile_split - nth * a.splits;
     const Seq seq = sequence(p, b);
     const int prefix = p.prefix ? p.prefix[b] : 0;
     const int cols = seq.nq * a.group;
@@ -125,7 +133,8 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
         thi = max(thi, 0);
         tlo = min(tlo, thi);
         const int base = p.window > 0 ? tlo / kKeys * kKeys : 0;
-        const int tiles = thi > base ? (thi - base + kKeys - 1) / kKeys : 0;
+        const int all = thi > base ? (thi - base + kKeys - 1) / kKeys : 0;
+        const int first = (int)((int64_t)all * split / a.splits), tiles = (int)((int64_t)all * (split + 1) / a.splits);
         int wlo = lo, whi = hi;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
@@ -326,13 +335,13 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
             return ((uint64_t)__builtin_amdgcn_readfirstlane(hi32) << 32) | (uint32_t)__builtin_amdgcn_readfirstlane(lo32);
         };
 
-        if (tiles > 0) {
+        if (tiles > first) {
             auto sees = [&](int t) { return base + t * kKeys < whi && base + (t + 1) * kKeys > wlo; };
-            uint32_t m0 = rows_of(0, page_of(0));
-            int page = page_of(1);
-            load_k(0);
-            load_v(0);
-            for (int t = 0; t < tiles; ++t) {
+            uint32_t m0 = rows_of(first, page_of(first));
+            int page = page_of(first + 1);
+            load_k(first);
+            load_v(first);
+            for (int t = first; t < tiles; ++t) {
                 store_k(t);
                 store_v(t, m0);
                 m0 = rows_of(t + 1, page);
@@ -350,7 +359,16 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
 
         // ---- results
         l += swap32(l);
-        if (has) {
+        if (has && a.splits > 1) {
+            const int64_t at = (row * p.Hq + head) * a.splits + split;
+            if (h == 0) a.part_ml[at] = make_float2(limit == kPLimit ? m : kNoRef, l);
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<float4*>(a.part_o + at * D + 32 * db + 2 * i + 4 * h) =
+                        make_float4(o[db][i], o[db][i + 1], o[db][i + 2], o[db][i + 3]);
+        } else if (has) {
 #pragma unroll
             for (int db = 0; db < DB; ++db)
 #pragma unroll
@@ -376,8 +394,8 @@ hipError_t launch_tile(const TileArgs& a, dim3 grid, hipStream_t stream) {
 template <int D, int TERMS>
 hipError_t launch(TileArgs a, int fmt, int64_t max_q, hipStream_t stream) {
     const int64_t tiles = (max_q * a.group + kTileCols - 1) / kTileCols, per_tile = (int64_t)a.p.B * a.p.Hkv;
-    a.col_tiles = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, (int64_t(1) << 30) / per_tile));
-    const dim3 grid((unsigned)(a.col_tiles * per_tile));
+    a.col_tiles = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, (int64_t(1) << 30) / (per_tile * a.splits)));
+    const dim3 grid((unsigned)(a.col_tiles * per_tile * a.splits));
     const bool bias = a.p.softcap > 0.0f || a.p.alibi != nullptr;
     if (fmt == kKvE5M2)
         return bias ? launch_tile<D, kKvE5M2, true, TERMS>(a, grid, stream) : launch_tile<D, kKvE5M2, false, TERMS>(a, grid, stream);
@@ -386,20 +404,56 @@ hipError_t launch(TileArgs a, int fmt, int64_t max_q, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_attn_tiled(const PagedAttn& p, int D, int fmt, int64_t max_q, hipStream_t stream) {
+// Workgroups that share a column tile's keys: as many as the card holds at once
+// (two a CU, one with D = 256), where column tiles alone are fewer, each with at
+// least 4 key tiles.  64 tokens over 16384 keys, 64 / 8 heads of 128: 59 us with
+// one round of workgroups, 67 and 76 with one and a half and two (a second
+// round that is not full), 367 without shares.  At 2048 keys: 27 us with 2 key
+// tiles at least, 21 with 4, 25 with 8.  With long keys also two or three, where
+// that leaves rounds fuller by a tenth or more (560 tokens: 527 us without, 404
+// with 3; 1100: 903 and 749); at 2048 keys their parts cost what that gains (83
+// and 85, 151 and 162).
+static int64_t tile_splits(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_len) {
+    const int64_t group = Hq / Hkv, planned = B * ((max_q * group + kTileCols - 1) / kTileCols);
+    const int64_t full = rows * group / kTileCols;  // at least; `planned` may come from too small a max_q
+    const int64_t tiles = std::max<int64_t>(1, std::max(full, std::min(planned, full + B)) * Hkv);
+    const int64_t fill = D == 256 ? 256 : 512;
+    int64_t s = std::max<int64_t>(1, std::min<int64_t>({fill / tiles, 64, max_len / (4 * kKeys)}));
+    if (max_len >= 4096) {
+        auto rounds = [&](int64_t n) { return (tiles * n + fill - 1) / fill; };
+        for (int64_t n = s + 1; n <= 3; ++n)
+            if (10 * rounds(n) * s < 9 * rounds(s) * n) s = n;
+    }
+    return s;
+}
+
+size_t attn_tiled_ws_bytes(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_len) {
+    const int64_t splits = tile_splits(B, rows, Hq, Hkv, D, max_q, max_len);
+    return splits > 1 ? (size_t)(splits * rows * Hq) * ((size_t)D * 4 + 8) : 0;
+}
+
+hipError_t launch_attn_tiled(const PagedAttn& p, int D, int fmt, int64_t max_q, int64_t max_len, void* ws,
+                             hipStream_t stream) {
     TileArgs a = {};
     a.p = p;
     a.group = p.Hq / p.Hkv;
+    a.splits = (int)tile_splits(p.B, p.rows, p.Hq, p.Hkv, D, max_q, max_len);
+    a.part_o = static_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)a.splits * p.rows * p.Hq * D);
     a.by_block = FastDiv(p.block);
     a.by_group = FastDiv(a.group);
     a.by_kv_heads = FastDiv(p.Hkv);
     a.by_batch = FastDiv(p.B);
+    a.by_splits = FastDiv(a.splits);
     const bool one = p.dtype == kKvBF16;
+    hipError_t e;
     switch (D) {
-        case 64: return one ? launch<64, 1>(a, fmt, max_q, stream) : launch<64, 2>(a, fmt, max_q, stream);
-        case 128: return one ? launch<128, 1>(a, fmt, max_q, stream) : launch<128, 2>(a, fmt, max_q, stream);
-        default: return one ? launch<256, 1>(a, fmt, max_q, stream) : launch<256, 2>(a, fmt, max_q, stream);
+        case 64: e = one ? launch<64, 1>(a, fmt, max_q, stream) : launch<64, 2>(a, fmt, max_q, stream); break;
+        case 128: e = one ? launch<128, 1>(a, fmt, max_q, stream) : launch<128, 2>(a, fmt, max_q, stream); break;
+        default: e = one ? launch<256, 1>(a, fmt, max_q, stream) : launch<256, 2>(a, fmt, max_q, stream);
     }
+    if (e != hipSuccess || a.splits == 1) return e;
+    return launch_attn_join(p, D, a.splits, a.part_o, a.part_ml, max_q, stream);
 }
 
 }  // namespace fp8k

@@ -99,7 +99,13 @@ size_t attn_paged_ws_bytes(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int
                            int64_t all_len);
 hipError_t launch_attn_paged(const PagedAttn& p, int D, int fmt, int64_t max_q, int64_t max_len, void* ws,
                              hipStream_t stream);
-hipError_t launch_attn_tiled(const PagedAttn& p, int D, int fmt, int64_t max_q, hipStream_t stream);
+size_t attn_tiled_ws_bytes(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_len);
+hipError_t launch_attn_tiled(const PagedAttn& p, int D, int fmt, int64_t max_q, int64_t max_len, void* ws,
+                             hipStream_t stream);
+// Output rows from `splits` parts each: part_o [rows][Hq][splits][D], part_ml
+// (reference in log2, sum) [rows][Hq][splits].
+hipError_t launch_attn_join(const PagedAttn& p, int D, int splits, float* part_o, float2* part_ml, int64_t max_q,
+                            hipStream_t stream);
 
 // The dense GEMM launchers write BF16 y, or, when y32 is not null, the fp32
 // value acc * (s_tok * s_ch) before rounding to y32 (same row stride ldy).

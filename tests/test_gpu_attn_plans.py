@@ -1,0 +1,157 @@
+"""GPU parity of paged attention over the ways a call is divided among workgroups: whole sequences or equal shares of
+the keys, one to four KV heads a workgroup, the search for a share's sequence in small and large batches, key shares
+of the tiled kernel.  The rules look at sizes and hints alone, so small caches with wide tables reach them all."""
+import pytest
+import torch
+
+import fp8_w8a8_quantized_quantize_amd as fp8
+from tests._attn import assert_close, assert_lse, make, reference
+from tests._gpu import DEV, log
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def spread(B, longest, seed):
+    """Lengths with many empty and one-token sequences, empty ones first and last."""
+    g = torch.Generator().manual_seed(seed)
+    lens = torch.randint(0, 60, (B,), generator=g)
+    lens[torch.rand(B, generator=g) < 0.3] = 0
+    lens[torch.rand(B, generator=g) < 0.1] = 1
+    lens[B // 3], lens[B // 2] = longest, longest // 2
+    lens[0] = lens[-1] = 0
+    return [int(n) for n in lens]
+
+
+def arguments(s):
+    return [s[k].to(DEV) for k in ("q", "cache", "table", "lens", "scales")]
+
+
+def decode(s, what, max_len, **kw):
+    log(f"  {what}")
+    q, cache, table, lens, scales = arguments(s)
+    width = table.shape[1]
+    need = fp8.fp8_attn_decode_workspace_bytes(q.shape[0], s["Hq"], s["Hkv"], s["D"], s["block"], width, max_len)
+    ws = torch.full((max(need, 16),), 0xFF, dtype=torch.uint8, device=DEV)
+    lse = torch.full(q.shape[:2], 7.0, dtype=torch.float32, device=DEV)
+    out = fp8.fp8_attn_decode_paged(q, cache, table, lens, scales, s["block"], fmt=s["fmt"], lse=lse, max_len=max_len,
+                                    ws=ws, **kw)
+    torch.cuda.synchronize()
+    want, want_lse, tol = reference(s, **kw)
+    assert_close(out, want, tol, what)
+    assert_lse(lse, want_lse, s, what)
+    return need
+
+
+def prefill(s, what, max_q, max_len, **kw):
+    log(f"  {what}")
+    q, cache, table, lens, scales = arguments(s)
+    need = fp8.fp8_attn_prefill_workspace_bytes(q.shape[0], table.shape[0], s["Hq"], s["Hkv"], s["D"], s["block"],
+                                                table.shape[1], max_q, max_len)
+    ws = torch.full((max(need, 16),), 0xFF, dtype=torch.uint8, device=DEV)
+    lse = torch.full(q.shape[:2], 7.0, dtype=torch.float32, device=DEV)
+    call = dict(kw)
+    if call.get("prefix") is not None:
+        call["prefix_lens"] = call.pop("prefix").to(DEV)
+    if call.get("alibi") is not None:
+        call["alibi_slopes"] = call.pop("alibi").to(DEV)
+    out = fp8.fp8_attn_prefill_paged(q, s["cu"].to(DEV), cache, table, lens, scales, s["block"], fmt=s["fmt"],
+                                     lse=lse, max_q=max_q, max_len=max_len, ws=ws, **call)
+    torch.cuda.synchronize()
+    want, want_lse, tol = reference(s, **kw)
+    assert_close(out, want, tol, what)
+    assert_lse(lse, want_lse, s, what)
+    return need
+
+
+@pytest.mark.parametrize("B", [3, 63, 64, 65, 255, 256, 257, 600])
+@pytest.mark.parametrize("D,Hkv", [(64, 2), (128, 1)])
+def test_shares_over_batches(B, D, Hkv):
+    """A share's sequence is looked up by a lane, a wave or a workgroup per sequence, in one pass or several."""
+    s = make(spread(B, 2500, B), 2 * Hkv, Hkv, D, 16, "e5m2", BF16, seed=B)
+    assert decode(s, f"shares B={B} D={D}", 2500) > 0
+
+
+@pytest.mark.parametrize("B", [3, 70, 300])
+def test_a_batch_of_empty_sequences(B):
+    s = make([0] * B, 4, 2, 64, 16, "e4m3", BF16, seed=B, width_extra=200)
+    decode(s, f"empty B={B}", 3000)
+    s = make([0] * (B - 1) + [1], 4, 2, 64, 16, "e4m3", BF16, seed=B, width_extra=200)
+    decode(s, f"all but one empty B={B}", 3000)
+
+
+@pytest.mark.parametrize("Hkv", [2, 4, 6, 8, 12, 5])
+@pytest.mark.parametrize("D,fmt,dtype", [(64, "e4m3", FP32), (128, "e5m2", BF16), (256, "e4m3", BF16)])
+def test_shares_of_several_heads(Hkv, D, fmt, dtype):
+    """Wide tables and a large bound of the length: as many KV heads a workgroup as divide their number."""
+    s = make(spread(66, 700, Hkv), Hkv, Hkv, D, 16, fmt, dtype, seed=Hkv, width_extra=1900)
+    assert decode(s, f"heads {Hkv} D={D} {fmt} {dtype}", 30000) > 0
+
+
+@pytest.mark.parametrize("max_len", [600, 1000])
+@pytest.mark.parametrize("B,Hkv,D,dtype", [(130, 8, 64, BF16), (132, 16, 64, FP16), (66, 16, 128, BF16), (70, 12, 256, BF16)])
+def test_whole_sequences_of_several_heads(B, Hkv, D, dtype, max_len):
+    s = make(spread(B, 500, B), Hkv, Hkv, D, 16, "e5m2", dtype, seed=B)
+    decode(s, f"whole B={B} heads {Hkv} D={D} {max_len}", max_len)
+
+
+@pytest.mark.parametrize("kw", [{}, dict(window=90), dict(causal=False), dict(softcap=6.0)], ids=str)
+@pytest.mark.parametrize("Hq,Hkv,D,new,dtype", [
+    (24, 3, 128, [3, 2, 0, 3], BF16), (16, 2, 64, [8, 1, 0, 7], FP32), (10, 2, 256, [12, 5, 0, 9], BF16),
+    (8, 4, 128, [4, 4, 0, 4], FP16)])
+def test_shares_over_several_column_tiles(Hq, Hkv, D, new, dtype, kw):
+    s = make([3000, 40, 10, 1500], Hq, Hkv, D, 16, "e5m2", dtype, seed=Hq, new=new)
+    assert prefill(s, f"column tiles {Hq}/{Hkv} D={D} {kw}", max(new), 3000, **kw) > 0
+
+
+@pytest.mark.parametrize("kw", [{}, dict(window=300), dict(causal=False), dict(softcap=6.0, alibi=True), dict(prefix=True)],
+                         ids=str)
+@pytest.mark.parametrize("D,dtype", [(64, BF16), (128, BF16), (256, BF16), (128, FP32)])
+def test_key_shares_of_the_tiled_kernel(D, dtype, kw):
+    new = [70, 1, 0, 40, 5]
+    s = make([2500, 300, 0, 35, 900], 8, 4, D, 16, "e5m2", dtype, seed=D, new=new)
+    kw = dict(kw)
+    if kw.get("alibi"):
+        kw["alibi"] = torch.linspace(0.001, 1.0, 8)
+    if kw.get("prefix"):
+        kw["prefix"] = torch.tensor([2480, 400, 3, 30, 0], dtype=torch.int32)
+    assert prefill(s, f"key shares D={D} {dtype} {kw}", 70, 2500, **kw) > 0
+
+
+@pytest.mark.parametrize("max_q,max_len", [(17, 2500), (70, 300), (70, 0), (33, 100000), (5000, 2500)])
+def test_key_shares_with_wrong_hints(max_q, max_len):
+    new = [170, 1, 0, 40, 5]
+    s = make([2500, 300, 0, 35, 900], 8, 4, 128, 16, "e4m3", BF16, seed=4, new=new, width_extra=300)
+    prefill(s, f"hints {max_q} {max_len}", max_q, max_len)
+
+
+@pytest.mark.parametrize("group", [31, 32, 40, 128, 130])
+@pytest.mark.parametrize("D,dtype", [(64, BF16), (128, FP16), (256, BF16)])
+def test_decode_with_many_heads_on_a_kv_head(group, D, dtype):
+    """From 32 (64) query rows a KV head on, decode takes the tiled kernel, with lse and empty sequences."""
+    s = make([2000, 0, 1, 130], group, 1, D, 16, "e5m2", dtype, seed=group)
+    decode(s, f"group {group} D={D} {dtype}", 2000)
+    decode(s, f"group {group} D={D} {dtype} window", 2000, window=200)
+    decode(s, f"group {group} D={D} {dtype} short", 100)
+
+
+@pytest.mark.parametrize("new", [[3, 2], [90, 60]])
+def test_two_streams_with_their_own_workspaces(new):
+    """Two calls at once: each with its own workspace, results as alone."""
+    s = make([9000, 5000], 8, 4, 128, 16, "e5m2", BF16, seed=2, new=new)
+    args = [t.to(DEV) for t in (s["q"], s["cu"], s["cache"], s["table"], s["lens"], s["scales"])]
+    call = dict(max_q=max(new), max_len=9000)
+    alone = fp8.fp8_attn_prefill_paged(*args, 16, **call)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for st in streams:
+            with torch.cuda.stream(st):
+                outs.append(fp8.fp8_attn_prefill_paged(*args, 16, **call))
+    torch.cuda.synchronize()
+    for out in outs:
+        assert torch.equal(out, alone)
