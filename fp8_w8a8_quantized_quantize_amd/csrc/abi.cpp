@@ -136,7 +136,7 @@ int64_t hint(int64_t v, int64_t most) { return v > 0 ? std::min(v, most) : most;
 //     1 sequence      22.6/23.4   21.4/21.4   25.6/26.1   35.6/35.1   89/59
 //     8 sequences     100/84      99/66       116/85      196/110     616/348
 //     32 sequences    265/288     246/229     412/294     823/386     3922/1452
-// Two-term products (fp16 and fp32) fill the tiled kernel's matrix cores twice,
+// Two-term products (fp16, fp32, lse) fill the tiled kernel's matrix cores twice,
 // and D = 256 leaves it one workgroup a CU; two sequences, 16384 keys:
 //     rows                    24          64          256
 //     fp16, D = 128           39/55       53/58       131/100
@@ -146,7 +146,7 @@ bool attn_tiled(int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, bool two_term
     return two_terms || D == 256 ? columns > 64 : columns >= 32;
 }
 
-// The same for every type, which the queries are not told.
+// Either way: the queries are not told the type, nor whether lse is wanted.
 size_t attn_ws(int64_t rows, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size, int64_t max_blocks,
                int64_t max_q, int64_t max_len) {
     const int64_t all_len = block_size * max_blocks;
@@ -198,8 +198,9 @@ fp8_status_t attn(fp8k::PagedAttn p, fp8_kv_dtype_t dtype, fp8_kv_format_t fmt, 
     p.window = (int)std::min(window, kMaxAttn);  // no key is further back
     p.dtype = (int)dtype;
     max_len = hint(max_len, block_size * max_blocks);
-    return from_hip(attn_tiled(Hq, Hkv, D, max_q, dtype != FP8_KV_BF16) ? fp8k::launch_attn_tiled(p, (int)D, (int)fmt, max_q, max_len, ws, stream)
-                                               : fp8k::launch_attn_paged(p, (int)D, (int)fmt, max_q, max_len, ws, stream));
+    const bool tiled = attn_tiled(Hq, Hkv, D, max_q, fp8k::two_terms(p));
+    return from_hip(tiled ? fp8k::launch_attn_tiled(p, (int)D, (int)fmt, max_q, max_len, ws, stream)
+                          : fp8k::launch_attn_paged(p, (int)D, (int)fmt, max_q, max_len, ws, stream));
 }
 
 // Bytes the GEMM path itself needs for an M x N x K problem: the skinny

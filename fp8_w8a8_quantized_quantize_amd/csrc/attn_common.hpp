@@ -11,9 +11,23 @@ typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.44269504088896341f;
-constexpr float kPShift = 8.0f;   // a new reference leaves the largest p at 2^8,
-constexpr float kPLimit = 12.0f;  // and stays until one passes 2^12
 constexpr float kNoRef = -3.0e38f;
+
+// p in fp16: a new reference leaves the largest at 2^8 and stays until one
+// passes 2^12.  With one term the reference itself is 2^8 below the largest
+// score; with two, scores next to the largest keep their last bits (their
+// distance to 2^8 would round at 2^-21), and p is multiplied instead.
+constexpr float kPUnit = 256.0f;
+template <int TERMS>
+struct PScale {
+    static constexpr float kShift = TERMS == 1 ? 8.0f : 0.0f;
+    static constexpr float kLimit = kShift + 4.0f;
+
+    static __device__ __forceinline__ float p(float x) {
+        const float y = __builtin_amdgcn_exp2f(x);
+        return TERMS == 1 ? y : y * kPUnit;
+    }
+};
 
 // n / d for 0 <= n < 2^31 by a product: magic = ceil(2^shift / d) with shift =
 // 31 + ceil(log2(d)) is off by e < 1, which adds n e / 2^shift < 1 / d.
@@ -84,7 +98,7 @@ __device__ __forceinline__ v8h row_f16(uint32_t lo, uint32_t hi) {
 }
 
 // 8 consecutive elements of a query row, as they are and as fp32.
-template <int TERMS>  // 1: bf16, 2: fp16 or fp32
+template <int TERMS>  // 1: bf16 rows alone
 __device__ __forceinline__ void load_q8(const PagedAttn& p, int64_t e, v4u (&raw)[2]) {
     if (TERMS == 2 && p.dtype == kKvF32) {
         const v4u* f = reinterpret_cast<const v4u*>(static_cast<const float*>(p.q) + e);
@@ -100,7 +114,7 @@ template <int TERMS>
 __device__ __forceinline__ void unpack_q8(const PagedAttn& p, const v4u (&raw)[2], float (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (TERMS == 1) {
+        if (TERMS == 1 || p.dtype == kKvBF16) {
             x[2 * i] = __uint_as_float(raw[0][i] << 16);
             x[2 * i + 1] = __uint_as_float(raw[0][i] & 0xFFFF0000u);
         } else if (p.dtype == kKvF32) {
@@ -144,14 +158,26 @@ __device__ __forceinline__ float max_over_groups(float v) {
 }
 
 // cap * tanh(x / cap) in fp32: 1 - 2 / (exp(2 x / cap) + 1), whose absolute
-// error is that of a few roundings at the cap's magnitude.
+// error is that of a few roundings at the cap's magnitude.  Beside two terms
+// that would show in scores far below the cap: there x (1 + t), t from the series
+// of tanh(y) / y - 1 up to y^10, off by 3e-8 of the score at most.
+template <int TERMS>
 __device__ __forceinline__ float soft_cap(float x, float cap, float two_log2e_over_cap) {
-    const float e = __builtin_amdgcn_exp2f(x * two_log2e_over_cap);
-    return cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(e + 1.0f));
+    const float u = x * two_log2e_over_cap;
+    const float e = __builtin_amdgcn_exp2f(u);
+    const float far = cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(e + 1.0f));
+    if constexpr (TERMS == 1) return far;
+    const float y = u * (0.5f * kLn2), z = y * y;
+    float t = __builtin_fmaf(z, -1382.0f / 155925.0f, 62.0f / 2835.0f);
+    t = __builtin_fmaf(z, t, -17.0f / 315.0f);
+    t = __builtin_fmaf(z, t, 2.0f / 15.0f);
+    t = __builtin_fmaf(z, t, -1.0f / 3.0f) * z;
+    return z < 0.14f ? __builtin_fmaf(x, t, x) : far;
 }
 
 // Four channels of an output row from its sum r of p_j code(v_j), reference M
-// and sum L of p_j; an empty row (L == 0) is zeros, its log-sum-exp -inf.
+// and sum L of p_j; an empty row (L == 0) is zeros, its log-sum-exp -inf.  Where
+// lse is wanted there are two terms, and M is the score at which p is kPUnit.
 __device__ __forceinline__ void write_row(const PagedAttn& p, int64_t row, int h, int hk, int D, int d, float M,
                                           float L, const float4& r) {
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
@@ -159,7 +185,7 @@ __device__ __forceinline__ void write_row(const PagedAttn& p, int64_t row, int h
     store_o4(p, row * p.ldo + (int64_t)h * D + d,
              make_float4(r.x * inv * fmaxf(sc.x, kScaleFloor), r.y * inv * fmaxf(sc.y, kScaleFloor),
                          r.z * inv * fmaxf(sc.z, kScaleFloor), r.w * inv * fmaxf(sc.w, kScaleFloor)));
-    if (p.lse && d == 0) p.lse[row * p.Hq + h] = L == 0.0f ? -INFINITY : kLn2 * (M + __builtin_amdgcn_logf(L));
+    if (p.lse && d == 0) p.lse[row * p.Hq + h] = L == 0.0f ? -INFINITY : kLn2 * (M + __builtin_amdgcn_logf(L * (1.0f / kPUnit)));
 }
 
 }  // namespace fp8k

@@ -14,14 +14,14 @@
 // to the output.  q_c ks_c and p_j are rounded to fp16 (2^-11 of half a step),
 // scaled by a power of two first so that nothing underflows that matters (q per
 // column to 2^15, p to 2^8): an eighth of the rounding that bf16 outputs get at
-// the end.  For fp16 and fp32 outputs, where it would show, each is fed as two
-// fp16 terms, high part and rest (2^-22), at the cost of a second matrix
-// instruction.  Scores, references, sums and outputs are fp32; the sum of p is
+// the end.  For fp16 and fp32 outputs and for lse, which is fp32 (two_terms),
+// where it would show, each is fed as two fp16 terms, high part and rest (2^-22),
+// at the cost of a second matrix instruction.  Scores, references, sums and outputs are fp32; the sum of p is
 // a product with ones, so numerator and denominator see the same p.
 //
-// One pass with a running reference m.  m is 2^8 below the largest score of the
-// first tile and moves only when a score passes it by 2^12 (p stays below 2^13
-// in fp16, and the result does not depend on m beyond rounding), so most tiles
+// One pass with a running reference m.  p is 2^8 at the largest score of the
+// first tile, and m moves only when p would pass 2^12 (p stays below 2^13 in
+// fp16, and the result does not depend on m beyond rounding), so most tiles
 // need no other lane.  Scores are formed transposed, S^T = K Q^T, so that a
 // lane's four results belong to one column: its reference and rescale need no
 // lane but the three others of that column, and its p are, as they stand, the
@@ -243,6 +243,7 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
     constexpr int RI = kWave / UR;       // rows of one DMA instruction
     constexpr int NI = kTile / RI;       // DMA instructions of a tile's K, and of its V
     using Lds = StreamLds<D>;
+    using P = PScale<TERMS>;
     constexpr int S = Lds::kStages;
     constexpr int kTileBytes = 2 * kTile * D;
     constexpr int kOutRow = D + 4;       // floats of a joined row, padded off the banks
@@ -461,7 +462,7 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float x = s[t][i] * c;
-                        if (p.softcap > 0.0f) x = kLog2e * soft_cap(x, p.softcap, cap_in);
+                        if (p.softcap > 0.0f) x = kLog2e * soft_cap<TERMS>(x, p.softcap, cap_in);
                         s[t][i] = x + slope * (float)(key0 + 16 * t + 4 * g + i - pos);
                     }
             }
@@ -485,16 +486,16 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
             above();
             if (!whole) hide();
             float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-            if (__any(top > kPLimit)) {
-                // move the references of the columns that need it, kPShift below the largest score; scores past 2^24 are
-                // themselves too coarse for the shift, and one of them takes all the weight
+            if (__any(top > P::kLimit)) {
+                // move the references of the columns that need it to the largest score, less the shift; scores past 2^24
+                // are themselves too coarse for the shift, and one of them takes all the weight
                 const float old = m;
                 m = 0.0f;
                 above();
                 if (!whole) hide();
                 top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
                 top = max_over_groups(top);
-                m = top > old + kPLimit ? (fabsf(top) < 16777216.0f ? top - kPShift : top) : old;
+                m = top > old + P::kLimit ? (fabsf(top) < 16777216.0f ? top - P::kShift : top) : old;
                 const float f = __builtin_amdgcn_exp2f(old - m);
                 l *= f;
 #pragma unroll
@@ -505,7 +506,7 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
             v8h ph, pl;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float y = __builtin_amdgcn_exp2f(x[e]);
+                const float y = P::p(x[e]);
                 ph[e] = (_Float16)y;
                 if constexpr (TERMS == 2) pl[e] = (_Float16)(y - (float)ph[e]);
             }
@@ -759,7 +760,7 @@ hipError_t launch_join(StreamArgs a, int64_t max_q, hipStream_t stream) {
 
 template <int D>
 hipError_t launch(const StreamArgs& a, int fmt, int64_t max_q, hipStream_t stream) {
-    const bool bias = a.p.softcap > 0.0f || a.p.alibi != nullptr, one = a.p.dtype == kKvBF16;
+    const bool bias = a.p.softcap > 0.0f || a.p.alibi != nullptr, one = !two_terms(a.p);
     hipError_t e;
     if (fmt == kKvE5M2)
         e = bias ? (one ? launch_stream<D, kKvE5M2, true, 1>(a, stream) : launch_stream<D, kKvE5M2, true, 2>(a, stream))

@@ -93,6 +93,7 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
     constexpr int DB = D / 32;  // 32-channel blocks of the output
     constexpr int VB = D / 32;  // V channels a thread stages
     using Lds = TileLds<D>;
+    using P = PScale<TERMS>;
     typedef typename std::conditional<D == 64, uint16_t, typename std::conditional<D == 128, uint32_t, v2u>::type>::type vpiece;
 
     const int tid = threadIdx.x, lane = tid % kWave;
@@ -269,7 +270,7 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
             if constexpr (BIAS) {
                 if (p.softcap > 0.0f) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) s[j / 16][j % 16] = kLog2e * soft_cap(s[j / 16][j % 16] * cs, p.softcap, cap_in);
+                    for (int j = 0; j < 32; ++j) s[j / 16][j % 16] = kLog2e * soft_cap<TERMS>(s[j / 16][j % 16] * cs, p.softcap, cap_in);
                 }
                 const float by = p.softcap > 0.0f ? 1.0f : cs, dist = (float)(key0 + 4 * h - pos);
 #pragma unroll
@@ -292,14 +293,14 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
 #pragma unroll
             for (int j = 1; j < 32; ++j) top = fmaxf(top, s[j / 16][j % 16]);
             if (__any(top > limit)) {
-                // Move the references of the columns that need it, kPShift below the largest score (scores past 2^24 are
-                // themselves too coarse for the shift).  A column without a reference has m = 0 and no sum yet.
+                // Move the references of the columns that need it to the largest score, less the shift (scores past 2^24
+                // are themselves too coarse for it).  A column without a reference has m = 0 and no sum yet.
                 top = fmaxf(top, swap32(top));
                 const bool move = top > limit;
-                const float by = move ? (fabsf(top + m) < 16777216.0f ? top - kPShift : top) : 0.0f;
-                const float f = limit == kPLimit ? __builtin_amdgcn_exp2f(-by) : 1.0f;
+                const float by = move ? (fabsf(top + m) < 16777216.0f ? top - P::kShift : top) : 0.0f;
+                const float f = limit == P::kLimit ? __builtin_amdgcn_exp2f(-by) : 1.0f;
                 m += by;
-                limit = move ? kPLimit : limit;
+                limit = move ? P::kLimit : limit;
                 l *= f;
 #pragma unroll
                 for (int d = 0; d < DB; ++d) o[d] *= f;
@@ -315,7 +316,7 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
                 v8h ph[TERMS];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float y = __builtin_amdgcn_exp2f(s[u / 2][8 * (u % 2) + e]);
+                    const float y = P::p(s[u / 2][8 * (u % 2) + e]);
                     l += y;
                     ph[0][e] = (_Float16)y;
                     if constexpr (TERMS == 2) ph[TERMS - 1][e] = (_Float16)(y - (float)ph[0][e]);
@@ -361,7 +362,7 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
         l += swap32(l);
         if (has && a.splits > 1) {
             const int64_t at = (row * p.Hq + head) * a.splits + split;
-            if (h == 0) a.part_ml[at] = make_float2(limit == kPLimit ? m : kNoRef, l);
+            if (h == 0) a.part_ml[at] = make_float2(limit == P::kLimit ? m : kNoRef, l);
 #pragma unroll
             for (int db = 0; db < DB; ++db)
 #pragma unroll
@@ -445,7 +446,7 @@ hipError_t launch_attn_tiled(const PagedAttn& p, int D, int fmt, int64_t max_q, 
     a.by_kv_heads = FastDiv(p.Hkv);
     a.by_batch = FastDiv(p.B);
     a.by_splits = FastDiv(a.splits);
-    const bool one = p.dtype == kKvBF16;
+    const bool one = !two_terms(p);
     hipError_t e;
     switch (D) {
         case 64: e = one ? launch<64, 1>(a, fmt, max_q, stream) : launch<64, 2>(a, fmt, max_q, stream); break;

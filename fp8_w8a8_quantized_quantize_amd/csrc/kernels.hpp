@@ -95,6 +95,10 @@ struct PagedAttn {
 // max_q and max_len plan the launch; longer rows and sequences are still
 // computed whole.  ws: attn_paged_ws_bytes bytes (all_len = max_blocks * block),
 // 16-byte aligned.
+// Whether the scaled query and p are fed as two fp16 terms: an fp16 or fp32
+// output, or lse, would show the rounding of one.
+inline bool two_terms(const PagedAttn& p) { return p.dtype != kKvBF16 || p.lse != nullptr; }
+
 size_t attn_paged_ws_bytes(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_len,
                            int64_t all_len);
 hipError_t launch_attn_paged(const PagedAttn& p, int D, int fmt, int64_t max_q, int64_t max_len, void* ws,

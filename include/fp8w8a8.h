@@ -409,8 +409,8 @@ fp8_status_t fp8_kv_append_rope_paged(const void* q, int64_t ldq, void* q_out, i
  * rounded once, RNE, to q's type.
  * q, out: dtype elements [rows, Hq, D], heads adjacent, row strides ldq, ldo,
  * rows 16-byte aligned; lse fp32 [rows, Hq] or NULL; out does not overlap q.
- * cache: u8 [num_blocks * block_size, 2 Hkv D]; scales fp32 [2 Hkv D];
- * block_table int32 [B, max_blocks], row stride ld_table.  D is 64, 128 or
+ * cu_q does not decrease.  cache: u8 [num_blocks * block_size, 2 Hkv D];
+ * scales fp32 [2 Hkv D]; block_table int32 [B, max_blocks], row stride ld_table.  D is 64, 128 or
  * 256 and Hq a multiple of Hkv, Hkv <= 65535; any block_size >= 1; positions,
  * rows * Hq and block_size * max_blocks up to 2^30.
  * max_q and max_len plan the launch: bounds of the new rows and of the length
@@ -423,7 +423,8 @@ fp8_status_t fp8_kv_append_rope_paged(const void* q, int64_t ldq, void* q_out, i
  * codes among them) do not matter; within a sequence inputs are assumed finite.
  * ws: at least the matching *_workspace_bytes of the same arguments, 16-byte
  * aligned (key shares of long sequences; may be NULL when that is 0; contents
- * on entry do not matter).  Results do not depend on timing: shares are joined
+ * on entry do not matter).  Calls that may run at the same time, captured ones
+ * among them, need one each.  Results do not depend on timing: shares are joined
  * in a fixed order.
  */
 fp8_status_t fp8_attn_decode_paged(const void* q, int64_t ldq, fp8_kv_dtype_t dtype, const uint8_t* cache,

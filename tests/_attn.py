@@ -38,19 +38,19 @@ def make(lens, Hq, Hkv, D, block, fmt, dtype, seed, new=None, extra_pages=3, wid
                 block=block, fmt=fmt, Hq=Hq, Hkv=Hkv, D=D)
 
 
-def reference(s, causal=True, softcap=0.0, alibi=None, window=0, prefix=None, sm_scale=None):
+def reference(s, causal=True, softcap=0.0, alibi=None, window=0, prefix=None, sm_scale=None, lse=True):
     """(out, lse, tol) in float64.  tol: how far out may be off, elementwise, for an output of q's type.
 
     The operator's own arithmetic, against the exact value: q times the key scale and p each go through one fp16 term
-    where the output is bf16 (off by half a step, 2^-11 relative) and two where it is fp16 or fp32 (2^-22), `term`
-    below, a score is a sum of D products in fp32 (at most (D + 8) roundings of 2^-24 of sum |q k|, twice for the two
+    where the output is bf16 and lse is not asked for (off by half a step, 2^-11 relative) and two otherwise (2^-22),
+    `term` below, a score is a sum of D products in fp32 (at most (D + 8) roundings of 2^-24 of sum |q k|, twice for the two
     terms), its exponential is good to 2^-22 plus the rounding of its argument
     (2^-23 of |score| in base 2, under 2^-22 of the natural one), the cap and the bias add roundings of their own
     magnitude (2^-20 of the cap: 1 - 2 / (e + 1) and two approximations of 1 ulp; 2^-23 of the bias).  With ds the sum
     of those, p is off by the factor 1 +- ds, numerator and denominator both, so out by 2 ds * A with
     A = sum p |v| / sum p; the fp32 sums over n keys add n 2^-24 A at the most, and the value scale and the
     division 2^-22 A.  Then one rounding to the type.  s["lse_tol"] receives the same for lse."""
-    term = 2.0 ** -11 if s["q"].dtype == torch.bfloat16 else 2.0 ** -22
+    term = 2.0 ** -11 if s["q"].dtype == torch.bfloat16 and not lse else 2.0 ** -22
     q, D, Hq, Hkv, block = s["q"].double(), s["D"], s["Hq"], s["Hkv"], s["block"]
     G = Hq // Hkv
     scale = D ** -0.5 if sm_scale is None else sm_scale

@@ -176,7 +176,7 @@ def test_prompt_then_decode_steps(fmt):
     same(qr, want_q, "prompt queries")
     s = dict(q=want_q, cache=torch.from_numpy(want_cache), table=tab, lens=lens, scales=scales, cu=cu, block=block,
              fmt=fmt, Hq=Hq, Hkv=Hkv, D=D)
-    want, _, tol = reference(s)
+    want, _, tol = reference(s, lse=False)
     assert_close(out, want, tol, "prompt attention")
 
     # the decode step, captured once: its inputs are refilled for every replay
@@ -212,5 +212,5 @@ def test_prompt_then_decode_steps(fmt):
         s = dict(q=want_q, cache=torch.from_numpy(want_cache), table=tab,
                  lens=torch.tensor(at, dtype=torch.int32) + 1, scales=scales,
                  cu=torch.arange(B + 1, dtype=torch.int32), block=block, fmt=fmt, Hq=Hq, Hkv=Hkv, D=D)
-        want, _, tol = reference(s)
+        want, _, tol = reference(s, lse=False)
         assert_close(out, want, tol, f"decode step {i}")
