@@ -14,8 +14,11 @@
 // element.  A thread owns 16 elements of a head, laid out so that a pair never
 // leaves it: two runs of 8 half the rotated width apart (or 16 neighbours when
 // pairs are interleaved), so every access is 16 bytes of a 16-bit row, and the
-// same slot of kTokens tokens in turn, so its scales are read and inverted
-// once and the loads of all its tokens are in flight together.
+// same slot of two tokens, so its scales are read and inverted once and the
+// loads of both are in flight together.  32768 tokens, 64 / 8 heads of 128, bf16:
+// 227 us, 5.7 TB/s; one token: 2.7 us, a launch.  Workgroups of 128 threads: 256
+// leave a sixth of the lanes without a slot there (229 us; 32 / 8 heads 79.7
+// against 70.2 at 16384 tokens).
 #include <algorithm>
 
 #include "kv_common.hpp"
@@ -24,7 +27,7 @@ namespace fp8k {
 
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 
 // 8 consecutive row elements as fp32.
 template <int DT>
@@ -162,10 +165,15 @@ template <int FMT, int DT>
 hipError_t launch(KvAppend p, bool pairs, hipStream_t stream) {
     const int64_t units = (int64_t)(p.Hq + 2 * p.Hkv) * (p.D / 16);
     const int64_t cols = (units + kAppendThreads - 1) / kAppendThreads;
-    // About 2048 workgroups (8 per CU) once there are tokens for them; below
-    // that a workgroup takes one token, since latency is what counts there.
-    const int64_t rows = std::min<int64_t>(p.T, std::max<int64_t>(1, 2048 / cols));
-    p.tokens_per_block = (int)((p.T + rows - 1) / rows);
+    // Two tokens a thread, whose loads travel together; one where that leaves
+    // CUs idle (latency is what counts there).  us for 512 / 1777 / 32768 tokens
+    // (64 / 8 heads of 128, bf16; 1777: 24 / 3 of 256, fp16): one token 7.7 /
+    // 16.0 / 257, two 6.4 / 14.5 / 227, four 7.6 / 16.0 / 266, two in a loop of
+    // 2048 workgroups 7.7 / 14.4 / 279.
+    const int64_t work = p.T * cols;
+    p.tokens_per_block = work < 2048 ? 1 : 2;
+    // more rows than a grid has: loops
+    while ((p.T + p.tokens_per_block - 1) / p.tokens_per_block > 65535) p.tokens_per_block *= 2;
     const dim3 grid((unsigned)cols, (unsigned)((p.T + p.tokens_per_block - 1) / p.tokens_per_block));
     const bool many = p.tokens_per_block > 1;
     if (pairs) {

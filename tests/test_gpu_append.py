@@ -125,6 +125,17 @@ def test_positions_outside_the_table_write_nothing():
     assert_codes_equal(to_host(cache), want_cache, "cache")
 
 
+def test_more_tokens_than_a_grid_has_rows():
+    T = 140001
+    qkv, slot, pos, cs, scales, prior = problem(T, 1, 1, 16, 16, BF16, seed=5)
+    want_q, want_cache = expect(*split(qkv, 1, 1, 16), pos, cs, 16, False, scales, slot, "e5m2", prior)
+    q, k, v = split(qkv.to(DEV), 1, 1, 16)
+    cache = prior.to(DEV)
+    out = fp8.fp8_kv_append_rope_paged(k, v, pos.to(DEV), cs.to(DEV), scales.to(DEV), slot.to(DEV), cache, q=q)
+    same(out, want_q, "q_out")
+    assert_codes_equal(to_host(cache), want_cache, "cache")
+
+
 def test_far_positions_and_rows_past_32_bits():
     T, Hkv, D = 20, 8, 128
     P = 300000
