@@ -718,14 +718,20 @@ StreamPlan stream_plan(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t
     s.hw = most;
     s.shares = 0;
     s.min_share = 2;
+    // Short sequences go whole, with as many heads a workgroup as still fill the card: shares cost a scan and a second
+    // kernel.  Whole / shares, us, 64 / 8 heads of 128, bf16:  1 x 640 keys 11.5 / 12.5, 1 x 1000 14.8 / 12.4, 16 x 700
+    // 13.6 / 17.4, 32 x 1000 16.3 / 23.9, 256 x 500 54 / 73; 16 x 2000 23.8 / 22.9, 16 x 8000 75 / 67, 1 x 8000 68 / 15.
     if (max_len <= 1024) {
         while (s.hw > 1 && B * (Hkv / s.hw) * s.col_tiles < fill) s.hw /= 2;
-        if (max_len <= 640 || B * (Hkv / s.hw) * s.col_tiles >= fill) return s;
+        if (max_len <= 640 || B * (Hkv / s.hw) * s.col_tiles >= fill / 4) return s;
     }
     // costs of all sequences are added up in 32 bits
     const int64_t cost = (ceil_div(all_len, kTile) + kItemCost) * (rows * (Hq / Hkv) / kCols + B);
     if (cost >= (int64_t(1) << 30)) return s;
     s.hw = most;
+    // Several heads a workgroup read longer runs of a cache row; with few rounds a share, its four waves on one head
+    // shorten the chain instead.  Four heads / one, us: 48 x 4096 ... 32768 keys 297 / 318, 64 x 1000 ... 8000 102 / 112,
+    // 1 x 8000 17.2 / 14.7, 19 x 1 ... 9001 of 256 channels 25.8 / 23.9.
     const int64_t items = B * (Hkv / most) * s.col_tiles;
     if (items < 32 || items * max_len * most / (kTile * kWaves) < 16 * fill) s.hw = 1;
     s.shares = (int)std::max<int64_t>(1, fill / (Hkv / s.hw));
