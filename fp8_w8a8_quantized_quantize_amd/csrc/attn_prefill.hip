@@ -11,16 +11,19 @@
 // takes 128 columns, 32 a wave, and walks over 64-key tiles that all its waves
 // share in LDS: K as fp16 rows, V as fp16 transposed, eight keys of a channel in
 // 16 bytes in the order in which a lane holds its p.  Codes become fp16 once per
-// workgroup, on the way into LDS.  D = 128 takes 231 registers and 72 KB of LDS,
+// workgroup, on the way into LDS.  D = 128 takes 232 registers and 72 KB of LDS,
 // two workgroups a CU: the softmax of one wave runs beside the matrix work of
 // the other on its SIMD.  64 columns a wave (half the LDS reads per matrix
-// instruction, one wave per SIMD) spilled and took 3.7 ms where this takes 1.2
-// (8192 tokens, 64 / 8 heads of 128, bf16), and so did forming the next tile's
-// scores during the softmax (2.3 ms).
+// instruction, one wave per SIMD) spilled and took 3.7 ms where this takes 1.17
+// (8192 tokens, 64 / 8 heads of 128, bf16: 940 TFLOP/s), and so did forming the
+// next tile's scores during the softmax (2.3 ms).  Two terms with D = 128 and 256
+// spill some 40 and 170 registers and still beat the streaming form from 128
+// rows on.
 //
 // Bound: matrix cores 42 %, vector unit 50 % of the cycles (240 instructions per
 // 32 columns x 64 keys, 32 of them exponentials, beside 32 matrix instructions
-// of 32 cycles), LDS 55 %; what is lost is waves of a SIMD wanting the same unit.
+// of 32 cycles), LDS 41 %; the two waves of a SIMD seldom want different units
+// (wave priorities around either phase changed nothing).
 //
 // One barrier per tile: step t writes K and V of tile t into the buffers last
 // read in step t - 2, starts the loads of tile t + 1 into registers, and computes
@@ -54,9 +57,10 @@ struct TileArgs {
     FastDiv by_block, by_group, by_kv_heads, by_batch, by_splits;
 };
 
-// LDS rows are padded by 16 bytes, so that the operand reads (32 neighbouring
-// rows) spread over the banks; V is written for every D / 32-nd channel at once,
-// so its 16-byte units also sit at unit ^ (channel / 16 % 8).
+// LDS rows are padded by 16 bytes, so that 32 neighbouring rows spread over the
+// banks.  V's channel d, byte d % VB of the piece that lane d / VB stages, is
+// row 32 (d % VB) + d / VB: writes and operand reads both take neighbouring
+// rows, and the output blocks hold a lane's channels in order.
 // LDS: two K tiles, two V tiles, cache offsets of 16 rows per wave for two
 // tiles, and which keys of four tiles are there.
 template <int D>
@@ -243,8 +247,7 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
                 v4u r;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) r[i] = pair_f16<FMT>(vword(2 * i, j / 4), vword(2 * i + 1, j / 4), j % 4);
-                const int d = c * VB + j;
-                *reinterpret_cast<v4u*>(dst + d * Lds::kVRow + ((2 * wave + h) ^ (d / 16 % 8)) * 16) = r;
+                *reinterpret_cast<v4u*>(dst + (32 * j + c) * Lds::kVRow + (2 * wave + h) * 16) = r;
             }
         };
         v16f s[2];
@@ -310,7 +313,7 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
         };
         // p and its product with V, 16 keys at a time
         auto product = [&](int t) {
-            const uint8_t* src = tile_smem + Lds::kV + t % 2 * Lds::kVTile + c * Lds::kVRow + (h ^ (c / 16)) * 16;
+            const uint8_t* src = tile_smem + Lds::kV + t % 2 * Lds::kVTile + c * Lds::kVRow + h * 16;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 v8h ph[TERMS];
@@ -323,7 +326,7 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
                 }
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
-                    const v8h v = *reinterpret_cast<const v8h*>(src + 32 * db * Lds::kVRow + 32 * (u ^ (db % 4)));
+                    const v8h v = *reinterpret_cast<const v8h*>(src + 32 * db * Lds::kVRow + 32 * u);
 #pragma unroll
                     for (int x = 0; x < TERMS; ++x) o[db] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, ph[x], o[db], 0, 0, 0);
                 }
@@ -360,22 +363,20 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
 
         // ---- results
         l += swap32(l);
-        if (has && a.splits > 1) {
+        if (has) {
             const int64_t at = (row * p.Hq + head) * a.splits + split;
-            if (h == 0) a.part_ml[at] = make_float2(limit == P::kLimit ? m : kNoRef, l);
+            if (a.splits > 1 && h == 0) a.part_ml[at] = make_float2(limit == P::kLimit ? m : kNoRef, l);
 #pragma unroll
-            for (int db = 0; db < DB; ++db)
-#pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                    *reinterpret_cast<float4*>(a.part_o + at * D + 32 * db + 2 * i + 4 * h) =
-                        make_float4(o[db][i], o[db][i + 1], o[db][i + 2], o[db][i + 3]);
-        } else if (has) {
-#pragma unroll
-            for (int db = 0; db < DB; ++db)
-#pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                    write_row(p, row, head, hk, D, 32 * db + 2 * i + 4 * h, m, l,
-                              make_float4(o[db][i], o[db][i + 1], o[db][i + 2], o[db][i + 3]));
+            for (int x = 0; x < 16 * DB; x += 4) {
+                // four channels in a row: elements x .. x + 3 of [row][block]
+                const float4 r = make_float4(o[x % DB][x / DB], o[(x + 1) % DB][(x + 1) / DB], o[(x + 2) % DB][(x + 2) / DB],
+                                             o[(x + 3) % DB][(x + 3) / DB]);
+                const int i = x / DB, d = (8 * (i / 4) + 4 * h + i % 4) * VB + x % DB;
+                if (a.splits > 1)
+                    *reinterpret_cast<float4*>(a.part_o + at * D + d) = r;
+                else
+                    write_row(p, row, head, hk, D, d, m, l, r);
+            }
         }
         __syncthreads();
     }
