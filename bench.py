@@ -63,7 +63,7 @@ TRAFFIC_FILE = os.path.join(ROOT, "profiles", "hbm_traffic.txt")
 KERNEL_SOURCES = {
     "skinny": ["gemm_skinny.hip", "device_common.hpp"],
     "mfma": ["gemm_mfma.hip", "device_common.hpp"],
-    "kv": ["kv_cache.hip", "device_common.hpp"],
+    "kv": ["kv_cache.hip", "kv_common.hpp", "device_common.hpp"],
     "stream": ["stream_read.hip", "device_common.hpp"],
 }
 

@@ -138,9 +138,9 @@ int64_t hint(int64_t v, int64_t most) { return v > 0 ? std::min(v, most) : most;
 //     32 sequences    265/288     246/229     412/294     823/386     3922/1452
 // Two-term products (fp16, fp32, lse) fill the tiled kernel's matrix cores twice,
 // and D = 256 leaves it one workgroup a CU; two sequences, 16384 keys:
-//     rows                    24          64          256
-//     fp16, D = 128           39/55       53/58       131/100
-//     bf16, D = 256 (32/8)    39/73 (12)  50/66 (32)  116/80 (128)
+//     rows                    24          64          96     128    256
+//     fp16, D = 128           39/55       53/58       55/55  95/64  131/100
+//     bf16, D = 256 (32/8)    39/73 (12)  50/66 (32)                116/80 (128)
 bool attn_tiled(int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, bool two_terms) {
     const int64_t columns = max_q * (Hq / Hkv);
     return two_terms || D == 256 ? columns > 64 : columns >= 32;

@@ -17,7 +17,7 @@
 // instruction, one wave per SIMD) spilled and took 3.7 ms where this takes 1.17
 // (8192 tokens, 64 / 8 heads of 128, bf16: 940 TFLOP/s), and so did forming the
 // next tile's scores during the softmax (2.3 ms).  Two terms with D = 128 and 256
-// spill some 40 and 170 registers and still beat the streaming form from 128
+// spill some 40 and 170 registers and still beat the streaming form from 96
 // rows on.
 //
 // Bound: matrix cores 42 %, vector unit 50 % of the cycles (240 instructions per
