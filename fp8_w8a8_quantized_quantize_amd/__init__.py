@@ -466,20 +466,23 @@ def _on_stream(fn):
     then belongs to the stream that uses it, so the allocator cannot hand it to
     other work while the call still runs."""
 
+    first = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(t, *args, stream=None, **kwargs):
+    def call(*args, stream=None, **kwargs):
         torch = _torch()
+        t = args[0] if args else kwargs.get(first)
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{fn.__name__}: expected CUDA tensors")
         if stream is not None:
             if stream.device != t.device:
                 raise ValueError(f"stream: on {stream.device}, expected {t.device}")
             with torch.cuda.stream(stream):
-                return fn(t, *args, **kwargs)
+                return fn(*args, **kwargs)
         if t.get_device() != torch.cuda.current_device():
             with torch.cuda.device(t.device):
-                return fn(t, *args, **kwargs)
-        return fn(t, *args, **kwargs)
+                return fn(*args, **kwargs)
+        return fn(*args, **kwargs)
 
     return call
 

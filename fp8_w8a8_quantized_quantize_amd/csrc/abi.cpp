@@ -502,8 +502,9 @@ fp8_status_t fp8_attn_prefill_paged(const void* q, int64_t ldq, fp8_kv_dtype_t d
     p.cache = cache, p.num_blocks = num_blocks, p.scales = scales;
     p.block_table = block_table, p.ld_table = ld_table, p.seq_lens = seq_lens, p.prefix = prefix_lens;
     p.softcap = softcap, p.alibi = alibi_slopes, p.causal = causal != 0;
-    return attn(p, dtype, fmt, T, B, Hq, Hkv, D, block_size, max_blocks, max_q < 0 ? max_q : hint(max_q, std::max<int64_t>(T, 0)), max_len, window,
-                sm_scale, ws, ws_bytes, stream);
+    if (max_q >= 0) max_q = hint(max_q, std::max<int64_t>(T, 0));
+    return attn(p, dtype, fmt, T, B, Hq, Hkv, D, block_size, max_blocks, max_q, max_len, window, sm_scale, ws, ws_bytes,
+                stream);
 }
 
 fp8_status_t fp8_gemm_scaled(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw,

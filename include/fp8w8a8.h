@@ -406,7 +406,9 @@ fp8_status_t fp8_kv_append_rope_paged(const void* q, int64_t ldq, void* q_out, i
  * values are in the cache already (append first).  A query that sees no key
  * (an empty sequence, more new tokens than keys) gives a row of +0 and
  * lse -inf.  The softmax, its sums and the products accumulate in fp32; out is
- * rounded once, RNE, to q's type.
+ * rounded once, RNE, to q's type.  Codes enter the products exactly; q times the
+ * key scales and p as fp16 terms: one where q is bf16 and lse NULL (off by 2^-11
+ * of the value at most), else two (2^-22).
  * q, out: dtype elements [rows, Hq, D], heads adjacent, row strides ldq, ldo,
  * rows 16-byte aligned; lse fp32 [rows, Hq] or NULL; out does not overlap q.
  * cu_q does not decrease.  cache: u8 [num_blocks * block_size, 2 Hkv D];

@@ -142,6 +142,15 @@ def test_decode_with_many_heads_on_a_kv_head(group, D, dtype):
     decode(s, f"group {group} D={D} {dtype} short", 100)
 
 
+def test_arguments_by_name():
+    s = make([50, 7], 4, 2, 64, 16, "e5m2", BF16, seed=1)
+    q, cache, table, lens, scales = arguments(s)
+    a = fp8.fp8_attn_decode_paged(q, cache, table, lens, scales, 16)
+    b = fp8.fp8_attn_decode_paged(q=q, cache=cache, block_table=table, seq_lens=lens, scales=scales, block_size=16)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("new", [[3, 2], [90, 60]])
 def test_two_streams_with_their_own_workspaces(new):
     """Two calls at once: each with its own workspace, results as alone."""
