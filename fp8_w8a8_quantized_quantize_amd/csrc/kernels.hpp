@@ -51,7 +51,8 @@ hipError_t launch_kv_dequantize_paged(const uint8_t* cache, int64_t num_slots, c
                                       hipStream_t stream);
 
 // Append with rotation (kv_append.hip): strides in elements, rows 16-byte
-// aligned, D and rot multiples of 16, q may be null with Hq == 0.
+// aligned, D and rot multiples of 16; q and q_out may be null with Hq == 0, k,
+// v, scales, slot and cache with Hkv == 0.
 // tokens_per_block is the launcher's.
 struct KvAppend {
     const void *q, *k, *v;

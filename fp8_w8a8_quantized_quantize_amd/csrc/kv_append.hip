@@ -108,7 +108,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_rope(KvAppend p) {
             load8<DT>(src, tt * ld + (int64_t)h * p.D + e0, a[n]);
             load8<DT>(src, tt * ld + (int64_t)h * p.D + e1, b[n]);
             const int pos = p.positions[tt];
-            slot[n] = p.slot[tt];
+            slot[n] = is_q ? -1 : p.slot[tt];  // null without KV heads
             live[n] = t + n < t1 && pos >= 0 && pos < p.P;
             if (turns) {
                 const float* row = p.cos_sin + (int64_t)(live[n] ? pos : 0) * p.rot + 8 * i;

@@ -369,7 +369,8 @@ fp8_status_t fp8_kv_dequantize_paged(const uint8_t* cache, int64_t num_slots, co
  * D), row strides ldq, ldk, ldv, ldqo elements, rows 16-byte aligned (slices
  * of one QKV projection output qualify).  q_out may be q itself (same pointer
  * and stride), else they must not overlap; q and q_out may be NULL with
- * Hq == 0, k and v with Hkv == 0.  cos_sin: fp32 [P, rot_dim], rot_dim / 2
+ * Hq == 0, k, v, scales, slot_mapping and cache with Hkv == 0 (a rotation of
+ * queries alone).  cos_sin: fp32 [P, rot_dim], rot_dim / 2
  * cosines then rot_dim / 2 sines, 16-byte aligned.  A token whose slot is
  * outside [0, num_slots) (padding carries -1) writes no cache row; one whose
  * position is outside [0, P) writes nothing at all, q_out included.  Two

@@ -225,3 +225,24 @@ def test_prompt_then_decode_steps(fmt):
                  cu=torch.arange(B + 1, dtype=torch.int32), block=block, fmt=fmt, Hq=Hq, Hkv=Hkv, D=D)
         want, _, tol = reference(s, lse=False)
         assert_close(out, want, tol, f"decode step {i}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("T", [1, 7, 4000])
+def test_queries_alone(T, dtype):
+    """Without KV heads nothing of the cache's side is there: k, v, scales, slot_mapping and cache are null."""
+    Hq, D, P = 12, 128, 500
+    log(f"  queries alone T={T} {dtype}")
+    g = torch.Generator().manual_seed(T)
+    q = torch.randn((T, Hq, D), generator=g).to(dtype)
+    pos = torch.randint(0, P, (T,), generator=g).int()
+    cs = table(P, D)
+    qd, pd, cd = q.to(DEV), pos.to(DEV), cs.to(DEV)
+    out = torch.full((T, Hq, D), 9.0, dtype=dtype, device=DEV)
+    kind = {FP32: fp8.FP8_KV_F32, BF16: fp8.FP8_KV_BF16, FP16: fp8.FP8_KV_F16}[dtype]
+    code = fp8.lib().fp8_kv_append_rope_paged(qd.data_ptr(), Hq * D, out.data_ptr(), Hq * D, 0, 0, 0, 0, kind, T, Hq, 0, D,
+                                              pd.data_ptr(), cd.data_ptr(), P, D, 0, 0, 1, 0, 0, 0,
+                                              torch.cuda.current_stream().cuda_stream)
+    assert code == fp8.FP8_OK
+    want = torch.from_numpy(turn(q.float().numpy(), cs.numpy()[pos.numpy()], D, False)).to(dtype)
+    same(out, want, "q_out")
