@@ -58,20 +58,19 @@
 #include <type_traits>
 
 #include "attn_common.hpp"
+#include "attn_plan.hpp"
 
 namespace fp8k {
 
 namespace {
 
-constexpr int kTile = 32;      // keys per step of a wave
-constexpr int kWaves = 4;      // waves of a workgroup
-constexpr int kCols = 16;      // query columns of a tile
 constexpr int kLogRound = 7;   // of kTile * kWaves
 struct StreamArgs {
     PagedAttn p;
     int group;         // query heads per KV head
     int hw, log_hw;    // KV heads of a workgroup
     int head_groups;   // workgroups that share a sequence's rows
+    int item0;         // whole items (sequence, head group): the first one of this launch
     int col_tiles;     // whole items: column tiles a KV head is planned for
     int shares;        // equal shares: their number for every head group, 0 for whole items
     int min_share;     // and their least cost
@@ -81,6 +80,8 @@ struct StreamArgs {
     int splits;        // the join alone: parts of every row, laid out [rows][Hq][splits], 0 for cut rows as above
     int spread, log_spread;  // the join's thread groups per output row
     int join_rows;     // and the new rows of a sequence it takes at a time
+    int join_batch;    // of the p.B sequences; 1 with `splits`, whose parts go by row
+    int join_unit0;    // the first workgroup's worth of rows of this launch
     FastDiv by_block, by_group, by_head_groups, by_heads, by_batch;
 
     __device__ __forceinline__ int page(int key) const { return by_block.of(key); }
@@ -116,10 +117,6 @@ __device__ __forceinline__ Run run_of(const StreamArgs& a, const Seq& s, int pre
     r.items = r.rounds > 0 ? (s.nq * a.group + kCols - 1) / kCols : 0;
     return r;
 }
-
-// Cost of an item's start (page and length look-ups, the first tiles' latency,
-// the join of its waves) in rounds: measured about 6 us against 1.5 us a round.
-constexpr int kItemCost = 4;
 
 // Inclusive sums over the lanes of a wave.
 __device__ __forceinline__ int wave_scan(int v) {
@@ -277,8 +274,9 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
         at_item = __builtin_amdgcn_readfirstlane(at - ct * (r.rounds + kItemCost));
         __syncthreads();
     } else {
-        b = a.by_head_groups.of(blockIdx.x);
-        hg = blockIdx.x - b * a.head_groups;
+        const int item = a.item0 + blockIdx.x;
+        b = a.by_head_groups.of(item);
+        hg = item - b * a.head_groups;
         ct = blockIdx.y;
     }
 
@@ -622,21 +620,29 @@ __global__ __launch_bounds__(kWaves* kWave) void attn_join(StreamArgs a) {
     __shared__ float4 sums[kThreads];
     __shared__ float2 group_ml[kGroups];
     const int tid = threadIdx.x, d4 = tid % kLanes, grp = tid / kLanes, part = grp & (a.spread - 1);
-    const int nth = blockIdx.x * (kGroups >> a.log_spread) + (grp >> a.log_spread);  // row of the launch: (i0, b, h)
+    const int nth = (a.join_unit0 + blockIdx.x) * (kGroups >> a.log_spread) + (grp >> a.log_spread);  // row of the launch: (i0, b, h)
     const int rest = a.by_heads.of(nth), i0 = a.by_batch.of(rest);
-    const int h = nth - rest * p.Hq, b = rest - i0 * p.B;
+    const int h = nth - rest * p.Hq, b = rest - i0 * a.join_batch;
     const int hk = a.by_group.of(h);
-    const bool live = i0 < a.join_rows;
     Seq seq = {0, 0, 0};
-    if (live) seq = sequence(p, b);
-    const int prefix = live && p.prefix ? p.prefix[b] : 0;
+    int prefix = 0, first_row = 0;
+    if (i0 < a.join_rows) {
+        if (a.splits > 0) {
+            // the rows of all sequences, without regard to whose they are
+            seq.nq = p.rows;
+            if (p.cu_q) first_row = p.cu_q[0], seq.nq = min(p.cu_q[p.B], p.rows);
+        } else {
+            seq = sequence(p, b);
+            prefix = p.prefix ? p.prefix[b] : 0;
+        }
+    }
     // Every thread goes through as many rounds as the longest sequence of its workgroup: the barriers are for all.
     for (int i = i0; __syncthreads_or(i < seq.nq); i += a.join_rows) {
         float M = kNoRef, L = 0.0f;
         float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         int shares = 0;
         bool cut = false;  // else the first kernel has written the row
-        if (i < seq.nq) {
+        if (i >= first_row && i < seq.nq) {
             const int col = i * a.group + h - hk * a.group;
             int first = 0;
             shares = a.splits;
@@ -699,83 +705,44 @@ __global__ __launch_bounds__(kWaves* kWave) void attn_join(StreamArgs a) {
     }
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Workgroups of one launch; rows beyond what they are planned for are taken in turn.
-constexpr int64_t kMaxGrid = 1 << 26;
-
-struct StreamPlan {
-    int hw, shares, min_share;
-    int64_t col_tiles;
-};
-
-StreamPlan stream_plan(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_len,
-                       int64_t all_len) {
-    StreamPlan s;
-    B = std::max<int64_t>(B, 1);
-    s.col_tiles = ceil_div(std::max<int64_t>(max_q, 1) * (Hq / Hkv), kCols);
-    s.col_tiles = std::max<int64_t>(1, std::min<int64_t>({s.col_tiles, kMaxGrid / (B * Hkv), 65535}));
-    const int most = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
-    const int64_t fill = D == 256 ? 256 : 512;  // workgroups that are resident at once
-    s.hw = most;
-    s.shares = 0;
-    s.min_share = 2;
-    // Short sequences go whole, with as many heads a workgroup as still fill the card: shares cost a scan and a second
-    // kernel.  Whole / shares, us, 64 / 8 heads of 128, bf16:  1 x 640 keys 11.5 / 12.5, 1 x 1000 14.8 / 12.4, 16 x 700
-    // 13.6 / 17.4, 32 x 1000 16.3 / 23.9, 256 x 500 54 / 73; 16 x 2000 23.8 / 22.9, 16 x 8000 75 / 67, 1 x 8000 68 / 15.
-    if (max_len <= 1024) {
-        while (s.hw > 1 && B * (Hkv / s.hw) * s.col_tiles < fill) s.hw /= 2;
-        if (max_len <= 640 || B * (Hkv / s.hw) * s.col_tiles >= fill / 4) return s;
-    }
-    // costs of all sequences are added up in 32 bits
-    const int64_t cost = (ceil_div(all_len, kTile) + kItemCost) * (rows * (Hq / Hkv) / kCols + B);
-    if (cost >= (int64_t(1) << 30)) return s;
-    s.hw = most;
-    // Several heads a workgroup read longer runs of a cache row; with few rounds a share, its four waves on one head
-    // shorten the chain instead.  Four heads / one, us: 48 x 4096 ... 32768 keys 297 / 318, 64 x 1000 ... 8000 102 / 112,
-    // 1 x 8000 17.2 / 14.7, 19 x 1 ... 9001 of 256 channels 25.8 / 23.9.
-    const int64_t items = B * (Hkv / most) * s.col_tiles;
-    if (items < 32 || items * max_len * most / (kTile * kWaves) < 16 * fill) s.hw = 1;
-    s.shares = (int)std::max<int64_t>(1, fill / (Hkv / s.hw));
-    return s;
-}
-
 template <int D, int FMT, bool BIAS, int TERMS>
-hipError_t launch_stream(const StreamArgs& a, hipStream_t stream) {
+hipError_t launch_stream(StreamArgs a, const StreamPlan& s, hipStream_t stream) {
     constexpr int lds = StreamLds<D>::kBytes;
-    const unsigned groups = a.head_groups;
-    const dim3 grid = a.shares > 0 ? dim3(a.shares * groups) : dim3(a.p.B * groups, (unsigned)a.col_tiles);
     if constexpr (lds > 64 * 1024) {
         const hipError_t e = FP8K_SET_LDS((attn_stream<D, FMT, BIAS, TERMS>), lds);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((attn_stream<D, FMT, BIAS, TERMS>), grid, dim3(kWaves * kWave), lds, stream, a);
-    return hipGetLastError();
+    return in_launches(s.units, [&](int64_t first, int64_t n) {
+        a.item0 = (int)first;
+        hipLaunchKernelGGL((attn_stream<D, FMT, BIAS, TERMS>), dim3((unsigned)n, (unsigned)s.rows_y), dim3(kWaves * kWave),
+                           lds, stream, a);
+        return hipGetLastError();
+    });
 }
 
 template <int D>
 hipError_t launch_join(StreamArgs a, int64_t max_q, hipStream_t stream) {
-    const int64_t heads = (int64_t)a.p.B * a.p.Hq;
-    a.join_rows = (int)std::max<int64_t>(1, std::min(max_q, kMaxGrid / heads));
-    constexpr int kGroups = kWaves * kWave / (D / 4);
-    a.spread = 1, a.log_spread = 0;
-    while (a.spread < kGroups && heads * a.join_rows * a.spread < 2048) a.spread *= 2, ++a.log_spread;
-    const int64_t per_block = kGroups / a.spread;
-    const unsigned grid = (unsigned)ceil_div(heads * a.join_rows, per_block);
-    hipLaunchKernelGGL((attn_join<D>), dim3(grid), dim3(kWaves * kWave), 0, stream, a);
-    return hipGetLastError();
+    const JoinPlan j = join_plan((int64_t)a.join_batch * a.p.Hq, D, max_q);
+    a.join_rows = (int)j.rows;
+    a.spread = j.spread, a.log_spread = j.log_spread;
+    a.by_batch = FastDiv(a.join_batch);
+    return in_launches(j.units, [&](int64_t first, int64_t n) {
+        a.join_unit0 = (int)first;
+        hipLaunchKernelGGL((attn_join<D>), dim3((unsigned)n), dim3(kWaves * kWave), 0, stream, a);
+        return hipGetLastError();
+    });
 }
 
 template <int D>
-hipError_t launch(const StreamArgs& a, int fmt, int64_t max_q, hipStream_t stream) {
+hipError_t launch(const StreamArgs& a, const StreamPlan& s, int fmt, int64_t max_q, hipStream_t stream) {
     const bool bias = a.p.softcap > 0.0f || a.p.alibi != nullptr, one = !two_terms(a.p);
     hipError_t e;
     if (fmt == kKvE5M2)
-        e = bias ? (one ? launch_stream<D, kKvE5M2, true, 1>(a, stream) : launch_stream<D, kKvE5M2, true, 2>(a, stream))
-                 : (one ? launch_stream<D, kKvE5M2, false, 1>(a, stream) : launch_stream<D, kKvE5M2, false, 2>(a, stream));
+        e = bias ? (one ? launch_stream<D, kKvE5M2, true, 1>(a, s, stream) : launch_stream<D, kKvE5M2, true, 2>(a, s, stream))
+                 : (one ? launch_stream<D, kKvE5M2, false, 1>(a, s, stream) : launch_stream<D, kKvE5M2, false, 2>(a, s, stream));
     else
-        e = bias ? (one ? launch_stream<D, kKvE4M3, true, 1>(a, stream) : launch_stream<D, kKvE4M3, true, 2>(a, stream))
-                 : (one ? launch_stream<D, kKvE4M3, false, 1>(a, stream) : launch_stream<D, kKvE4M3, false, 2>(a, stream));
+        e = bias ? (one ? launch_stream<D, kKvE4M3, true, 1>(a, s, stream) : launch_stream<D, kKvE4M3, true, 2>(a, s, stream))
+                 : (one ? launch_stream<D, kKvE4M3, false, 1>(a, s, stream) : launch_stream<D, kKvE4M3, false, 2>(a, s, stream));
     if (e != hipSuccess || a.shares == 0) return e;
     return launch_join<D>(a, max_q, stream);
 }
@@ -789,21 +756,20 @@ size_t attn_paged_ws_bytes(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int
     return (size_t)s.shares * Hkv * 2 * kCols * ((size_t)D * 4 + 8) + ((size_t)B + 1) * 4;
 }
 
-hipError_t launch_attn_join(const PagedAttn& p, int D, int splits, float* part_o, float2* part_ml, int64_t max_q,
-                            hipStream_t stream) {
+hipError_t launch_attn_join(const PagedAttn& p, int D, int splits, float* part_o, float2* part_ml, hipStream_t stream) {
     StreamArgs a = {};
     a.p = p;
     a.group = p.Hq / p.Hkv;
     a.splits = splits;
     a.part_o = part_o;
     a.part_ml = part_ml;
+    a.join_batch = 1;
     a.by_group = FastDiv(a.group);
     a.by_heads = FastDiv(p.Hq);
-    a.by_batch = FastDiv(p.B);
     switch (D) {
-        case 64: return launch_join<64>(a, max_q, stream);
-        case 128: return launch_join<128>(a, max_q, stream);
-        default: return launch_join<256>(a, max_q, stream);
+        case 64: return launch_join<64>(a, p.rows, stream);
+        case 128: return launch_join<128>(a, p.rows, stream);
+        default: return launch_join<256>(a, p.rows, stream);
     }
 }
 
@@ -828,13 +794,13 @@ hipError_t launch_attn_paged(const PagedAttn& p, int D, int fmt, int64_t max_q, 
     a.by_block = FastDiv(p.block);
     a.by_group = FastDiv(a.group);
     a.by_heads = FastDiv(p.Hq);
-    a.by_batch = FastDiv(p.B);
+    a.join_batch = p.B;
     a.by_head_groups = FastDiv(a.head_groups);
     const int64_t q = std::max<int64_t>(1, max_q);
     switch (D) {
-        case 64: return launch<64>(a, fmt, q, stream);
-        case 128: return launch<128>(a, fmt, q, stream);
-        default: return launch<256>(a, fmt, q, stream);
+        case 64: return launch<64>(a, s, fmt, q, stream);
+        case 128: return launch<128>(a, s, fmt, q, stream);
+        default: return launch<256>(a, s, fmt, q, stream);
     }
 }
 

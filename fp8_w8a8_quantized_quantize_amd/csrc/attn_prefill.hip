@@ -35,6 +35,7 @@
 #include <algorithm>
 
 #include "attn_common.hpp"
+#include "attn_plan.hpp"
 
 namespace fp8k {
 
@@ -44,18 +45,37 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr int kWavesT = 4;
 constexpr int kThreadsT = kWavesT * kWave;
-constexpr int kKeys = 64;  // keys of a tile
-constexpr int kTileCols = kWavesT * 32;  // query columns of a workgroup
+constexpr int kKeys = kTileKeys;
+static_assert(kTileCols == kWavesT * 32, "32 columns a wave");
 
 struct TileArgs {
     PagedAttn p;
     int group;
-    int col_tiles;  // planned per KV head; further ones are taken in turn
     int splits;     // workgroups that share a column tile's keys
+    int slots;      // of column tiles
+    int row_tiles;  // column tiles of one new row
+    int unit0;      // the launch's first of the units (slot, split, KV head)
     float* part_o;    // [rows][Hq][splits][D], with splits > 1
     float2* part_ml;  // [rows][Hq][splits]: reference (log2), sum
-    FastDiv by_block, by_group, by_kv_heads, by_batch, by_splits;
+    FastDiv by_block, by_group, by_kv_heads, by_splits, by_row_tiles;
+
+    // The first slot of sequence b, whose new rows start at `row`.
+    __device__ __forceinline__ int slot0(int row, int b) const { return (int)((uint32_t)min(row, p.rows) * group / kTileCols) + b; }
 };
+
+// The sequence that a slot is for: the last one that starts at or before it.
+// Starts rise with b, so a wave finds b by 64 probes a step.
+__device__ __forceinline__ int slot_sequence(const TileArgs& a, int slot, int lane) {
+    int b = 0;
+    for (int n = a.p.B; n > 1;) {  // one of n sequences from b on
+        const int step = (n + kWave - 1) / kWave, at = lane * step;
+        const uint64_t starts = __ballot(at < n && a.slot0(max(a.p.cu_q[b + min(at, n - 1)], 0), b + at) <= slot);
+        const int last = starts ? (kWave - 1 - __builtin_clzll(starts)) * step : 0;
+        b += last;
+        n = min(step, n - last);
+    }
+    return b;
+}
 
 // LDS rows are padded by 16 bytes, so that 32 neighbouring rows spread over the
 // banks.  V's channel d, byte d % VB of the piece that lane d / VB stages, is
@@ -103,331 +123,307 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int c = lane % 32, h = lane / 32;
-    // KV heads vary fastest (with 8 of them an XCD keeps to one head's keys), then sequences; every sequence's last column
-    // tiles, which see the most keys, come first.
-    const int rest = a.by_kv_heads.of(blockIdx.x), hk = blockIdx.x - rest * p.Hkv;
-    const int tile_split = a.by_batch.of(rest), b = rest - tile_split * p.B;
-    const int nth = a.by_splits.of(tile_split), split = tile_split - nth * a.splits;
+    // KV heads vary fastest (with 8 of them an XCD keeps to one head's keys); every sequence's last column tiles, which
+    // see the most keys, come first.
+    const int unit = a.unit0 + blockIdx.x;
+    const int rest = a.by_kv_heads.of(unit), hk = unit - rest * p.Hkv;
+    const int nth = a.by_splits.of(rest), split = rest - nth * a.splits;
+    const int slot = a.slots - 1 - nth;
+    const int b = p.cu_q ? slot_sequence(a, slot, lane) : a.by_row_tiles.of(slot);
     const Seq seq = sequence(p, b);
     const int prefix = p.prefix ? p.prefix[b] : 0;
     const int cols = seq.nq * a.group;
+    const int ct = slot - (p.cu_q ? a.slot0(seq.row0, b) : b * a.row_tiles);
+    if (ct < 0 || ct * kTileCols >= cols) return;  // before the first sequence, or past this one's tiles
     const uint32_t C = 2u * p.Hkv * D;
     const int32_t* table = p.block_table + (int64_t)b * p.ld_table;
     const int last_page = max(p.max_blocks - 1, 0);
     uint64_t* const rows = reinterpret_cast<uint64_t*>(tile_smem + Lds::kRows) + wave * 16;  // [tile % 2][4 waves][16]
     uint32_t* const there = reinterpret_cast<uint32_t*>(tile_smem + Lds::kMask);             // [tile % 4][4 waves]
 
-    const int rounds = cols > 0 ? (cols - 1) / (a.col_tiles * kTileCols) : 0;  // more than planned: taken in turn
-    for (int ct = rounds * a.col_tiles + a.col_tiles - 1 - nth; ct >= 0; ct -= a.col_tiles) {
-        if (ct * kTileCols >= cols) continue;
-        // this lane's column
-        const int col = ct * kTileCols + wave * 32 + c;
-        const bool has = col < cols;
-        const int qi = has ? a.by_group.of(col) : 0;
-        const int head = hk * a.group + (has ? col - qi * a.group : 0);
-        const int64_t row = seq.row0 + qi;
-        const int pos = seq.len - seq.nq + qi;
-        const float slope = p.alibi ? p.alibi[head] * kLog2e : 0.0f;
-        int lo, hi;
-        visible(p, seq, prefix, qi, lo, hi);
-        if (!has) lo = 0x7FFFFFFF, hi = 0;
-        // the keys any column of the workgroup sees, and of this wave
-        int tlo, thi, unused;
-        visible(p, seq, prefix, a.by_group.of(ct * kTileCols), tlo, unused);
-        visible(p, seq, prefix, a.by_group.of(min(cols - 1, ct * kTileCols + kTileCols - 1)), unused, thi);
-        thi = max(thi, 0);
-        tlo = min(tlo, thi);
-        const int base = p.window > 0 ? tlo / kKeys * kKeys : 0;
-        const int all = thi > base ? (thi - base + kKeys - 1) / kKeys : 0;
-        const int first = (int)((int64_t)all * split / a.splits), tiles = (int)((int64_t)all * (split + 1) / a.splits);
-        int wlo = lo, whi = hi;
+    // the keys any column of the workgroup sees
+    int tlo, thi, unused;
+    visible(p, seq, prefix, a.by_group.of(ct * kTileCols), tlo, unused);
+    visible(p, seq, prefix, a.by_group.of(min(cols - 1, ct * kTileCols + kTileCols - 1)), unused, thi);
+    thi = max(thi, 0);
+    tlo = min(tlo, thi);
+    const int base = p.window > 0 ? tlo / kKeys * kKeys : 0;
+    const int all = thi > base ? (thi - base + kKeys - 1) / kKeys : 0;
+    const int first = a.by_splits.of(all * split), tiles = a.by_splits.of(all * (split + 1));  // 2^24 tiles, 64 shares at most
+    // this lane's column
+    const int col = ct * kTileCols + wave * 32 + c;
+    const bool has = col < cols;
+    const int qi = has ? a.by_group.of(col) : 0;
+    const int head = hk * a.group + (has ? col - qi * a.group : 0);
+    const int64_t row = seq.row0 + qi;
+    const int pos = seq.len - seq.nq + qi;
+    const float slope = p.alibi ? p.alibi[head] * kLog2e : 0.0f;
+    int lo, hi;
+    visible(p, seq, prefix, qi, lo, hi);
+    if (!has) lo = 0x7FFFFFFF, hi = 0;
+    int wlo = lo, whi = hi;  // the keys any column of this wave sees
 #pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            wlo = min(wlo, __shfl_xor(wlo, off, kWave));
-            whi = max(whi, __shfl_xor(whi, off, kWave));
-        }
-        wlo = __builtin_amdgcn_readfirstlane(wlo);
-        whi = __builtin_amdgcn_readfirstlane(whi);
+    for (int off = 1; off < 64; off <<= 1) {
+        wlo = min(wlo, __shfl_xor(wlo, off, kWave));
+        whi = max(whi, __shfl_xor(whi, off, kWave));
+    }
+    wlo = __builtin_amdgcn_readfirstlane(wlo);
+    whi = __builtin_amdgcn_readfirstlane(whi);
 
-        // q times the key scales, in fp16 terms
-        v8h qt[TERMS][NK];
-        float cs;
-        {
-            float x[NK][8], top = 0.0f;
+    // q times the key scales, in fp16 terms
+    v8h qt[TERMS][NK];
+    float cs;
+    {
+        float x[NK][8], top = 0.0f;
 #pragma unroll
-            for (int st = 0; st < NK; ++st) {
-                v4u raw[2];
-                load_q8<TERMS>(p, row * p.ldq + (int64_t)head * D + 16 * st + 8 * h, raw);
-                unpack_q8<TERMS>(p, raw, x[st]);
-                const float4* ks = reinterpret_cast<const float4*>(p.scales + hk * D + 16 * st + 8 * h);
-                const float4 k0 = ks[0], k1 = ks[1];
-                const float k[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+        for (int st = 0; st < NK; ++st) {
+            v4u raw[2];
+            load_q8<TERMS>(p, row * p.ldq + (int64_t)head * D + 16 * st + 8 * h, raw);
+            unpack_q8<TERMS>(p, raw, x[st]);
+            const float4* ks = reinterpret_cast<const float4*>(p.scales + hk * D + 16 * st + 8 * h);
+            const float4 k0 = ks[0], k1 = ks[1];
+            const float k[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[st][e] *= fmaxf(k[e], kScaleFloor);
-                    top = fmaxf(top, fabsf(x[st][e]));
-                }
+            for (int e = 0; e < 8; ++e) {
+                x[st][e] *= fmaxf(k[e], kScaleFloor);
+                top = fmaxf(top, fabsf(x[st][e]));
             }
-            top = fmaxf(top, swap32(top));
-            const int shift = 15 - __builtin_amdgcn_frexp_expf(top);
-#pragma unroll
-            for (int st = 0; st < NK; ++st)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float y = __builtin_amdgcn_ldexpf(x[st][e], shift);
-                    qt[0][st][e] = (_Float16)y;
-                    if constexpr (TERMS == 2) qt[TERMS - 1][st][e] = (_Float16)(y - (float)qt[0][st][e]);
-                }
-            cs = __builtin_amdgcn_ldexpf(p.scale, -shift);
         }
-        if (p.softcap > 0.0f) cs *= kLn2;  // the cap takes the natural score
-        const float cap_in = p.softcap > 0.0f ? 2.0f * kLog2e / p.softcap : 0.0f;
+        top = fmaxf(top, swap32(top));
+        const int shift = 15 - __builtin_amdgcn_frexp_expf(top);
+#pragma unroll
+        for (int st = 0; st < NK; ++st)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float y = __builtin_amdgcn_ldexpf(x[st][e], shift);
+                qt[0][st][e] = (_Float16)y;
+                if constexpr (TERMS == 2) qt[TERMS - 1][st][e] = (_Float16)(y - (float)qt[0][st][e]);
+            }
+        cs = __builtin_amdgcn_ldexpf(p.scale, -shift);
+    }
+    if (p.softcap > 0.0f) cs *= kLn2;  // the cap takes the natural score
+    const float cap_in = p.softcap > 0.0f ? 2.0f * kLog2e / p.softcap : 0.0f;
 
-        float m = 0.0f, l = 0.0f, limit = kNoRef;
-        v16f o[DB];
+    float m = 0.0f, l = 0.0f, limit = kNoRef;
+    v16f o[DB];
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
+    for (int d = 0; d < DB; ++d)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+        for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
 
-        // ---- staging.  A wave stages keys 16 wave .. + 15 of a tile: K, a quarter row per thread; V, the eight keys of
-        // two lane groups, VB channels per thread.
-        auto page_of = [&](int t) { return table[min(a.by_block.of(base + t * kKeys + 16 * wave + lane % 16), last_page)]; };
-        // cache offsets of the wave's 16 rows of tile t, 0 for keys that are not there
-        auto rows_of = [&](int t, int page) {
-            const int key = base + t * kKeys + 16 * wave + lane % 16;
-            const bool ok = key >= tlo && key < thi && page >= 0 && page < p.num_blocks;
-            const uint32_t r = ok ? (page - a.by_block.of(key)) * p.block + key : 0;
-            if (lane < 16) rows[t % 2 * kKeys + lane] = (uint64_t)r * C;
-            const uint32_t mask = (uint32_t)__ballot(ok) & 0xFFFFu;
-            if (lane == 0) there[t % 4 * kWavesT + wave] = mask;
-            __builtin_amdgcn_wave_barrier();
-            return mask;
-        };
-        v4u kreg[D / 64];
-        vpiece vreg[8];
-        auto load_k = [&](int t) {
-            const uint8_t* src = p.cache + rows[t % 2 * kKeys + lane / 4] + hk * D + lane % 4 * (D / 4);
+    // ---- staging.  A wave stages keys 16 wave .. + 15 of a tile: K, a quarter row per thread; V, the eight keys of
+    // two lane groups, VB channels per thread.
+    auto page_of = [&](int t) { return table[min(a.by_block.of(base + t * kKeys + 16 * wave + lane % 16), last_page)]; };
+    // cache offsets of the wave's 16 rows of tile t, 0 for keys that are not there
+    auto rows_of = [&](int t, int page) {
+        const int key = base + t * kKeys + 16 * wave + lane % 16;
+        const bool ok = key >= tlo && key < thi && page >= 0 && page < p.num_blocks;
+        const uint32_t r = ok ? (page - a.by_block.of(key)) * p.block + key : 0;
+        if (lane < 16) rows[t % 2 * kKeys + lane] = (uint64_t)r * C;
+        const uint32_t mask = (uint32_t)__ballot(ok) & 0xFFFFu;
+        if (lane == 0) there[t % 4 * kWavesT + wave] = mask;
+        __builtin_amdgcn_wave_barrier();
+        return mask;
+    };
+    v4u kreg[D / 64];
+    vpiece vreg[8];
+    auto load_k = [&](int t) {
+        const uint8_t* src = p.cache + rows[t % 2 * kKeys + lane / 4] + hk * D + lane % 4 * (D / 4);
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) kreg[i] = *reinterpret_cast<const v4u*>(src + 16 * i);
-        };
-        auto load_v = [&](int t) {
-            const uint8_t* src = p.cache + (int64_t)(p.Hkv + hk) * D + c * VB;
+        for (int i = 0; i < D / 64; ++i) kreg[i] = *reinterpret_cast<const v4u*>(src + 16 * i);
+    };
+    auto load_v = [&](int t) {
+        const uint8_t* src = p.cache + (int64_t)(p.Hkv + hk) * D + c * VB;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            vreg[e] = *reinterpret_cast<const vpiece*>(src + rows[t % 2 * kKeys + 8 * (e / 4) + 4 * h + e % 4]);
+    };
+    auto store_k = [&](int t) {
+        uint8_t* dst = tile_smem + t % 2 * Lds::kKTile + (16 * wave + lane / 4) * Lds::kKRow;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int unit = (lane % 4 * (D / 64) + i) * 2 + k;
+                *reinterpret_cast<v8h*>(dst + unit * 16) =
+                    row_f16<FMT>(kreg[i][2 * k], kreg[i][2 * k + 1]);
+            }
+    };
+    auto vword = [&](int e, int i) -> uint32_t {
+        if constexpr (D == 256)
+            return vreg[e][i];
+        else
+            return vreg[e];
+    };
+    auto store_v = [&](int t, uint32_t mask) {
+        uint8_t* const dst = tile_smem + Lds::kV + t % 2 * Lds::kVTile;
+        if (mask != 0xFFFFu) {
+            // a code behind the sequence may be anything, NaN too: 0 * NaN must not reach the sum
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                vreg[e] = *reinterpret_cast<const vpiece*>(src + rows[t % 2 * kKeys + 8 * (e / 4) + 4 * h + e % 4]);
-        };
-        auto store_k = [&](int t) {
-            uint8_t* dst = tile_smem + t % 2 * Lds::kKTile + (16 * wave + lane / 4) * Lds::kKRow;
+                vreg[e] = ((mask >> (8 * (e / 4) + 4 * h + e % 4)) & 1u) ? vreg[e] : vpiece(0);
+        }
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i)
+        for (int j = 0; j < VB; ++j) {
+            v4u r;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int unit = (lane % 4 * (D / 64) + i) * 2 + k;
-                    *reinterpret_cast<v8h*>(dst + unit * 16) =
-                        row_f16<FMT>(kreg[i][2 * k], kreg[i][2 * k + 1]);
-                }
-        };
-        auto vword = [&](int e, int i) -> uint32_t {
-            if constexpr (D == 256)
-                return vreg[e][i];
+            for (int i = 0; i < 4; ++i) r[i] = pair_f16<FMT>(vword(2 * i, j / 4), vword(2 * i + 1, j / 4), j % 4);
+            *reinterpret_cast<v4u*>(dst + (32 * j + c) * Lds::kVRow + (2 * wave + h) * 16) = r;
+        }
+    };
+    v16f s[2];
+    auto scores = [&](int t) {
+        const uint8_t* src = tile_smem + t % 2 * Lds::kKTile + c * Lds::kKRow + h * 16;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) s[j / 16][j % 16] = 0.0f;
+#pragma unroll
+        for (int st = 0; st < NK; ++st)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const v8h k = *reinterpret_cast<const v8h*>(src + 32 * kb * Lds::kKRow + 32 * st);
+#pragma unroll
+                for (int x = 0; x < TERMS; ++x) s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, qt[x][st], s[kb], 0, 0, 0);
+            }
+        reads_ahead<2 * NK, TERMS, 4>();
+    };
+    // key of a lane's score j, less 4 h
+    auto key_of = [](int j) { return 32 * (j / 16) + 8 * (j % 16 / 4) + j % 4; };
+    // Scores of tile t above the reference, in place.
+    auto above = [&](int t, uint64_t mask) {
+        const int key0 = base + t * kKeys;
+        if constexpr (BIAS) {
+            if (p.softcap > 0.0f) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) s[j / 16][j % 16] = kLog2e * soft_cap<TERMS>(s[j / 16][j % 16] * cs, p.softcap, cap_in);
+            }
+            const float by = p.softcap > 0.0f ? 1.0f : cs, dist = (float)(key0 + 4 * h - pos);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                s[j / 16][j % 16] = __builtin_fmaf(slope, dist + (float)key_of(j), __builtin_fmaf(s[j / 16][j % 16], by, -m));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j / 16][j % 16] = __builtin_fmaf(s[j / 16][j % 16], cs, -m);
+        }
+        if (mask != ~0ull || __any(key0 < lo || key0 + kKeys > hi)) {
+            const uint64_t mine = mask >> (4 * h);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const int key = key0 + 4 * h + key_of(j);
+                const bool see = ((mine >> key_of(j)) & 1u) & (key >= lo) & (key < hi);
+                s[j / 16][j % 16] = see ? s[j / 16][j % 16] : -INFINITY;
+            }
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int j = 1; j < 32; ++j) top = fmaxf(top, s[j / 16][j % 16]);
+        if (__any(top > limit)) {
+            // Move the references of the columns that need it to the largest score, less the shift (scores past 2^24
+            // are themselves too coarse for it).  A column without a reference has m = 0 and no sum yet.
+            top = fmaxf(top, swap32(top));
+            const bool move = top > limit;
+            const float by = move ? (fabsf(top + m) < 16777216.0f ? top - P::kShift : top) : 0.0f;
+            const float f = limit == P::kLimit ? __builtin_amdgcn_exp2f(-by) : 1.0f;
+            m += by;
+            limit = move ? P::kLimit : limit;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DB; ++d) o[d] *= f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j / 16][j % 16] -= by;
+        }
+    };
+    // p and its product with V, 16 keys at a time
+    auto product = [&](int t) {
+        const uint8_t* src = tile_smem + Lds::kV + t % 2 * Lds::kVTile + c * Lds::kVRow + h * 16;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            v8h ph[TERMS];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float y = P::p(s[u / 2][8 * (u % 2) + e]);
+                l += y;
+                ph[0][e] = (_Float16)y;
+                if constexpr (TERMS == 2) ph[TERMS - 1][e] = (_Float16)(y - (float)ph[0][e]);
+            }
+#pragma unroll
+            for (int db = 0; db < DB; ++db) {
+                const v8h v = *reinterpret_cast<const v8h*>(src + 32 * db * Lds::kVRow + 32 * u);
+#pragma unroll
+                for (int x = 0; x < TERMS; ++x) o[db] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, ph[x], o[db], 0, 0, 0);
+            }
+        }
+        reads_ahead<4 * DB, TERMS, 4>();
+    };
+    auto mask_of = [&](int t) {
+        const uint32_t* w = there + t % 4 * kWavesT;
+        const uint32_t lo32 = w[0] | (w[1] << 16), hi32 = w[2] | (w[3] << 16);
+        return ((uint64_t)__builtin_amdgcn_readfirstlane(hi32) << 32) | (uint32_t)__builtin_amdgcn_readfirstlane(lo32);
+    };
+
+    if (tiles > first) {
+        auto sees = [&](int t) { return base + t * kKeys < whi && base + (t + 1) * kKeys > wlo; };
+        uint32_t m0 = rows_of(first, page_of(first));
+        int page = page_of(first + 1);
+        load_k(first);
+        load_v(first);
+        for (int t = first; t < tiles; ++t) {
+            store_k(t);
+            store_v(t, m0);
+            m0 = rows_of(t + 1, page);
+            page = page_of(t + 2);
+            load_k(t + 1);
+            load_v(t + 1);
+            __syncthreads();
+            if (sees(t)) {
+                scores(t);
+                above(t, mask_of(t));
+                product(t);
+            }
+        }
+    }
+
+    // ---- results
+    l += swap32(l);
+    if (has) {
+        const int64_t at = (row * p.Hq + head) * a.splits + split;
+        if (a.splits > 1 && h == 0) a.part_ml[at] = make_float2(limit == P::kLimit ? m : kNoRef, l);
+#pragma unroll
+        for (int x = 0; x < 16 * DB; x += 4) {
+            // four channels in a row: elements x .. x + 3 of [row][block]
+            const float4 r = make_float4(o[x % DB][x / DB], o[(x + 1) % DB][(x + 1) / DB], o[(x + 2) % DB][(x + 2) / DB],
+                                         o[(x + 3) % DB][(x + 3) / DB]);
+            const int i = x / DB, d = (8 * (i / 4) + 4 * h + i % 4) * VB + x % DB;
+            if (a.splits > 1)
+                *reinterpret_cast<float4*>(a.part_o + at * D + d) = r;
             else
-                return vreg[e];
-        };
-        auto store_v = [&](int t, uint32_t mask) {
-            uint8_t* const dst = tile_smem + Lds::kV + t % 2 * Lds::kVTile;
-            if (mask != 0xFFFFu) {
-                // a code behind the sequence may be anything, NaN too: 0 * NaN must not reach the sum
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    vreg[e] = ((mask >> (8 * (e / 4) + 4 * h + e % 4)) & 1u) ? vreg[e] : vpiece(0);
-            }
-#pragma unroll
-            for (int j = 0; j < VB; ++j) {
-                v4u r;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) r[i] = pair_f16<FMT>(vword(2 * i, j / 4), vword(2 * i + 1, j / 4), j % 4);
-                *reinterpret_cast<v4u*>(dst + (32 * j + c) * Lds::kVRow + (2 * wave + h) * 16) = r;
-            }
-        };
-        v16f s[2];
-        auto scores = [&](int t) {
-            const uint8_t* src = tile_smem + t % 2 * Lds::kKTile + c * Lds::kKRow + h * 16;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[j / 16][j % 16] = 0.0f;
-#pragma unroll
-            for (int st = 0; st < NK; ++st)
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    const v8h k = *reinterpret_cast<const v8h*>(src + 32 * kb * Lds::kKRow + 32 * st);
-#pragma unroll
-                    for (int x = 0; x < TERMS; ++x) s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, qt[x][st], s[kb], 0, 0, 0);
-                }
-            reads_ahead<2 * NK, TERMS, 4>();
-        };
-        // key of a lane's score j, less 4 h
-        auto key_of = [](int j) { return 32 * (j / 16) + 8 * (j % 16 / 4) + j % 4; };
-        // Scores of tile t above the reference, in place.
-        auto above = [&](int t, uint64_t mask) {
-            const int key0 = base + t * kKeys;
-            if constexpr (BIAS) {
-                if (p.softcap > 0.0f) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) s[j / 16][j % 16] = kLog2e * soft_cap<TERMS>(s[j / 16][j % 16] * cs, p.softcap, cap_in);
-                }
-                const float by = p.softcap > 0.0f ? 1.0f : cs, dist = (float)(key0 + 4 * h - pos);
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    s[j / 16][j % 16] = __builtin_fmaf(slope, dist + (float)key_of(j), __builtin_fmaf(s[j / 16][j % 16], by, -m));
-            } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) s[j / 16][j % 16] = __builtin_fmaf(s[j / 16][j % 16], cs, -m);
-            }
-            if (mask != ~0ull || __any(key0 < lo || key0 + kKeys > hi)) {
-                const uint64_t mine = mask >> (4 * h);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int key = key0 + 4 * h + key_of(j);
-                    const bool see = ((mine >> key_of(j)) & 1u) & (key >= lo) & (key < hi);
-                    s[j / 16][j % 16] = see ? s[j / 16][j % 16] : -INFINITY;
-                }
-            }
-            float top = s[0][0];
-#pragma unroll
-            for (int j = 1; j < 32; ++j) top = fmaxf(top, s[j / 16][j % 16]);
-            if (__any(top > limit)) {
-                // Move the references of the columns that need it to the largest score, less the shift (scores past 2^24
-                // are themselves too coarse for it).  A column without a reference has m = 0 and no sum yet.
-                top = fmaxf(top, swap32(top));
-                const bool move = top > limit;
-                const float by = move ? (fabsf(top + m) < 16777216.0f ? top - P::kShift : top) : 0.0f;
-                const float f = limit == P::kLimit ? __builtin_amdgcn_exp2f(-by) : 1.0f;
-                m += by;
-                limit = move ? P::kLimit : limit;
-                l *= f;
-#pragma unroll
-                for (int d = 0; d < DB; ++d) o[d] *= f;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) s[j / 16][j % 16] -= by;
-            }
-        };
-        // p and its product with V, 16 keys at a time
-        auto product = [&](int t) {
-            const uint8_t* src = tile_smem + Lds::kV + t % 2 * Lds::kVTile + c * Lds::kVRow + h * 16;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                v8h ph[TERMS];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float y = P::p(s[u / 2][8 * (u % 2) + e]);
-                    l += y;
-                    ph[0][e] = (_Float16)y;
-                    if constexpr (TERMS == 2) ph[TERMS - 1][e] = (_Float16)(y - (float)ph[0][e]);
-                }
-#pragma unroll
-                for (int db = 0; db < DB; ++db) {
-                    const v8h v = *reinterpret_cast<const v8h*>(src + 32 * db * Lds::kVRow + 32 * u);
-#pragma unroll
-                    for (int x = 0; x < TERMS; ++x) o[db] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, ph[x], o[db], 0, 0, 0);
-                }
-            }
-            reads_ahead<4 * DB, TERMS, 4>();
-        };
-        auto mask_of = [&](int t) {
-            const uint32_t* w = there + t % 4 * kWavesT;
-            const uint32_t lo32 = w[0] | (w[1] << 16), hi32 = w[2] | (w[3] << 16);
-            return ((uint64_t)__builtin_amdgcn_readfirstlane(hi32) << 32) | (uint32_t)__builtin_amdgcn_readfirstlane(lo32);
-        };
-
-        if (tiles > first) {
-            auto sees = [&](int t) { return base + t * kKeys < whi && base + (t + 1) * kKeys > wlo; };
-            uint32_t m0 = rows_of(first, page_of(first));
-            int page = page_of(first + 1);
-            load_k(first);
-            load_v(first);
-            for (int t = first; t < tiles; ++t) {
-                store_k(t);
-                store_v(t, m0);
-                m0 = rows_of(t + 1, page);
-                page = page_of(t + 2);
-                load_k(t + 1);
-                load_v(t + 1);
-                __syncthreads();
-                if (sees(t)) {
-                    scores(t);
-                    above(t, mask_of(t));
-                    product(t);
-                }
-            }
+                write_row(p, row, head, hk, D, d, m, l, r);
         }
-
-        // ---- results
-        l += swap32(l);
-        if (has) {
-            const int64_t at = (row * p.Hq + head) * a.splits + split;
-            if (a.splits > 1 && h == 0) a.part_ml[at] = make_float2(limit == P::kLimit ? m : kNoRef, l);
-#pragma unroll
-            for (int x = 0; x < 16 * DB; x += 4) {
-                // four channels in a row: elements x .. x + 3 of [row][block]
-                const float4 r = make_float4(o[x % DB][x / DB], o[(x + 1) % DB][(x + 1) / DB], o[(x + 2) % DB][(x + 2) / DB],
-                                             o[(x + 3) % DB][(x + 3) / DB]);
-                const int i = x / DB, d = (8 * (i / 4) + 4 * h + i % 4) * VB + x % DB;
-                if (a.splits > 1)
-                    *reinterpret_cast<float4*>(a.part_o + at * D + d) = r;
-                else
-                    write_row(p, row, head, hk, D, d, m, l, r);
-            }
-        }
-        __syncthreads();
     }
 }
 
 template <int D, int FMT, bool BIAS, int TERMS>
-hipError_t launch_tile(const TileArgs& a, dim3 grid, hipStream_t stream) {
+hipError_t launch_tile(TileArgs a, int64_t units, hipStream_t stream) {
     constexpr int lds = TileLds<D>::kBytes;
     if constexpr (lds > 64 * 1024) {
         const hipError_t e = FP8K_SET_LDS((attn_tile<D, FMT, BIAS, TERMS>), lds);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((attn_tile<D, FMT, BIAS, TERMS>), grid, dim3(kThreadsT), lds, stream, a);
-    return hipGetLastError();
+    return in_launches(units, [&](int64_t first, int64_t n) {
+        a.unit0 = (int)first;
+        hipLaunchKernelGGL((attn_tile<D, FMT, BIAS, TERMS>), dim3((unsigned)n), dim3(kThreadsT), lds, stream, a);
+        return hipGetLastError();
+    });
 }
 
 template <int D, int TERMS>
-hipError_t launch(TileArgs a, int fmt, int64_t max_q, hipStream_t stream) {
-    const int64_t tiles = (max_q * a.group + kTileCols - 1) / kTileCols, per_tile = (int64_t)a.p.B * a.p.Hkv;
-    a.col_tiles = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, (int64_t(1) << 30) / (per_tile * a.splits)));
-    const dim3 grid((unsigned)(a.col_tiles * per_tile * a.splits));
+hipError_t launch(const TileArgs& a, int64_t units, int fmt, hipStream_t stream) {
     const bool bias = a.p.softcap > 0.0f || a.p.alibi != nullptr;
     if (fmt == kKvE5M2)
-        return bias ? launch_tile<D, kKvE5M2, true, TERMS>(a, grid, stream) : launch_tile<D, kKvE5M2, false, TERMS>(a, grid, stream);
-    return bias ? launch_tile<D, kKvE4M3, true, TERMS>(a, grid, stream) : launch_tile<D, kKvE4M3, false, TERMS>(a, grid, stream);
+        return bias ? launch_tile<D, kKvE5M2, true, TERMS>(a, units, stream) : launch_tile<D, kKvE5M2, false, TERMS>(a, units, stream);
+    return bias ? launch_tile<D, kKvE4M3, true, TERMS>(a, units, stream) : launch_tile<D, kKvE4M3, false, TERMS>(a, units, stream);
 }
 
 }  // namespace
-
-// Workgroups that share a column tile's keys: as many as the card holds at once
-// (two a CU, one with D = 256), where column tiles alone are fewer, each with at
-// least 4 key tiles.  64 tokens over 16384 keys, 64 / 8 heads of 128: 59 us with
-// one round of workgroups, 67 and 76 with one and a half and two (a second
-// round that is not full), 367 without shares.  At 2048 keys: 27 us with 2 key
-// tiles at least, 21 with 4, 25 with 8.  With long keys also two or three, where
-// that leaves rounds fuller by a tenth or more (560 tokens: 527 us without, 404
-// with 3; 1100: 903 and 749); at 2048 keys their parts cost what that gains (83
-// and 85, 151 and 162).
-static int64_t tile_splits(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_len) {
-    const int64_t group = Hq / Hkv, planned = B * ((max_q * group + kTileCols - 1) / kTileCols);
-    const int64_t full = rows * group / kTileCols;  // at least; `planned` may come from too small a max_q
-    const int64_t tiles = std::max<int64_t>(1, std::max(full, std::min(planned, full + B)) * Hkv);
-    const int64_t fill = D == 256 ? 256 : 512;
-    int64_t s = std::max<int64_t>(1, std::min<int64_t>({fill / tiles, 64, max_len / (4 * kKeys)}));
-    if (max_len >= 4096) {
-        auto rounds = [&](int64_t n) { return (tiles * n + fill - 1) / fill; };
-        for (int64_t n = s + 1; n <= 3; ++n)
-            if (10 * rounds(n) * s < 9 * rounds(s) * n) s = n;
-    }
-    return s;
-}
 
 size_t attn_tiled_ws_bytes(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_len) {
     const int64_t splits = tile_splits(B, rows, Hq, Hkv, D, max_q, max_len);
@@ -439,23 +435,26 @@ hipError_t launch_attn_tiled(const PagedAttn& p, int D, int fmt, int64_t max_q, 
     TileArgs a = {};
     a.p = p;
     a.group = p.Hq / p.Hkv;
-    a.splits = (int)tile_splits(p.B, p.rows, p.Hq, p.Hkv, D, max_q, max_len);
+    const TilePlan t = tile_plan(p.B, p.rows, p.Hq, p.Hkv, D, p.cu_q == nullptr, max_q, max_len);
+    a.splits = (int)t.splits;
+    a.slots = (int)t.slots;
+    a.row_tiles = (int)ceil_div(a.group, kTileCols);
     a.part_o = static_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)a.splits * p.rows * p.Hq * D);
     a.by_block = FastDiv(p.block);
     a.by_group = FastDiv(a.group);
     a.by_kv_heads = FastDiv(p.Hkv);
-    a.by_batch = FastDiv(p.B);
     a.by_splits = FastDiv(a.splits);
+    a.by_row_tiles = FastDiv(a.row_tiles);
     const bool one = !two_terms(p);
     hipError_t e;
     switch (D) {
-        case 64: e = one ? launch<64, 1>(a, fmt, max_q, stream) : launch<64, 2>(a, fmt, max_q, stream); break;
-        case 128: e = one ? launch<128, 1>(a, fmt, max_q, stream) : launch<128, 2>(a, fmt, max_q, stream); break;
-        default: e = one ? launch<256, 1>(a, fmt, max_q, stream) : launch<256, 2>(a, fmt, max_q, stream);
+        case 64: e = one ? launch<64, 1>(a, t.units, fmt, stream) : launch<64, 2>(a, t.units, fmt, stream); break;
+        case 128: e = one ? launch<128, 1>(a, t.units, fmt, stream) : launch<128, 2>(a, t.units, fmt, stream); break;
+        default: e = one ? launch<256, 1>(a, t.units, fmt, stream) : launch<256, 2>(a, t.units, fmt, stream);
     }
     if (e != hipSuccess || a.splits == 1) return e;
-    return launch_attn_join(p, D, a.splits, a.part_o, a.part_ml, max_q, stream);
+    return launch_attn_join(p, D, a.splits, a.part_o, a.part_ml, stream);
 }
 
 }  // namespace fp8k

@@ -109,8 +109,7 @@ hipError_t launch_attn_tiled(const PagedAttn& p, int D, int fmt, int64_t max_q, 
                              hipStream_t stream);
 // Output rows from `splits` parts each: part_o [rows][Hq][splits][D], part_ml
 // (reference in log2, sum) [rows][Hq][splits].
-hipError_t launch_attn_join(const PagedAttn& p, int D, int splits, float* part_o, float2* part_ml, int64_t max_q,
-                            hipStream_t stream);
+hipError_t launch_attn_join(const PagedAttn& p, int D, int splits, float* part_o, float2* part_ml, hipStream_t stream);
 
 // The dense GEMM launchers write BF16 y, or, when y32 is not null, the fp32
 // value acc * (s_tok * s_ch) before rounding to y32 (same row stride ldy).

@@ -1,0 +1,124 @@
+"""How the attention calls are divided into workgroups, on the host: grids that the runtime takes (less than 2^32
+threads along an axis) at every size the entry points accept, whatever the launch hints say, and slots that hold every
+column tile of a ragged batch."""
+import ctypes
+import os
+import random
+import subprocess
+import tempfile
+
+import pytest
+
+_HERE = os.path.dirname(os.path.abspath(__file__))
+_lib = None
+THREADS, MAX_ATTN = 256, 1 << 30
+
+
+def lib():
+    global _lib
+    if _lib is None:
+        out = os.path.join(tempfile.mkdtemp(prefix="fp8planpin_"), "libplan_pin.so")
+        subprocess.run(["g++", "-O2", "-fPIC", "-shared", "-std=c++17", "-Wall", "-Werror",
+                        os.path.join(_HERE, "pins", "attn_plan_pin.cpp"), "-o", out], check=True)
+        _lib = ctypes.CDLL(out)
+    return _lib
+
+
+def plan(fn, *args):
+    out = (ctypes.c_int64 * 4)()
+    getattr(lib(), fn)(*[ctypes.c_int64(int(a)) for a in args], out)
+    return list(out)
+
+
+def launches(units):
+    """A kernel's workgroups, in launches that the runtime takes."""
+    assert 1 <= units < 1 << 31
+    n, total, largest = plan("pin_launches", units)[:3]
+    assert total == units and largest * THREADS < 1 << 32
+    assert n == -(-units // (((1 << 32) - 1) // THREADS))
+    return n
+
+
+def check(B, rows, Hq, Hkv, D, max_q, max_len, all_len, decode):
+    """Every launch that the call may make."""
+    what = (B, rows, Hq, Hkv, D, max_q, max_len, all_len, decode)
+    units, y, shares = plan("pin_stream", B, rows, Hq, Hkv, D, max_q, max_len, all_len)[:3]
+    assert 1 <= y <= 65535 and (y == 1 or not shares), what
+    launches(units)
+    units, slots, splits = plan("pin_tiled", B, rows, Hq, Hkv, D, decode, max_q, max_len)[:3]
+    assert units == slots * Hkv * splits, what
+    launches(units)
+    for heads, q in ((B * Hq, max_q), (Hq, rows)):
+        units, per, spread = plan("pin_join", heads, D, q)[:3]
+        launches(units)
+        assert 1 <= per <= q and units * (THREADS // (D // 4)) // spread >= heads * per, what
+    return slots * Hkv
+
+
+@pytest.mark.parametrize("T,B", [(65536, 512), (131072, 256), (32768, 1024)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_ragged_batches_without_a_hint(T, B, D):
+    """An unknown max_q counts as T; the launch is as large as the batch all the same."""
+    tiles = check(B, T, 64, 8, D, T, 4096, 4096, False)
+    assert tiles <= (T * 8 // 128 + B) * 8
+
+
+@pytest.mark.parametrize("B,rows,Hq,Hkv,max_q,all_len", [
+    (1 << 26, 1 << 26, 1, 1, 1, 1), (1 << 26, 1 << 26, 1, 1, 1 << 26, 1 << 30), (1 << 25, 1 << 25, 2, 1, 1, 700),
+    (1 << 25, 1 << 25, 2, 2, 1, 1 << 30), (1024, 1 << 14, 1 << 16, 65535 // 3, 1 << 14, 1 << 20), (1, 1 << 30, 1, 1, 1 << 30, 1 << 30),
+    (1 << 10, 1 << 14, 1 << 16, 1 << 15, 1, 64), (1 << 26, 1, 1, 1, 1, 1 << 30), (1, 1, 1 << 22, 1, 1, 1 << 30)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_largest_sizes(B, rows, Hq, Hkv, max_q, all_len, D):
+    Hq = Hq // Hkv * Hkv
+    for max_len in (1, min(700, all_len), all_len):
+        for decode in (False, True):
+            check(B, rows, Hq, Hkv, D, max_q, max_len, all_len, decode)
+
+
+def test_any_accepted_size():
+    rng = random.Random(5)
+
+    def upto(n):
+        return min(n, 1 << rng.randint(0, max(0, n.bit_length() - 1))) + rng.randint(0, 3)
+
+    for _ in range(20000):
+        D = rng.choice([64, 128, 256])
+        B = min(upto(1 << 26), 1 << 26)
+        Hq = max(1, min(upto((1 << 26) // B), (1 << 26) // B, MAX_ATTN // D))
+        Hkv = rng.choice([d for d in range(1, min(Hq, 65535) + 1) if Hq % d == 0][:40])
+        decode = rng.random() < 0.4
+        rows = B if decode else max(1, min(upto(MAX_ATTN // Hq), MAX_ATTN // Hq))
+        all_len = min(upto(MAX_ATTN), MAX_ATTN)
+        max_q = 1 if decode else rng.choice([rows, min(rows, upto(rows)), 1])
+        check(B, rows, Hq, Hkv, D, max_q, min(all_len, upto(all_len)), all_len, decode)
+
+
+def test_slots_hold_every_column_tile():
+    """The kernel's arithmetic: sequence b's slots start at floor(cu[b] * group / 128) + b; the last sequence that starts
+    at or before a slot owns it."""
+    rng = random.Random(7)
+    for _ in range(300):
+        B, group = rng.randint(1, 90), rng.choice([1, 2, 3, 8, 16, 127, 128, 129, 300])
+        new = [rng.choice([0, 0, 1, 2, rng.randint(0, 40), rng.randint(0, 700)]) for _ in range(B)]
+        first = rng.choice([0, 0, 5])
+        cu = [first]
+        for n in new:
+            cu.append(cu[-1] + n)
+        rows = cu[-1] + rng.choice([0, 0, 9])
+        slots = plan("pin_tiled", B, max(rows, 1), group, 1, 128, False, max(rows, 1), 4096)[1]
+        starts = [c * group // 128 + b for b, c in enumerate(cu[:-1])]
+        seen = set()
+        for slot in range(slots):
+            own = [b for b in range(B) if starts[b] <= slot]
+            if not own:
+                continue
+            b, ct = own[-1], slot - starts[own[-1]]
+            if ct * 128 < new[b] * group:
+                assert (b, ct) not in seen
+                seen.add((b, ct))
+        assert len(seen) == sum(-(-n * group // 128) for n in new), (new, group, first)
+
+
+def test_launches_past_a_grid():
+    most = ((1 << 32) - 1) // THREADS
+    assert [launches(n) for n in (1, most, most + 1, 2 * most, 2 * most + 1)] == [1, 1, 2, 2, 3]

@@ -170,3 +170,47 @@ def test_two_streams_with_their_own_workspaces(new):
     torch.cuda.synchronize()
     for out in outs:
         assert torch.equal(out, alone)
+
+
+@pytest.mark.parametrize("max_q", [16384, 600])
+def test_many_sequences_and_a_long_one(max_q):
+    """Column tiles of a batch of mostly empty sequences, as many sequences as rows: the launch goes by the rows, where
+    tiles for max_q rows of every sequence would be 2^24 workgroups and more; rows behind the last sequence stay."""
+    B, rows = 16384, 16384
+    new = [0] * B
+    new[0], new[63], new[64], new[4095], new[4096], new[9000], new[B - 1] = 3, 130, 1, 64, 600, 129, 200
+    lens = [0] * B
+    for b, n in enumerate(new):
+        lens[b] = n + n // 3
+    s = make(lens, 8, 8, 64, 16, "e5m2", BF16, seed=22, new=new)
+    owned = sum(new)
+    q, cache, table, lens_d, scales = arguments(s)
+    q = torch.cat([q, torch.zeros((rows - owned, 8, 64), dtype=BF16, device=DEV)])
+    for max_len in (800, 8000):  # without and with shares of the keys
+        log(f"  many sequences, max_q {max_q}, max_len {max_len}")
+        out = torch.full((rows, 8, 64), -5.0, dtype=BF16, device=DEV)
+        lse = torch.full((rows, 8), 7.0, dtype=torch.float32, device=DEV)
+        fp8.fp8_attn_prefill_paged(q, s["cu"].to(DEV), cache, table, lens_d, scales, 16, max_q=max_q, max_len=max_len,
+                                   out=out, lse=lse)
+        torch.cuda.synchronize()
+        want, want_lse, tol = reference(s)
+        assert_close(out[:owned], want, tol, "owned rows")
+        assert_lse(lse[:owned], want_lse, s, "owned rows")
+        assert bool((out[owned:] == -5).all()) and bool((lse[owned:] == 7).all())
+
+
+def test_more_sequences_than_a_grid_has_workgroups():
+    """2^24 + 37 sequences of one key or none: the last ones are taken in turn."""
+    B, D = (1 << 24) + 37, 64
+    s = make([1], 1, 1, D, 1, "e4m3", BF16, seed=23)
+    q = torch.ones((B, 1, D), dtype=BF16, device=DEV)
+    table = torch.full((B, 1), int(s["table"][0, 0]), dtype=torch.int32, device=DEV)
+    lens = torch.ones(B, dtype=torch.int32, device=DEV)
+    lens[torch.arange(3, B, 7, device=DEV)] = 0
+    out = torch.full((B, 1, D), 7.0, dtype=BF16, device=DEV)
+    fp8.fp8_attn_decode_paged(q, s["cache"].to(DEV), table, lens, s["scales"].to(DEV), 1, fmt="e4m3", max_len=1, out=out)
+    torch.cuda.synchronize()
+    want, _, tol = reference(s, lse=False)
+    row, some = out[0].clone(), (lens > 0)[:, None, None]
+    assert_close(row[None], want, tol, "one key")
+    assert bool((out == torch.where(some, row, torch.zeros_like(row))).all())
