@@ -13,6 +13,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "attn_plan.hpp"
 #include "kernels.hpp"
 
 namespace {
@@ -128,23 +129,17 @@ fp8_status_t check_attn_dims(int64_t rows, int64_t B, int64_t Hq, int64_t Hkv, i
 // they hold.  A wrong hint changes no result.
 int64_t hint(int64_t v, int64_t most) { return v > 0 ? std::min(v, most) : most; }
 
-// Whether the tiled kernel takes a call, by the query rows of a sequence that
-// share a KV head.  The streaming kernel walks over the keys once per 16 of
-// them, the tiled one once per 128, but has its products wait on LDS.
-// Streaming / tiled, us, 64 / 8 heads of 128, bf16, 16384 keys:
-//     rows            24          32          64          128         512
-//     1 sequence      22.6/23.4   21.4/21.4   25.6/26.1   35.6/35.1   89/59
-//     8 sequences     100/84      99/66       116/85      196/110     616/348
-//     32 sequences    265/288     246/229     412/294     823/386     3922/1452
-// Two-term products (fp16, fp32, lse) fill the tiled kernel's matrix cores twice,
-// and D = 256 leaves it one workgroup a CU; two sequences, 16384 keys:
-//     rows                    24          64          96     128    256
-//     fp16, D = 128           39/55       53/58       55/55  95/64  131/100
-//     bf16, D = 256 (32/8)    39/73 (12)  50/66 (32)                116/80 (128)
-bool attn_tiled(int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, bool two_terms) {
-    const int64_t columns = max_q * (Hq / Hkv);
-    return two_terms || D == 256 ? columns > 64 : columns >= 32;
-}
+// The new rows of a sequence: the most to expect, by the hint or, without one, by
+// the keys that rows past them would not have; and those of most sequences, by
+// the hint or the mean.
+struct NewRows {
+    int64_t most, typical;
+
+    NewRows(int64_t max_q, int64_t rows, int64_t B, int64_t max_len)
+        : most(hint(max_q, rows)), typical(max_q > 0 ? most : fp8k::ceil_div(rows, std::max<int64_t>(B, 1))) {
+        if (max_q == 0) most = std::max(typical, std::min(most, max_len));
+    }
+};
 
 // Either way: the queries are not told the type, nor whether lse is wanted.
 size_t attn_ws(int64_t rows, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size, int64_t max_blocks,
@@ -152,10 +147,11 @@ size_t attn_ws(int64_t rows, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int6
     const int64_t all_len = block_size * max_blocks;
     max_len = hint(max_len, all_len);
     if (B == 0 || rows == 0) return 0;
-    const bool one = attn_tiled(Hq, Hkv, D, max_q, false), two = attn_tiled(Hq, Hkv, D, max_q, true);
+    const NewRows q(max_q, rows, B, max_len);
+    const bool one = fp8k::attn_tiled(Hq, Hkv, D, q.typical, false), two = fp8k::attn_tiled(Hq, Hkv, D, q.typical, true);
     size_t need = 0;
-    if (one || two) need = fp8k::attn_tiled_ws_bytes(B, rows, Hq, Hkv, D, max_q, max_len);
-    if (!one || !two) need = std::max(need, fp8k::attn_paged_ws_bytes(B, rows, Hq, Hkv, D, max_q, max_len, all_len));
+    if (one || two) need = fp8k::attn_tiled_ws_bytes(B, rows, Hq, Hkv, D, q.most, max_len);
+    if (!one || !two) need = std::max(need, fp8k::attn_paged_ws_bytes(B, rows, Hq, Hkv, D, q.most, max_len, all_len));
     return round_up(need, kAlign);
 }
 
@@ -198,9 +194,10 @@ fp8_status_t attn(fp8k::PagedAttn p, fp8_kv_dtype_t dtype, fp8_kv_format_t fmt, 
     p.window = (int)std::min(window, kMaxAttn);  // no key is further back
     p.dtype = (int)dtype;
     max_len = hint(max_len, block_size * max_blocks);
-    const bool tiled = attn_tiled(Hq, Hkv, D, max_q, fp8k::two_terms(p));
-    return from_hip(tiled ? fp8k::launch_attn_tiled(p, (int)D, (int)fmt, max_q, max_len, ws, stream)
-                          : fp8k::launch_attn_paged(p, (int)D, (int)fmt, max_q, max_len, ws, stream));
+    const NewRows n(max_q, rows, B, max_len);
+    const bool tiled = fp8k::attn_tiled(Hq, Hkv, D, n.typical, fp8k::two_terms(p));
+    return from_hip(tiled ? fp8k::launch_attn_tiled(p, (int)D, (int)fmt, n.most, max_len, ws, stream)
+                          : fp8k::launch_attn_paged(p, (int)D, (int)fmt, n.most, n.typical, max_len, ws, stream));
 }
 
 // Bytes the GEMM path itself needs for an M x N x K problem: the skinny
@@ -485,7 +482,7 @@ fp8_status_t fp8_attn_decode_paged(const void* q, int64_t ldq, fp8_kv_dtype_t dt
 size_t fp8_attn_prefill_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size,
                                         int64_t max_blocks, int64_t max_q, int64_t max_len) {
     if (check_attn_dims(T, B, Hq, Hkv, D, block_size, max_blocks, max_q, max_len) != FP8_OK) return SIZE_MAX;
-    return attn_ws(T, B, Hq, Hkv, D, block_size, max_blocks, hint(max_q, T), max_len);
+    return attn_ws(T, B, Hq, Hkv, D, block_size, max_blocks, max_q, max_len);
 }
 
 fp8_status_t fp8_attn_prefill_paged(const void* q, int64_t ldq, fp8_kv_dtype_t dtype, const int32_t* cu_q, int64_t T,
@@ -502,7 +499,6 @@ fp8_status_t fp8_attn_prefill_paged(const void* q, int64_t ldq, fp8_kv_dtype_t d
     p.cache = cache, p.num_blocks = num_blocks, p.scales = scales;
     p.block_table = block_table, p.ld_table = ld_table, p.seq_lens = seq_lens, p.prefix = prefix_lens;
     p.softcap = softcap, p.alibi = alibi_slopes, p.causal = causal != 0;
-    if (max_q >= 0) max_q = hint(max_q, std::max<int64_t>(T, 0));
     return attn(p, dtype, fmt, T, B, Hq, Hkv, D, block_size, max_blocks, max_q, max_len, window, sm_scale, ws, ws_bytes,
                 stream);
 }

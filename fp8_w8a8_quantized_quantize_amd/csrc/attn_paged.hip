@@ -721,8 +721,8 @@ hipError_t launch_stream(StreamArgs a, const StreamPlan& s, hipStream_t stream) 
 }
 
 template <int D>
-hipError_t launch_join(StreamArgs a, int64_t max_q, hipStream_t stream) {
-    const JoinPlan j = join_plan((int64_t)a.join_batch * a.p.Hq, D, max_q);
+hipError_t launch_join(StreamArgs a, int64_t max_q, int64_t typical, hipStream_t stream) {
+    const JoinPlan j = join_plan((int64_t)a.join_batch * a.p.Hq, D, max_q, typical);
     a.join_rows = (int)j.rows;
     a.spread = j.spread, a.log_spread = j.log_spread;
     a.by_batch = FastDiv(a.join_batch);
@@ -734,7 +734,7 @@ hipError_t launch_join(StreamArgs a, int64_t max_q, hipStream_t stream) {
 }
 
 template <int D>
-hipError_t launch(const StreamArgs& a, const StreamPlan& s, int fmt, int64_t max_q, hipStream_t stream) {
+hipError_t launch(const StreamArgs& a, const StreamPlan& s, int fmt, int64_t max_q, int64_t typical, hipStream_t stream) {
     const bool bias = a.p.softcap > 0.0f || a.p.alibi != nullptr, one = !two_terms(a.p);
     hipError_t e;
     if (fmt == kKvE5M2)
@@ -744,7 +744,7 @@ hipError_t launch(const StreamArgs& a, const StreamPlan& s, int fmt, int64_t max
         e = bias ? (one ? launch_stream<D, kKvE4M3, true, 1>(a, s, stream) : launch_stream<D, kKvE4M3, true, 2>(a, s, stream))
                  : (one ? launch_stream<D, kKvE4M3, false, 1>(a, s, stream) : launch_stream<D, kKvE4M3, false, 2>(a, s, stream));
     if (e != hipSuccess || a.shares == 0) return e;
-    return launch_join<D>(a, max_q, stream);
+    return launch_join<D>(a, max_q, typical, stream);
 }
 
 }  // namespace
@@ -767,13 +767,13 @@ hipError_t launch_attn_join(const PagedAttn& p, int D, int splits, float* part_o
     a.by_group = FastDiv(a.group);
     a.by_heads = FastDiv(p.Hq);
     switch (D) {
-        case 64: return launch_join<64>(a, p.rows, stream);
-        case 128: return launch_join<128>(a, p.rows, stream);
-        default: return launch_join<256>(a, p.rows, stream);
+        case 64: return launch_join<64>(a, p.rows, p.rows, stream);
+        case 128: return launch_join<128>(a, p.rows, p.rows, stream);
+        default: return launch_join<256>(a, p.rows, p.rows, stream);
     }
 }
 
-hipError_t launch_attn_paged(const PagedAttn& p, int D, int fmt, int64_t max_q, int64_t max_len, void* ws,
+hipError_t launch_attn_paged(const PagedAttn& p, int D, int fmt, int64_t max_q, int64_t typical, int64_t max_len, void* ws,
                              hipStream_t stream) {
     const StreamPlan s = stream_plan(p.B, p.rows, p.Hq, p.Hkv, D, max_q, max_len, (int64_t)p.max_blocks * p.block);
     StreamArgs a = {};
@@ -796,11 +796,10 @@ hipError_t launch_attn_paged(const PagedAttn& p, int D, int fmt, int64_t max_q, 
     a.by_heads = FastDiv(p.Hq);
     a.join_batch = p.B;
     a.by_head_groups = FastDiv(a.head_groups);
-    const int64_t q = std::max<int64_t>(1, max_q);
     switch (D) {
-        case 64: return launch<64>(a, s, fmt, q, stream);
-        case 128: return launch<128>(a, s, fmt, q, stream);
-        default: return launch<256>(a, s, fmt, q, stream);
+        case 64: return launch<64>(a, s, fmt, max_q, typical, stream);
+        case 128: return launch<128>(a, s, fmt, max_q, typical, stream);
+        default: return launch<256>(a, s, fmt, max_q, typical, stream);
     }
 }
 

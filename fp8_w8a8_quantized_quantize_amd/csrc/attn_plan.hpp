@@ -23,6 +23,26 @@ inline auto in_launches(int64_t units, Launch launch) {
     return e;
 }
 
+// ---- which form ----
+
+// Whether the tiled kernel takes a call, by the query rows of a sequence that
+// share a KV head.  The streaming kernel walks over the keys once per 16 of
+// them, the tiled one once per 128, but has its products wait on LDS.
+// Streaming / tiled, us, 64 / 8 heads of 128, bf16, 16384 keys:
+//     rows            24          32          64          128         512
+//     1 sequence      22.6/23.4   21.4/21.4   25.6/26.1   35.6/35.1   89/59
+//     8 sequences     100/84      99/66       116/85      196/110     616/348
+//     32 sequences    265/288     246/229     412/294     823/386     3922/1452
+// Two-term products (fp16, fp32, lse) fill the tiled kernel's matrix cores twice,
+// and D = 256 leaves it one workgroup a CU; two sequences, 16384 keys:
+//     rows                    24          64          96     128    256
+//     fp16, D = 128           39/55       53/58       55/55  95/64  131/100
+//     bf16, D = 256 (32/8)    39/73 (12)  50/66 (32)                116/80 (128)
+inline bool attn_tiled(int64_t Hq, int64_t Hkv, int64_t D, int64_t new_rows, bool two_terms) {
+    const int64_t columns = new_rows * (Hq / Hkv);
+    return two_terms || D == 256 ? columns > 64 : columns >= 32;
+}
+
 // ---- the streaming form ----
 
 constexpr int kTile = 32;     // keys per step of a wave
@@ -44,9 +64,14 @@ inline StreamPlan stream_plan(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, 
     StreamPlan s;
     B = std::max<int64_t>(B, 1);
     s.col_tiles = ceil_div(std::max<int64_t>(max_q, 1) * (Hq / Hkv), kCols);
-    s.col_tiles = std::max<int64_t>(1, std::min<int64_t>({s.col_tiles, kMaxGrid / (B * Hkv), 65535}));
     const int most = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
     const int64_t fill = D == 256 ? 256 : 512;  // workgroups that are resident at once
+    // Where max_q is far from most sequences' new rows, a grid of it would be empty for the most part: some more column
+    // tiles than the mean (a few rounds of the card's workgroups at the least), and the others in turn.
+    const int64_t least = rows * (Hq / Hkv) / kCols + B;  // column tiles of all sequences, B fewer at the least
+    const bool uneven = B * s.col_tiles > 4 * least;
+    if (uneven) s.col_tiles = std::min(s.col_tiles, std::max(4 * ceil_div(least, B), 4 * fill * most / (B * Hkv)));
+    s.col_tiles = std::max<int64_t>(1, std::min<int64_t>({s.col_tiles, kMaxGrid / (B * Hkv), 65535}));
     s.hw = most;
     s.shares = 0;
     s.min_share = 2;
@@ -60,16 +85,16 @@ inline StreamPlan stream_plan(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, 
     // 13.6 / 17.4, 32 x 1000 16.3 / 23.9, 256 x 500 54 / 73; 16 x 2000 23.8 / 22.9, 16 x 8000 75 / 67, 1 x 8000 68 / 15.
     if (max_len <= 1024) {
         while (s.hw > 1 && B * (Hkv / s.hw) * s.col_tiles < fill) s.hw /= 2;
-        if (max_len <= 640 || B * (Hkv / s.hw) * s.col_tiles >= fill / 4) return whole();
+        if (max_len <= 640 || (!uneven && B * (Hkv / s.hw) * s.col_tiles >= fill / 4)) return whole();
     }
     // costs of all sequences are added up in 32 bits
-    const int64_t cost = (ceil_div(all_len, kTile) + kItemCost) * (rows * (Hq / Hkv) / kCols + B);
+    const int64_t cost = (ceil_div(all_len, kTile) + kItemCost) * least;
     if (cost >= (int64_t(1) << 30)) return whole();
     s.hw = most;
     // Several heads a workgroup read longer runs of a cache row; with few rounds a share, its four waves on one head
     // shorten the chain instead.  Four heads / one, us: 48 x 4096 ... 32768 keys 297 / 318, 64 x 1000 ... 8000 102 / 112,
     // 1 x 8000 17.2 / 14.7, 19 x 1 ... 9001 of 256 channels 25.8 / 23.9.
-    const int64_t items = B * (Hkv / most) * s.col_tiles;
+    const int64_t items = (uneven ? least : B * s.col_tiles) * (Hkv / most);
     if (items < 32 || items * max_len * most / (kTile * kWaves) < 16 * fill) s.hw = 1;
     s.shares = (int)std::max<int64_t>(1, fill / (Hkv / s.hw));
     s.units = s.shares * (Hkv / s.hw);
@@ -134,8 +159,11 @@ struct JoinPlan {
     int64_t units;
 };
 
-inline JoinPlan join_plan(int64_t heads, int64_t D, int64_t max_q) {
+// max_q: the most new rows of a sequence; where most have far fewer, `typical`,
+// units for some more than those, and for the rest in turn.
+inline JoinPlan join_plan(int64_t heads, int64_t D, int64_t max_q, int64_t typical) {
     JoinPlan j;
+    if (typical < max_q) max_q = std::min(max_q, std::max(2 * typical, (int64_t(1) << 17) / heads));
     j.rows = std::max<int64_t>(1, std::min<int64_t>(max_q, (int64_t(1) << 26) / heads));
     const int64_t groups = 256 / (D / 4);
     j.spread = 1, j.log_spread = 0;

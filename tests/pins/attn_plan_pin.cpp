@@ -3,6 +3,11 @@
 
 extern "C" {
 
+/* whether the tiled form takes the call */
+void pin_form(int64_t Hq, int64_t Hkv, int64_t D, int64_t new_rows, int64_t two_terms, int64_t* out) {
+    out[0] = fp8k::attn_tiled(Hq, Hkv, D, new_rows, two_terms != 0);
+}
+
 /* units, column tiles, equal shares or 0 */
 void pin_stream(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_len,
                 int64_t all_len, int64_t* out) {
@@ -18,8 +23,8 @@ void pin_tiled(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int6
 }
 
 /* units, rows a sequence, thread groups a row */
-void pin_join(int64_t heads, int64_t D, int64_t max_q, int64_t* out) {
-    const fp8k::JoinPlan j = fp8k::join_plan(heads, D, max_q);
+void pin_join(int64_t heads, int64_t D, int64_t max_q, int64_t typical, int64_t* out) {
+    const fp8k::JoinPlan j = fp8k::join_plan(heads, D, max_q, typical);
     out[0] = j.units, out[1] = j.rows, out[2] = j.spread;
 }
 

@@ -48,8 +48,8 @@ def check(B, rows, Hq, Hkv, D, max_q, max_len, all_len, decode):
     units, slots, splits = plan("pin_tiled", B, rows, Hq, Hkv, D, decode, max_q, max_len)[:3]
     assert units == slots * Hkv * splits, what
     launches(units)
-    for heads, q in ((B * Hq, max_q), (Hq, rows)):
-        units, per, spread = plan("pin_join", heads, D, q)[:3]
+    for heads, q, typical in ((B * Hq, max_q, max_q), (B * Hq, max_q, -(-rows // B)), (Hq, rows, rows)):
+        units, per, spread = plan("pin_join", heads, D, q, typical)[:3]
         launches(units)
         assert 1 <= per <= q and units * (THREADS // (D // 4)) // spread >= heads * per, what
     return slots * Hkv
@@ -122,3 +122,22 @@ def test_slots_hold_every_column_tile():
 def test_launches_past_a_grid():
     most = ((1 << 32) - 1) // THREADS
     assert [launches(n) for n in (1, most, most + 1, 2 * most, 2 * most + 1)] == [1, 1, 2, 2, 3]
+
+
+@pytest.mark.parametrize("B,new,Hq,Hkv", [(32, 4, 32, 8), (256, 3, 64, 8), (64, 1, 64, 8), (1024, 2, 64, 8), (3, 2, 8, 2)])
+@pytest.mark.parametrize("max_len", [500, 1000, 30000])
+def test_few_new_tokens_without_a_hint(B, new, Hq, Hkv, max_len):
+    """Drafted tokens whose bound is not told (all T rows) take the streaming form by their mean, and workgroups of the
+    order of what there is to do, not B times T."""
+    T = B * new
+    assert plan("pin_form", Hq, Hkv, 128, new, 0)[0] == 0
+    tiles = B + T * (Hq // Hkv) // 16
+    units, y, shares = plan("pin_stream", B, T, Hq, Hkv, 128, T, max_len, 40000)[:3]
+    assert units * y <= max(4096, 4 * tiles * Hkv)
+    units, per, spread = plan("pin_join", B * Hq, 128, T, new)[:3]
+    assert units <= max(16384, T * Hq)
+
+
+def test_whole_prompts_without_a_hint():
+    assert plan("pin_form", 64, 8, 128, 8192, 0)[0] == 1
+    assert plan("pin_form", 8, 8, 64, 256, 1)[0] == 1

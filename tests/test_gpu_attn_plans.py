@@ -214,3 +214,22 @@ def test_more_sequences_than_a_grid_has_workgroups():
     row, some = out[0].clone(), (lens > 0)[:, None, None]
     assert_close(row[None], want, tol, "one key")
     assert bool((out == torch.where(some, row, torch.zeros_like(row))).all())
+
+
+@pytest.mark.parametrize("max_len", [0, 600, 1000, 3000])
+@pytest.mark.parametrize("D,Hq,Hkv,dtype", [(128, 16, 4, BF16), (64, 6, 3, FP32), (256, 8, 2, BF16)])
+def test_uneven_new_tokens_without_a_hint(D, Hq, Hkv, dtype, max_len):
+    """Mostly one new token a sequence, some with none, one with many, and no bound told: by their mean they take the
+    streaming form, and the long one is computed whole."""
+    new = [1] * 70
+    new[3], new[40], new[41], new[69] = 0, 45, 0, 7
+    lens = [(37 * b) % 300 + n for b, n in enumerate(new)]
+    lens[5], lens[40], lens[60] = 2700, 900, 0
+    s = make(lens, Hq, Hkv, D, 16, "e5m2", dtype, seed=D, new=new)
+    prefill(s, f"uneven D={D} {dtype} max_len {max_len}", 0, max_len)
+    prefill(s, f"uneven D={D} {dtype} max_len {max_len} window", 0, max_len, window=100)
+
+
+def test_even_drafted_tokens_without_a_hint():
+    s = make([(61 * b) % 900 + 4 for b in range(32)], 32, 8, 128, 16, "e5m2", BF16, seed=33, new=[4] * 32)
+    prefill(s, "32 x 4, no hints", 0, 0)
