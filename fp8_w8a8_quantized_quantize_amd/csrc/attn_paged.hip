@@ -77,10 +77,10 @@ struct StreamArgs {
     float* part_o;     // [workgroups][2][hw][kCols][D]: parts of rows, a share's first and last
     float2* part_ml;   // [workgroups][2][hw][kCols]: reference (log2), sum
     int* starts;       // [B + 1]: cost before every sequence, cost of all
-    int splits;        // the join alone: parts of every row, laid out [rows][Hq][splits], 0 for cut rows as above
+    int splits;        // the join of parts: parts of every row, laid out [rows][Hq][splits]
     int spread, log_spread;  // the join's thread groups per output row
     int join_rows;     // and the new rows of a sequence it takes at a time
-    int join_batch;    // of the p.B sequences; 1 with `splits`, whose parts go by row
+    int join_batch;    // of the p.B sequences; 1 for parts, which go by row
     int join_unit0;    // the first workgroup's worth of rows of this launch
     FastDiv by_block, by_group, by_head_groups, by_heads, by_batch;
 
@@ -610,7 +610,8 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
 // Joins the key shares of the output rows.  A group of D / 4 threads adds up a
 // row's weighted shares, four channels a thread, every `spread`-th of them when
 // several groups of the workgroup take one row; LDS joins those in order.
-template <int D>
+// PARTS: of all rows, each in `splits` parts; else of those that equal shares cut.
+template <int D, bool PARTS>
 __global__ __launch_bounds__(kWaves* kWave) void attn_join(StreamArgs a) {
     const PagedAttn& p = a.p;
     constexpr int kThreads = kWaves * kWave;
@@ -624,18 +625,20 @@ __global__ __launch_bounds__(kWaves* kWave) void attn_join(StreamArgs a) {
     const int rest = a.by_heads.of(nth), i0 = a.by_batch.of(rest);
     const int h = nth - rest * p.Hq, b = rest - i0 * a.join_batch;
     const int hk = a.by_group.of(h);
-    Seq seq = {0, 0, 0};
-    int prefix = 0, first_row = 0;
-    if (i0 < a.join_rows) {
-        if (a.splits > 0) {
-            // the rows of all sequences, without regard to whose they are
-            seq.nq = p.rows;
-            if (p.cu_q) first_row = p.cu_q[0], seq.nq = min(p.cu_q[p.B], p.rows);
-        } else {
-            seq = sequence(p, b);
-            prefix = p.prefix ? p.prefix[b] : 0;
-        }
+    Seq seq = {0, p.rows, 0};
+    int prefix = 0, first_row = 0, start = 0, share = 1;
+    if constexpr (PARTS) {
+        // the rows of all sequences, without regard to whose they are
+        if (p.cu_q) first_row = p.cu_q[0], seq.nq = min(p.cu_q[p.B], p.rows);
+    } else {
+        // looked up together and before the barrier: one trip to memory
+        start = a.starts[b];
+        share = a.starts[p.B];
+        seq = sequence(p, b);
+        prefix = p.prefix ? p.prefix[b] : 0;
+        share = a.share_of(share);
     }
+    if (i0 >= a.join_rows) seq.nq = 0;
     // Every thread goes through as many rounds as the longest sequence of its workgroup: the barriers are for all.
     for (int i = i0; __syncthreads_or(i < seq.nq); i += a.join_rows) {
         float M = kNoRef, L = 0.0f;
@@ -646,11 +649,10 @@ __global__ __launch_bounds__(kWaves* kWave) void attn_join(StreamArgs a) {
             const int col = i * a.group + h - hk * a.group;
             int first = 0;
             shares = a.splits;
-            if (a.splits == 0) {
+            if constexpr (!PARTS) {
                 // the shares that its item was cut into, as the first kernel dealt them out
                 const Run run = run_of(a, seq, prefix);
-                const int at = a.starts[b] + col / kCols * (run.rounds + kItemCost) + kItemCost;
-                const int share = a.share_of(a.starts[p.B]);
+                const int at = start + col / kCols * (run.rounds + kItemCost) + kItemCost;
                 first = at / share;
                 shares = run.rounds == 0 ? 0 : (at + run.rounds - 1) / share - first + 1;
             }
@@ -665,8 +667,8 @@ __global__ __launch_bounds__(kWaves* kWave) void attn_join(StreamArgs a) {
                     for (int k = 0; k < kBatch; ++k) {
                         const int s = min(s0 + k * a.spread, shares - 1);
                         const int group = (first + s) * a.head_groups + (hk >> a.log_hw);
-                        const int64_t x = a.splits > 0 ? ((int64_t)(seq.row0 + i) * p.Hq + h) * a.splits + s
-                                                       : ((2 * group + (s == 0)) * a.hw + (hk & (a.hw - 1))) * kCols + col % kCols;
+                        const int64_t x = PARTS ? ((int64_t)i * p.Hq + h) * a.splits + s
+                                                : ((2 * group + (s == 0)) * a.hw + (hk & (a.hw - 1))) * kCols + col % kCols;
                         y[k] = a.part_ml[x];
                         v[k] = *reinterpret_cast<const float4*>(a.part_o + x * D + 4 * d4);
                         if (s0 + k * a.spread >= shares) y[k].x = kNoRef;
@@ -678,8 +680,8 @@ __global__ __launch_bounds__(kWaves* kWave) void attn_join(StreamArgs a) {
                     r = make_float4(r.x * g, r.y * g, r.z * g, r.w * g);
 #pragma unroll
                     for (int k = 0; k < kBatch; ++k) {
-                        if (s0 + k * a.spread >= shares) break;
-                        const float f = __builtin_amdgcn_exp2f(y[k].x - M);
+                        // by a weight of zero: a branch would sink the loads into it, one after the other
+                        const float f = s0 + k * a.spread < shares ? __builtin_amdgcn_exp2f(y[k].x - M) : 0.0f;
                         L += f * y[k].y;
                         r = make_float4(r.x + f * v[k].x, r.y + f * v[k].y, r.z + f * v[k].z, r.w + f * v[k].w);
                     }
@@ -720,7 +722,7 @@ hipError_t launch_stream(StreamArgs a, const StreamPlan& s, hipStream_t stream) 
     });
 }
 
-template <int D>
+template <int D, bool PARTS>
 hipError_t launch_join(StreamArgs a, int64_t max_q, int64_t typical, hipStream_t stream) {
     const JoinPlan j = join_plan((int64_t)a.join_batch * a.p.Hq, D, max_q, typical);
     a.join_rows = (int)j.rows;
@@ -728,7 +730,7 @@ hipError_t launch_join(StreamArgs a, int64_t max_q, int64_t typical, hipStream_t
     a.by_batch = FastDiv(a.join_batch);
     return in_launches(j.units, [&](int64_t first, int64_t n) {
         a.join_unit0 = (int)first;
-        hipLaunchKernelGGL((attn_join<D>), dim3((unsigned)n), dim3(kWaves * kWave), 0, stream, a);
+        hipLaunchKernelGGL((attn_join<D, PARTS>), dim3((unsigned)n), dim3(kWaves * kWave), 0, stream, a);
         return hipGetLastError();
     });
 }
@@ -744,7 +746,7 @@ hipError_t launch(const StreamArgs& a, const StreamPlan& s, int fmt, int64_t max
         e = bias ? (one ? launch_stream<D, kKvE4M3, true, 1>(a, s, stream) : launch_stream<D, kKvE4M3, true, 2>(a, s, stream))
                  : (one ? launch_stream<D, kKvE4M3, false, 1>(a, s, stream) : launch_stream<D, kKvE4M3, false, 2>(a, s, stream));
     if (e != hipSuccess || a.shares == 0) return e;
-    return launch_join<D>(a, max_q, typical, stream);
+    return launch_join<D, false>(a, max_q, typical, stream);
 }
 
 }  // namespace
@@ -767,9 +769,9 @@ hipError_t launch_attn_join(const PagedAttn& p, int D, int splits, float* part_o
     a.by_group = FastDiv(a.group);
     a.by_heads = FastDiv(p.Hq);
     switch (D) {
-        case 64: return launch_join<64>(a, p.rows, p.rows, stream);
-        case 128: return launch_join<128>(a, p.rows, p.rows, stream);
-        default: return launch_join<256>(a, p.rows, p.rows, stream);
+        case 64: return launch_join<64, true>(a, p.rows, p.rows, stream);
+        case 128: return launch_join<128, true>(a, p.rows, p.rows, stream);
+        default: return launch_join<256, true>(a, p.rows, p.rows, stream);
     }
 }
 
