@@ -646,8 +646,8 @@ def fp8_attn_decode_paged(q, cache, block_table, seq_lens, scales, block_size, f
     ws, wp, wn = _attn_ws(ws, fp8_attn_decode_workspace_bytes(B, Hq, Hkv, D, block_size, width, max_len), q.device)
     _check("fp8_attn_decode_paged",
            lib().fp8_attn_decode_paged(qp, ldq, dt, cp, blocks, block_size, sp, _kv_fmt(fmt), tp, ld_table, width, lp, B,
-                                       Hq, Hkv, D, max_len, D ** -0.5 if sm_scale is None else sm_scale, softcap, ap,
-                                       window, op, ldo, ep, wp, wn, _raw_stream(q.get_device())))
+                                       Hq, Hkv, D, max_len, D ** -0.5 if sm_scale is None else sm_scale,
+                                       softcap or 0.0, ap, window or 0, op, ldo, ep, wp, wn, _raw_stream(q.get_device())))
     return out
 
 
@@ -676,8 +676,8 @@ def fp8_attn_prefill_paged(q, cu_q, cache, block_table, seq_lens, scales, block_
     _check("fp8_attn_prefill_paged",
            lib().fp8_attn_prefill_paged(qp, ldq, dt, cup, T, cp, blocks, block_size, sp, _kv_fmt(fmt), tp, ld_table,
                                         width, lp, B, Hq, Hkv, D, max_q, max_len, 1 if causal else 0, pp,
-                                        D ** -0.5 if sm_scale is None else sm_scale, softcap, ap, window, op, ldo, ep,
-                                        wp, wn, _raw_stream(di)))
+                                        D ** -0.5 if sm_scale is None else sm_scale, softcap or 0.0, ap, window or 0, op,
+                                        ldo, ep, wp, wn, _raw_stream(di)))
     return out
 
 

@@ -233,3 +233,15 @@ def test_uneven_new_tokens_without_a_hint(D, Hq, Hkv, dtype, max_len):
 def test_even_drafted_tokens_without_a_hint():
     s = make([(61 * b) % 900 + 4 for b in range(32)], 32, 8, 128, 16, "e5m2", BF16, seed=33, new=[4] * 32)
     prefill(s, "32 x 4, no hints", 0, 0)
+
+
+def test_none_turns_a_score_option_off():
+    s = make([50, 7], 4, 2, 64, 16, "e5m2", BF16, seed=1, new=[2, 1])
+    q, cache, table, lens, scales = arguments(s)
+    off = dict(softcap=None, alibi_slopes=None, window=None, sm_scale=None, max_len=None)
+    a = fp8.fp8_attn_decode_paged(q[:2], cache, table, lens, scales, 16)
+    b = fp8.fp8_attn_decode_paged(q[:2], cache, table, lens, scales, 16, **off)
+    c = fp8.fp8_attn_prefill_paged(q, s["cu"].to(DEV), cache, table, lens, scales, 16)
+    d = fp8.fp8_attn_prefill_paged(q, s["cu"].to(DEV), cache, table, lens, scales, 16, prefix_lens=None, max_q=None, **off)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and torch.equal(c, d)
