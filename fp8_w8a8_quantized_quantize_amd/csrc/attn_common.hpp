@@ -158,15 +158,24 @@ __device__ __forceinline__ float max_over_groups(float v) {
 }
 
 // cap * tanh(x / cap) in fp32: 1 - 2 / (exp(2 x / cap) + 1), whose absolute
-// error is that of a few roundings at the cap's magnitude.  Beside two terms
-// that would show in scores far below the cap: there x (1 + t), t from the series
-// of tanh(y) / y - 1 up to y^10, off by 3e-8 of the score at most.
+// error is that of a few roundings at the cap's magnitude.  In scores far below
+// the cap that shows beside two terms, and beside one (2^-11 of the operands)
+// from caps of some hundreds on, where a score below 2^-23 of the cap would
+// vanish: there x (1 + t), t from the series of tanh(y) / y - 1 up to y^10, off
+// by 3e-8 of the score at most.
+constexpr float kSmallCap = 256.0f;
 template <int TERMS>
+__device__ __forceinline__ bool cap_by_series(float cap) { return TERMS == 2 || cap > kSmallCap; }
+
+// 2 log2(e) / cap, finite for the smallest caps too (0 times it is 0).
+__device__ __forceinline__ float cap_factor(float cap) { return cap > 0.0f ? fminf(2.0f * kLog2e / cap, 3.4e38f) : 0.0f; }
+
+template <bool SERIES>
 __device__ __forceinline__ float soft_cap(float x, float cap, float two_log2e_over_cap) {
     const float u = x * two_log2e_over_cap;
     const float e = __builtin_amdgcn_exp2f(u);
     const float far = cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(e + 1.0f));
-    if constexpr (TERMS == 1) return far;
+    if constexpr (!SERIES) return far;
     const float y = u * (0.5f * kLn2), z = y * y;
     float t = __builtin_fmaf(z, -1382.0f / 155925.0f, 62.0f / 2835.0f);
     t = __builtin_fmaf(z, t, -17.0f / 315.0f);

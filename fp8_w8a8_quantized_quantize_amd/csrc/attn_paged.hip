@@ -320,7 +320,7 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
 
         const float slope = p.alibi ? p.alibi[head] * kLog2e : 0.0f;
         const int pos = seq.len - seq.nq + qi;
-        const float cap_in = p.softcap > 0.0f ? 2.0f * kLog2e / p.softcap : 0.0f;
+        const float cap_in = cap_factor(p.softcap);
 
         float m = kNoRef;
         v4f o[VB], l = {0.0f, 0.0f, 0.0f, 0.0f};  // the sum of p, four times over
@@ -457,14 +457,22 @@ __global__ __launch_bounds__(kWaves* kWave, D == 256 ? 1 : 2) void attn_stream(S
                 s[t] = TERMS == 2 ? acc + rest : acc;
             }
             if constexpr (BIAS) {
+                auto capped = [&](auto series) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        s[j / 4][j % 4] = kLog2e * soft_cap<decltype(series)::value>(s[j / 4][j % 4] * c, p.softcap, cap_in);
+                };
+                if (p.softcap > 0.0f) {
+                    if (cap_by_series<TERMS>(p.softcap)) capped(std::true_type());
+                    else capped(std::false_type());
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s[j / 4][j % 4] *= c;
+                }
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float x = s[t][i] * c;
-                        if (p.softcap > 0.0f) x = kLog2e * soft_cap<TERMS>(x, p.softcap, cap_in);
-                        s[t][i] = x + slope * (float)(key0 + 16 * t + 4 * g + i - pos);
-                    }
+                    for (int i = 0; i < 4; ++i) s[t][i] += slope * (float)(key0 + 16 * t + 4 * g + i - pos);
             }
             const bool whole = mask == 0xFFFFFFFFu && !__any(key0 < lo || key0 + kTile > hi);
             float x[8];  // scores above the reference

@@ -33,6 +33,7 @@
 // leaves its unscaled fp32 sums, its reference and its sum of p in the
 // workspace, and the streaming form's join adds them in their order.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_common.hpp"
 #include "attn_plan.hpp"
@@ -202,7 +203,7 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
         cs = __builtin_amdgcn_ldexpf(p.scale, -shift);
     }
     if (p.softcap > 0.0f) cs *= kLn2;  // the cap takes the natural score
-    const float cap_in = p.softcap > 0.0f ? 2.0f * kLog2e / p.softcap : 0.0f;
+    const float cap_in = cap_factor(p.softcap);
 
     float m = 0.0f, l = 0.0f, limit = kNoRef;
     v16f o[DB];
@@ -292,9 +293,14 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
     auto above = [&](int t, uint64_t mask) {
         const int key0 = base + t * kKeys;
         if constexpr (BIAS) {
-            if (p.softcap > 0.0f) {
+            auto capped = [&](auto series) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) s[j / 16][j % 16] = kLog2e * soft_cap<TERMS>(s[j / 16][j % 16] * cs, p.softcap, cap_in);
+                for (int j = 0; j < 32; ++j)
+                    s[j / 16][j % 16] = kLog2e * soft_cap<decltype(series)::value>(s[j / 16][j % 16] * cs, p.softcap, cap_in);
+            };
+            if (p.softcap > 0.0f) {
+                if (cap_by_series<TERMS>(p.softcap)) capped(std::true_type());
+                else capped(std::false_type());
             }
             const float by = p.softcap > 0.0f ? 1.0f : cs, dist = (float)(key0 + 4 * h - pos);
 #pragma unroll

@@ -180,3 +180,52 @@ def test_graph_replay_follows_its_inputs():
         torch.cuda.synchronize()
         want, _, tol = reference(s, lse=False)
         assert_close(out, want, tol, "replay")
+
+
+@pytest.mark.parametrize("cap", [1e3, 1e5, 1e8, 1e30])
+@pytest.mark.parametrize("D,dtype,new", [(64, BF16, 1), (128, BF16, 1), (256, BF16, 1), (128, FP32, 1), (128, BF16, 90), (64, FP16, 90)])
+def test_a_cap_far_above_the_scores(D, dtype, new, cap):
+    """cap tanh(x / cap) is x less x^3 / (3 cap^2), under 2^-11 for the scores here (|x| < 10) and a cap of 1000 or more:
+    the uncapped result, with that and the cap's own roundings (4 of 2^-24 of the score) added to every score's error."""
+    s = make([700, 5, 0, 130], 8, 4, D, 16, "e5m2", dtype, seed=D + 3, new=None if new == 1 else [new, 2, 0, 30])
+    want, _, tol = reference(s, lse=False)
+    # both sums of p: at most exp(2 ds) - 1 < 3 ds of the largest value
+    q, cache, table, lens, scales = [s[k].to(DEV) for k in ("q", "cache", "table", "lens", "scales")]
+    kw = dict(softcap=cap)
+    if new == 1:
+        out = fp8.fp8_attn_decode_paged(q, cache, table, lens, scales, 16, **kw)
+    else:
+        out = fp8.fp8_attn_prefill_paged(q, s["cu"].to(DEV), cache, table, lens, scales, 16, max_q=new, **kw)
+    torch.cuda.synchronize()
+    v = s["cache"].view(torch.float8_e5m2).float().nan_to_num(0.0).abs().amax() * s["scales"].max()
+    ds = 10.0 ** 3 / (3 * cap * cap) + 10 * 4 * 2.0 ** -24
+    assert largest_score(s, D ** -0.5) < 10.0
+    assert_close(out, want, tol + 3 * ds * float(v), f"cap {cap} D={D} {dtype} {new}")
+
+
+def largest_score(s, scale):
+    """Of all queries and keys, masked ones too."""
+    top, block = 0.0, s["block"]
+    for b in range(s["lens"].numel()):
+        n = int(s["lens"][b])
+        rows = s["q"][int(s["cu"][b]):int(s["cu"][b + 1])].double()
+        if not n or not rows.numel():
+            continue
+        j = torch.arange(n)
+        k = s["cache"][s["table"][b, (j // block).long()].long() * block + j % block].view(torch.float8_e5m2).double()
+        k = (k * s["scales"].double()).view(n, 2, s["Hkv"], s["D"])[:, 0]
+        for h in range(s["Hq"]):
+            top = max(top, float((rows[:, h] @ k[:, h // (s["Hq"] // s["Hkv"])].T).abs().max()) * scale)
+    return top
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("cap", [1e-38, 1e-39, 1e-45])
+def test_the_smallest_caps_and_zero_queries(cap, dtype):
+    """Scores of 0 and of +-cap, which is nothing: every key weighs the same."""
+    s = make([300, 1, 0, 40], 4, 2, 64, 16, "e5m2", dtype, seed=5)
+    s["q"][0] = 0
+    want, _, tol = reference(s, lse=False, sm_scale=0.0)
+    out = fp8.fp8_attn_decode_paged(*[s[k].to(DEV) for k in ("q", "cache", "table", "lens", "scales")], 16, softcap=cap)
+    torch.cuda.synchronize()
+    assert_close(out, want, tol, f"cap {cap} {dtype}")
