@@ -4,6 +4,7 @@ import torch
 
 import fp8_w8a8_quantized_quantize_amd as fp8
 from tests._attn import F8, make
+from tests._attn_rms import assert_rms, lse_excess, model
 from tests._gpu import DEV, log
 
 pytestmark = pytest.mark.gpu
@@ -50,3 +51,39 @@ def test_equal_values_come_out_as_they_are(D, new, dtype, fmt):
     else:
         half = {FP16: 2.0 ** -11, FP32: 2.0 ** -24}[dtype]
         assert float(((out - want) / want).abs().max()) <= half + 2.0 ** -19
+
+
+SHAPES = [
+    # lens, new, Hq, Hkv, D: both kernels, whole sequences and shares of keys
+    ([33, 90, 64, 7, 12], None, 16, 4, 64), ([577], None, 32, 8, 128), ([300, 1000], None, 6, 3, 256), ([2500], None, 10, 5, 64),
+    ([4000, 9, 2222], None, 16, 4, 128), ([9000], None, 4, 2, 128), ([2000, 130], None, 40, 1, 128),
+    ([500, 140], [130, 40], 4, 2, 128), ([900], [900], 4, 2, 64), ([150, 700], [150, 129], 4, 2, 256), ([4000], [70], 8, 4, 128),
+    ([200, 3000], [4, 3], 8, 2, 128)]
+
+
+@pytest.mark.parametrize("kw", [{}, dict(softcap=20.0), dict(window=100), dict(alibi=True)], ids=str)
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"L{s[0][0]}x{len(s[0])}h{s[2]}d{s[4]}" + (f"n{s[1][0]}" if s[1] else ""))
+def test_mean_square_error(shape, fmt, kw):
+    """No larger than the operands' terms and fp32 explain: one term for bf16 alone, two for the other types and beside
+    log-sum-exp (whose outputs are held to two)."""
+    lens, new, Hq, Hkv, D = shape
+    kw = dict(kw)
+    launch = dict(kw)
+    if kw.get("alibi"):
+        kw["alibi"] = torch.linspace(0.001, 0.3, Hq)
+        del launch["alibi"]
+        launch["alibi_slopes"] = kw["alibi"].to(DEV)
+    if new:
+        launch["max_q"] = max(new)
+    for dtype, terms, want_lse in ((BF16, 1, False), (BF16, 2, True), (FP16, 2, True), (FP32, 2, True), (FP32, 2, False)):
+        s = make(lens, Hq, Hkv, D, 16, fmt, dtype, seed=len(lens) + D, new=new)
+        what = f"{shape} {fmt} {dtype} {kw.keys()} lse={want_lse}"
+        log(f"  {what}")
+        lse = torch.full(s["q"].shape[:2], 7.0, dtype=torch.float32, device=DEV) if want_lse else None
+        out = call(s, decode=new is None, max_len=max(lens), lse=lse, **launch)
+        want, var, ref, lvar = model(s, terms, **kw)
+        assert_rms(out, want, var, dtype, what)
+        if want_lse:
+            x = lse_excess(lse, ref, lvar)
+            assert x <= 1, f"{what}: lse {x:.3g}"
