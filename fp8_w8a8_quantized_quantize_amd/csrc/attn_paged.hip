@@ -118,17 +118,6 @@ __device__ __forceinline__ Run run_of(const StreamArgs& a, const Seq& s, int pre
     return r;
 }
 
-// Inclusive sums over the lanes of a wave.
-__device__ __forceinline__ int wave_scan(int v) {
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // row_shr:1
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);   // row_shr:2
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);   // row_shr:4
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);   // row_shr:8
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
-    return v;
-}
-
 // The sequence in which this workgroup's share starts, the cost before that
 // sequence, and the cost of all: thread i scans sequence i, 256 at a time.
 // Workgroup 0 leaves the starts for the join.

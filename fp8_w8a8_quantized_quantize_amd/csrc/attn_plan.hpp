@@ -130,11 +130,16 @@ inline int64_t tile_splits(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int
     return s;
 }
 
-// Slots for the column tiles of all sequences, laid end to end whatever their
-// new tokens are: sequence b's start at floor(c / kTileCols) + b, c its first
-// column, which leaves it the tiles it needs and one more at the most.  One new
-// token per sequence takes the same number of tiles everywhere.  A unit of work
-// is a slot, a key share and a KV head.
+// Slots for the column tiles of all sequences, end to end whatever their new
+// tokens are; there are rows * group / kTileCols + B at the most.  Every workgroup
+// adds up the tiles of up to kMaxScan sequences to find its own; of more, a
+// sequence has one slot to spare among the others.  (Empty ones in between take
+// CUs in turn with full ones, which shows where the card is filled once: 32 chunks
+// of 16 tokens over 16384 keys 571 us, so 365.)  One new token per sequence takes
+// the same number of tiles everywhere.  A unit of work is a slot, a key share and
+// a KV head.
+constexpr int kMaxScan = 1024;
+
 struct TilePlan {
     int64_t splits, slots, units;
 };

@@ -53,29 +53,58 @@ struct TileArgs {
     PagedAttn p;
     int group;
     int splits;     // workgroups that share a column tile's keys
-    int slots;      // of column tiles
     int row_tiles;  // column tiles of one new row
     int unit0;      // the launch's first of the units (slot, split, KV head)
     float* part_o;    // [rows][Hq][splits][D], with splits > 1
     float2* part_ml;  // [rows][Hq][splits]: reference (log2), sum
     FastDiv by_block, by_group, by_kv_heads, by_splits, by_row_tiles;
 
-    // The first slot of sequence b, whose new rows start at `row`.
-    __device__ __forceinline__ int slot0(int row, int b) const { return (int)((uint32_t)min(row, p.rows) * group / kTileCols) + b; }
 };
 
-// The sequence that a slot is for: the last one that starts at or before it.
-// Starts rise with b, so a wave finds b by 64 probes a step.
-__device__ __forceinline__ int slot_sequence(const TileArgs& a, int slot, int lane) {
+// The column tile of slot `slot`: the sequences' tiles end to end, a sequence's
+// last ones, which see the most keys, first.
+struct TileAt {
+    int b, ct;  // either below 0: none
+};
+
+__device__ __forceinline__ TileAt tile_at(const TileArgs& a, int slot, int lane) {
+    const PagedAttn& p = a.p;
+    if (p.cu_q == nullptr) {  // the same number of tiles everywhere
+        const int b = a.by_row_tiles.of(slot);
+        return TileAt{b, slot - b * a.row_tiles};
+    }
+    if (p.B == 1) {
+        const Seq s = sequence(p, 0);
+        return TileAt{0, (s.nq * a.group + kTileCols - 1) / kTileCols - 1 - slot};
+    }
+    if (p.B <= kMaxScan) {
+        int before = 0;
+        for (int b0 = 0; b0 < p.B; b0 += kWave) {
+            const int b = min(b0 + lane, p.B - 1);
+            const int lo = min(max(p.cu_q[b], 0), p.rows), n = max(min(p.cu_q[b + 1], p.rows) - lo, 0);
+            const int tiles = b0 + lane < p.B ? (int)(((uint32_t)n * a.group + kTileCols - 1) / kTileCols) : 0;
+            const int upto = before + wave_scan(tiles);
+            const uint64_t past = __ballot(upto > slot);
+            if (past) {
+                const int k = __builtin_ctzll(past);
+                return TileAt{b0 + k, __builtin_amdgcn_readlane(upto, k) - 1 - slot};
+            }
+            before = __builtin_amdgcn_readlane(upto, kWave - 1);
+        }
+        return TileAt{-1, 0};
+    }
+    // Too many to add up: sequence b's tiles start at slot floor(c / kTileCols) + b, c its first column, with one slot to
+    // spare at the most.  Starts rise with b, so a wave finds b by 64 probes a step.
+    auto start = [&](int b) { return (int)((uint32_t)min(max(p.cu_q[b], 0), p.rows) * a.group / kTileCols) + b; };
     int b = 0;
-    for (int n = a.p.B; n > 1;) {  // one of n sequences from b on
+    for (int n = p.B; n > 1;) {  // one of n sequences from b on
         const int step = (n + kWave - 1) / kWave, at = lane * step;
-        const uint64_t starts = __ballot(at < n && a.slot0(max(a.p.cu_q[b + min(at, n - 1)], 0), b + at) <= slot);
+        const uint64_t starts = __ballot(at < n && start(b + min(at, n - 1)) <= slot);
         const int last = starts ? (kWave - 1 - __builtin_clzll(starts)) * step : 0;
         b += last;
         n = min(step, n - last);
     }
-    return b;
+    return TileAt{b, slot - start(b)};
 }
 
 // LDS rows are padded by 16 bytes, so that 32 neighbouring rows spread over the
@@ -124,18 +153,17 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int c = lane % 32, h = lane / 32;
-    // KV heads vary fastest (with 8 of them an XCD keeps to one head's keys); every sequence's last column tiles, which
-    // see the most keys, come first.
+    // KV heads vary fastest: with 8 of them an XCD keeps to one head's keys.
     const int unit = a.unit0 + blockIdx.x;
     const int rest = a.by_kv_heads.of(unit), hk = unit - rest * p.Hkv;
     const int nth = a.by_splits.of(rest), split = rest - nth * a.splits;
-    const int slot = a.slots - 1 - nth;
-    const int b = p.cu_q ? slot_sequence(a, slot, lane) : a.by_row_tiles.of(slot);
+    const TileAt at = tile_at(a, nth, lane);
+    const int b = at.b, ct = at.ct;
+    if (b < 0 || ct < 0) return;
     const Seq seq = sequence(p, b);
     const int prefix = p.prefix ? p.prefix[b] : 0;
     const int cols = seq.nq * a.group;
-    const int ct = slot - (p.cu_q ? a.slot0(seq.row0, b) : b * a.row_tiles);
-    if (ct < 0 || ct * kTileCols >= cols) return;  // before the first sequence, or past this one's tiles
+    if (ct * kTileCols >= cols) return;
     const uint32_t C = 2u * p.Hkv * D;
     const int32_t* table = p.block_table + (int64_t)b * p.ld_table;
     const int last_page = max(p.max_blocks - 1, 0);
@@ -451,7 +479,6 @@ hipError_t launch_attn_tiled(const PagedAttn& p, int D, int fmt, int64_t max_q, 
     a.group = p.Hq / p.Hkv;
     const TilePlan t = tile_plan(p.B, p.rows, p.Hq, p.Hkv, D, p.cu_q == nullptr, max_q, max_len);
     a.splits = (int)t.splits;
-    a.slots = (int)t.slots;
     a.row_tiles = (int)ceil_div(a.group, kTileCols);
     a.part_o = static_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)a.splits * p.rows * p.Hq * D);

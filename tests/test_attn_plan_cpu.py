@@ -93,30 +93,27 @@ def test_any_accepted_size():
         check(B, rows, Hq, Hkv, D, max_q, min(all_len, upto(all_len)), all_len, decode)
 
 
-def test_slots_hold_every_column_tile():
-    """The kernel's arithmetic: sequence b's slots start at floor(cu[b] * group / 128) + b; the last sequence that starts
-    at or before a slot owns it."""
+@pytest.mark.parametrize("spare", [False, True])
+def test_slots_hold_every_column_tile(spare):
+    """The kernel's arithmetic: the tiles of the sequences end to end, or, for many sequences, the last one that starts
+    at or before a slot when sequence b starts at floor(cu[b] * group / 128) + b."""
     rng = random.Random(7)
     for _ in range(300):
         B, group = rng.randint(1, 90), rng.choice([1, 2, 3, 8, 16, 127, 128, 129, 300])
-        new = [rng.choice([0, 0, 1, 2, rng.randint(0, 40), rng.randint(0, 700)]) for _ in range(B)]
-        first = rng.choice([0, 0, 5])
-        cu = [first]
+        new = [rng.choice([0, 0, 1, 2, 16, rng.randint(0, 40), rng.randint(0, 700)]) for _ in range(B)]
+        cu = [rng.choice([0, 0, 5])]
         for n in new:
             cu.append(cu[-1] + n)
-        rows = cu[-1] + rng.choice([0, 0, 9])
-        slots = plan("pin_tiled", B, max(rows, 1), group, 1, 128, False, max(rows, 1), 4096)[1]
-        starts = [c * group // 128 + b for b, c in enumerate(cu[:-1])]
+        rows = max(cu[-1] + rng.choice([0, 0, 9]), 1)
+        slots = plan("pin_tiled", B, rows, group, 1, 128, False, rows, 4096)[1]
+        tiles = [-(-n * group // 128) for n in new]
+        starts = [c * group // 128 + b for b, c in enumerate(cu[:-1])] if spare else [sum(tiles[:b]) for b in range(B)]
         seen = set()
         for slot in range(slots):
-            own = [b for b in range(B) if starts[b] <= slot]
-            if not own:
-                continue
-            b, ct = own[-1], slot - starts[own[-1]]
-            if ct * 128 < new[b] * group:
-                assert (b, ct) not in seen
-                seen.add((b, ct))
-        assert len(seen) == sum(-(-n * group // 128) for n in new), (new, group, first)
+            b = max([b for b in range(B) if starts[b] <= slot], default=-1)
+            if b >= 0 and slot - starts[b] < tiles[b]:
+                seen.add((b, slot - starts[b]))
+        assert len(seen) == sum(tiles), (new, group, cu[0])
 
 
 def test_launches_past_a_grid():

@@ -245,3 +245,29 @@ def test_none_turns_a_score_option_off():
     d = fp8.fp8_attn_prefill_paged(q, s["cu"].to(DEV), cache, table, lens, scales, 16, prefix_lens=None, max_q=None, **off)
     torch.cuda.synchronize()
     assert torch.equal(a, b) and torch.equal(c, d)
+
+
+@pytest.mark.parametrize("max_len", [400, 8000])
+@pytest.mark.parametrize("B", [2, 64, 65, 130, 1024, 1025])
+def test_column_tiles_over_batches(B, max_len):
+    """A workgroup finds its column tile by adding up the sequences' tiles, 64 at a time, or, for more than 1024 of them,
+    by their first columns: sequences of none, one and many tiles, empty ones first and last, rows before and behind."""
+    new = [0] * B
+    for b, n in ((B // 3, 70), (B // 2, 300), (B - 2, 1), (B // 2 + 1, 64)):
+        new[min(b, B - 1)] = n
+    for b in range(7, B, 61):
+        new[b] = b % 9
+    lens = [n + (b % 5) * 20 if n else 0 for b, n in enumerate(new)]
+    s = make(lens, 6, 3, 64, 16, "e5m2", BF16, seed=B, new=new)
+    first, owned = 5, sum(new)
+    s["q"] = torch.cat([torch.ones((first, 6, 64), dtype=BF16), s["q"], torch.ones((7, 6, 64), dtype=BF16)])
+    s["cu"] = s["cu"] + first
+    q, cache, table, lens_d, scales = arguments(s)
+    log(f"  tiles of {B} sequences, max_len {max_len}")
+    out = torch.full(q.shape, -5.0, dtype=BF16, device=DEV)
+    fp8.fp8_attn_prefill_paged(q, s["cu"].to(DEV), cache, table, lens_d, scales, 16, max_q=300, max_len=max_len, out=out)
+    torch.cuda.synchronize()
+    want, _, tol = reference(s, lse=False)
+    rows = slice(first, first + owned)
+    assert_close(out[rows], want[rows], tol[rows], "owned rows")
+    assert bool((out[:first] == -5).all()) and bool((out[first + owned:] == -5).all())
