@@ -634,7 +634,8 @@ def fp8_attn_decode_paged(q, cache, block_table, seq_lens, scales, block_size, f
     max_len: the longest sequence's length when the host knows it (plans the
     launch; by default the block table's width).  sm_scale: D ** -0.5 by default.
     softcap, alibi_slopes fp32 [Hq], window: 0 / None for off.  lse: fp32 [B, Hq]
-    that receives the log-sum-exp.  ws: uint8 workspace of at least
+    that receives the log-sum-exp; with it a bfloat16 out is computed from operands
+    of 2^-22, as other types are, without it of 2^-11.  ws: uint8 workspace of at least
     fp8_attn_decode_workspace_bytes(...) bytes, allocated when not given.
     stream: the stream to run on."""
     dt = _kv_dtype(q, "q")
@@ -662,8 +663,8 @@ def fp8_attn_prefill_paged(q, cu_q, cache, block_table, seq_lens, scales, block_
     keys, and the first prefix_lens[b] int32 [B] of them in any case), or every key
     of the sequence when causal is false.  Rows no sequence owns are left as they
     were (uninitialised when out is allocated here).  max_q: the most new tokens of
-    one sequence when the host knows it.  The other arguments as for
-    fp8_attn_decode_paged."""
+    one sequence when the host knows it; by default the launch goes by their mean.
+    The other arguments as for fp8_attn_decode_paged."""
     dt = _kv_dtype(q, "q")
     (T, B, width, Hq, Hkv, D, blocks, ldq, ldo, ld_table, out, qp, cp, sp, tp, lp, ap, op, ep) = _attn_args(
         q, cache, block_table, seq_lens, scales, block_size, alibi_slopes, out, lse)

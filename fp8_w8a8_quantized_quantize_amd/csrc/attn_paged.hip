@@ -13,11 +13,13 @@
 // value is exact in fp16, the key scales move to the query and the value scales
 // to the output.  q_c ks_c and p_j are rounded to fp16 (off by 2^-11 at most),
 // scaled by a power of two first so that nothing underflows that matters (q per
-// column to 2^15, p to 2^8): an eighth of the rounding that bf16 outputs get at
-// the end.  For fp16 and fp32 outputs and for lse, which is fp32 (two_terms),
-// where it would show, each is fed as two fp16 terms, high part and rest (2^-22),
-// at the cost of a second matrix instruction.  Scores, references, sums and outputs are fp32; the sum of p is
-// a product with ones, so numerator and denominator see the same p.
+// column to 2^15, p to 2^8): each an eighth of the rounding that bf16 outputs get
+// at the end, together, in the outputs' mean square, about a quarter of it.  For
+// fp16 and fp32 outputs and for lse, which is fp32 (two_terms), where it would
+// show, each is fed as two fp16 terms, high part and rest (2^-22), at the cost of
+// a second matrix instruction; a call that asks for lse has its output from two
+// terms too.  Scores, references, sums and outputs are fp32; the sum of p is a
+// product with ones, so numerator and denominator see the same p.
 //
 // One pass with a running reference m.  p is 2^8 at the largest score of the
 // first tile, and m moves only when p would pass 2^12 (p stays below 2^13 in
@@ -33,8 +35,8 @@
 // E5M2, a cut-off fp16, the same instruction decodes).
 //
 // The codes come through LDS: whole rows by DMA (16 bytes a lane, D / 16
-// adjacent lanes a row), two tiles in flight per wave, each wave its own ring
-// and its own waits.  Read straight into the operand's registers, a key's row
+// adjacent lanes a row), into a ring of two tiles per wave (four of 64 channels),
+// each wave its own ring and its own waits.  Read straight into the operand's registers, a key's row
 // is touched by lanes 16 apart: every lane is a request of its own, and with
 // about 70 of them outstanding per CU the kernel stood at 4.4 TB/s whatever it
 // computed (131072 tokens x 8 heads of 128: 72 us with the arithmetic taken out;
@@ -50,10 +52,10 @@
 // all items, laid end to end, are cut into equal shares, whatever the lengths
 // are: every workgroup adds up the rounds of all sequences (a scan) and finds
 // its own share.  Workgroups of the same share and neighbouring heads are
-// neighbours in the grid: together they read whole cache rows.  A share's first and last
-// item may be part of one; those parts go to the workspace, and a second kernel
-// joins them, in order, into the rows that were cut.  No wave waits for another
-// workgroup.
+// neighbours in the grid: together they read whole cache rows.  A share's first
+// and last item may be part of one; those parts go to the workspace, and a second
+// kernel joins them, in order, into the rows that were cut (4 to 8 us a call).  No
+// wave waits for another workgroup.
 #include <algorithm>
 #include <type_traits>
 
@@ -201,9 +203,9 @@ __device__ __forceinline__ void dma16(const uint8_t* src, uint8_t* lds) {
     __builtin_amdgcn_global_load_lds(src, lds, 16, 0, 0);
 }
 
-// LDS of a workgroup: every wave's ring of two tiles (K rows, then V rows), the
-// rows' cache offsets and page numbers, and the waves' references and sums; the ring is free again
-// when the waves' outputs are joined in it.
+// LDS of a workgroup: every wave's ring of kStages tiles (K rows, then V rows),
+// the rows' cache offsets and page numbers, and the waves' references and sums;
+// the ring is free again when the waves' outputs are joined in it.
 template <int D>
 struct StreamLds {
     static constexpr int kStages = D == 64 ? 4 : 2;

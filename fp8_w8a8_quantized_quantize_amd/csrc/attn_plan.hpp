@@ -30,14 +30,15 @@ inline auto in_launches(int64_t units, Launch launch) {
 // them, the tiled one once per 128, but has its products wait on LDS.
 // Streaming / tiled, us, 64 / 8 heads of 128, bf16, 16384 keys:
 //     rows            24          32          64          128         512
-//     1 sequence      22.6/23.4   21.4/21.4   25.6/26.1   35.6/35.1   89/59
-//     8 sequences     100/84      99/66       116/85      196/110     616/348
-//     32 sequences    265/288     246/229     412/294     823/386     3922/1452
+//     1 sequence      22.2/22.8   21.1/20.9   25.3/26.5   35.5/37.6   89/63
+//     8 sequences     99/84       100/66      115/84      197/111     622/348
+//     32 sequences    270/289     250/230     420/289     838/382     3980/1322
 // Two-term products (fp16, fp32, lse) fill the tiled kernel's matrix cores twice,
 // and D = 256 leaves it one workgroup a CU; two sequences, 16384 keys:
-//     rows                    24          64          96     128    256
-//     fp16, D = 128           39/55       53/58       55/55  95/64  131/100
-//     bf16, D = 256 (32/8)    39/73 (12)  50/66 (32)                116/80 (128)
+//     rows                    12      24      32      48      64      96     128    256
+//     fp16, D = 128                   34/41                   48/46   57/52  97/62  130/91
+//     bf16, D = 256 (32/8)    39/73           50/64   74/76   74/68          115/81
+//     fp16, D = 256 (32/8)                    43/61   53/68   56/64          89/74
 inline bool attn_tiled(int64_t Hq, int64_t Hkv, int64_t D, int64_t new_rows, bool two_terms) {
     const int64_t columns = new_rows * (Hq / Hkv);
     return two_terms || D == 256 ? columns > 64 : columns >= 32;

@@ -4,34 +4,39 @@
 // Mathematics, operand terms and visibility are those of the streaming form
 // (attn_paged.hip): codes exact in fp16, key scales in the query, value scales
 // at the output, scores transposed so that a lane's results belong to one query
-// column, p straight from the scores' registers into the second product.
+// column, p straight from the scores' registers into the second product.  The
+// sum of p, here on the vector unit, takes p as the product does: with one term
+// rounded to fp16, with two as it is, which they give to 2^-22.
 //
 // Tile.  The columns are a KV head's query rows, token times group, so one pass
 // over the keys serves all query heads of the group.  A workgroup of four waves
 // takes 128 columns, 32 a wave, and walks over 64-key tiles that all its waves
 // share in LDS: K as fp16 rows, V as fp16 transposed, eight keys of a channel in
 // 16 bytes in the order in which a lane holds its p.  Codes become fp16 once per
-// workgroup, on the way into LDS.  D = 128 takes 232 registers and 72 KB of LDS,
-// two workgroups a CU: the softmax of one wave runs beside the matrix work of
-// the other on its SIMD.  64 columns a wave (half the LDS reads per matrix
-// instruction, one wave per SIMD) spilled and took 3.7 ms where this takes 1.17
-// (8192 tokens, 64 / 8 heads of 128, bf16: 940 TFLOP/s), and so did forming the
-// next tile's scores during the softmax (2.3 ms).  Two terms with D = 128 and 256
-// spill some 40 and 170 registers and still beat the streaming form from 96
-// rows on.
+// workgroup, on the way into LDS.  D = 128 takes 200 registers and 72 KB of LDS
+// (two terms 252), two workgroups a CU: the softmax of one wave runs beside the
+// matrix work of the other on its SIMD.  64 columns a wave (half the LDS reads per
+// matrix instruction, one wave per SIMD) spilled and took 3.7 ms where this takes
+// 1.15 to 1.24 by the card's clock (8192 tokens, 64 / 8 heads of 128, bf16: 890 to
+// 960 TFLOP/s), and so did forming the next tile's scores during the softmax (2.3
+// ms).  One workgroup does one unit of work: a loop around it cost up to 40 more
+// registers and, with two terms, spills.  Two terms with D = 256 spill 9 registers,
+// 25 under a bias or a cap.
 //
-// Bound: matrix cores 42 %, vector unit 50 % of the cycles (240 instructions per
+// Bound: matrix cores 42 %, vector unit 49 % of the cycles (230 instructions per
 // 32 columns x 64 keys, 32 of them exponentials, beside 32 matrix instructions
-// of 32 cycles), LDS 41 %; the two waves of a SIMD seldom want different units
+// of 32 cycles), LDS 42 %; the two waves of a SIMD seldom want different units
 // (wave priorities around either phase changed nothing).
 //
 // One barrier per tile: step t writes K and V of tile t into the buffers last
 // read in step t - 2, starts the loads of tile t + 1 into registers, and computes
 // after the barrier.
 //
-// Where column tiles are few, several workgroups share a tile's keys: each
-// leaves its unscaled fp32 sums, its reference and its sum of p in the
-// workspace, and the streaming form's join adds them in their order.
+// Column tiles of all sequences lie end to end in the grid, so its size is the
+// batch's own and no hint is needed for it.  Where they are few, several
+// workgroups share a tile's keys: each leaves its unscaled fp32 sums, its
+// reference and its sum of p in the workspace, and the streaming form's join adds
+// them in their order, row by row.
 #include <algorithm>
 #include <type_traits>
 

@@ -71,7 +71,7 @@ hipError_t launch_kv_append_rope(const KvAppend& p, int dtype, int fmt, bool int
 // Attention over the paged cache (attn_paged.hip).  Sequence b owns q rows
 // [cu_q[b], cu_q[b + 1]) (row b when cu_q is null) of `rows` rows in all;
 // its key j lies in cache row block_table[b][j / block] * block + j % block.
-// scale2: the score scale times log2(e); softcap 0, window 0, alibi null and
+// scale: the score scale times log2(e); softcap 0, window 0, alibi null and
 // prefix null turn those off.  block_table holds one entry and
 // cache one row at least.
 struct PagedAttn {
@@ -91,15 +91,15 @@ struct PagedAttn {
     float scale, softcap;
     int B, rows, Hq, Hkv, block, max_blocks, window, causal, dtype;
 };
-// The streaming form (attn_paged.hip), for few rows per sequence, and the tiled
-// one (attn_prefill.hip), for many.
-// max_q and max_len plan the launch; longer rows and sequences are still
-// computed whole.  ws: attn_paged_ws_bytes bytes (all_len = max_blocks * block),
-// 16-byte aligned.
 // Whether the scaled query and p are fed as two fp16 terms: an fp16 or fp32
 // output, or lse, would show the rounding of one.
 inline bool two_terms(const PagedAttn& p) { return p.dtype != kKvBF16 || p.lse != nullptr; }
 
+// The streaming form (attn_paged.hip), for few rows per sequence, and the tiled
+// one (attn_prefill.hip), for many (attn_plan.hpp says which).  max_q, the most
+// new rows of a sequence, typical, those of most, and max_len plan the launch;
+// more rows and longer sequences are still computed whole.  ws: the matching
+// *_ws_bytes bytes (all_len = max_blocks * block), 16-byte aligned.
 size_t attn_paged_ws_bytes(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_len,
                            int64_t all_len);
 hipError_t launch_attn_paged(const PagedAttn& p, int D, int fmt, int64_t max_q, int64_t typical, int64_t max_len, void* ws,

@@ -409,7 +409,7 @@ fp8_status_t fp8_kv_append_rope_paged(const void* q, int64_t ldq, void* q_out, i
  * lse -inf.  The softmax, its sums and the products accumulate in fp32; out is
  * rounded once, RNE, to q's type.  Codes enter the products exactly; q times the
  * key scales and p as fp16 terms: one where q is bf16 and lse NULL (off by 2^-11
- * of the value at most), else two (2^-22).
+ * of the value at most), else two (2^-22): asking for lse refines out as well.
  * q, out: dtype elements [rows, Hq, D], heads adjacent, row strides ldq, ldo,
  * rows 16-byte aligned; lse fp32 [rows, Hq] or NULL; out does not overlap q.
  * cu_q does not decrease.  cache: u8 [num_blocks * block_size, 2 Hkv D];
@@ -417,8 +417,9 @@ fp8_status_t fp8_kv_append_rope_paged(const void* q, int64_t ldq, void* q_out, i
  * 256 and Hq a multiple of Hkv, Hkv <= 65535; any block_size >= 1; positions,
  * rows * Hq and block_size * max_blocks up to 2^30.
  * max_q and max_len plan the launch: bounds of the new rows and of the length
- * of one sequence, 0 for not known.  They may be wrong: longer sequences are
- * still computed whole, only slower.
+ * of one sequence, 0 for not known (then it goes by T / B and by the table's
+ * width).  They may be wrong: longer sequences are still computed whole, only
+ * slower.
  * The device arrays are not validated: lengths are taken within
  * [0, max_blocks * block_size], rows within [0, T); a page number outside
  * [0, num_blocks) hides its keys.  Rows of q that no sequence owns are left as
