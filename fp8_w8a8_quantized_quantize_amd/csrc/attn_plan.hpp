@@ -131,27 +131,38 @@ inline int64_t tile_splits(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int
     return s;
 }
 
-// Slots for the column tiles of all sequences, end to end whatever their new
-// tokens are; there are rows * group / kTileCols + B at the most.  Every workgroup
-// adds up the tiles of up to kMaxScan sequences to find its own; of more, a
-// sequence has one slot to spare among the others.  (Empty ones in between take
-// CUs in turn with full ones, which shows where the card is filled once: 32 chunks
-// of 16 tokens over 16384 keys 571 us, so 365.)  One new token per sequence takes
-// the same number of tiles everywhere.  A unit of work is a slot, a key share and
-// a KV head.
+// Slots for the column tiles of a ragged batch, of which it has rows * group /
+// kTileCols + B at the most, end to end whatever the sequences' new tokens are, so
+// no hint is needed.  How a workgroup finds its tile, with 64/8 heads:
+//   - the tiles of up to kMaxScan sequences added up, 64 of them at a time, the
+//     empty slots last;
+//   - or, of more than 64 with many workgroups, by the sequences' first columns,
+//     with a slot to spare for each among the others.  Empty ones take CUs in turn
+//     with full ones, which shows where the card is filled once or twice, but there
+//     is less to look up: 32 x 16 tokens over 16384 keys 565 us so and 370 added
+//     up, 300 x 64 over 100 keys 349 and 371;
+//   - where by max_q one tile each will do, those come first and only the others,
+//     if any, are looked for: 1024 x 8 over 512 keys 441 us, 465 by first columns,
+//     473 all added up.
+// One new token per sequence takes the same number of tiles everywhere.  A unit of
+// work is a slot, a key share and a KV head.
 constexpr int kMaxScan = 1024;
 
 struct TilePlan {
-    int64_t splits, slots, units;
+    int64_t splits, col_tiles, slots, units;
+    bool exact;
 };
 
 inline TilePlan tile_plan(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, bool decode, int64_t max_q,
                           int64_t max_len) {
-    const int64_t group = Hq / Hkv;
+    const int64_t group = Hq / Hkv, each = ceil_div(max_q * group, kTileCols);
     TilePlan t;
     t.splits = tile_splits(B, rows, Hq, Hkv, D, max_q, max_len);
-    t.slots = decode ? B * ceil_div(group, kTileCols) : rows * group / kTileCols + B;
+    // each sequence's tiles but the first are fewer than its columns / kTileCols, so one tile each leaves slots for them
+    t.slots = decode ? B * each : rows * group / kTileCols + B;
+    t.col_tiles = decode ? each : each == 1 && B <= kMaxScan ? 1 : 0;
     t.units = t.slots * Hkv * t.splits;
+    t.exact = B <= 64 || (B <= kMaxScan && (t.col_tiles > 0 || t.units <= 8 * 512));
     return t;
 }
 

@@ -58,49 +58,59 @@ struct TileArgs {
     PagedAttn p;
     int group;
     int splits;     // workgroups that share a column tile's keys
-    int row_tiles;  // column tiles of one new row
+    int col_tiles;  // column tiles laid out for every sequence, 0: none
+    bool exact;     // no slot to spare among the others
+    int slots;
     int unit0;      // the launch's first of the units (slot, split, KV head)
     float* part_o;    // [rows][Hq][splits][D], with splits > 1
     float2* part_ml;  // [rows][Hq][splits]: reference (log2), sum
-    FastDiv by_block, by_group, by_kv_heads, by_splits, by_row_tiles;
-
+    FastDiv by_block, by_group, by_kv_heads, by_splits, by_batch;
 };
 
-// The column tile of slot `slot`: the sequences' tiles end to end, a sequence's
-// last ones, which see the most keys, first.
+// The column tile of slot `slot`.  The first slots are for the tiles laid out for
+// every sequence, the last ones, which see the most keys, first; then come all
+// other tiles, the sequences' end to end.
 struct TileAt {
-    int b, ct;  // either below 0: none
+    int b, ct;  // b < 0, or ct below 0 or past the sequence's tiles: none
 };
 
 __device__ __forceinline__ TileAt tile_at(const TileArgs& a, int slot, int lane) {
     const PagedAttn& p = a.p;
-    if (p.cu_q == nullptr) {  // the same number of tiles everywhere
-        const int b = a.by_row_tiles.of(slot);
-        return TileAt{b, slot - b * a.row_tiles};
+    if (slot < p.B * a.col_tiles) {
+        const int tile = a.by_batch.of(slot);
+        return TileAt{slot - tile * p.B, a.col_tiles - 1 - tile};
     }
+    slot -= p.B * a.col_tiles;
     if (p.B == 1) {
         const Seq s = sequence(p, 0);
         return TileAt{0, (s.nq * a.group + kTileCols - 1) / kTileCols - 1 - slot};
     }
-    if (p.B <= kMaxScan) {
-        int before = 0;
-        for (int b0 = 0; b0 < p.B; b0 += kWave) {
-            const int b = min(b0 + lane, p.B - 1);
-            const int lo = min(max(p.cu_q[b], 0), p.rows), n = max(min(p.cu_q[b + 1], p.rows) - lo, 0);
-            const int tiles = b0 + lane < p.B ? (int)(((uint32_t)n * a.group + kTileCols - 1) / kTileCols) : 0;
-            const int upto = before + wave_scan(tiles);
-            const uint64_t past = __ballot(upto > slot);
-            if (past) {
-                const int k = __builtin_ctzll(past);
-                return TileAt{b0 + k, __builtin_amdgcn_readlane(upto, k) - 1 - slot};
-            }
-            before = __builtin_amdgcn_readlane(upto, kWave - 1);
-        }
-        return TileAt{-1, 0};
+    if (a.exact) {
+        auto others = [&](int b) {
+            // past the last sequence both are its end; a branch would wait for every load by itself
+            const int lo = min(max(p.cu_q[min(b, p.B)], 0), p.rows), hi = min(p.cu_q[min(b + 1, p.B)], p.rows);
+            return max((int)(((uint32_t)max(hi - lo, 0) * a.group + kTileCols - 1) / kTileCols) - a.col_tiles, 0);
+        };
+        // lane l adds up the sequences 64 i + l, which come before lane l + 1's
+        int mine = 0;
+#pragma unroll 8
+        for (int b0 = 0; b0 < p.B; b0 += kWave) mine += others(b0 + lane);
+        int upto = wave_scan(mine);
+        uint64_t past = __ballot(upto > slot);
+        if (past == 0) return TileAt{-1, 0};
+        const int l = __builtin_ctzll(past);
+        if (p.B <= kWave) return TileAt{l, a.col_tiles + __builtin_amdgcn_readlane(upto, l) - 1 - slot};
+        // and then lane i stands for sequence 64 i + l
+        slot -= __builtin_amdgcn_readlane(upto - mine, l);
+        upto = wave_scan(others(kWave * lane + l));
+        past = __ballot(upto > slot);
+        const int i = past ? __builtin_ctzll(past) : 0;
+        return TileAt{kWave * i + l, a.col_tiles + __builtin_amdgcn_readlane(upto, i) - 1 - slot};
     }
-    // Too many to add up: sequence b's tiles start at slot floor(c / kTileCols) + b, c its first column, with one slot to
+    // Or not added up: sequence b's tiles start at slot floor(c / kTileCols) + b, c its first column, with one slot to
     // spare at the most.  Starts rise with b, so a wave finds b by 64 probes a step.
     auto start = [&](int b) { return (int)((uint32_t)min(max(p.cu_q[b], 0), p.rows) * a.group / kTileCols) + b; };
+    slot = a.slots - 1 - slot;  // every sequence's last tile first
     int b = 0;
     for (int n = p.B; n > 1;) {  // one of n sequences from b on
         const int step = (n + kWave - 1) / kWave, at = lane * step;
@@ -164,11 +174,11 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
     const int nth = a.by_splits.of(rest), split = rest - nth * a.splits;
     const TileAt at = tile_at(a, nth, lane);
     const int b = at.b, ct = at.ct;
-    if (b < 0 || ct < 0) return;
+    if (b < 0) return;
     const Seq seq = sequence(p, b);
     const int prefix = p.prefix ? p.prefix[b] : 0;
     const int cols = seq.nq * a.group;
-    if (ct * kTileCols >= cols) return;
+    if ((uint32_t)ct >= (uint32_t)((cols + kTileCols - 1) / kTileCols)) return;
     const uint32_t C = 2u * p.Hkv * D;
     const int32_t* table = p.block_table + (int64_t)b * p.ld_table;
     const int last_page = max(p.max_blocks - 1, 0);
@@ -484,14 +494,16 @@ hipError_t launch_attn_tiled(const PagedAttn& p, int D, int fmt, int64_t max_q, 
     a.group = p.Hq / p.Hkv;
     const TilePlan t = tile_plan(p.B, p.rows, p.Hq, p.Hkv, D, p.cu_q == nullptr, max_q, max_len);
     a.splits = (int)t.splits;
-    a.row_tiles = (int)ceil_div(a.group, kTileCols);
+    a.col_tiles = (int)t.col_tiles;
+    a.exact = t.exact;
+    a.slots = (int)t.slots;
     a.part_o = static_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)a.splits * p.rows * p.Hq * D);
     a.by_block = FastDiv(p.block);
     a.by_group = FastDiv(a.group);
     a.by_kv_heads = FastDiv(p.Hkv);
     a.by_splits = FastDiv(a.splits);
-    a.by_row_tiles = FastDiv(a.row_tiles);
+    a.by_batch = FastDiv(p.B);
     const bool one = !two_terms(p);
     hipError_t e;
     switch (D) {

@@ -15,11 +15,11 @@ void pin_stream(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int
     out[0] = s.units, out[1] = s.rows_y, out[2] = s.shares;
 }
 
-/* units, slots, splits */
+/* units, slots, splits, column tiles laid out for every sequence (and 1000 when the others are added up) */
 void pin_tiled(int64_t B, int64_t rows, int64_t Hq, int64_t Hkv, int64_t D, int64_t decode, int64_t max_q, int64_t max_len,
                int64_t* out) {
     const fp8k::TilePlan t = fp8k::tile_plan(B, rows, Hq, Hkv, D, decode != 0, max_q, max_len);
-    out[0] = t.units, out[1] = t.slots, out[2] = t.splits;
+    out[0] = t.units, out[1] = t.slots, out[2] = t.splits, out[3] = t.col_tiles + (t.exact ? 1000 : 0);
 }
 
 /* units, rows a sequence, thread groups a row */

@@ -1,6 +1,7 @@
 """How the attention calls are divided into workgroups, on the host: grids that the runtime takes (less than 2^32
 threads along an axis) at every size the entry points accept, whatever the launch hints say, and slots that hold every
 column tile of a ragged batch."""
+import bisect
 import ctypes
 import os
 import random
@@ -71,8 +72,8 @@ def test_ragged_batches_without_a_hint(T, B, D):
 def test_largest_sizes(B, rows, Hq, Hkv, max_q, all_len, D):
     Hq = Hq // Hkv * Hkv
     for max_len in (1, min(700, all_len), all_len):
-        for decode in (False, True):
-            check(B, rows, Hq, Hkv, D, max_q, max_len, all_len, decode)
+        check(B, rows, Hq, Hkv, D, max_q, max_len, all_len, False)
+        check(B, B, Hq, Hkv, D, 1, max_len, all_len, True)
 
 
 def test_any_accepted_size():
@@ -93,27 +94,42 @@ def test_any_accepted_size():
         check(B, rows, Hq, Hkv, D, max_q, min(all_len, upto(all_len)), all_len, decode)
 
 
-@pytest.mark.parametrize("spare", [False, True])
-def test_slots_hold_every_column_tile(spare):
-    """The kernel's arithmetic: the tiles of the sequences end to end, or, for many sequences, the last one that starts
-    at or before a slot when sequence b starts at floor(cu[b] * group / 128) + b."""
+@pytest.mark.parametrize("Hkv,most", [(1, 90), (400, 90), (2, 1500)])
+def test_slots_hold_every_column_tile(Hkv, most):
+    """The kernel's arithmetic: a first tile for every sequence where the hint, right or wrong, says that one will do, and
+    all others end to end; or the last sequence that starts at or before a slot, when b starts at
+    floor(cu[b] * group / 128) + b."""
     rng = random.Random(7)
-    for _ in range(300):
-        B, group = rng.randint(1, 90), rng.choice([1, 2, 3, 8, 16, 127, 128, 129, 300])
+    forms = set()
+    for _ in range(300 if most < 100 else 12):
+        B, group = rng.randint(1, most), rng.choice([1, 2, 3, 8, 16, 127, 128, 129, 300])
         new = [rng.choice([0, 0, 1, 2, 16, rng.randint(0, 40), rng.randint(0, 700)]) for _ in range(B)]
+        if rng.random() < 0.3:
+            new = [rng.randint(max(0, new[0] - 2), new[0]) for _ in range(B)]
         cu = [rng.choice([0, 0, 5])]
         for n in new:
             cu.append(cu[-1] + n)
         rows = max(cu[-1] + rng.choice([0, 0, 9]), 1)
-        slots = plan("pin_tiled", B, rows, group, 1, 128, False, rows, 4096)[1]
+        hint = max(1, min(rows, rng.choice([rows, max(new), max(new), 1, 20])))
+        slots, _, form = plan("pin_tiled", B, rows, group * Hkv, Hkv, 128, False, hint, 4096)[1:]
+        exact, each = form >= 1000, form % 1000
+        forms.add((exact, each))
         tiles = [-(-n * group // 128) for n in new]
-        starts = [c * group // 128 + b for b, c in enumerate(cu[:-1])] if spare else [sum(tiles[:b]) for b in range(B)]
-        seen = set()
-        for slot in range(slots):
-            b = max([b for b in range(B) if starts[b] <= slot], default=-1)
-            if b >= 0 and slot - starts[b] < tiles[b]:
-                seen.add((b, slot - starts[b]))
-        assert len(seen) == sum(tiles), (new, group, cu[0])
+        others = [max(t - each, 0) for t in tiles]
+        starts = [c * group // 128 + b for b, c in enumerate(cu[:-1])]
+        if exact:
+            starts = [0]
+            for t in others:
+                starts.append(starts[-1] + t)
+        seen = [(slot % B, each - 1 - slot // B) for slot in range(B * each)]
+        seen = [(b, ct) for b, ct in seen if ct < tiles[b]]
+        for slot in range(slots - B * each):
+            slot = slot if exact else slots - 1 - slot
+            b = bisect.bisect_right(starts, slot, 0, B) - 1
+            if b >= 0 and slot - starts[b] < others[b]:
+                seen.append((b, each + slot - starts[b]))
+        assert sorted(seen) == [(b, ct) for b in range(B) for ct in range(tiles[b])], (new, group, cu[0], hint)
+    assert len(forms) > 1
 
 
 def test_launches_past_a_grid():
