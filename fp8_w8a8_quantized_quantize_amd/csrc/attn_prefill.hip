@@ -83,7 +83,8 @@ __device__ __forceinline__ TileAt tile_at(const TileArgs& a, int slot, int lane)
     slot -= p.B * a.col_tiles;
     if (p.B == 1) {
         const Seq s = sequence(p, 0);
-        return TileAt{0, (s.nq * a.group + kTileCols - 1) / kTileCols - 1 - slot};
+        const int ct = (s.nq * a.group + kTileCols - 1) / kTileCols - 1 - slot;
+        return TileAt{ct >= a.col_tiles ? 0 : -1, ct};
     }
     if (a.exact) {
         auto others = [&](int b) {
