@@ -249,7 +249,7 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
     if (p.softcap > 0.0f) cs *= kLn2;  // the cap takes the natural score
     const float cap_in = cap_factor(p.softcap);
 
-    float m = 0.0f, l = 0.0f, limit = kNoRef;
+    float m = 0.0f, l = 0.0f, l2 = 0.0f, limit = kNoRef;
     v16f o[DB];
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -376,6 +376,7 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
             m += by;
             limit = move ? P::kLimit : limit;
             l *= f;
+            l2 *= f;
 #pragma unroll
             for (int d = 0; d < DB; ++d) o[d] *= f;
 #pragma unroll
@@ -398,10 +399,14 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
             if constexpr (TERMS == 1) {
                 // The sum takes p as the product does, rounded to fp16, or the rounding would not cancel.  Two at a time,
                 // fp16 subnormals kept, off by 3 2^-24 of the result at most and without bias (measured on random sums);
-                // converted back and added one by one the 8192-token prompt took 1233 us, so 1176.
+                // converted back and added one by one the 8192-token prompt took 1233 us, so 1176.  Two running sums: with
+                // one, 1200 tokens over 2048 keys took 165 us, with four 157, so 156.
                 const v2h one = {1, 1};
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) l = __builtin_amdgcn_fdot2(v2h{ph[0][e], ph[0][e + 1]}, one, l, false);
+                for (int e = 0; e < 8; e += 4) {
+                    l = __builtin_amdgcn_fdot2(v2h{ph[0][e], ph[0][e + 1]}, one, l, false);
+                    l2 = __builtin_amdgcn_fdot2(v2h{ph[0][e + 2], ph[0][e + 3]}, one, l2, false);
+                }
             }
 #pragma unroll
             for (int db = 0; db < DB; ++db) {
@@ -441,6 +446,7 @@ __global__ __launch_bounds__(kThreadsT, D == 256 ? 1 : 2) void attn_tile(TileArg
     }
 
     // ---- results
+    l += l2;
     l += swap32(l);
     if (has) {
         const int64_t at = (row * p.Hq + head) * a.splits + split;
