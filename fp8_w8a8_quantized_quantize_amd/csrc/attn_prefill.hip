@@ -14,16 +14,16 @@
 // share in LDS: K as fp16 rows, V as fp16 transposed, eight keys of a channel in
 // 16 bytes in the order in which a lane holds its p.  Codes become fp16 once per
 // workgroup, on the way into LDS.  D = 128 takes 200 registers and 72 KB of LDS
-// (two terms 252), two workgroups a CU: the softmax of one wave runs beside the
+// (two terms 255), two workgroups a CU: the softmax of one wave runs beside the
 // matrix work of the other on its SIMD.  64 columns a wave (half the LDS reads per
 // matrix instruction, one wave per SIMD) spilled and took 3.7 ms where this takes
 // 1.15 to 1.24 by the card's clock (8192 tokens, 64 / 8 heads of 128, bf16: 890 to
 // 960 TFLOP/s), and so did forming the next tile's scores during the softmax (2.3
 // ms).  One workgroup does one unit of work: a loop around it cost up to 40 more
 // registers and, with two terms, spills.  Two terms with D = 256 spill 9 registers,
-// 25 under a bias or a cap.
+// 27 under a bias or a cap.
 //
-// Bound: matrix cores 42 %, vector unit 49 % of the cycles (230 instructions per
+// Bound: matrix cores 42 %, vector unit 48 % of the cycles (230 instructions per
 // 32 columns x 64 keys, 32 of them exponentials, beside 32 matrix instructions
 // of 32 cycles), LDS 42 %; the two waves of a SIMD seldom want different units
 // (wave priorities around either phase changed nothing).
@@ -33,7 +33,7 @@
 // after the barrier.
 //
 // Column tiles of all sequences lie end to end in the grid, so its size is the
-// batch's own and no hint is needed for it.  Where they are few, several
+// batch's own whatever the hint says.  Where they are few, several
 // workgroups share a tile's keys: each leaves its unscaled fp32 sums, its
 // reference and its sum of p in the workspace, and the streaming form's join adds
 // them in their order, row by row.
