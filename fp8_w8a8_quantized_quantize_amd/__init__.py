@@ -18,6 +18,13 @@ Entry points (same names as the C ABI):
   fp8_kv_append_rope_paged(k, v, positions, cos_sin, scales, slot_mapping, cache, q=q) -> q_out  rotate + FP8 append
   fp8_attn_decode_paged(q, cache, block_table, seq_lens, scales, block_size)  -> out  one new token per sequence
   fp8_attn_prefill_paged(q, cu_q, cache, block_table, seq_lens, scales, block_size) -> out  several new tokens
+  fp8_gemm_scaled_act(qa, s_tok, qw, s_ch, bias, act, residual) -> y [M,N]  bias, activation, residual in the epilogue
+  fp8_gemm_grouped_scaled_act(qa, s_tok, row_token, expert_offsets, qw, s_ch, bias, act) -> y [R,N]
+  fp8_act_quantize(h, act, gated)          -> (q uint8 [M,F], scales fp32 [M])  (gated) activation, quantized per token
+  fp8_moe_sort(expert_ids, num_experts)    -> (expert_offsets, row_token, row_of)  choices in the experts' order
+  fp8_moe_permute(x, row_of)               -> out [R,H]  tokens moved into that order
+  fp8_moe_combine(y, row_of, weights, residual) -> out [T,H]  the experts' rows back to their tokens
+  fp8_moe_combine_grad(dout, y, row_of, weights) -> (dy [R,H], dweights fp32 [T,topk])
   fp8_workspace_bytes(M, N, K) (fused call), fp8_gemm_workspace_bytes(M, N, K),
   fp8_fp8out_workspace_bytes(M, N, K), fp8_grouped_workspace_bytes(T, R, E, N, K)
   fp8_status_string(code)
@@ -43,6 +50,8 @@ EXPORTS = ("fp8_quantize_per_token", "fp8_quantize_static", "fp8_quantize_per_to
            "fp8_kv_channel_scales", "fp8_kv_scales_workspace_bytes",
            "fp8_kv_quantize_paged", "fp8_kv_dequantize_paged", "fp8_kv_append_rope_paged", "fp8_attn_decode_paged",
            "fp8_attn_prefill_paged", "fp8_attn_decode_workspace_bytes", "fp8_attn_prefill_workspace_bytes",
+           "fp8_gemm_scaled_act", "fp8_gemm_act_workspace_bytes", "fp8_gemm_grouped_scaled_act", "fp8_act_quantize",
+           "fp8_moe_sort", "fp8_moe_sort_workspace_bytes", "fp8_moe_permute", "fp8_moe_combine", "fp8_moe_combine_grad",
            "fp8_stream_read", "fp8_quant_gemm_fused_noalloc",
            "fp8_status_string")
 
@@ -120,6 +129,26 @@ def lib():
                                              i64, i64, i64, i64, i32, vp, f32, f32, vp, i64, vp, i64, vp, vp, sz, vp]
         L.fp8_quant_gemm_fused_noalloc.restype = st
         L.fp8_quant_gemm_fused_noalloc.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, i64, i64, vp, vp, vp]
+        L.fp8_gemm_act_workspace_bytes.restype = sz
+        L.fp8_gemm_act_workspace_bytes.argtypes = [i64, i64, i64]
+        L.fp8_gemm_scaled_act.restype = st
+        L.fp8_gemm_scaled_act.argtypes = [vp, i64, vp, vp, i64, vp, vp, st, vp, i64, vp, st, i64, i64, i64, i64, vp, sz,
+                                          vp]
+        L.fp8_gemm_grouped_scaled_act.restype = st
+        L.fp8_gemm_grouped_scaled_act.argtypes = [vp, vp, vp, vp, vp, vp, vp, st, vp, st, i64, i64, i64, i64, i64, i64,
+                                                  vp, sz, vp]
+        L.fp8_act_quantize.restype = st
+        L.fp8_act_quantize.argtypes = [vp, i64, st, i64, i64, st, i32, vp, i64, vp, vp, vp]
+        L.fp8_moe_sort_workspace_bytes.restype = sz
+        L.fp8_moe_sort_workspace_bytes.argtypes = [i64, i64, i64]
+        L.fp8_moe_sort.restype = st
+        L.fp8_moe_sort.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, sz, vp]
+        L.fp8_moe_permute.restype = st
+        L.fp8_moe_permute.argtypes = [vp, i64, vp, vp, i64, i64, i64, i64, i64, vp, i64, vp, vp]
+        L.fp8_moe_combine.restype = st
+        L.fp8_moe_combine.argtypes = [vp, i64, st, vp, vp, vp, i64, vp, st, i64, i64, i64, i64, i64, vp]
+        L.fp8_moe_combine_grad.restype = st
+        L.fp8_moe_combine_grad.argtypes = [vp, i64, st, vp, i64, st, vp, vp, vp, i64, vp, i64, i64, i64, i64, vp]
         L.fp8_stream_read.restype = st
         L.fp8_stream_read.argtypes = [vp, sz, ctypes.c_int32, ctypes.c_int32, vp, vp]
         L.fp8_status_string.restype = ctypes.c_char_p
@@ -831,6 +860,295 @@ def fp8_gemm_grouped_scaled(qa, s_tok, row_token, expert_offsets, qw, s_ch, y=No
            lib().fp8_gemm_grouped_scaled(_ptr(qa), _ptr(s_tok), _ptr(row_token), _ptr(expert_offsets), _ptr(qw),
                                          _ptr(s_ch), _ptr(y), T, R, E, N, K, _ptr(ws), _nbytes(ws), _stream(stream)))
     return y
+
+
+FP8_ACT_NONE = 0
+FP8_ACT_RELU = 1
+FP8_ACT_SILU = 2
+FP8_ACT_GELU = 3
+FP8_ACT_GELU_TANH = 4
+_ACTS = {None: FP8_ACT_NONE, "none": FP8_ACT_NONE, "relu": FP8_ACT_RELU, "silu": FP8_ACT_SILU, "gelu": FP8_ACT_GELU,
+         "gelu_tanh": FP8_ACT_GELU_TANH}
+_ACTS.update({v: v for v in list(_ACTS.values())})
+
+
+def _act(act):
+    if act not in _ACTS:
+        raise ValueError(f"act: expected 'none', 'relu', 'silu', 'gelu' or 'gelu_tanh', got {act!r}")
+    return _ACTS[act]
+
+
+# Like the attention calls, the calls below run on the device and stream of their
+# first argument and check a tensor's facts once.
+
+def _mat(t, name, di, dtype=None, cols=None, rows=None):
+    """A 2-D row-major tensor on device number di, of dtype, rows and cols when given -> (rows, cols, row stride, address)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or (dtype is not None and t.dtype is not dtype):
+        raise TypeError(f"{name}: expected a {dtype or 'CUDA'} CUDA tensor" if dtype else f"{name}: expected a CUDA tensor")
+    if t.get_device() != di:
+        raise ValueError(f"{name}: on {t.device}, expected device {di}")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D row-major tensor (unit stride along the last dim)")
+    n, c = t.shape
+    s0, s1 = t.stride()
+    if s1 != 1 and c > 1 and n > 0:
+        raise ValueError(f"{name}: expected a 2-D row-major tensor (unit stride along the last dim)")
+    if (rows is not None and n != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name}: expected shape [{'*' if rows is None else rows}, {'*' if cols is None else cols}]")
+    return n, c, (s0 if n > 1 else c), t.data_ptr()
+
+
+_DTYPE_CODES = {}
+
+
+def _dtype_code(dtype, name):
+    """fp8_kv_dtype_t of a row element type."""
+    if not _DTYPE_CODES:
+        torch = _torch()
+        _DTYPE_CODES.update({torch.float32: FP8_KV_F32, torch.bfloat16: FP8_KV_BF16, torch.float16: FP8_KV_F16})
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"{name}: expected float32, bfloat16 or float16")
+    return code
+
+
+def fp8_gemm_act_workspace_bytes(M, N, K):
+    """Workspace bytes of fp8_gemm_scaled_act."""
+    return int(lib().fp8_gemm_act_workspace_bytes(M, N, K))
+
+
+def _y_type(y, y_dtype, residual):
+    """The output's type: y's, else y_dtype, else the residual's, else bfloat16."""
+    if y is not None:
+        return y.dtype
+    return y_dtype or (residual.dtype if residual is not None else _torch().bfloat16)
+
+
+@_on_stream
+def fp8_gemm_scaled_act(qa, s_tok, qw, s_ch, bias=None, act="none", residual=None, y=None, y_dtype=None, ws=None):
+    """y[m,n] = round(act(sum_k e4m3(qa[m,k]) e4m3(qw[n,k]) * s_tok[m] * s_ch[n] + bias[n]) + residual[m,n]).
+
+    bias: fp32 [N] or None.  act: 'none', 'relu', 'silu', 'gelu' (erf) or 'gelu_tanh'.
+    residual: [M, N] in y's type or None; it may be y itself.  y: [M, N] float32,
+    bfloat16 or float16 with any row stride; allocated when not given, in y_dtype
+    (by default the residual's type, else bfloat16).  ws: uint8 workspace of at least
+    fp8_gemm_act_workspace_bytes(M, N, K) bytes, allocated when not given.
+    stream: the stream to run on."""
+    torch = _torch()
+    di, u8, f32 = qa.get_device(), torch.uint8, torch.float32
+    M, K, lda, qp = _mat(qa, "qa", di, u8)
+    N, _, ldw, wp = _mat(qw, "qw", di, u8, cols=K)
+    tp, cp = _flat(s_tok, f32, "s_tok", M, di), _flat(s_ch, f32, "s_ch", N, di)
+    bp = 0 if bias is None else _flat(bias, f32, "bias", N, di)
+    dtype = _y_type(y, y_dtype, residual)
+    code = _dtype_code(dtype, "y")
+    if y is None:
+        y = torch.empty((M, N), dtype=dtype, device=qa.device)
+    _, _, ldy, yp = _mat(y, "y", di, dtype, N, M)
+    ldr = rp = 0
+    if residual is not None:
+        _, _, ldr, rp = _mat(residual, "residual", di, dtype, N, M)
+    ws, wsp, wsn = _attn_ws(ws, fp8_gemm_act_workspace_bytes(M, N, K), qa.device)
+    _check("fp8_gemm_scaled_act",
+           lib().fp8_gemm_scaled_act(qp, lda, tp, wp, ldw, cp, bp, _act(act), rp, ldr, yp, code, ldy, M, N, K, wsp, wsn,
+                                     _raw_stream(di)))
+    return y
+
+
+@_on_stream
+def fp8_gemm_grouped_scaled_act(qa, s_tok, row_token, expert_offsets, qw, s_ch, bias=None, act="none", y=None,
+                                y_dtype=None, ws=None):
+    """The expert product over rows sorted by expert, with an epilogue: row r of expert e is
+    y[r,n] = round(act(sum_k e4m3(qa[t,k]) e4m3(qw[e,n,k]) * s_tok[t] * s_ch[e,n] + bias[e,n])), t = row_token[r].
+
+    qa uint8 [T, K], qw uint8 [E, N, K], s_ch and bias fp32 [E, N] (bias may be
+    None), row_token int32 [R], expert_offsets int32 [E + 1] as fp8_moe_sort gives
+    them; rows from expert_offsets[E] on are left as they were (uninitialised when y
+    is allocated here).  y and y_dtype as for fp8_gemm_scaled_act."""
+    torch = _torch()
+    di, u8, f32, i32 = qa.get_device(), torch.uint8, torch.float32, torch.int32
+    T, K, _, qp = _mat(qa, "qa", di, u8)
+    if not qa.is_contiguous():
+        raise ValueError("qa: expected contiguous [T, K]")
+    _on_device(qw, u8, "qw", qa.device)
+    if qw.dim() != 3 or not qw.is_contiguous() or qw.shape[2] != K:
+        raise ValueError("qw: expected a contiguous uint8 CUDA tensor [E, N, K] with qa's K")
+    E, N, _ = qw.shape
+    _on_device(row_token, i32, "row_token", qa.device)
+    R = row_token.numel()
+    tp, rp = _flat(s_tok, f32, "s_tok", T, di), _flat(row_token, i32, "row_token", R, di)
+    op = _flat(expert_offsets, i32, "expert_offsets", E + 1, di)
+    cp = _flat(s_ch, f32, "s_ch", E * N, di)
+    bp = 0 if bias is None else _flat(bias, f32, "bias", E * N, di)
+    dtype = _y_type(y, y_dtype, None)
+    code = _dtype_code(dtype, "y")
+    if y is None:
+        y = torch.empty((R, N), dtype=dtype, device=qa.device)
+    _, _, ldy, yp = _mat(y, "y", di, dtype, N, R)
+    ws, wsp, wsn = _attn_ws(ws, fp8_grouped_workspace_bytes(T, R, E, N, K), qa.device)
+    _check("fp8_gemm_grouped_scaled_act",
+           lib().fp8_gemm_grouped_scaled_act(qp, tp, rp, op, qw.data_ptr(), cp, bp, _act(act), yp, code, ldy, T, R, E, N,
+                                             K, wsp, wsn, _raw_stream(di)))
+    return y
+
+
+@_on_stream
+def fp8_act_quantize(h, act="silu", gated=True, q=None, scales=None, live_rows=None):
+    """v = act(h[:, :F]) * h[:, F:] (gated) or act(h), quantized per token to E4M3 ->
+    (q uint8 [M, F], scales fp32 [M]).
+
+    h: [M, 2 F] (gated) or [M, F], float32, bfloat16 or float16.  live_rows: int32
+    tensor of one element on the device (e.g. expert_offsets[-1:]): rows from it on
+    are left as they were (uninitialised when q is allocated here)."""
+    torch = _torch()
+    di = h.get_device()
+    code = _dtype_code(h.dtype, "h")
+    M, C, ldh, hp = _mat(h, "h", di)
+    if gated and C % 2:
+        raise ValueError("h: expected [M, 2 F] (gated)")
+    F = C // 2 if gated else C
+    if q is None:
+        q = torch.empty((M, F), dtype=torch.uint8, device=h.device)
+    if scales is None:
+        scales = torch.empty(M, dtype=torch.float32, device=h.device)
+    _, _, ldq, qp = _mat(q, "q", di, torch.uint8, F, M)
+    lp = 0 if live_rows is None else _flat(live_rows, torch.int32, "live_rows", 1, di)
+    _check("fp8_act_quantize",
+           lib().fp8_act_quantize(hp, ldh, code, M, F, _act(act), 1 if gated else 0, qp, ldq,
+                                  _flat(scales, torch.float32, "scales", M, di), lp, _raw_stream(di)))
+    return q, scales
+
+
+def fp8_moe_sort_workspace_bytes(T, topk, E):
+    """Workspace bytes of fp8_moe_sort."""
+    return int(lib().fp8_moe_sort_workspace_bytes(T, topk, E))
+
+
+@_on_stream
+def fp8_moe_sort(expert_ids, num_experts, expert_offsets=None, row_token=None, row_of=None, ws=None):
+    """The choices expert_ids [T, topk] (int32 or int64, contiguous) in the stable order of
+    their experts -> (expert_offsets int32 [num_experts + 1], row_token int32 [T * topk],
+    row_of int32 [T, topk]): choice (t, j) is row row_of[t, j] of token
+    row_token[row] == t.  An id outside [0, num_experts) has row_of -1; row_token is -1
+    from row expert_offsets[num_experts] on."""
+    torch = _torch()
+    di, i32 = expert_ids.get_device(), torch.int32
+    if expert_ids.dtype is not i32 and expert_ids.dtype is not torch.int64:
+        raise TypeError("expert_ids: expected an int32 or int64 CUDA tensor")
+    if expert_ids.dim() != 2 or not expert_ids.is_contiguous():
+        raise ValueError("expert_ids: expected a contiguous tensor [T, topk]")
+    T, topk = expert_ids.shape
+    R = T * topk
+    if expert_offsets is None:
+        expert_offsets = torch.empty(max(num_experts, 0) + 1, dtype=i32, device=expert_ids.device)
+    if row_token is None:
+        row_token = torch.empty(R, dtype=i32, device=expert_ids.device)
+    if row_of is None:
+        row_of = torch.empty((T, topk), dtype=i32, device=expert_ids.device)
+    op = _flat(expert_offsets, i32, "expert_offsets", max(num_experts, 0) + 1, di)
+    ws, wsp, wsn = _attn_ws(ws, fp8_moe_sort_workspace_bytes(T, topk, num_experts), expert_ids.device)
+    _check("fp8_moe_sort",
+           lib().fp8_moe_sort(expert_ids.data_ptr(), 0 if expert_ids.dtype is i32 else 1, T, topk, num_experts, op,
+                              _flat(row_token, i32, "row_token", R, di), _flat(row_of, i32, "row_of", R, di), wsp, wsn,
+                              _raw_stream(di)))
+    return expert_offsets, row_token, row_of
+
+
+def _choices(row_of, di):
+    """(T, topk, address) of row_of int32 [T, topk]."""
+    torch = _torch()
+    if not isinstance(row_of, torch.Tensor) or row_of.dtype is not torch.int32 or row_of.get_device() != di:
+        _on_device(row_of, torch.int32, "row_of", torch.device("cuda", di))
+    if row_of.dim() != 2 or not row_of.is_contiguous():
+        raise ValueError("row_of: expected a contiguous int32 tensor [T, topk]")
+    return row_of.shape[0], row_of.shape[1], row_of.data_ptr()
+
+
+@_on_stream
+def fp8_moe_permute(x, row_of, num_rows=None, s_tok=None, out=None, s_out=None):
+    """Tokens x [T, H] (uint8 codes, float32, bfloat16 or float16) moved to the rows
+    row_of int32 [T, topk] -> out [num_rows, H], or (out, s_out) with the tokens' scales
+    s_tok fp32 [T].  num_rows: T * topk by default (out's rows when out is given).
+    Entries outside [0, num_rows) are skipped and rows no entry names left as they
+    were (uninitialised when out is allocated here).  The gradient with respect to x
+    is fp8_moe_combine(dout, row_of)."""
+    torch = _torch()
+    di = x.get_device()
+    if x.dtype not in (torch.uint8, torch.bfloat16, torch.float16, torch.float32):
+        raise TypeError("x: expected uint8, float32, bfloat16 or float16")
+    T, topk, rp = _choices(row_of, di)
+    _, H, ldx, xp = _mat(x, "x", di, rows=T)
+    if out is None:
+        out = torch.empty((T * topk if num_rows is None else num_rows, H), dtype=x.dtype, device=x.device)
+    R, _, ldo, op = _mat(out, "out", di, x.dtype, H, num_rows)
+    tp = sp = 0
+    if s_tok is not None:
+        tp = _flat(s_tok, torch.float32, "s_tok", T, di)
+        if s_out is None:
+            s_out = torch.empty(R, dtype=torch.float32, device=x.device)
+        sp = _flat(s_out, torch.float32, "s_out", R, di)
+    elif s_out is not None:
+        raise ValueError("s_out: given without s_tok")
+    _check("fp8_moe_permute",
+           lib().fp8_moe_permute(xp, ldx, tp, rp, T, topk, R, H, x.element_size(), op, ldo, sp, _raw_stream(di)))
+    return out if s_tok is None else (out, s_out)
+
+
+@_on_stream
+def fp8_moe_combine(y, row_of, weights=None, residual=None, out=None, out_dtype=None):
+    """out[t] = round(residual[t] + sum_j weights[t, j] * y[row_of[t, j]]): the experts' rows
+    y [R, H] back to the tokens, weights fp32 [T, topk] (None: ones), residual [T, H] in
+    out's type (None: nothing; it may be out itself) -> out [T, H].  Entries of row_of
+    int32 [T, topk] outside [0, R) add nothing.  out_dtype: the residual's type by
+    default, else y's."""
+    torch = _torch()
+    di = y.get_device()
+    code = _dtype_code(y.dtype, "y")
+    T, topk, rp = _choices(row_of, di)
+    R, H, ldy, yp = _mat(y, "y", di)
+    wp = 0 if weights is None else _flat(weights, torch.float32, "weights", T * topk, di)
+    dtype = out.dtype if out is not None else out_dtype or (y if residual is None else residual).dtype
+    out_code = _dtype_code(dtype, "out")
+    if out is None:
+        out = torch.empty((T, H), dtype=dtype, device=y.device)
+    _, _, ldo, op = _mat(out, "out", di, dtype, H, T)
+    ldr = sp = 0
+    if residual is not None:
+        _, _, ldr, sp = _mat(residual, "residual", di, dtype, H, T)
+    _check("fp8_moe_combine",
+           lib().fp8_moe_combine(yp, ldy, code, rp, wp, sp, ldr, op, out_code, ldo, T, topk, R, H, _raw_stream(di)))
+    return out
+
+
+@_on_stream
+def fp8_moe_combine_grad(dout, y, row_of, weights=None, dy=None, dweights=None, need_dy=True, need_dweights=True):
+    """The gradient of fp8_moe_combine for dout [T, H]: dy[row_of[t, j]] = round(weights[t, j] *
+    dout[t]) in y's type and dweights[t, j] = <dout[t], y[row_of[t, j]]> -> (dy [R, H],
+    dweights fp32 [T, topk]), None for the one not needed.  The residual's gradient is
+    dout.  Entries outside [0, R) write no row and a dweights of 0; rows no entry names
+    are left as they were (uninitialised when dy is allocated here).  dy may be y itself."""
+    torch = _torch()
+    di = dout.get_device()
+    code = _dtype_code(dout.dtype, "dout")
+    T, topk, rp = _choices(row_of, di)
+    _, H, ldd, dp = _mat(dout, "dout", di, rows=T)
+    R, _, ldy, yp = _mat(y, "y", di, cols=H)
+    y_code = _dtype_code(y.dtype, "y")
+    wp = 0 if weights is None else _flat(weights, torch.float32, "weights", T * topk, di)
+    lddy = yg = wg = 0
+    if dy is not None or need_dy:
+        if dy is None:
+            dy = torch.empty((R, H), dtype=y.dtype, device=y.device)
+        _, _, lddy, yg = _mat(dy, "dy", di, y.dtype, H, R)
+    if dweights is not None or need_dweights:
+        if dweights is None:
+            dweights = torch.empty((T, topk), dtype=torch.float32, device=y.device)
+        wg = _flat(dweights, torch.float32, "dweights", T * topk, di)
+    _check("fp8_moe_combine_grad",
+           lib().fp8_moe_combine_grad(dp, ldd, code, yp, ldy, y_code, rp, wp, yg, lddy, wg, T, topk, R, H,
+                                      _raw_stream(di)))
+    return dy, dweights
 
 
 def fp8_stream_read(buf, workgroups=256, nontemporal=False, sink=None, stream=None):

@@ -20,6 +20,7 @@ namespace {
 
 constexpr int64_t kMaxDim = INT32_MAX;  // kernels index rows and columns with 32-bit ints
 constexpr size_t kAlign = 256;          // workspace sub-buffer alignment
+constexpr int64_t kMaxExperts = 1024;   // of the grouped products and of the sort
 constexpr int64_t kMaxTiles = INT32_MAX - 8;  // launch grids count output tiles in 32 bits
 
 // Output tiles of 128 x 128 (no GEMM kernel uses smaller tiles along both axes
@@ -220,6 +221,47 @@ fp8_status_t gemm_dispatch(const uint8_t* qa, int64_t lda, const float* s_tok, c
     if (K % 128 == 0)
         return from_hip(fp8k::launch_gemm_mfma(qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, stream));
     return from_hip(fp8k::launch_gemm_tiled(qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, stream));
+}
+
+static_assert(FP8_ACT_NONE == fp8k::kActNone && FP8_ACT_RELU == fp8k::kActRelu && FP8_ACT_SILU == fp8k::kActSilu &&
+                  FP8_ACT_GELU == fp8k::kActGelu && FP8_ACT_GELU_TANH == fp8k::kActGeluTanh,
+              "activation ids");
+
+fp8_status_t check_act(fp8_act_t act) {
+    return act >= FP8_ACT_NONE && act <= FP8_ACT_GELU_TANH ? FP8_OK : FP8_ERR_INVALID_ARGUMENT;
+}
+
+// Output tiles of 128 x 128 of the products with an epilogue: one workgroup of 256
+// threads each, of which the runtime takes less than 2^32.
+bool act_tiles_ok(int64_t row_tiles, int64_t N) { return row_tiles * ((N + 127) / 128) < fp8k::kMaxGrid; }
+
+// A vector of 32-bit words that is read one by one.
+fp8_status_t check_words(const void* p, int64_t n) {
+    if (n > 0 && p == nullptr) return FP8_ERR_INVALID_ARGUMENT;
+    return n > 0 && (reinterpret_cast<uintptr_t>(p) & 3u) != 0 ? FP8_ERR_UNSUPPORTED : FP8_OK;
+}
+
+// A 16-byte aligned row-major matrix whose row stride is free.
+fp8_status_t check_rows(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t elem) {
+    return check_matrix(p, rows, cols, ld, elem, true);
+}
+
+// Extents of the expert-row calls: T tokens of topk choices, R expert rows of H elements.
+fp8_status_t check_choices(int64_t T, int64_t topk, int64_t R, int64_t H) {
+    if (T < 0 || topk < 0 || R < 0 || H < 0) return FP8_ERR_INVALID_ARGUMENT;
+    if (T > kMaxDim || topk > kMaxDim || R > kMaxDim || H > kMaxDim) return FP8_ERR_UNSUPPORTED;
+    return T * topk > kMaxDim ? FP8_ERR_UNSUPPORTED : FP8_OK;
+}
+
+// The output and the residual of a product's epilogue.
+fp8_status_t check_epilogue(const fp8k::Epilogue& e, fp8_act_t act, fp8_kv_dtype_t type, int64_t bias, int64_t M,
+                            int64_t N) {
+    FP8_TRY(check_act(act));
+    const int64_t eb = kv_elem_bytes(type);
+    if (eb == 0) return FP8_ERR_INVALID_ARGUMENT;
+    FP8_TRY(check_rows(e.y, M, N, e.ldy, eb));
+    if (e.residual != nullptr) FP8_TRY(check_rows(e.residual, M, N, e.ldr, eb));
+    return e.bias != nullptr ? check_vector(e.bias, bias) : FP8_OK;
 }
 
 // Bytes of the fp32 output staged by the FP8-output GEMM.
@@ -608,6 +650,160 @@ fp8_status_t fp8_gemm_grouped_scaled(const uint8_t* qa, const float* s_tok, cons
                                                        N, K, stream));
     return from_hip(fp8k::launch_gemm_grouped(qa, s_tok, row_token, expert_offsets, qw, s_ch, y, T, R, E, N, K,
                                               stream));
+}
+
+size_t fp8_gemm_act_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (check_dims(M, N, K) != FP8_OK || !act_tiles_ok((M + 127) / 128, N)) return SIZE_MAX;
+    return gemm_ws_bytes(M, N, K);
+}
+
+fp8_status_t fp8_gemm_scaled_act(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw, int64_t ldw,
+                                 const float* s_ch, const float* bias, fp8_act_t act, const void* residual, int64_t ldr,
+                                 void* y, fp8_kv_dtype_t y_dtype, int64_t ldy, int64_t M, int64_t N, int64_t K, void* ws,
+                                 size_t ws_bytes, hipStream_t stream) {
+    FP8_TRY(check_dims(M, N, K));
+    if (!act_tiles_ok((M + 127) / 128, N)) return FP8_ERR_UNSUPPORTED;
+    FP8_TRY(check_matrix(qa, M, K, lda, 1));
+    FP8_TRY(check_matrix(qw, N, K, ldw, 1));
+    FP8_TRY(check_vector(s_tok, M));
+    FP8_TRY(check_vector(s_ch, N));
+    const fp8k::Epilogue epi{bias, residual, y, ldr, ldy, (int)act, (int)y_dtype};
+    FP8_TRY(check_epilogue(epi, act, y_dtype, N, M, N));
+    const size_t need = fp8_gemm_act_workspace_bytes(M, N, K);
+    if (ws_bytes < need) return FP8_ERR_WORKSPACE;
+    if (need > 0 && ws == nullptr) return FP8_ERR_INVALID_ARGUMENT;
+    if (need > 0 && !aligned16(ws)) return FP8_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0) return FP8_OK;
+    if (M <= fp8k::kSkinnyMaxM)
+        return from_hip(fp8k::launch_gemm_skinny_act(qa, lda, s_tok, qw, ldw, s_ch, epi, M, N, K, ws, stream));
+    return from_hip(fp8k::launch_gemm_mfma_act(qa, lda, s_tok, qw, ldw, s_ch, epi, M, N, K, stream));
+}
+
+fp8_status_t fp8_gemm_grouped_scaled_act(const uint8_t* qa, const float* s_tok, const int32_t* row_token,
+                                         const int32_t* expert_offsets, const uint8_t* qw, const float* s_ch,
+                                         const float* bias, fp8_act_t act, void* y, fp8_kv_dtype_t y_dtype, int64_t ldy,
+                                         int64_t T, int64_t R, int64_t E, int64_t N, int64_t K, void* ws,
+                                         size_t ws_bytes, hipStream_t stream) {
+    (void)ws;
+    FP8_TRY(check_dims(T, N, K));
+    if (R < 0 || E < 0) return FP8_ERR_INVALID_ARGUMENT;
+    if (R > kMaxDim || E > kMaxExperts) return FP8_ERR_UNSUPPORTED;
+    if (!act_tiles_ok((R + 127) / 128 + E + 1, N)) return FP8_ERR_UNSUPPORTED;
+    if (R > 0 && (E == 0 || T == 0)) return FP8_ERR_INVALID_ARGUMENT;
+    FP8_TRY(check_matrix(qa, T, K, K, 1));
+    FP8_TRY(check_vector(s_tok, T));
+    FP8_TRY(check_vector(row_token, R));
+    FP8_TRY(check_vector(expert_offsets, R > 0 ? E + 1 : 0));
+    FP8_TRY(check_matrix(qw, E * N, K, K, 1));
+    FP8_TRY(check_vector(s_ch, E * N));
+    const fp8k::Epilogue epi{bias, nullptr, y, 0, ldy, (int)act, (int)y_dtype};
+    FP8_TRY(check_epilogue(epi, act, y_dtype, E * N, R, N));
+    if (ws_bytes < fp8_grouped_workspace_bytes(T, R, E, N, K)) return FP8_ERR_WORKSPACE;
+    if (R == 0 || N == 0) return FP8_OK;
+    return from_hip(fp8k::launch_gemm_grouped_mfma_act(qa, s_tok, row_token, expert_offsets, qw, s_ch, epi, T, R, E, N, K,
+                                                       stream));
+}
+
+fp8_status_t fp8_act_quantize(const void* h, int64_t ldh, fp8_kv_dtype_t dtype, int64_t rows, int64_t F, fp8_act_t act,
+                              int32_t gated, uint8_t* q, int64_t ldq, float* scales, const int32_t* live_rows,
+                              hipStream_t stream) {
+    FP8_TRY(check_dims(rows, 1, F));
+    FP8_TRY(check_act(act));
+    const int64_t eb = kv_elem_bytes(dtype);
+    if (eb == 0) return FP8_ERR_INVALID_ARGUMENT;
+    FP8_TRY(check_matrix(h, rows, gated ? 2 * F : F, ldh, eb));
+    FP8_TRY(check_matrix(q, rows, F, ldq, 1));
+    FP8_TRY(check_vector(scales, rows));
+    if (live_rows != nullptr) FP8_TRY(check_words(live_rows, 1));
+    if (rows == 0) return FP8_OK;
+    return from_hip(fp8k::launch_act_quantize(h, ldh, (int)dtype, rows, F, (int)act, gated != 0, q, ldq, scales,
+                                              live_rows, stream));
+}
+
+size_t fp8_moe_sort_workspace_bytes(int64_t T, int64_t topk, int64_t E) {
+    if (check_choices(T, topk, 0, 0) != FP8_OK || E < 0 || E > kMaxExperts) return SIZE_MAX;
+    return round_up(fp8k::moe_sort_ws_bytes(T * topk, E), kAlign);
+}
+
+fp8_status_t fp8_moe_sort(const void* expert_ids, int32_t ids_64, int64_t T, int64_t topk, int64_t E,
+                          int32_t* expert_offsets, int32_t* row_token, int32_t* row_of, void* ws, size_t ws_bytes,
+                          hipStream_t stream) {
+    FP8_TRY(check_choices(T, topk, 0, 0));
+    if (E < 0) return FP8_ERR_INVALID_ARGUMENT;
+    if (E > kMaxExperts) return FP8_ERR_UNSUPPORTED;
+    const int64_t R = T * topk;
+    FP8_TRY(check_vector(expert_ids, R));
+    FP8_TRY(check_vector(expert_offsets, E + 1));
+    FP8_TRY(check_vector(row_token, R));
+    FP8_TRY(check_vector(row_of, R));
+    const size_t need = fp8_moe_sort_workspace_bytes(T, topk, E);
+    if (ws_bytes < need) return FP8_ERR_WORKSPACE;
+    if (need > 0 && ws == nullptr) return FP8_ERR_INVALID_ARGUMENT;
+    if (need > 0 && !aligned16(ws)) return FP8_ERR_UNSUPPORTED;
+    return from_hip(fp8k::launch_moe_sort(expert_ids, ids_64 != 0, R, topk, E, expert_offsets, row_token, row_of, ws,
+                                          stream));
+}
+
+fp8_status_t fp8_moe_permute(const void* x, int64_t ldx, const float* s_tok, const int32_t* row_of, int64_t T,
+                             int64_t topk, int64_t R, int64_t H, int64_t elem_bytes, void* out, int64_t ldo,
+                             float* s_out, hipStream_t stream) {
+    FP8_TRY(check_choices(T, topk, R, H));
+    if (elem_bytes != 1 && elem_bytes != 2 && elem_bytes != 4) return FP8_ERR_INVALID_ARGUMENT;
+    FP8_TRY(check_rows(x, T, H, ldx, elem_bytes));
+    FP8_TRY(check_rows(out, R, H, ldo, elem_bytes));
+    FP8_TRY(check_vector(row_of, T * topk));
+    if ((s_tok == nullptr) != (s_out == nullptr)) return FP8_ERR_INVALID_ARGUMENT;
+    if (s_tok != nullptr) {
+        FP8_TRY(check_vector(s_tok, T));
+        FP8_TRY(check_vector(s_out, R));
+    }
+    if (T == 0 || topk == 0 || R == 0 || (H == 0 && s_tok == nullptr)) return FP8_OK;
+    return from_hip(fp8k::launch_moe_permute(x, ldx * elem_bytes, s_tok, row_of, T, topk, R, H * elem_bytes, out,
+                                             ldo * elem_bytes, s_out, stream));
+}
+
+fp8_status_t fp8_moe_combine(const void* y, int64_t ldy, fp8_kv_dtype_t y_dtype, const int32_t* row_of,
+                             const float* weights, const void* residual, int64_t ldr, void* out,
+                             fp8_kv_dtype_t out_dtype, int64_t ldo, int64_t T, int64_t topk, int64_t R, int64_t H,
+                             hipStream_t stream) {
+    FP8_TRY(check_choices(T, topk, R, H));
+    const int64_t yb = kv_elem_bytes(y_dtype), ob = kv_elem_bytes(out_dtype);
+    if (yb == 0 || ob == 0) return FP8_ERR_INVALID_ARGUMENT;
+    FP8_TRY(check_rows(y, R, H, ldy, yb));
+    FP8_TRY(check_rows(out, T, H, ldo, ob));
+    if (residual != nullptr) FP8_TRY(check_rows(residual, T, H, ldr, ob));
+    FP8_TRY(check_vector(row_of, T * topk));
+    if (weights != nullptr) FP8_TRY(check_vector(weights, T * topk));
+    if (T == 0 || H == 0) return FP8_OK;
+    fp8k::MoeCombine p = {};
+    p.y = y, p.row_of = row_of, p.weights = weights, p.residual = residual, p.out = out;
+    p.ldy = ldy, p.ldr = ldr, p.ldo = ldo, p.H = H;
+    p.T = (int)T, p.R = (int)R;
+    p.topk = R > 0 ? (int)topk : 0;  // without rows every choice is without one
+    return from_hip(fp8k::launch_moe_combine(p, (int)y_dtype, (int)out_dtype, stream));
+}
+
+fp8_status_t fp8_moe_combine_grad(const void* dout, int64_t ldd, fp8_kv_dtype_t dout_dtype, const void* y, int64_t ldy,
+                                  fp8_kv_dtype_t y_dtype, const int32_t* row_of, const float* weights, void* dy,
+                                  int64_t lddy, float* dweights, int64_t T, int64_t topk, int64_t R, int64_t H,
+                                  hipStream_t stream) {
+    FP8_TRY(check_choices(T, topk, R, H));
+    const int64_t db = kv_elem_bytes(dout_dtype), yb = kv_elem_bytes(y_dtype);
+    if (db == 0 || yb == 0) return FP8_ERR_INVALID_ARGUMENT;
+    FP8_TRY(check_rows(dout, T, H, ldd, db));
+    if (dweights != nullptr) {
+        FP8_TRY(check_rows(y, R, H, ldy, yb));
+        FP8_TRY(check_vector(dweights, T * topk));
+    }
+    if (dy != nullptr) FP8_TRY(check_rows(dy, R, H, lddy, yb));
+    FP8_TRY(check_vector(row_of, T * topk));
+    if (weights != nullptr) FP8_TRY(check_vector(weights, T * topk));
+    if (T == 0 || topk == 0 || (dy == nullptr && dweights == nullptr)) return FP8_OK;
+    fp8k::MoeCombineGrad p = {};
+    p.dout = dout, p.y = y, p.row_of = row_of, p.weights = weights, p.dy = dy, p.dweights = dweights;
+    p.ldd = ldd, p.ldy = ldy, p.lddy = lddy, p.H = H;
+    p.T = (int)T, p.topk = (int)topk, p.R = (int)R;
+    return from_hip(fp8k::launch_moe_combine_grad(p, (int)dout_dtype, (int)y_dtype, stream));
 }
 
 fp8_status_t fp8_stream_read(const void* p, size_t bytes, int32_t workgroups, int32_t nontemporal, uint32_t* sink,

@@ -43,6 +43,7 @@
 
 #include "device_common.hpp"
 #include "kernels.hpp"
+#include "rows_common.hpp"
 
 namespace fp8k {
 
@@ -61,6 +62,20 @@ __device__ __forceinline__ v16f mfma_32x32x64_e4m3(const v8i& a, const v8i& b, c
 // (the fragment layout of read_frag below; measured on gfx950).
 __device__ __forceinline__ v16f mfma_32x32x64_e4m3_mx(const v8i& a, const v8i& b, const v16f& c, int sa, int sb) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, sa, 0, sb);
+}
+
+// The same 64 k in fp16 (E4M3 values are fp16 values): the FP8 matrix
+// instructions line the products of 8 neighbouring k up with the largest of them
+// and keep about 14 bits below its leading one, whatever the accumulator holds
+// (measured), which leaves sums of normal data off by 1e-5 of their norm; the
+// fp16 ones keep fp32's.  Half the rate, for fp32 outputs alone: 16-bit ones
+// round by 2^-9 or 2^-12 themselves.
+__device__ __forceinline__ v16f mfma_32x32x64_half(const v8i& a, const v8i& b, v16f c) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+        c = __builtin_amdgcn_mfma_f32_32x32x16_f16(half8_of(a[2 * t], a[2 * t + 1]), half8_of(b[2 * t], b[2 * t + 1]), c, 0,
+                                                   0, 0);
+    return c;
 }
 
 __device__ __forceinline__ int dswz(int row) { return (row ^ (row >> 3)) & 7; }
@@ -146,7 +161,11 @@ struct MfmaArgs {
     const int32_t* offsets;
     int E;
     MxScales mx;  // block-scaled operands (MX kernels only)
+    Epilogue epi;  // ACT kernels only
 };
+
+// What a DMA lane past K reads (a K that is no whole number of stages).
+__device__ const v4i kZero16 = {0, 0, 0, 0};
 
 // Number of output tiles of expert e (row tiles x column tiles).
 template <int BM>
@@ -218,9 +237,15 @@ __device__ void find_expert_tile(const MfmaArgs& p, int b, int* sh) {
 // grouped kernel always does; the launcher takes it only when the whole grid
 // is one row of tiles with at most 192 real rows (M in 65..192), because the
 // extra instantiations cost the full-tile loop about 1 % (measured on 8192^3).
-template <int BN, int BM, int WN, int WM, int GROUP_M, bool GROUPED, bool MX = false, bool SKIP = false>
+// ACT: the tile leaves through an Epilogue (bias, activation, residual, output
+// type).  TAIL: K is no multiple of 128; the last stage's pieces past K are read
+// from a block of zeros, for both operands (a zero code times a NaN code is NaN).
+// HALF: products in fp16 (mfma_32x32x64_half).
+template <int BN, int BM, int WN, int WM, int GROUP_M, bool GROUPED, bool MX = false, bool SKIP = false, bool ACT = false,
+          bool TAIL = false, bool HALF = false>
 __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) {
     static_assert(!(MX && GROUPED), "block scales: dense GEMM only");
+    static_assert(!(MX && (ACT || TAIL)), "block scales: plain epilogue, whole stages");
     constexpr int NW = WN * WM;                 // waves: WN along the weight rows, WM along the activations
     constexpr int NTH = 64 * NW;
     constexpr int FN = BN / (32 * WN);          // 32-row weight fragments per wave
@@ -239,8 +264,7 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
     // during step s (one 4-byte DMA per row into a dummy LDS slot), so the
     // stage's own DMA one step later finds them there: expert weights stream
     // from HBM, whose latency one step of MFMAs does not always cover.
-    constexpr bool PF = GROUPED;
-    static_assert(!PF || BN == 64 * NW, "one prefetch row per lane");
+    constexpr bool PF = GROUPED && BN == 64 * NW;  // one prefetch row per lane
     uint8_t* pf_lds = smem + 2 * STAGE + 4 * (BN + BM) + 16;
 
     const int tid = threadIdx.x;
@@ -308,6 +332,12 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
     float* s_ch_t = reinterpret_cast<float*>(smem + RING);
     float* s_tok_t = s_ch_t + BN;
     for (int i = tid; i < BN; i += NTH) s_ch_t[i] = MX ? 1.0f : s_ch[min(n0 + i, p.N - 1)];
+    float* bias_t = reinterpret_cast<float*>(smem + RING + 4 * (BN + BM) + (GROUPED ? 16 + 256 : 0));  // ACT only
+    if constexpr (ACT) {
+        // no bias enters as -0, which leaves every value as it is
+        const float* bias = p.epi.bias != nullptr ? p.epi.bias + (int64_t)expert * p.N : nullptr;
+        for (int i = tid; i < BN; i += NTH) bias_t[i] = bias != nullptr ? bias[min(n0 + i, p.N - 1)] : -0.0f;
+    }
     for (int i = tid; i < BM; i += NTH) {
         const int ml = min(i, rows_valid - 1);
         if constexpr (MX)
@@ -358,6 +388,14 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
                                          smem + SRING + slot * 4 * (BN + BM) + (wave * DS + j) * 256, 4, 0, 0);
     };
 
+    const int KT = p.K / kBK + (TAIL ? 1 : 0);
+    // The lane's source in stage kt, piece c of its row's 128 bytes: src, or zeros past K.
+    auto within = [&](const uint8_t* src, int kt, int c) {
+        if constexpr (TAIL) {
+            if (kt == KT - 1 && kt * kBK + (c << 4) >= p.K) src = reinterpret_cast<const uint8_t*>(&kZero16);
+        }
+        return src;
+    };
     // DMA instruction j (0 .. PER_STAGE - 1) of stage kt into ring slot `slot`.
     auto issue_one = [&](int kt, int slot, int j) {
         uint8_t* base = smem + slot * STAGE;
@@ -367,10 +405,12 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
         } else if (j < DA) {
             const int row = (wave * DA + j) * 8 + lrow;
             const int n = min(n0 + row, nlast);  // rows past N feed discarded columns
-            dma16(qw + (int64_t)n * ldw + koff + ((lpos ^ dswz(row)) << 4), base + (wave * DA + j) * 1024);
+            const int c = lpos ^ dswz(row);
+            dma16(within(qw + (int64_t)n * ldw + koff + (c << 4), kt, c), base + (wave * DA + j) * 1024);
         } else {
             const int jb = j - DA;
-            dma16(bsrc[jb] + koff, base + BN * kBK + (wave * DB + jb) * 1024);
+            dma16(within(bsrc[jb] + koff, kt, lpos ^ dswz((wave * DB + jb) * 8 + lrow)),
+                  base + BN * kBK + (wave * DB + jb) * 1024);
         }
     };
     // Stage kt goes to ring slot `slot` (0 or 1).
@@ -381,10 +421,13 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
         for (int j = 0; j < DA; ++j) {
             const int row = (wave * DA + j) * 8 + lrow;
             const int n = min(n0 + row, nlast);  // rows past N feed discarded columns
-            dma16(qw + (int64_t)n * ldw + koff + ((lpos ^ dswz(row)) << 4), base + (wave * DA + j) * 1024);
+            const int c = lpos ^ dswz(row);
+            dma16(within(qw + (int64_t)n * ldw + koff + (c << 4), kt, c), base + (wave * DA + j) * 1024);
         }
 #pragma unroll
-        for (int j = 0; j < DB; ++j) dma16(bsrc[j] + koff, base + BN * kBK + (wave * DB + j) * 1024);
+        for (int j = 0; j < DB; ++j)
+            dma16(within(bsrc[j] + koff, kt, lpos ^ dswz((wave * DB + j) * 8 + lrow)),
+                  base + BN * kBK + (wave * DB + j) * 1024);
         if constexpr (MX) {
 #pragma unroll
             for (int j = 0; j < DS; ++j) issue_scale(kt, slot, j);
@@ -399,7 +442,6 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[a][b][v] = 0.0f;
 
-    const int KT = p.K / kBK;
     const int arow0 = wn * (BN / WN) + r32;
     // Activation fragment b of wave (wn, wm) covers tile rows
     // (b * WM + wm) * 32 .. + 31: the waves along M take alternate 32-row
@@ -436,6 +478,8 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
     auto mma = [&](const v8i& x, const v8i& w2, const v16f& c, int a, int b, int h) {
         if constexpr (MX)
             return mfma_32x32x64_e4m3_mx(x, w2, c, sbyte(sc_a[a], h), sbyte(sc_b[b], h));
+        else if constexpr (HALF)
+            return mfma_32x32x64_half(x, w2, c);
         else
             return mfma_32x32x64_e4m3(x, w2, c);
     };
@@ -568,6 +612,88 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
         k_loop(std::integral_constant<int, FM>{});
     }
 
+    if constexpr (ACT) {
+        // The accumulators leave through LDS as fp32, two fragments (64 WM rows)
+        // at a time: there a thread takes 8 columns of its own, whose scales and
+        // bias stay in its registers, and whole row pieces of the residual and of
+        // the output, and the activation's code is there once, not once per
+        // accumulator.  16-byte pieces are XOR-swizzled by row.
+        constexpr int FP = 2, ROWS = FP * 32 * WM;
+        constexpr int CG = BN / 8;      // column groups of a row
+        constexpr int STEP = NTH / CG;  // rows the workgroup covers at once
+        constexpr int U = 4;            // of a thread's rows, residuals loaded ahead
+        static_assert(FM % FP == 0 && NTH % CG == 0 && ROWS % (STEP * U) == 0, "whole passes");
+        static_assert(ROWS * BN * 4 <= 2 * STAGE, "the fp32 rows of a pass must fit in the ring");
+        float* ct = reinterpret_cast<float*>(smem);
+        const int cg = tid % CG, row0 = tid / CG;
+        const int n = n0 + cg * 8;
+        const int left = p.N - n;
+        auto run_pass = [&](auto pass_number) {
+            constexpr int pass = decltype(pass_number)::value;
+            wait_lds_reads();
+            block_barrier();
+#pragma unroll
+            for (int b = pass * FP; b < (pass + 1) * FP; ++b) {
+                const int ml = (b * WM + wm) * 32 + r32 - pass * ROWS;
+#pragma unroll
+                for (int a = 0; a < FN; ++a) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int nl = wn * (BN / WN) + a * 32 + 8 * q + 4 * g;
+                        *reinterpret_cast<float4*>(ct + ml * BN + (((nl >> 2) ^ (ml & 31)) << 2)) = make_float4(
+                            acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]);
+                    }
+                }
+            }
+            block_barrier();
+            auto finish = [&](auto dt) {
+                constexpr int DT = decltype(dt)::value;
+                float sc[8], bi[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sc[i] = s_ch_t[cg * 8 + i], bi[i] = bias_t[cg * 8 + i];
+                const int rows = min(ROWS, rows_valid - pass * ROWS);
+                const int64_t m_first = (int64_t)row_begin + m0 + pass * ROWS;
+                for (int r0 = row0; r0 < rows && left > 0; r0 += STEP * U) {
+                    float res[U][8];
+                    if (p.epi.residual != nullptr) {
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const int r = min(r0 + u * STEP, rows - 1);
+                            load_run<DT, 8>(p.epi.residual, (m_first + r) * p.epi.ldr + n, left, res[u]);
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int r = min(r0 + u * STEP, rows - 1);  // the last row again: the same values
+                        const float st = s_tok_t[pass * ROWS + r];
+                        const float4 lo = *reinterpret_cast<const float4*>(ct + r * BN + (((2 * cg) ^ (r & 31)) << 2));
+                        const float4 hi = *reinterpret_cast<const float4*>(ct + r * BN + (((2 * cg + 1) ^ (r & 31)) << 2));
+                        float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(x[i], st * sc[i], bi[i]);
+                        activate<8>(x, p.epi.act);
+                        if (p.epi.residual != nullptr) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[i] += res[u][i];
+                        }
+                        store_run<DT, 8>(p.epi.y, (m_first + r) * p.epi.ldy + n, left, x);
+                    }
+                }
+            };
+            if (p.epi.type == kKvBF16)
+                finish(std::integral_constant<int, kKvBF16>{});
+            else if (p.epi.type == kKvF16)
+                finish(std::integral_constant<int, kKvF16>{});
+            else
+                finish(std::integral_constant<int, kKvF32>{});
+        };
+        static_assert(FM <= 2 * FP, "one pass or two");
+        run_pass(std::integral_constant<int, 0>{});
+        if constexpr (FM > FP) {
+            if (rows_valid > ROWS) run_pass(std::integral_constant<int, 1>{});  // uniform
+        }
+        return;
+    }
     // ---- epilogue: y = bf16_rne(acc * (s_tok * s_ch)) ----------------------
     // The scaled BF16 tile is staged in LDS (the stage ring is free now) as
     // [BM rows][BN columns] with 16-byte chunks XOR-swizzled by row, then
@@ -679,6 +805,70 @@ hipError_t launch_gemm_mfma(const uint8_t* qa, int64_t lda, const float* s_tok, 
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((gemm_mfma_kernel<BN, BM, WN, WM, 4, false>), dim3(grid), dim3(64 * WN * WM), LDS, stream, p);
     return hipGetLastError();
+}
+
+// Dense products with an epilogue.
+template <int BN, int BM, bool SKIP, bool TAIL, bool HALF>
+static hipError_t launch_dense_act(MfmaArgs p, hipStream_t stream) {
+    constexpr int LDS = 2 * (BN + BM) * kBK + 4 * (BN + BM) + 4 * BN;  // ring + tile scales + bias
+    p.tiles_m = (p.M - 1) / BM + 1;
+    p.tiles_n = (p.N - 1) / BN + 1;
+    const hipError_t e = FP8K_SET_LDS((gemm_mfma_kernel<BN, BM, 2, 2, 4, false, false, SKIP, true, TAIL, HALF>), LDS);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((gemm_mfma_kernel<BN, BM, 2, 2, 4, false, false, SKIP, true, TAIL, HALF>),
+                       dim3((unsigned)p.tiles_m * (unsigned)p.tiles_n), dim3(256), LDS, stream, p);
+    return hipGetLastError();
+}
+
+// fp32 outputs take products in fp16, and tiles of 128 x 128 for them: twice the
+// operands' registers leave no room for a 256 x 256 tile's accumulators.
+template <bool TAIL>
+static hipError_t launch_dense_tail(const MfmaArgs& p, hipStream_t stream) {
+    if (p.epi.type == kKvF32) return launch_dense_act<128, 128, false, TAIL, true>(p, stream);
+    if (p.M <= 192) return launch_dense_act<256, 256, true, TAIL, false>(p, stream);
+    return launch_dense_act<256, 256, false, TAIL, false>(p, stream);
+}
+
+hipError_t launch_gemm_mfma_act(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw, int64_t ldw,
+                                const float* s_ch, const Epilogue& epi, int64_t M, int64_t N, int64_t K,
+                                hipStream_t stream) {
+    if (M <= 0 || N <= 0) return hipSuccess;
+    MfmaArgs p{};
+    p.qa = qa; p.lda = lda; p.s_tok = s_tok; p.qw = qw; p.ldw = ldw; p.s_ch = s_ch; p.epi = epi;
+    p.M = (int)M; p.N = (int)N; p.K = (int)K;
+    return K % kBK == 0 ? launch_dense_tail<false>(p, stream) : launch_dense_tail<true>(p, stream);
+}
+
+template <int BN, int BM, bool TAIL, bool HALF>
+static hipError_t launch_grouped_act(MfmaArgs p, int64_t R, int64_t E, hipStream_t stream) {
+    // ring + tile scales + tile lookup + prefetch slot + bias
+    constexpr int LDS = 2 * (BN + BM) * kBK + 4 * (BN + BM) + 16 + 256 + 4 * BN;
+    p.tiles_n = (p.N - 1) / BN + 1;
+    const hipError_t e = FP8K_SET_LDS((gemm_mfma_kernel<BN, BM, 2, 2, 4, true, false, false, true, TAIL, HALF>), LDS);
+    if (e != hipSuccess) return e;
+    const int64_t tiles_max = ((R + BM - 1) / BM + E) * p.tiles_n;
+    hipLaunchKernelGGL((gemm_mfma_kernel<BN, BM, 2, 2, 4, true, false, false, true, TAIL, HALF>),
+                       dim3((unsigned)(8 * ((tiles_max + 7) / 8))), dim3(256), LDS, stream, p);
+    return hipGetLastError();
+}
+
+template <bool TAIL>
+static hipError_t launch_grouped_tail(const MfmaArgs& p, int64_t R, int64_t E, hipStream_t stream) {
+    if (p.epi.type == kKvF32) return launch_grouped_act<128, 128, TAIL, true>(p, R, E, stream);
+    return launch_grouped_act<256, 256, TAIL, false>(p, R, E, stream);
+}
+
+hipError_t launch_gemm_grouped_mfma_act(const uint8_t* qa, const float* s_tok, const int32_t* row_token,
+                                        const int32_t* offsets, const uint8_t* qw, const float* s_ch,
+                                        const Epilogue& epi, int64_t T, int64_t R, int64_t E, int64_t N, int64_t K,
+                                        hipStream_t stream) {
+    (void)T;
+    if (R <= 0 || N <= 0 || E <= 0) return hipSuccess;
+    MfmaArgs p{};
+    p.qa = qa; p.lda = K; p.s_tok = s_tok; p.qw = qw; p.ldw = K; p.s_ch = s_ch; p.epi = epi;
+    p.M = (int)R; p.N = (int)N; p.K = (int)K;
+    p.row_token = row_token; p.offsets = offsets; p.E = (int)E;
+    return K % kBK == 0 ? launch_grouped_tail<false>(p, R, E, stream) : launch_grouped_tail<true>(p, R, E, stream);
 }
 
 hipError_t launch_gemm_mfma_mx(const uint8_t* qa, int64_t lda, const uint8_t* sa, const uint8_t* qw, int64_t ldw,

@@ -17,6 +17,7 @@
 // row (one 8-byte BF16 store).
 #include "device_common.hpp"
 #include "kernels.hpp"
+#include "rows_common.hpp"
 
 namespace fp8k {
 
@@ -26,6 +27,53 @@ namespace fp8k {
 // operand selects cannot be hoisted above this step's MFMAs (a hoisted select
 // would wait for loads that are meant to stay in flight).
 __device__ __forceinline__ void issue_order_fence() { __builtin_amdgcn_sched_barrier(0); }
+
+// The epilogue of four neighbouring outputs from their sums.  A missing bias
+// enters as -0, which leaves every value as it is, signed zeros included.
+template <int DT>
+__device__ __forceinline__ void finish4_typed(const Epilogue& e, const v4f& sum, float st,
+                                              const float* __restrict__ s_ch, int m, int nb, int N) {
+    const int left = N - nb;
+    float sc[4], x[4];
+    load_run<kKvF32, 4>(s_ch, nb, left, sc);
+    if (e.bias != nullptr) {
+        load_run<kKvF32, 4>(e.bias, nb, left, x);
+    } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x[v] = -0.0f;
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) x[v] = __builtin_fmaf(sum[v], st * sc[v], x[v]);
+    activate<4>(x, e.act);
+    if (e.residual != nullptr) {
+        float r[4];
+        load_run<DT, 4>(e.residual, (int64_t)m * e.ldr + nb, left, r);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x[v] += r[v];
+    }
+    store_run<DT, 4>(e.y, (int64_t)m * e.ldy + nb, left, x);
+}
+
+__device__ __forceinline__ void finish4(const Epilogue& e, const v4f& sum, float st, const float* __restrict__ s_ch,
+                                        int m, int nb, int N) {
+    if (e.type == kKvBF16)
+        finish4_typed<kKvBF16>(e, sum, st, s_ch, m, nb, N);
+    else if (e.type == kKvF16)
+        finish4_typed<kKvF16>(e, sum, st, s_ch, m, nb, N);
+    else
+        finish4_typed<kKvF32>(e, sum, st, s_ch, m, nb, N);
+}
+
+// The 128-k product in fp16, for fp32 outputs: the FP8 instruction keeps about 14
+// bits below the largest of 8 neighbouring products (measured; sums off by 1e-5
+// of their norm), the fp16 ones fp32's.  The weights' stream hides the rest.
+__device__ __forceinline__ v4f mfma_16x16x128_half(const v8i& a, const v8i& b, v4f c) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+        c = __builtin_amdgcn_mfma_f32_16x16x32_f16(half8_of(a[2 * t], a[2 * t + 1]), half8_of(b[2 * t], b[2 * t + 1]), c, 0,
+                                                   0, 0);
+    return c;
+}
 
 // Lane `lane` supplies bytes [16g, 16g+16) and [64+16g, 64+16g+16) of a
 // 128-byte k chunk (g = lane / 16) for A and B alike.
@@ -42,12 +90,15 @@ __device__ __forceinline__ void issue_order_fence() { __builtin_amdgcn_sched_bar
 // lane group g supplies covers k [32g, 32g + 32) of the 128-byte chunk
 // (measured on gfx950), so each lane passes byte g of its row's chunk word.
 // K must be a multiple of 128.
-template <int MT, int NT, int KW, int DEPTH, bool MX>
+//
+// ACT: the sums leave through an Epilogue (bias, activation, residual, output
+// type) instead of y; HALF: products in fp16.
+template <int MT, int NT, int KW, int DEPTH, bool MX, bool ACT = false, bool HALF = false>
 __global__ __launch_bounds__(KW * 64) void gemm_skinny_kernel(
     const uint8_t* __restrict__ qa, int64_t lda, const float* __restrict__ s_tok,
     const uint8_t* __restrict__ qw, int64_t ldw, const float* __restrict__ s_ch,
     uint16_t* __restrict__ y, float* __restrict__ y32, int64_t ldy, int M, int N, int K, float* __restrict__ part,
-    int split_chunks, MxScales mx) {
+    int split_chunks, MxScales mx, Epilogue epi) {
     const int lane = threadIdx.x & 63;
     const int wave = threadIdx.x >> 6;
     const int r16 = lane & 15;
@@ -164,6 +215,8 @@ __global__ __launch_bounds__(KW * 64) void gemm_skinny_kernel(
                             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                                 a, xf[i], acc[i][j], 0, 0, 0, (int)((wsc[d % SD][j] >> (8 * g)) & 0xFFu), 0,
                                 (int)((xsc[d % SD][i] >> (8 * g)) & 0xFFu));
+                        else if constexpr (HALF)
+                            acc[i][j] = mfma_16x16x128_half(a, xf[i], acc[i][j]);
                         else
                             acc[i][j] = mfma_16x16x128_e4m3(a, xf[i], acc[i][j]);
                     }
@@ -197,6 +250,10 @@ __global__ __launch_bounds__(KW * 64) void gemm_skinny_kernel(
             } else {
                 for (int v = 0; v < 4 && nb + v < N; ++v) pr[nb + v] = sum[v];
             }
+            continue;
+        }
+        if constexpr (ACT) {
+            finish4(epi, sum, s_tok[m], s_ch, m, nb, N);
             continue;
         }
         if constexpr (MX) {  // block scales already applied: y = bf16_rne(acc)
@@ -458,32 +515,56 @@ __global__ __launch_bounds__(256) void skinny_splitk_reduce(const float* __restr
     }
 }
 
-template <int MT, int NT, int KW, bool MX>
+// The same sums through an epilogue.
+__global__ __launch_bounds__(256) void skinny_splitk_reduce_act(const float* __restrict__ part, int splits, int M, int N,
+                                                               const float* __restrict__ s_tok,
+                                                               const float* __restrict__ s_ch, Epilogue epi) {
+    const int n4 = (N + 3) >> 2;
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (t >= (int64_t)M * n4) return;
+    const int m = (int)(t / n4);
+    const int nb = (int)(t - (int64_t)m * n4) * 4;
+    const int64_t plane = (int64_t)M * N;
+    const float* p = part + (int64_t)m * N + nb;
+    v4f sum;
+    float x[4];
+    load_run<kKvF32, 4>(p, 0, N - nb, x);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) sum[v] = x[v];
+    for (int z = 1; z < splits; ++z) {
+        load_run<kKvF32, 4>(p, z * plane, N - nb, x);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) sum[v] += x[v];
+    }
+    finish4(epi, sum, s_tok[m], s_ch, m, nb, N);
+}
+
+template <int MT, int NT, int KW, bool MX, bool ACT, bool HALF>
 static void launch_cfg(dim3 grid, hipStream_t stream, const uint8_t* qa, int64_t lda, const float* s_tok,
                        const uint8_t* qw, int64_t ldw, const float* s_ch, uint16_t* y, float* y32, int64_t ldy, int M,
-                       int N, int K, float* part, int split_chunks, MxScales mx) {
+                       int N, int K, float* part, int split_chunks, MxScales mx, const Epilogue& epi) {
     // The block-scaled MFMA keeps its operands in VGPRs (the plain one also
     // reads AGPRs), so the MX kernels keep fewer steps in flight to stay
     // within the register file without spills (checked in the compiler's
     // register report for every instantiation).
     constexpr int DEPTH = MX ? (MT * NT == 1 ? 4 : ((NT == 8 ? MT == 1 : MT * NT <= 6) ? 2 : 1))
                              : ((MT * NT <= 2) ? 4 : 2);
-    hipLaunchKernelGGL((gemm_skinny_kernel<MT, NT, KW, DEPTH, MX>), grid, dim3(KW * 64), 0, stream, qa, lda, s_tok,
-                       qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx);
+    hipLaunchKernelGGL((gemm_skinny_kernel<MT, NT, KW, DEPTH, MX, ACT, HALF>), grid, dim3(KW * 64), 0, stream, qa, lda, s_tok,
+                       qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx, epi);
 }
 
-template <int MT, bool MX>
+template <int MT, bool MX, bool ACT, bool HALF>
 static void launch_mt(int nt, dim3 grid, hipStream_t stream, const uint8_t* qa, int64_t lda, const float* s_tok,
                       const uint8_t* qw, int64_t ldw, const float* s_ch, uint16_t* y, float* y32, int64_t ldy, int M,
-                      int N, int K, float* part, int split_chunks, MxScales mx) {
+                      int N, int K, float* part, int split_chunks, MxScales mx, const Epilogue& epi) {
     switch (nt) {
-        case 8: launch_cfg<MT, 8, 4, MX>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx); break;
-        case 7: launch_cfg<MT, 7, 4, MX>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx); break;
-        case 6: launch_cfg<MT, 6, 4, MX>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx); break;
-        case 5: launch_cfg<MT, 5, 4, MX>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx); break;
-        case 4: launch_cfg<MT, 4, 8, MX>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx); break;
-        case 2: launch_cfg<MT, 2, 8, MX>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx); break;
-        default: launch_cfg<MT, 1, 8, MX>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx); break;
+        case 8: launch_cfg<MT, 8, 4, MX, ACT, HALF>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx, epi); break;
+        case 7: launch_cfg<MT, 7, 4, MX, ACT, HALF>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx, epi); break;
+        case 6: launch_cfg<MT, 6, 4, MX, ACT, HALF>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx, epi); break;
+        case 5: launch_cfg<MT, 5, 4, MX, ACT, HALF>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx, epi); break;
+        case 4: launch_cfg<MT, 4, 8, MX, ACT, HALF>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx, epi); break;
+        case 2: launch_cfg<MT, 2, 8, MX, ACT, HALF>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx, epi); break;
+        default: launch_cfg<MT, 1, 8, MX, ACT, HALF>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx, epi); break;
     }
 }
 
@@ -547,31 +628,37 @@ size_t gemm_skinny_ws_bytes(int64_t M, int64_t N, int64_t K) {
     return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * sizeof(float) : 0;
 }
 
-template <bool MX>
+template <bool MX, bool ACT, bool HALF>
 static hipError_t launch_skinny_any(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw,
                                     int64_t ldw, const float* s_ch, uint16_t* y, float* y32, int64_t ldy, int64_t M,
-                                    int64_t N, int64_t K, void* ws, MxScales mx, hipStream_t stream) {
+                                    int64_t N, int64_t K, void* ws, MxScales mx, const Epilogue& epi,
+                                    hipStream_t stream) {
     if (M <= 0 || N <= 0) return hipSuccess;
     SkinnyPlan p = skinny_plan(M, N, K);
-    // MX: 4 activation tiles with nt = 4 (8 waves, 256 VGPRs each) would
+    // MX and HALF: 4 activation tiles with nt = 4 (8 waves, 256 VGPRs each) would
     // spill; take nt = 8 (4 waves) there (same splits: none on this branch).
     // The shallower MX prefetch also measured slower with nt = 5..7 than
     // with nt = 8 (70B gate/up: 62.8 vs 60.8 us), so MX keeps nt = 8.
-    if (MX && p.mt == 4 && p.nt == 4) p.nt = 8;
+    if ((MX || HALF) && p.mt == 4 && p.nt == 4) p.nt = 8;
     if (MX && p.nt >= 5 && p.nt <= 7) p.nt = 8;
     float* part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
     const dim3 grid((unsigned)((N + 16 * p.nt - 1) / (16 * p.nt)), 1, (unsigned)p.splits);
     const int m = (int)M, n = (int)N, k = (int)K;
     switch (p.mt) {
-        case 1: launch_mt<1, MX>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx); break;
-        case 2: launch_mt<2, MX>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx); break;
-        case 3: launch_mt<3, MX>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx); break;
-        default: launch_mt<4, MX>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx); break;
+        case 1: launch_mt<1, MX, ACT, HALF>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx, epi); break;
+        case 2: launch_mt<2, MX, ACT, HALF>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx, epi); break;
+        case 3: launch_mt<3, MX, ACT, HALF>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx, epi); break;
+        default: launch_mt<4, MX, ACT, HALF>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx, epi); break;
     }
     if (part != nullptr) {
         const int64_t threads = M * ((N + 3) / 4);
-        hipLaunchKernelGGL(skinny_splitk_reduce, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, part,
-                           p.splits, m, n, MX ? nullptr : s_tok, MX ? nullptr : s_ch, y, y32, ldy);
+        const dim3 blocks((unsigned)((threads + 255) / 256));
+        if constexpr (ACT)
+            hipLaunchKernelGGL(skinny_splitk_reduce_act, blocks, dim3(256), 0, stream, part, p.splits, m, n, s_tok, s_ch,
+                               epi);
+        else
+            hipLaunchKernelGGL(skinny_splitk_reduce, blocks, dim3(256), 0, stream, part, p.splits, m, n,
+                               MX ? nullptr : s_tok, MX ? nullptr : s_ch, y, y32, ldy);
     }
     return hipGetLastError();
 }
@@ -579,14 +666,22 @@ static hipError_t launch_skinny_any(const uint8_t* qa, int64_t lda, const float*
 hipError_t launch_gemm_skinny(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw,
                               int64_t ldw, const float* s_ch, uint16_t* y, float* y32, int64_t ldy, int64_t M, int64_t N,
                               int64_t K, void* ws, hipStream_t stream) {
-    return launch_skinny_any<false>(qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, ws, MxScales{}, stream);
+    return launch_skinny_any<false, false, false>(qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, ws, MxScales{},
+                                           Epilogue{}, stream);
+}
+
+hipError_t launch_gemm_skinny_act(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw, int64_t ldw,
+                                  const float* s_ch, const Epilogue& epi, int64_t M, int64_t N, int64_t K, void* ws,
+                                  hipStream_t stream) {
+    const auto launch = epi.type == kKvF32 ? launch_skinny_any<false, true, true> : launch_skinny_any<false, true, false>;
+    return launch(qa, lda, s_tok, qw, ldw, s_ch, nullptr, nullptr, 0, M, N, K, ws, MxScales{}, epi, stream);
 }
 
 hipError_t launch_gemm_skinny_mx(const uint8_t* qa, int64_t lda, const uint8_t* sa, const uint8_t* qw, int64_t ldw,
                                  const uint8_t* sw, uint16_t* y, int64_t ldy, int64_t M, int64_t N, int64_t K, void* ws,
                                  hipStream_t stream) {
-    return launch_skinny_any<true>(qa, lda, nullptr, qw, ldw, nullptr, y, nullptr, ldy, M, N, K, ws,
-                                   MxScales{sa, sw}, stream);
+    return launch_skinny_any<true, false, false>(qa, lda, nullptr, qw, ldw, nullptr, y, nullptr, ldy, M, N, K, ws,
+                                          MxScales{sa, sw}, Epilogue{}, stream);
 }
 
 // The one-kernel path pays for every workgroup reading all of x (fp32) from

@@ -127,6 +127,24 @@ struct MxScales {
     const uint8_t* sw;
 };
 
+// Activations of the product epilogues and of the activation quantizer.
+constexpr int kActNone = 0;
+constexpr int kActRelu = 1;
+constexpr int kActSilu = 2;
+constexpr int kActGelu = 3;      // x Phi(x)
+constexpr int kActGeluTanh = 4;  // its tanh form
+
+// What a product's *_act launchers make of acc: v = acc * (s_tok * s_ch) + bias[n]
+// (null: none), act(v), plus residual[m][n] (null: none), rounded once to `type`
+// (kKvF32, kKvBF16, kKvF16; the residual's too).  Grouped: bias is [E][N].
+struct Epilogue {
+    const float* bias;
+    const void* residual;
+    void* y;
+    int64_t ldr, ldy;
+    int act, type;
+};
+
 // Largest M the skinny (decode) kernel takes.
 constexpr int64_t kSkinnyMaxM = 64;
 
@@ -142,6 +160,10 @@ size_t gemm_skinny_ws_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_skinny(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw,
                               int64_t ldw, const float* s_ch, uint16_t* y, float* y32, int64_t ldy, int64_t M, int64_t N,
                               int64_t K, void* ws, hipStream_t stream);
+
+hipError_t launch_gemm_skinny_act(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw, int64_t ldw,
+                                  const float* s_ch, const Epilogue& epi, int64_t M, int64_t N, int64_t K, void* ws,
+                                  hipStream_t stream);
 
 // Block-scaled skinny GEMM (K % 128 == 0): y = bf16_rne(sum over blocks of
 // 2^(sa + sw - 254) * block dot); same plan and workspace as above.
@@ -174,6 +196,15 @@ hipError_t launch_gemm_mfma(const uint8_t* qa, int64_t lda, const float* s_tok, 
                             const float* s_ch, uint16_t* y, float* y32, int64_t ldy, int64_t M, int64_t N, int64_t K,
                             hipStream_t stream);
 
+// The same kernel with an epilogue, any K % 16 == 0.
+hipError_t launch_gemm_mfma_act(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw, int64_t ldw,
+                                const float* s_ch, const Epilogue& epi, int64_t M, int64_t N, int64_t K,
+                                hipStream_t stream);
+hipError_t launch_gemm_grouped_mfma_act(const uint8_t* qa, const float* s_tok, const int32_t* row_token,
+                                        const int32_t* offsets, const uint8_t* qw, const float* s_ch,
+                                        const Epilogue& epi, int64_t T, int64_t R, int64_t E, int64_t N, int64_t K,
+                                        hipStream_t stream);
+
 // Grouped (MoE) variant of the two-stage kernel, K % 128 == 0 (gemm_mfma.hip).
 hipError_t launch_gemm_grouped_mfma(const uint8_t* qa, const float* s_tok, const int32_t* row_token,
                                     const int32_t* offsets, const uint8_t* qw, const float* s_ch, uint16_t* y,
@@ -183,6 +214,50 @@ hipError_t launch_gemm_grouped_mfma(const uint8_t* qa, const float* s_tok, const
 hipError_t launch_gemm_grouped(const uint8_t* qa, const float* s_tok, const int32_t* row_token,
                                const int32_t* offsets, const uint8_t* qw, const float* s_ch, uint16_t* y,
                                int64_t T, int64_t R, int64_t E, int64_t N, int64_t K, hipStream_t stream);
+
+// Rows of a mixture of experts (moe_rows.hip).  The stable order of R = T * topk
+// choices by expert: offsets [E + 1], row_token [R] (-1 past the last row) and
+// row_of [R] (-1 without an expert).  ids: int32, or int64 when `wide`; ws:
+// moe_sort_ws_bytes(R, E) bytes.  E <= 1024.
+size_t moe_sort_ws_bytes(int64_t R, int64_t E);
+hipError_t launch_moe_sort(const void* ids, bool wide, int64_t R, int64_t topk, int64_t E, int32_t* offsets,
+                           int32_t* row_token, int32_t* row_of, void* ws, hipStream_t stream);
+// out[row_of[t][j]] = x[t], rows of row_bytes bytes (strides in bytes), and
+// s_out[row_of[t][j]] = s_tok[t] unless s_tok is null.
+hipError_t launch_moe_permute(const void* x, int64_t ldx_bytes, const float* s_tok, const int32_t* row_of, int64_t T,
+                              int64_t topk, int64_t R, int64_t row_bytes, void* out, int64_t ldo_bytes, float* s_out,
+                              hipStream_t stream);
+// out[t] = residual[t] + sum over j of weights[t][j] y[row_of[t][j]]; residual and
+// weights (ones) may be null.  R > 0 unless topk is 0.
+struct MoeCombine {
+    const void* y;
+    const int32_t* row_of;
+    const float* weights;
+    const void* residual;
+    void* out;
+    int64_t ldy, ldr, ldo, H;
+    int T, topk, R;
+};
+hipError_t launch_moe_combine(const MoeCombine& p, int dtype, int out_dtype, hipStream_t stream);
+// dy[row_of[t][j]] = weights[t][j] dout[t], dweights[t][j] = <dout[t], y[row_of[t][j]]>;
+// dy or dweights may be null.
+struct MoeCombineGrad {
+    const void* dout;
+    const void* y;
+    const int32_t* row_of;
+    const float* weights;
+    void* dy;
+    float* dweights;
+    int64_t ldd, ldy, lddy, H;
+    int T, topk, R;
+};
+hipError_t launch_moe_combine_grad(const MoeCombineGrad& p, int dtype, int y_dtype, hipStream_t stream);
+
+// Activation (times the gate's partner) and per-token quantization
+// (act_quantize.hip): v = act(h[:, :F]) * h[:, F:] when gated, else act(h); rows
+// from *live_rows on (null: none) are left out.  F % 16 == 0, 16-byte rows.
+hipError_t launch_act_quantize(const void* h, int64_t ldh, int dtype, int64_t rows, int64_t F, int act, bool gated,
+                               uint8_t* q, int64_t ldq, float* scales, const int32_t* live_rows, hipStream_t stream);
 
 // Plain streaming read of `bytes` bytes (multiple of 16, p 16-byte aligned)
 // by about `workgroups` workgroups of 256 threads (stream_read.hip); sink: one

@@ -455,6 +455,144 @@ size_t fp8_attn_prefill_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_
                                         int64_t max_blocks, int64_t max_q, int64_t max_len);
 
 /*
+ * Expert rows: from a router's choices to the rows that fp8_gemm_grouped_scaled
+ * takes, and back (experts entirely in FP8: DeepSeek V4 950 page, §2.3 item 5;
+ * the router itself stays in the caller's precision).  Element types are
+ * fp8_kv_dtype_t; sums are fp32, in the order of the choices, so results do not
+ * depend on timing.  Matrices are row-major with any row stride >= the row
+ * length; every pointer 16-byte aligned.  T, topk, R, H and T * topk up to
+ * 2^31 - 1.
+ *
+ * fp8_moe_sort: the stable order of the choices by expert.  expert_ids [T, topk]
+ * int32, or int64 when ids_64 != 0; an id outside [0, E) (dropped over capacity,
+ * padding) has no expert.
+ *   expert_offsets[e]     = choices of experts below e, e = 0 .. E  (int32 [E + 1])
+ *   row_of[t, j]          = the choice's row: expert_offsets[id] + the choices of
+ *                           the same expert before it (in the order t * topk + j),
+ *                           -1 without an expert                     (int32 [T, topk])
+ *   row_token[row_of]     = t; -1 from row expert_offsets[E] on      (int32 [T * topk])
+ * E <= 1024.  ws: at least fp8_moe_sort_workspace_bytes(T, topk, E) bytes,
+ * 16-byte aligned (may be NULL when that is 0; contents on entry do not matter).
+ */
+fp8_status_t fp8_moe_sort(const void* expert_ids, int32_t ids_64, int64_t T, int64_t topk, int64_t E,
+                          int32_t* expert_offsets, int32_t* row_token, int32_t* row_of, void* ws, size_t ws_bytes,
+                          hipStream_t stream);
+
+/* Workspace bytes fp8_moe_sort needs (host only; SIZE_MAX for sizes it refuses). */
+size_t fp8_moe_sort_workspace_bytes(int64_t T, int64_t topk, int64_t E);
+
+/*
+ * Tokens moved into the experts' order (what an exchange between GPUs sends, or
+ * what a product without a gather reads):
+ *   out[row_of[t, j]] = x[t],   s_out[row_of[t, j]] = s_tok[t]
+ * x [T, H], out [R, H] of elements of elem_bytes 1, 2 or 4 bytes, moved as they
+ * are; s_tok and s_out fp32 [T], [R], both or neither NULL.  Entries of row_of
+ * outside [0, R) are skipped; rows no entry names are left as they were; two
+ * entries of the same row race.  out does not overlap x.  Its gradient is
+ * fp8_moe_combine of out's without weights.  No workspace.
+ */
+fp8_status_t fp8_moe_permute(const void* x, int64_t ldx, const float* s_tok, const int32_t* row_of, int64_t T,
+                             int64_t topk, int64_t R, int64_t H, int64_t elem_bytes, void* out, int64_t ldo,
+                             float* s_out, hipStream_t stream);
+
+/*
+ * The experts' rows back to their tokens:
+ *   out[t, n] = round(residual[t, n] + sum_j weights[t, j] * y[row_of[t, j], n])
+ * j = 0, 1, .. added in order in fp32 onto the residual (0 when NULL), rounded
+ * once (RNE) to out_dtype, which is the residual's type too.  weights fp32
+ * [T, topk], NULL for ones.  Entries of row_of outside [0, R) add nothing (their
+ * weight does not matter); a token without any gets its residual, or +0.
+ * residual may be out itself (same pointer and stride), else neither overlaps
+ * out; y does not.  No workspace.
+ */
+fp8_status_t fp8_moe_combine(const void* y, int64_t ldy, fp8_kv_dtype_t y_dtype, const int32_t* row_of,
+                             const float* weights, const void* residual, int64_t ldr, void* out,
+                             fp8_kv_dtype_t out_dtype, int64_t ldo, int64_t T, int64_t topk, int64_t R, int64_t H,
+                             hipStream_t stream);
+
+/*
+ * The gradient of fp8_moe_combine (its residual's gradient is dout itself):
+ *   dy[row_of[t, j], n] = round(weights[t, j] * dout[t, n])          to y_dtype
+ *   dweights[t, j]      = sum_n dout[t, n] * y[row_of[t, j], n]      in fp32
+ * dy [R, H] and dweights fp32 [T, topk]; either may be NULL (y is read for
+ * dweights alone and may be NULL without it).  Entries of row_of outside [0, R)
+ * write no row and a weight's gradient of +0; rows no entry names are left as
+ * they were; two entries of the same row race.  dy may be y itself (same pointer
+ * and stride), else neither overlaps an input.  No workspace.
+ */
+fp8_status_t fp8_moe_combine_grad(const void* dout, int64_t ldd, fp8_kv_dtype_t dout_dtype, const void* y, int64_t ldy,
+                                  fp8_kv_dtype_t y_dtype, const int32_t* row_of, const float* weights, void* dy,
+                                  int64_t lddy, float* dweights, int64_t T, int64_t topk, int64_t R, int64_t H,
+                                  hipStream_t stream);
+
+/*
+ * Activations, evaluated in fp32 to a few units of 2^-24 of their value:
+ *   NONE x   RELU max(x, 0)   SILU x / (1 + e^-x)   GELU x Phi(x) = x (1 + erf(x / sqrt 2)) / 2
+ *   GELU_TANH x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2
+ */
+typedef enum {
+    FP8_ACT_NONE = 0,
+    FP8_ACT_RELU = 1,
+    FP8_ACT_SILU = 2,
+    FP8_ACT_GELU = 3,
+    FP8_ACT_GELU_TANH = 4
+} fp8_act_t;
+
+/*
+ * Scaled FP8 GEMM with bias, activation and residual in its epilogue (the
+ * dataflow without steps of their own between products: DeepSeek V4 950 page,
+ * §1.3 and §2.3):
+ *   v      = acc[m,n] * (s_tok[m] * s_ch[n]) + bias[n]      (acc as fp8_gemm_scaled)
+ *   y[m,n] = round(act(v) + residual[m,n])
+ * in fp32, rounded once (RNE) to y_dtype, which is the residual's type too: an
+ * fp32 y is what fp8_quantize_per_token takes next.  bias fp32 [N] and residual
+ * [M, N] (row stride ldr >= N) may be NULL; residual may be y itself (same
+ * pointer and stride), else it does not overlap y.  y [M, N], any row stride
+ * ldy >= N.  Without bias, activation and residual a bf16 y holds the bits of
+ * fp8_gemm_scaled wherever both take the same division of K.  ws: at least
+ * fp8_gemm_act_workspace_bytes(M, N, K) bytes (may be NULL when that is 0).
+ */
+fp8_status_t fp8_gemm_scaled_act(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw, int64_t ldw,
+                                 const float* s_ch, const float* bias, fp8_act_t act, const void* residual, int64_t ldr,
+                                 void* y, fp8_kv_dtype_t y_dtype, int64_t ldy, int64_t M, int64_t N, int64_t K, void* ws,
+                                 size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes fp8_gemm_scaled_act needs (host only; SIZE_MAX for sizes it refuses). */
+size_t fp8_gemm_act_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/*
+ * The same per expert, over rows sorted by expert (fp8_gemm_grouped_scaled with
+ * an epilogue): routed row r of expert e
+ *   y[r,n] = round(act(acc[r,n] * (s_tok[t] * s_ch[e,n]) + bias[e,n])),  t = row_token[r]
+ * bias fp32 [E, N] or NULL; y [R, N] of y_dtype, any row stride ldy >= N.  The
+ * routing arrays as there, but expert_offsets[E] may be below R: rows from it on
+ * are left as they were (fp8_moe_sort's arrays qualify as they are).  ws as there.
+ */
+fp8_status_t fp8_gemm_grouped_scaled_act(const uint8_t* qa, const float* s_tok, const int32_t* row_token,
+                                         const int32_t* expert_offsets, const uint8_t* qw, const float* s_ch,
+                                         const float* bias, fp8_act_t act, void* y, fp8_kv_dtype_t y_dtype, int64_t ldy,
+                                         int64_t T, int64_t R, int64_t E, int64_t N, int64_t K, void* ws,
+                                         size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Activation and per-token quantization in one pass: what stands between the two
+ * products of a feed-forward layer (per-token scales on the fly: DeepSeek V4 950
+ * page, §2.4, §3.1).  h [rows, gated ? 2 F : F] of `dtype` elements, row stride
+ * ldh:
+ *   v[r,k]    = act(h[r,k]) * h[r, F + k] when gated != 0, else act(h[r,k])   (fp32)
+ *   scales[r] = max(fl32(max_k |v[r,k]| / 448), 1e-12f)
+ *   q[r,k]    = E4M3 code of fl32(v[r,k] / scales[r]), RNE, saturating +-448
+ * (FP8_ACT_NONE, not gated: fp8_quantize_per_token of bf16, fp16 or fp32 rows).
+ * live_rows: one int32 on the device, or NULL: rows from *live_rows on are left
+ * as they were (e.g. &expert_offsets[E], past which rows have no expert).
+ * F % 16 == 0, rows of h and q 16-byte aligned; h and v are assumed finite.
+ * No workspace.
+ */
+fp8_status_t fp8_act_quantize(const void* h, int64_t ldh, fp8_kv_dtype_t dtype, int64_t rows, int64_t F, fp8_act_t act,
+                              int32_t gated, uint8_t* q, int64_t ldq, float* scales, const int32_t* live_rows,
+                              hipStream_t stream);
+
+/*
  * HBM read ceiling (a measurement utility beside the layer, not part of it):
  * reads the `bytes` bytes at p once with plain 16-byte vector loads
  * (nontemporal loads when `nontemporal` != 0) from about `workgroups`
