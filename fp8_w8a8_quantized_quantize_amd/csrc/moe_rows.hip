@@ -27,45 +27,82 @@ __device__ __forceinline__ int key_of(ID id, int E) {
     return id >= 0 && id < (ID)E ? (int)id : E;
 }
 
-// Few choices: workgroup e of E + 1 reads them all, counts those below e (its
-// first row) and those of e in front of each of its waves, and places its own in
-// a second reading.  One launch and no workspace; E + 1 readings of the ids.
+// Few choices: the workgroups of expert e (of E + 1) read them all, count those below
+// e (its first row) and those of e in front of each of their waves, and place its
+// own.  A wave holds its part of the choices in registers, KEYS per lane, so they
+// are read once, with all loads in flight together.  `parts` workgroups of an expert
+// do the same and share the placing, each taking every parts-th step of a wave: a
+// step's scattered stores cost more than its counting.  One launch, no workspace.
 constexpr int kSortOneThreads = 1024;
 
-template <typename ID, int T>
-__global__ __launch_bounds__(T) void moe_sort_one(const ID* __restrict__ ids, int R, int topk, int E,
-                                                  int32_t* __restrict__ offsets, int32_t* __restrict__ row_token,
+// Choices a lane takes side by side: 16 bytes.
+template <typename ID>
+constexpr int ids_per_load() {
+    return 16 / (int)sizeof(ID);
+}
+
+template <typename ID, int T, int KEYS>
+__global__ __launch_bounds__(T) void moe_sort_one(const ID* __restrict__ ids, int R, uint32_t per_topk, int E,
+                                                  int parts, int32_t* __restrict__ offsets, int32_t* __restrict__ row_token,
                                                   int32_t* __restrict__ row_of) {
-    constexpr int W = T / kWave;
+    constexpr int W = T / kWave, V = ids_per_load<ID>(), STEPS = KEYS / V;
+    static_assert(KEYS % V == 0, "whole loads");
+    typedef ID idv __attribute__((ext_vector_type(V)));
     __shared__ int below[W], equal[W];
-    const int e = blockIdx.x;
+    const int e = blockIdx.x / parts, part = blockIdx.x % parts;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int per = ((R + W - 1) / W + 63) & ~63;  // choices of a wave, contiguous
-    const int begin = min(R, wave * per), end = min(R, begin + per);
-    int lt = 0, eq = 0;
-    for (int i0 = begin; i0 < end; i0 += 64) {
-        const int i = i0 + lane;
-        const int key = i < end ? key_of(ids[i], E) : E + 1;
-        lt += __popcll(__ballot(key < e));
-        eq += __popcll(__ballot(key == e));
+    const int begin = wave * (64 * KEYS) + lane * V;  // of this lane's first load; further ones 64 V apart
+    int key[STEPS][V];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        const int i = begin + s * 64 * V;
+        if (i + V <= R) {
+            const idv id = *reinterpret_cast<const idv*>(ids + i);
+#pragma unroll
+            for (int v = 0; v < V; ++v) key[s][v] = key_of((ID)id[v], E);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) key[s][v] = i + v < R ? key_of(ids[i + v], E) : E + 1;
+        }
     }
-    if (lane == 0) below[wave] = lt, equal[wave] = eq;
+    int lt = 0, eq = 0;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int v = 0; v < V; ++v) lt += key[s][v] < e, eq += key[s][v] == e;
+    int sum = lt | eq << 16;  // a wave has fewer than 2^16 choices
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, kWave);
+    if (lane == 0) below[wave] = sum & 0xFFFF, equal[wave] = sum >> 16;
     __syncthreads();
     int row = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) row += below[w];
-    if (threadIdx.x == 0) offsets[e] = row;
-    for (int w = 0; w < wave; ++w) row += equal[w];
-    for (int i0 = begin; i0 < end; i0 += 64) {
-        const int i = i0 + lane;
-        const bool mine = i < end && key_of(ids[i], E) == e;
-        const unsigned long long all = __ballot(mine);
-        if (mine) {
-            const int r = row + __popcll(all & ((1ull << lane) - 1));
-            row_of[i] = e < E ? r : -1;
-            row_token[r] = e < E ? i / topk : -1;
+    if (threadIdx.x == 0 && part == 0) offsets[e] = row;
+#pragma unroll
+    for (int w = 0; w < W; ++w) row += w < wave ? equal[w] : 0;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        unsigned long long mine[V];
+        unsigned long long any = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) mine[v] = __ballot(key[s][v] == e), any |= mine[v];
+        int r = row;
+#pragma unroll
+        for (int v = 0; v < V; ++v) row += __popcll(mine[v]);
+        if (any == 0 || s % parts != part) continue;
+#pragma unroll
+        for (int v = 0; v < V; ++v) r += __popcll(mine[v] & ((1ull << lane) - 1));
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (key[s][v] == e) {
+                const uint32_t i = begin + s * 64 * V + v;
+                row_of[i] = e < E ? r : -1;
+                // i / topk: i topk < 2^32, so the rounded-up reciprocal gives the quotient
+                row_token[r] = e < E ? (int32_t)(per_topk != 0 ? __umulhi(i, per_topk) : i) : -1;
+                ++r;
+            }
         }
-        row += __popcll(all);
     }
 }
 
@@ -75,7 +112,7 @@ __global__ __launch_bounds__(T) void moe_sort_one(const ID* __restrict__ ids, in
 constexpr int kSortThreads = 512;
 constexpr int kSortWaves = kSortThreads / kWave;
 constexpr int kSortKeys = 1025;  // E <= 1024 and the key of choices without an expert
-constexpr int kSortPerKey = (kSortKeys + kSortThreads - 1) / kSortThreads;
+constexpr int kSortAhead = 4;    // steps of 64 choices loaded together
 
 template <typename ID>
 __global__ __launch_bounds__(kSortThreads) void moe_sort_count(const ID* __restrict__ ids, int R, int chunk, int E,
@@ -84,7 +121,15 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_count(const ID* __restr
     for (int k = threadIdx.x; k <= E; k += kSortThreads) cnt[k] = 0;
     __syncthreads();
     const int64_t begin = (int64_t)blockIdx.x * chunk, end = min((int64_t)R, begin + chunk);
-    for (int64_t i = begin + threadIdx.x; i < end; i += kSortThreads) atomicAdd(&cnt[key_of(ids[i], E)], 1);
+    for (int64_t i = begin + threadIdx.x; i < end; i += kSortAhead * kSortThreads) {
+        int key[kSortAhead];
+#pragma unroll
+        for (int a = 0; a < kSortAhead; ++a)
+            key[a] = i + a * kSortThreads < end ? key_of(ids[i + a * kSortThreads], E) : -1;
+#pragma unroll
+        for (int a = 0; a < kSortAhead; ++a)
+            if (key[a] >= 0) atomicAdd(&cnt[key[a]], 1);
+    }
     __syncthreads();
     for (int k = threadIdx.x; k <= E; k += kSortThreads) counts[(int64_t)blockIdx.x * (E + 1) + k] = cnt[k];
 }
@@ -96,32 +141,54 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_place(const ID* __restr
                                                                int32_t* __restrict__ row_token,
                                                                int32_t* __restrict__ row_of) {
     __shared__ int next[kSortWaves][kSortKeys];  // the next row of a key in a wave's part of the chunk
+    __shared__ int total[kSortKeys], before[kSortKeys];
     __shared__ int wave_sum[kSortWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int keys = E + 1;
-    for (int k = threadIdx.x; k < kSortWaves * kSortKeys; k += kSortThreads) (&next[0][0])[k] = 0;
-    __syncthreads();
+    for (int k = lane; k < keys; k += 64) next[wave][k] = 0;
+    for (int k = threadIdx.x; k < keys; k += kSortThreads) total[k] = before[k] = 0;
     const int64_t base = (int64_t)blockIdx.x * chunk;
     const int64_t chunk_end = min((int64_t)R, base + chunk);
-    const int per = chunk / kSortWaves;  // a multiple of 64
+    const int per = chunk / kSortWaves;  // a multiple of 64 kSortAhead
     const int64_t begin = min(chunk_end, base + (int64_t)wave * per), end = min(chunk_end, begin + per);
-    for (int64_t i = begin + lane; i < end; i += 64) atomicAdd(&next[wave][key_of(ids[i], E)], 1);
-
-    // Every key's count in all chunks and in those before this one; thread t takes
-    // the keys t * kSortPerKey + j, so that the scan over keys is one over threads.
-    int total[kSortPerKey], before[kSortPerKey], sum = 0;
+    auto load_keys = [&](int64_t i0, int (&key)[kSortAhead]) {
 #pragma unroll
-    for (int j = 0; j < kSortPerKey; ++j) {
-        total[j] = before[j] = 0;
-        const int k = threadIdx.x * kSortPerKey + j;
-        if (k < keys)
-            for (int b = 0; b < (int)gridDim.x; ++b) {
-                const int c = counts[(int64_t)b * keys + k];
-                total[j] += c;
-                before[j] += b < (int)blockIdx.x ? c : 0;
-            }
-        sum += total[j];
+        for (int a = 0; a < kSortAhead; ++a) {
+            const int64_t i = i0 + a * 64 + lane;
+            key[a] = i < end ? key_of(ids[i], E) : -1;
+        }
+    };
+    __syncthreads();
+    for (int64_t i0 = begin; i0 < end; i0 += 64 * kSortAhead) {
+        int key[kSortAhead];
+        load_keys(i0, key);
+#pragma unroll
+        for (int a = 0; a < kSortAhead; ++a)
+            if (key[a] >= 0) atomicAdd(&next[wave][key[a]], 1);
     }
+    // Every key's count in all chunks and in those before this one.  Threads side by
+    // side take neighbouring keys of one chunk; when the keys leave threads over,
+    // groups of threads take every group-th chunk.
+    const int wide = min(kSortThreads, (keys + 63) & ~63), groups = kSortThreads / wide;
+    const int group = threadIdx.x / wide;
+    if (group < groups) {
+        for (int k = threadIdx.x - group * wide; k < keys; k += wide) {
+            int all = 0, front = 0;
+#pragma unroll 32
+            for (int b = group; b < (int)gridDim.x; b += groups) {
+                const int c = counts[(int64_t)b * keys + k];
+                all += c;
+                front += b < (int)blockIdx.x ? c : 0;
+            }
+            atomicAdd(&total[k], all);
+            atomicAdd(&before[k], front);
+        }
+    }
+    __syncthreads();
+    // Keys' first rows: thread t scans the keys [t n, (t + 1) n).
+    const int n = (keys + kSortThreads - 1) / kSortThreads;
+    int sum = 0;
+    for (int k = threadIdx.x * n; k < min(keys, ((int)threadIdx.x + 1) * n); ++k) sum += total[k];
     int incl = sum;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -129,79 +196,111 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_place(const ID* __restr
         if (lane >= off) incl += v;
     }
     if (lane == 63) wave_sum[wave] = incl;
-    __syncthreads();  // also: next[] holds the counts of every wave
+    __syncthreads();
     int first = incl - sum;
     for (int w = 0; w < wave; ++w) first += wave_sum[w];
+    for (int k = threadIdx.x * n; k < min(keys, ((int)threadIdx.x + 1) * n); ++k) {
+        if (blockIdx.x == 0) offsets[k] = first;
+        int row = first + before[k];
 #pragma unroll
-    for (int j = 0; j < kSortPerKey; ++j) {
-        const int k = threadIdx.x * kSortPerKey + j;
-        if (k < keys) {
-            if (blockIdx.x == 0) offsets[k] = first;
-            int row = first + before[j];
-#pragma unroll
-            for (int w = 0; w < kSortWaves; ++w) {
-                const int c = next[w][k];
-                next[w][k] = row;
-                row += c;
-            }
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int c = next[w][k];
+            next[w][k] = row;
+            row += c;
         }
-        first += total[j];
+        first += total[k];
     }
     __syncthreads();
 
-    for (int64_t i0 = begin; i0 < end; i0 += 64) {
-        const int64_t i = i0 + lane;
-        const bool live = i < end;
-        const int key = live ? key_of(ids[i], E) : E;
-        // the lanes of the same key
-        unsigned long long same = __ballot(live);
-        for (int b = 0; b < key_bits; ++b) {
-            const unsigned long long set = __ballot((key >> b) & 1);
-            same &= (key >> b) & 1 ? set : ~set;
+    for (int64_t i0 = begin; i0 < end; i0 += 64 * kSortAhead) {
+        int keys_ahead[kSortAhead];
+        load_keys(i0, keys_ahead);
+#pragma unroll
+        for (int a = 0; a < kSortAhead; ++a) {
+            const int64_t i = i0 + a * 64 + lane;
+            const int key = keys_ahead[a];
+            // the lanes of the same key
+            unsigned long long same = __ballot(key >= 0);
+            for (int b = 0; b < key_bits; ++b) {
+                const unsigned long long set = __ballot((key >> b) & 1);
+                same &= (key >> b) & 1 ? set : ~set;
+            }
+            if (key >= 0) {
+                const int r = next[wave][key] + __popcll(same & ((1ull << lane) - 1));
+                row_of[i] = key < E ? r : -1;
+                row_token[r] = key < E ? (int32_t)((uint32_t)i / (uint32_t)topk) : -1;
+                if ((same >> lane) == 1) next[wave][key] = r + 1;  // the last of them
+            }
+            __builtin_amdgcn_wave_barrier();
         }
-        if (live) {
-            const int r = next[wave][key] + __popcll(same & ((1ull << lane) - 1));
-            row_of[i] = key < E ? r : -1;
-            row_token[r] = key < E ? (int32_t)((uint32_t)i / (uint32_t)topk) : -1;
-            if ((same >> lane) == 1) next[wave][key] = r + 1;  // the last of them
-        }
-        __builtin_amdgcn_wave_barrier();
     }
 }
 
 // ---------------------------------------------------------------- permute ----
 //
-// A workgroup's threads cover `lanes` 16-byte pieces of 256 / lanes tokens.
+// Lanes side by side take 16-byte pieces of a row: a wave 64 of one token's (a task
+// is then a token and one of its 64-piece columns), or, where a row has fewer, its
+// lanes 2^bits each of several tokens'.  A lane's piece is all it does, so its loads
+// are in flight together and rows of any length leave no lanes idle but in their
+// last column.
 
 constexpr int kRowThreads = 256;
 
+struct RowTasks {
+    int bits;      // lanes of a task: 2^bits
+    int64_t cols;  // tasks of a row
+};
+
+// Task `u` of this lane's group: its row and the lane's piece in it.
+struct RowTask {
+    int64_t row, piece;
+};
+
+__device__ __forceinline__ int64_t first_task(const RowTasks& k) {
+    return (int64_t)blockIdx.x * (kRowThreads >> k.bits) + (threadIdx.x >> k.bits);
+}
+__device__ __forceinline__ int64_t task_stride(const RowTasks& k) {
+    return (int64_t)gridDim.x * (kRowThreads >> k.bits);
+}
+// WAVE: k.bits is 6.  The task is then the same for the whole wave, and said to be
+// so: its indices and weights come by scalar loads.
+template <bool WAVE>
+__device__ __forceinline__ RowTask row_task(const RowTasks& k, int64_t u) {
+    if constexpr (WAVE)
+        u = (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)u) |
+            (int64_t)__builtin_amdgcn_readfirstlane((int)(u >> 32)) << 32;
+    const int64_t row = k.cols == 1 ? u : u / k.cols;
+    return {row, ((u - row * k.cols) << k.bits) + (threadIdx.x & ((1 << k.bits) - 1))};
+}
+
+template <bool WAVE>
 __global__ __launch_bounds__(kRowThreads) void moe_permute(const uint8_t* __restrict__ x, int64_t ldx,
                                                            const float* __restrict__ s_tok,
-                                                           const int32_t* __restrict__ row_of, int T, int topk, int R,
-                                                           int64_t row_bytes, int lane_bits, uint8_t* __restrict__ out,
-                                                           int64_t ldo, float* __restrict__ s_out) {
-    const int lanes = 1 << lane_bits;
-    const int l = threadIdx.x & (lanes - 1);
-    const int per_block = kRowThreads >> lane_bits;
-    for (int64_t t = (int64_t)blockIdx.x * per_block + (threadIdx.x >> lane_bits); t < T;
-         t += (int64_t)gridDim.x * per_block) {
-        const int32_t* rows = row_of + t * topk;
-        const uint8_t* src = x + t * ldx;
-        if (s_tok != nullptr)
-            for (int j = l; j < topk; j += lanes)
-                if ((uint32_t)rows[j] < (uint32_t)R) s_out[rows[j]] = s_tok[t];
-        for (int64_t b = 16 * (int64_t)l; b < row_bytes; b += 16 * (int64_t)lanes) {
-            if (b + 16 <= row_bytes) {
-                uint32_t w[4];
-                load_words(src + b, w);
+                                                           const int32_t* __restrict__ row_of, int64_t tasks, int topk,
+                                                           int R, int64_t row_bytes, RowTasks k,
+                                                           uint8_t* __restrict__ out, int64_t ldo,
+                                                           float* __restrict__ s_out) {
+    for (int64_t u = first_task(k); u < tasks; u += task_stride(k)) {
+        const RowTask at = row_task<WAVE>(k, u);
+        const int32_t* rows = row_of + at.row * topk;
+        const uint8_t* src = x + at.row * ldx;
+        const int64_t b = 16 * at.piece;
+        if (s_tok != nullptr && at.piece < topk)
+            for (int64_t j = at.piece; j < topk; j += k.cols << k.bits)
+                if ((uint32_t)rows[j] < (uint32_t)R) s_out[rows[j]] = s_tok[at.row];
+        if (b >= row_bytes) continue;
+        if (row_bytes >= 16) {
+            // a row's last piece overlaps the one before it: both write the same bytes there
+            const int64_t at0 = min(b, row_bytes - 16);
+            uint32_t w[4];
+            load_words(src + at0, w);
+            for (int j = 0; j < topk; ++j)
+                if ((uint32_t)rows[j] < (uint32_t)R) store_words(out + (int64_t)rows[j] * ldo + at0, w);
+        } else {
+            for (int64_t i = 0; i < row_bytes; ++i) {
+                const uint8_t v = src[i];
                 for (int j = 0; j < topk; ++j)
-                    if ((uint32_t)rows[j] < (uint32_t)R) store_words(out + (int64_t)rows[j] * ldo + b, w);
-            } else {
-                for (int64_t i = b; i < row_bytes; ++i) {
-                    const uint8_t v = src[i];
-                    for (int j = 0; j < topk; ++j)
-                        if ((uint32_t)rows[j] < (uint32_t)R) out[(int64_t)rows[j] * ldo + i] = v;
-                }
+                    if ((uint32_t)rows[j] < (uint32_t)R) out[(int64_t)rows[j] * ldo + i] = v;
             }
         }
     }
@@ -209,43 +308,80 @@ __global__ __launch_bounds__(kRowThreads) void moe_permute(const uint8_t* __rest
 
 // ---------------------------------------------------------------- combine ----
 
-template <int DT, int ODT, int U>
-__global__ __launch_bounds__(kRowThreads) void moe_combine(MoeCombine p, int lane_bits) {
+// U choices' pieces are in flight together: loads before anything that waits for
+// one, and no branch between them.  A row's last piece reaches back over the one
+// before it and stores only the elements that are its own (what it reads of the
+// others may have been written already, where the residual is the output).  Rows
+// shorter than a piece go element by element.
+template <int DT, int ODT, int U, bool WAVE>
+__global__ __launch_bounds__(kRowThreads) void moe_combine(MoeCombine p, int64_t tasks, RowTasks k) {
     constexpr int V = 16 / elem_size<DT>();
-    const int lanes = 1 << lane_bits;
-    const int l = threadIdx.x & (lanes - 1);
-    const int per_block = kRowThreads >> lane_bits;
-    for (int64_t t = (int64_t)blockIdx.x * per_block + (threadIdx.x >> lane_bits); t < p.T;
-         t += (int64_t)gridDim.x * per_block) {
-        for (int64_t n = (int64_t)V * l; n < p.H; n += (int64_t)V * lanes) {
-            const int left = (int)min((int64_t)V, p.H - n);
+    for (int64_t u0 = first_task(k); u0 < tasks; u0 += task_stride(k)) {
+        const RowTask at = row_task<WAVE>(k, u0);
+        const int64_t t = at.row, own = V * at.piece;
+        const int32_t* rows = p.row_of + t * p.topk;
+        const float* weights = p.weights != nullptr ? p.weights + t * p.topk : nullptr;
+        if (own >= p.H) continue;
+        if (p.H >= V) {
+            const int64_t n = min(own, p.H - V);
+            uint32_t res[V * elem_size<ODT>() / 4];
             float acc[V];
             if (p.residual != nullptr) {
-                load_run<ODT, V>(p.residual, t * p.ldr + n, left, acc);
+                load_words(static_cast<const uint8_t*>(p.residual) + (t * p.ldr + n) * elem_size<ODT>(), res);
             } else {
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+                for (int i = 0; i < V * elem_size<ODT>() / 4; ++i) res[i] = 0;
             }
-            for (int j0 = 0; j0 < p.topk; j0 += U) {
-                float v[U][V], w[U];
-                bool live[U];
+            auto choices = [&](int j0, bool first) {
+                int r[U];
+                float w[U];
+                uint32_t raw[U][4];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int j = min(j0 + u, p.topk - 1);
-                    const int r = p.row_of[t * p.topk + j];
-                    live[u] = j0 + u < p.topk && (uint32_t)r < (uint32_t)p.R;
-                    w[u] = p.weights != nullptr ? p.weights[t * p.topk + j] : 1.0f;
-                    // a choice without a row reads row 0 and leaves it unused
-                    load_run<DT, V>(p.y, (live[u] ? (int64_t)r : 0) * p.ldy + n, left, v[u]);
+                    r[u] = rows[j];
+                    r[u] = j0 + u < p.topk && (uint32_t)r[u] < (uint32_t)p.R ? r[u] : -1;
                 }
+                if (weights != nullptr) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) w[u] = weights[min(j0 + u, p.topk - 1)];
+                }
+                // a choice without a row reads row 0 and leaves it unused
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (live[u]) {
+                    load_words(static_cast<const uint8_t*>(p.y) + ((int64_t)max(r[u], 0) * p.ldy + n) * elem_size<DT>(), raw[u]);
+                if (first) unpack<ODT, V>(res, acc);
 #pragma unroll
-                        for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(w[u], v[u][i], acc[i]);
-                    }
+                for (int u = 0; u < U; ++u) {
+                    if (r[u] < 0) continue;
+                    float v[V];
+                    unpack<DT, V>(raw[u], v);
+                    const float wu = weights != nullptr ? w[u] : 1.0f;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(wu, v[i], acc[i]);
+                }
+            };
+            if (p.topk > 0)
+                choices(0, true);
+            else
+                unpack<ODT, V>(res, acc);
+            for (int j0 = U; j0 < p.topk; j0 += U) choices(j0, false);
+            if (n == own) {
+                store_run<ODT, V>(p.out, t * p.ldo + n, V, acc);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (n + i >= own) store_elem<ODT>(p.out, t * p.ldo + n + i, acc[i]);
             }
-            store_run<ODT, V>(p.out, t * p.ldo + n, left, acc);
+        } else {
+            for (int64_t i = 0; i < p.H; ++i) {
+                float acc = p.residual != nullptr ? load_elem<ODT>(p.residual, t * p.ldr + i) : 0.0f;
+                for (int j = 0; j < p.topk; ++j)
+                    if ((uint32_t)rows[j] < (uint32_t)p.R)
+                        acc = __builtin_fmaf(weights != nullptr ? weights[j] : 1.0f,
+                                             load_elem<DT>(p.y, (int64_t)rows[j] * p.ldy + i), acc);
+                store_elem<ODT>(p.out, t * p.ldo + i, acc);
+            }
         }
     }
 }
@@ -256,6 +392,7 @@ __global__ __launch_bounds__(kRowThreads) void moe_combine(MoeCombine p, int lan
 template <int DT, int YDT>
 __global__ __launch_bounds__(kRowThreads) void moe_combine_grad(MoeCombineGrad p, int lane_bits) {
     constexpr int V = 16 / elem_size<YDT>();
+    constexpr int U = 4;  // pieces of a lane in flight
     __shared__ float part[kRowThreads / kWave];
     const int lanes = 1 << lane_bits;
     const int l = threadIdx.x & (lanes - 1);
@@ -268,20 +405,52 @@ __global__ __launch_bounds__(kRowThreads) void moe_combine_grad(MoeCombineGrad p
         if ((uint32_t)r < (uint32_t)p.R) {
             const int64_t t = c / p.topk;
             const float w = p.weights != nullptr ? p.weights[c] : 1.0f;
-            for (int64_t n = (int64_t)V * l; n < p.H; n += (int64_t)V * lanes) {
-                const int left = (int)min((int64_t)V, p.H - n);
-                float d[V], y[V];
-                load_run<DT, V>(p.dout, t * p.ldd + n, left, d);
-                if (p.dweights != nullptr) {
-                    load_run<YDT, V>(p.y, (int64_t)r * p.ldy + n, left, y);
+            const int64_t d0 = t * p.ldd, y0 = (int64_t)r * p.ldy, g0 = (int64_t)r * p.lddy;
+            // M pieces of the lane, `lanes` apart, from element n on; its own begin at `own`
+            auto pieces = [&](auto many, int64_t n, int64_t own) {
+                constexpr int M = decltype(many)::value;
+                uint32_t dr[M][V * elem_size<DT>() / 4], yr[M][4];
 #pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (i < left) dot = __builtin_fmaf(d[i], y[i], dot);
+                for (int m = 0; m < M; ++m) {
+                    const int64_t at = n + (int64_t)m * V * lanes;
+                    load_words(static_cast<const uint8_t*>(p.dout) + (d0 + at) * elem_size<DT>(), dr[m]);
+                    if (p.dweights != nullptr)
+                        load_words(static_cast<const uint8_t*>(p.y) + (y0 + at) * elem_size<YDT>(), yr[m]);
                 }
-                if (p.dy != nullptr) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) d[i] *= w;
-                    store_run<YDT, V>(p.dy, (int64_t)r * p.lddy + n, left, d);
+                for (int m = 0; m < M; ++m) {
+                    float d[V], y[V];
+                    unpack<DT, V>(dr[m], d);
+                    if (p.dweights != nullptr) {
+                        unpack<YDT, V>(yr[m], y);
+#pragma unroll
+                        for (int i = 0; i < V; ++i)
+                            if (M > 1 || n + i >= own) dot = __builtin_fmaf(d[i], y[i], dot);
+                    }
+                    if (p.dy != nullptr) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) d[i] *= w;
+                        if (M > 1 || n == own) {
+                            store_run<YDT, V>(p.dy, g0 + n + (int64_t)m * V * lanes, V, d);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < V; ++i)
+                                if (n + i >= own) store_elem<YDT>(p.dy, g0 + n + i, d[i]);
+                        }
+                    }
+                }
+            };
+            int64_t n = (int64_t)V * l;
+            for (; n + (int64_t)(U - 1) * V * lanes + V <= p.H; n += (int64_t)U * V * lanes)
+                pieces(std::integral_constant<int, U>{}, n, n);
+            if (p.H >= V) {
+                // the row's last piece reaches back over the one before it, as in moe_combine
+                for (; n < p.H; n += (int64_t)V * lanes) pieces(std::integral_constant<int, 1>{}, min(n, p.H - V), n);
+            } else if (l == 0) {
+                for (int64_t i = 0; i < p.H; ++i) {
+                    const float d = load_elem<DT>(p.dout, d0 + i);
+                    if (p.dweights != nullptr) dot = __builtin_fmaf(d, load_elem<YDT>(p.y, y0 + i), dot);
+                    if (p.dy != nullptr) store_elem<YDT>(p.dy, g0 + i, d * w);
                 }
             }
         }
@@ -311,15 +480,15 @@ dim3 row_grid(int64_t groups) { return dim3((unsigned)std::min<int64_t>(std::max
 
 }  // namespace
 
-// One launch up to here: the ids are read E + 1 times.
+// One launch up to here: every workgroup reads all choices.
 constexpr int64_t kSortOneWork = 4 << 20;
-constexpr int64_t kSortOneMax = 65536;
+constexpr int64_t kSortOneMax = 32 * kSortOneThreads;
 
 static bool sort_one(int64_t R, int64_t E) { return R <= kSortOneMax && R * (E + 1) <= kSortOneWork; }
 
-// Chunks of whole waves' steps, at least 4096 choices and at most 256 of them.
+// Chunks of whole waves' loads, at least 4096 choices and at most 256 of them.
 static int64_t sort_chunk(int64_t R) {
-    const int64_t step = kSortWaves * kWave;
+    const int64_t step = kSortWaves * kWave * kSortAhead;
     return std::max<int64_t>(4096, ceil_div(ceil_div(R, 256), step) * step);
 }
 
@@ -331,12 +500,23 @@ template <typename ID>
 static hipError_t launch_sort(const ID* ids, int64_t R, int64_t topk, int64_t E, int32_t* offsets, int32_t* row_token,
                               int32_t* row_of, void* ws, hipStream_t stream) {
     if (sort_one(R, E)) {
-        if (R <= 4096)
-            hipLaunchKernelGGL((moe_sort_one<ID, 256>), dim3((unsigned)(E + 1)), dim3(256), 0, stream, ids, (int)R,
-                               (int)topk, (int)E, offsets, row_token, row_of);
+        // ceil(2^32 / topk); 0 for topk 1 (and for no choices at all)
+        const uint32_t per_topk = topk > 1 ? (uint32_t)(((uint64_t(1) << 32) + topk - 1) / topk) : 0;
+        const int parts = R <= 4 * 256 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(4, 256 / (E + 1)));
+#define FP8K_SORT_ONE(T, KEYS)                                                                                       \
+    hipLaunchKernelGGL((moe_sort_one<ID, T, KEYS>), dim3((unsigned)((E + 1) * parts)), dim3(T), 0, stream, ids, (int)R, \
+                       per_topk, (int)E, parts, offsets, row_token, row_of)
+        if (R <= 4 * 256)
+            FP8K_SORT_ONE(256, 4);
+        else if (R <= 4 * kSortOneThreads)
+            FP8K_SORT_ONE(kSortOneThreads, 4);
+        else if (R <= 8 * kSortOneThreads)
+            FP8K_SORT_ONE(kSortOneThreads, 8);
+        else if (R <= 16 * kSortOneThreads)
+            FP8K_SORT_ONE(kSortOneThreads, 16);
         else
-            hipLaunchKernelGGL((moe_sort_one<ID, kSortOneThreads>), dim3((unsigned)(E + 1)), dim3(kSortOneThreads), 0,
-                               stream, ids, (int)R, (int)topk, (int)E, offsets, row_token, row_of);
+            FP8K_SORT_ONE(kSortOneThreads, 32);
+#undef FP8K_SORT_ONE
         return hipGetLastError();
     }
     const int64_t chunk = sort_chunk(R);
@@ -354,13 +534,30 @@ hipError_t launch_moe_sort(const void* ids, bool wide, int64_t R, int64_t topk, 
                 : launch_sort(static_cast<const int32_t*>(ids), R, topk, E, offsets, row_token, row_of, ws, stream);
 }
 
+// Rows of `pieces` 16-byte pieces as tasks, and their workgroups.
+static RowTasks row_tasks(int64_t pieces) {
+    const int bits = bits_for(pieces, 6);
+    return {bits, std::max<int64_t>(ceil_div(pieces, int64_t(1) << bits), 1)};
+}
+static dim3 task_grid(int64_t tasks, const RowTasks& k) { return row_grid(ceil_div(tasks, kRowThreads >> k.bits)); }
+
 hipError_t launch_moe_permute(const void* x, int64_t ldx_bytes, const float* s_tok, const int32_t* row_of, int64_t T,
                               int64_t topk, int64_t R, int64_t row_bytes, void* out, int64_t ldo_bytes, float* s_out,
                               hipStream_t stream) {
-    const int bits = bits_for(ceil_div(row_bytes, 16), 8);
-    hipLaunchKernelGGL(moe_permute, row_grid(ceil_div(T, kRowThreads >> bits)), dim3(kRowThreads), 0, stream,
-                       static_cast<const uint8_t*>(x), ldx_bytes, s_tok, row_of, (int)T, (int)topk, (int)R, row_bytes,
-                       bits, static_cast<uint8_t*>(out), ldo_bytes, s_out);
+    const RowTasks k = row_tasks(ceil_div(row_bytes, 16));
+    const auto kernel = k.bits == 6 ? moe_permute<true> : moe_permute<false>;
+    hipLaunchKernelGGL(kernel, task_grid(T * k.cols, k), dim3(kRowThreads), 0, stream, static_cast<const uint8_t*>(x),
+                       ldx_bytes, s_tok, row_of, T * k.cols, (int)topk, (int)R, row_bytes, k, static_cast<uint8_t*>(out),
+                       ldo_bytes, s_out);
+    return hipGetLastError();
+}
+
+template <int DT, int ODT, int U>
+static hipError_t launch_combine(const MoeCombine& p, hipStream_t stream) {
+    const RowTasks k = row_tasks(ceil_div(p.H, 16 / elem_size<DT>()));
+    const int64_t tasks = p.T * k.cols;
+    const auto kernel = k.bits == 6 ? moe_combine<DT, ODT, U, true> : moe_combine<DT, ODT, U, false>;
+    hipLaunchKernelGGL(kernel, task_grid(tasks, k), dim3(kRowThreads), 0, stream, p, tasks, k);
     return hipGetLastError();
 }
 
@@ -368,17 +565,10 @@ hipError_t launch_moe_combine(const MoeCombine& p, int dtype, int out_dtype, hip
     return with_type(dtype, [&](auto dt) {
         return with_type(out_dtype, [&](auto odt) {
             constexpr int DT = decltype(dt)::value, ODT = decltype(odt)::value;
-            const int bits = bits_for(ceil_div(p.H, 16 / elem_size<DT>()), 8);
-            const dim3 grid = row_grid(ceil_div(p.T, kRowThreads >> bits));
-            if (p.topk <= 1)
-                hipLaunchKernelGGL((moe_combine<DT, ODT, 1>), grid, dim3(kRowThreads), 0, stream, p, bits);
-            else if (p.topk <= 2)
-                hipLaunchKernelGGL((moe_combine<DT, ODT, 2>), grid, dim3(kRowThreads), 0, stream, p, bits);
-            else if (p.topk <= 4)
-                hipLaunchKernelGGL((moe_combine<DT, ODT, 4>), grid, dim3(kRowThreads), 0, stream, p, bits);
-            else
-                hipLaunchKernelGGL((moe_combine<DT, ODT, 8>), grid, dim3(kRowThreads), 0, stream, p, bits);
-            return hipGetLastError();
+            if (p.topk <= 1) return launch_combine<DT, ODT, 1>(p, stream);
+            if (p.topk <= 2) return launch_combine<DT, ODT, 2>(p, stream);
+            if (p.topk <= 4) return launch_combine<DT, ODT, 4>(p, stream);
+            return launch_combine<DT, ODT, 8>(p, stream);
         });
     });
 }
