@@ -648,35 +648,66 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
             block_barrier();
             auto finish = [&](auto dt) {
                 constexpr int DT = decltype(dt)::value;
+                constexpr int ES = elem_size<DT>();
                 float sc[8], bi[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sc[i] = s_ch_t[cg * 8 + i], bi[i] = bias_t[cg * 8 + i];
                 const int rows = min(ROWS, rows_valid - pass * ROWS);
                 const int64_t m_first = (int64_t)row_begin + m0 + pass * ROWS;
-                for (int r0 = row0; r0 < rows && left > 0; r0 += STEP * U) {
-                    float res[U][8];
-                    if (p.epi.residual != nullptr) {
+                const bool add = p.epi.residual != nullptr;
+                // act(v) of the thread's 8 columns of row r
+                auto value = [&](int r, float (&x)[8]) {
+                    const float st = s_tok_t[pass * ROWS + r];
+                    const float4 lo = *reinterpret_cast<const float4*>(ct + r * BN + (((2 * cg) ^ (r & 31)) << 2));
+                    const float4 hi = *reinterpret_cast<const float4*>(ct + r * BN + (((2 * cg + 1) ^ (r & 31)) << 2));
+                    const float acc8[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(acc8[i], st * sc[i], bi[i]);
+                    activate<DT == kKvF32, 8>(x, p.epi.act);
+                };
+                if (left >= 8) {
+                    // the residuals of the next U rows are under way while these are worked on
+                    uint32_t res[U][2 * ES], ahead[U][2 * ES];
+                    auto load_rows = [&](int r0, uint32_t (&to)[U][2 * ES]) {
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+                            load_words(static_cast<const uint8_t*>(p.epi.residual) +
+                                           ((m_first + min(r0 + u * STEP, rows - 1)) * p.epi.ldr + n) * ES,
+                                       to[u]);
+                    };
+                    if (add) load_rows(row0, res);
+                    for (int r0 = row0; r0 < rows; r0 += STEP * U) {
+                        if (add) load_rows(r0 + STEP * U, ahead);
 #pragma unroll
                         for (int u = 0; u < U; ++u) {
-                            const int r = min(r0 + u * STEP, rows - 1);
-                            load_run<DT, 8>(p.epi.residual, (m_first + r) * p.epi.ldr + n, left, res[u]);
+                            const int r = r0 + u * STEP;
+                            float x[8];
+                            value(min(r, rows - 1), x);
+                            if (add) {
+                                float y[8];
+                                unpack<DT, 8>(res[u], y);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) x[i] += y[i];
+                            }
+                            if (r < rows) store_run<DT, 8>(p.epi.y, (m_first + r) * p.epi.ldy + n, 8, x);
+                        }
+                        if (add) {
+#pragma unroll
+                            for (int u = 0; u < U; ++u)
+#pragma unroll
+                                for (int i = 0; i < 2 * ES; ++i) res[u][i] = ahead[u][i];
                         }
                     }
+                } else {  // the last columns, less than 8
+                    for (int r = row0; r < rows && left > 0; r += STEP) {
+                        float x[8];
+                        value(r, x);
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int r = min(r0 + u * STEP, rows - 1);  // the last row again: the same values
-                        const float st = s_tok_t[pass * ROWS + r];
-                        const float4 lo = *reinterpret_cast<const float4*>(ct + r * BN + (((2 * cg) ^ (r & 31)) << 2));
-                        const float4 hi = *reinterpret_cast<const float4*>(ct + r * BN + (((2 * cg + 1) ^ (r & 31)) << 2));
-                        float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(x[i], st * sc[i], bi[i]);
-                        activate<8>(x, p.epi.act);
-                        if (p.epi.residual != nullptr) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) x[i] += res[u][i];
+                        for (int i = 0; i < 8; ++i) {
+                            if (i >= left) continue;
+                            if (add) x[i] += load_elem<DT>(p.epi.residual, (m_first + r) * p.epi.ldr + n + i);
+                            store_elem<DT>(p.epi.y, (m_first + r) * p.epi.ldy + n + i, x[i]);
                         }
-                        store_run<DT, 8>(p.epi.y, (m_first + r) * p.epi.ldy + n, left, x);
                     }
                 }
             };

@@ -44,7 +44,7 @@ __device__ __forceinline__ void finish4_typed(const Epilogue& e, const v4f& sum,
     }
 #pragma unroll
     for (int v = 0; v < 4; ++v) x[v] = __builtin_fmaf(sum[v], st * sc[v], x[v]);
-    activate<4>(x, e.act);
+    activate<DT == kKvF32, 4>(x, e.act);
     if (e.residual != nullptr) {
         float r[4];
         load_run<DT, 4>(e.residual, (int64_t)m * e.ldr + nb, left, r);

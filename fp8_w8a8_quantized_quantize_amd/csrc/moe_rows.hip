@@ -109,10 +109,24 @@ __global__ __launch_bounds__(T) void moe_sort_one(const ID* __restrict__ ids, in
 // Many choices: chunks of them, one per workgroup.  The first kernel counts each
 // chunk's keys; the second adds up the chunks' counts to every key's first row in
 // its own chunk, and places the chunk's choices in order.
-constexpr int kSortThreads = 512;
+constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / kWave;
 constexpr int kSortKeys = 1025;  // E <= 1024 and the key of choices without an expert
 constexpr int kSortAhead = 4;    // steps of 64 choices loaded together
+constexpr int kCountAhead = 4;   // choices of a thread counted together
+constexpr int kChunksAhead = 32; // chunks' counts of a key added together
+
+// cnt[key] += 1 for every lane with a key (not -1).  A wave of one key alone (the
+// padding at a buffer's end) adds once: its lanes' additions would wait for each other.
+__device__ __forceinline__ void count_key(int* cnt, int key) {
+    const int one = __builtin_amdgcn_readfirstlane(key);
+    const unsigned long long live = __ballot(key >= 0);
+    if (one >= 0 && __ballot(key == one) == live) {
+        if ((threadIdx.x & 63) == 0) atomicAdd(&cnt[one], __popcll(live));
+    } else if (key >= 0) {
+        atomicAdd(&cnt[key], 1);
+    }
+}
 
 template <typename ID>
 __global__ __launch_bounds__(kSortThreads) void moe_sort_count(const ID* __restrict__ ids, int R, int chunk, int E,
@@ -121,14 +135,14 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_count(const ID* __restr
     for (int k = threadIdx.x; k <= E; k += kSortThreads) cnt[k] = 0;
     __syncthreads();
     const int64_t begin = (int64_t)blockIdx.x * chunk, end = min((int64_t)R, begin + chunk);
-    for (int64_t i = begin + threadIdx.x; i < end; i += kSortAhead * kSortThreads) {
-        int key[kSortAhead];
+    for (int64_t i0 = begin; i0 < end; i0 += kCountAhead * kSortThreads) {
+        const int64_t i = i0 + threadIdx.x;
+        ID id[kCountAhead];  // read again past the end, and not counted: no branch between the loads
 #pragma unroll
-        for (int a = 0; a < kSortAhead; ++a)
-            key[a] = i + a * kSortThreads < end ? key_of(ids[i + a * kSortThreads], E) : -1;
+        for (int a = 0; a < kCountAhead; ++a) id[a] = ids[min(i + a * kSortThreads, end - 1)];
 #pragma unroll
-        for (int a = 0; a < kSortAhead; ++a)
-            if (key[a] >= 0) atomicAdd(&cnt[key[a]], 1);
+        for (int a = 0; a < kCountAhead; ++a)
+            count_key(cnt, i + a * kSortThreads < end ? key_of(id[a], E) : -1);
     }
     __syncthreads();
     for (int k = threadIdx.x; k <= E; k += kSortThreads) counts[(int64_t)blockIdx.x * (E + 1) + k] = cnt[k];
@@ -152,11 +166,11 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_place(const ID* __restr
     const int per = chunk / kSortWaves;  // a multiple of 64 kSortAhead
     const int64_t begin = min(chunk_end, base + (int64_t)wave * per), end = min(chunk_end, begin + per);
     auto load_keys = [&](int64_t i0, int (&key)[kSortAhead]) {
+        ID id[kSortAhead];  // no branch between the loads, as in the count
 #pragma unroll
-        for (int a = 0; a < kSortAhead; ++a) {
-            const int64_t i = i0 + a * 64 + lane;
-            key[a] = i < end ? key_of(ids[i], E) : -1;
-        }
+        for (int a = 0; a < kSortAhead; ++a) id[a] = ids[min(i0 + a * 64 + lane, end - 1)];
+#pragma unroll
+        for (int a = 0; a < kSortAhead; ++a) key[a] = i0 + a * 64 + lane < end ? key_of(id[a], E) : -1;
     };
     __syncthreads();
     for (int64_t i0 = begin; i0 < end; i0 += 64 * kSortAhead) {
@@ -164,7 +178,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_place(const ID* __restr
         load_keys(i0, key);
 #pragma unroll
         for (int a = 0; a < kSortAhead; ++a)
-            if (key[a] >= 0) atomicAdd(&next[wave][key[a]], 1);
+            count_key(next[wave], key[a]);
     }
     // Every key's count in all chunks and in those before this one.  Threads side by
     // side take neighbouring keys of one chunk; when the keys leave threads over,
@@ -174,11 +188,17 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_place(const ID* __restr
     if (group < groups) {
         for (int k = threadIdx.x - group * wide; k < keys; k += wide) {
             int all = 0, front = 0;
-#pragma unroll 32
-            for (int b = group; b < (int)gridDim.x; b += groups) {
-                const int c = counts[(int64_t)b * keys + k];
-                all += c;
-                front += b < (int)blockIdx.x ? c : 0;
+            for (int b0 = group; b0 < (int)gridDim.x; b0 += groups * kChunksAhead) {
+                int c[kChunksAhead];
+#pragma unroll
+                for (int a = 0; a < kChunksAhead; ++a)
+                    c[a] = counts[(int64_t)min(b0 + a * groups, (int)gridDim.x - 1) * keys + k];
+#pragma unroll
+                for (int a = 0; a < kChunksAhead; ++a) {
+                    const int b = b0 + a * groups;
+                    all += b < (int)gridDim.x ? c[a] : 0;
+                    front += b < (int)blockIdx.x ? c[a] : 0;
+                }
             }
             atomicAdd(&total[k], all);
             atomicAdd(&before[k], front);

@@ -148,64 +148,90 @@ __device__ __forceinline__ void store_run(void* base, int64_t e, int n, const fl
     }
 }
 
-// Activation functions on fp32, each in a form whose relative error stays a few
-// steps of 2^-24 in the tails too (no 1 - x of nearly equal values):
+// Activation functions on fp32, each in a form that keeps its relative accuracy in
+// the tails (no 1 - x of nearly equal values):
 //   silu(x)      = x / (1 + e^-x)
 //   gelu(x)      = x Phi(x), Phi(-a) = erfc(a / sqrt 2) / 2 and Phi(a) = 1 - Phi(-a) for a >= 0
 //   gelu_tanh(x) = x / (1 + e^-2u), u = sqrt(2 / pi) (x + 0.044715 x^3):
 //                  the same as x (1 + tanh u) / 2.
-
-// e^x: the rounding error of x log2 e (and log2 e's own) goes into a first-order
-// factor, so large |x| keep the accuracy of the hardware's 2^t.  Past the range
-// the error term is NaN (inf - inf); the clamp turns it into a number, the factor
-// stays above 0.3, and 2^t is 0 or inf whatever it is.
-__device__ __forceinline__ float exp_precise(float x) {
-    constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f;
-    const float t = x * kLog2e;
-    const float low = __builtin_amdgcn_fmed3f(__builtin_fmaf(x, kLog2e, -t) + x * kLog2eLow, -1.0f, 1.0f);
-    return __builtin_amdgcn_exp2f(t) * __builtin_fmaf(0.693147182f, low, 1.0f);
-}
+// FINE, for fp32 outputs: within a few units of 2^-24 (gelu 5e-7).  Otherwise, for
+// outputs of 16 bits or 8, which round by 2^-12 or more themselves: an exponent's
+// argument t costs |t| 2^-23 and gelu's fit 4.7e-6, for half the instructions (the
+// activation quantizer is bound by them as much as by its bytes, and the products'
+// epilogues run while the matrix units wait).
 
 // 1 / x, to one step of fp32; 0 for inf.
 __device__ __forceinline__ float fast_recip(float x) { return __builtin_amdgcn_rcpf(x); }
 
-__device__ __forceinline__ float sigmoid_times(float x, float minus_arg) {
-    return x * fast_recip(1.0f + exp_precise(minus_arg));
+// 2^(x c), c_low being what the constant c leaves out: the rounding error of the
+// product (and the constant's) goes into a first-order factor, so large |x| keep the
+// accuracy of the hardware's 2^t.  Past the range the error term is NaN (inf - inf);
+// the clamp turns it into a number, the factor stays above 0.3, and 2^t is 0 or inf
+// whatever it is.
+__device__ __forceinline__ float exp2_fine(float x, float c, float c_low, float more = 0.0f) {
+    const float t = x * c;
+    const float low = __builtin_amdgcn_fmed3f(__builtin_fmaf(x, c, -t) + __builtin_fmaf(x, c_low, more), -1.0f, 1.0f);
+    return __builtin_amdgcn_exp2f(t) * __builtin_fmaf(0.693147182f, low, 1.0f);
 }
 
-__device__ __forceinline__ float gelu_erf(float x) {
-    // erfc(a / sqrt 2) / 2 = e^(-a^2 / 2) t P(t), t = 1 / (1 + 0.21 a): P is fitted
-    // over 0 <= a <= 13.5 to a relative error of 1.4e-8 (past 13.5 the value is
-    // below fp32's range), the whole to 5e-7 in fp32.
+constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f;
+
+template <bool FINE>
+__device__ __forceinline__ float silu(float x) {
+    const float e = FINE ? exp2_fine(x, -kLog2e, -kLog2eLow) : __builtin_amdgcn_exp2f(x * -kLog2e);
+    return x * fast_recip(1.0f + e);
+}
+
+template <bool FINE>
+__device__ __forceinline__ float gelu(float x) {
+    // erfc(a / sqrt 2) / 2 = e^(-a^2 / 2) t P(t), t = 1 / (1 + q a), P fitted over
+    // 0 <= a <= 13.5 (past it the value is below fp32's range): to 1.4e-8 with nine
+    // coefficients, to 4.7e-6 with six.
     const float a = fabsf(x);
-    const float t = fast_recip(__builtin_fmaf(0.21f, a, 1.0f));
-    float p = -0.07203391939401627f;
-    p = __builtin_fmaf(p, t, 0.28545311093330383f);
-    p = __builtin_fmaf(p, t, -0.3341890871524811f);
-    p = __builtin_fmaf(p, t, 0.3540330231189728f);
-    p = __builtin_fmaf(p, t, -0.09724528342485428f);
-    p = __builtin_fmaf(p, t, 0.12635496258735657f);
-    p = __builtin_fmaf(p, t, 0.06879008561372757f);
-    p = __builtin_fmaf(p, t, 0.08512940257787704f);
-    p = __builtin_fmaf(p, t, 0.08370770514011383f);
-    // e^(-a^2 / 2), the square's rounding error carried along as in exp_precise
-    constexpr float kC = -0.72134751f, kCLow = -9.62981516e-9f;
+    const float t = fast_recip(__builtin_fmaf(FINE ? 0.21f : 0.31f, a, 1.0f));
+    float p, e;
     const float s = x * x;
-    const float r = s * kC;
-    const float low = __builtin_amdgcn_fmed3f(
-        __builtin_fmaf(s, kC, -r) + __builtin_fmaf(s, kCLow, __builtin_fmaf(x, x, -s) * kC), -1.0f, 1.0f);
-    const float phi = p * t * (__builtin_amdgcn_exp2f(r) * __builtin_fmaf(0.693147182f, low, 1.0f));
+    if constexpr (FINE) {
+        p = -0.07203391939401627f;
+        p = __builtin_fmaf(p, t, 0.28545311093330383f);
+        p = __builtin_fmaf(p, t, -0.3341890871524811f);
+        p = __builtin_fmaf(p, t, 0.3540330231189728f);
+        p = __builtin_fmaf(p, t, -0.09724528342485428f);
+        p = __builtin_fmaf(p, t, 0.12635496258735657f);
+        p = __builtin_fmaf(p, t, 0.06879008561372757f);
+        p = __builtin_fmaf(p, t, 0.08512940257787704f);
+        p = __builtin_fmaf(p, t, 0.08370770514011383f);
+        // the square's rounding error goes along
+        constexpr float kHalf = -0.5f * kLog2e;
+        e = exp2_fine(s, kHalf, -0.5f * kLog2eLow, __builtin_fmaf(x, x, -s) * kHalf);
+    } else {
+        p = -0.07392915338277817f;
+        p = __builtin_fmaf(p, t, 0.18045033514499664f);
+        p = __builtin_fmaf(p, t, 0.015744805335998535f);
+        p = __builtin_fmaf(p, t, 0.13342967629432678f);
+        p = __builtin_fmaf(p, t, 0.12044132500886917f);
+        p = __builtin_fmaf(p, t, 0.12386069446802139f);
+        e = __builtin_amdgcn_exp2f(s * (-0.5f * kLog2e));
+    }
+    const float phi = p * t * e;
     return x < 0.0f ? x * phi : __builtin_fmaf(-x, phi, x);
 }
 
+template <bool FINE>
 __device__ __forceinline__ float gelu_tanh(float x) {
-    // -2u = x (-2 sqrt(2 / pi) - 2 sqrt(2 / pi) 0.044715 x^2)
-    const float u2 = x * __builtin_fmaf(-0.0713548163f, x * x, -1.59576912f);
-    return sigmoid_times(x, u2);
+    // -2u = x (-2 sqrt(2 / pi) - 2 sqrt(2 / pi) 0.044715 x^2), times log2(e) right away when not FINE
+    constexpr float kA = -1.59576912f, kB = -0.0713548163f;
+    if constexpr (FINE) {
+        const float e = exp2_fine(x * __builtin_fmaf(kB, x * x, kA), kLog2e, kLog2eLow);
+        return x * fast_recip(1.0f + e);
+    } else {
+        const float e = __builtin_amdgcn_exp2f(x * __builtin_fmaf(kB * kLog2e, x * x, kA * kLog2e));
+        return x * fast_recip(1.0f + e);
+    }
 }
 
 // act of V values; `act` is the same for the whole launch, so the branch is uniform.
-template <int V>
+template <bool FINE, int V>
 __device__ __forceinline__ void activate(float (&x)[V], int act) {
     if (act == kActNone) return;
     if (act == kActRelu) {
@@ -213,13 +239,13 @@ __device__ __forceinline__ void activate(float (&x)[V], int act) {
         for (int i = 0; i < V; ++i) x[i] = x[i] < 0.0f ? 0.0f : x[i];  // NaN stays
     } else if (act == kActSilu) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = sigmoid_times(x[i], -x[i]);
+        for (int i = 0; i < V; ++i) x[i] = silu<FINE>(x[i]);
     } else if (act == kActGelu) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = gelu_erf(x[i]);
+        for (int i = 0; i < V; ++i) x[i] = gelu<FINE>(x[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = gelu_tanh(x[i]);
+        for (int i = 0; i < V; ++i) x[i] = gelu_tanh<FINE>(x[i]);
     }
 }
 

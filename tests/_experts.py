@@ -59,9 +59,10 @@ def act64(x, act):
     return x
 
 
-def act_bound(x, act):
+def act_bound(x, act, fine):
     """How far act(x) in fp32 may be from its value, for the fp32 x itself.  One hardware 2^t or reciprocal is off by
     2 u of its value.
+    fine (fp32 outputs):
       silu: e^-x 2 u (2^t), 2 u (two products), 2 u (the argument's second term); 1 + e^-x u; reciprocal 2 u; product
         u: 10 u, taken as 12.
       gelu_tanh: the same and the argument's four roundings (constants, square, fma, product), each u of an argument a
@@ -69,13 +70,20 @@ def act_bound(x, act):
       gelu: t has 3 u (constant and sum u each at most, reciprocal 2 u) and t P(t) at most doubles it, Horner's steps add
         less than 10 u (alternating signs at most triple the later terms), the exponential 6 u, products 3 u and the fit
         1.4e-8 < u: 26 u, taken as 32.
+    Otherwise the exponent's argument is one product, with u of itself and u of its constant, and gelu's fit is 4.7e-6 <
+    80 u: silu 8 + 2 |x|, gelu_tanh 8 + 6 |a|, gelu 112 + 2 x^2 / 2.
     Below 2^-126 the hardware's results may be 0."""
     v = act64(x, act).abs()
-    k = {"none": 0, "relu": 0, "silu": 12, "gelu": 32}.get(act)
-    if k is None:
+    if act in ("none", "relu"):
+        return torch.zeros_like(v)
+    if act == "silu":
+        k = 12 if fine else 8 + 2 * x.abs().clamp_max(200.0)
+    elif act == "gelu":
+        k = 32 if fine else 112 + x.abs().clamp_max(20.0) ** 2
+    else:
         a = (math.sqrt(8.0 / math.pi) * (x + 0.044715 * x ** 3)).abs().clamp_max(200.0)
-        k = 12 + 4 * a
-    return k * U * v + 2.0 ** -126 * (x.abs() + 1) * (0 if act in ("none", "relu") else 1)
+        k = 12 + 4 * a if fine else 8 + 6 * a
+    return k * U * v + 2.0 ** -126 * (x.abs() + 1)
 
 
 def round_bound(ref, dtype):

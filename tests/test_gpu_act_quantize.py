@@ -22,7 +22,7 @@ def quantize_ok(h, act, gated, q, s, what):
     """Scales and codes within the fp32 evaluation's error of the 64-bit values."""
     F = q.shape[1]
     x = h[:, :F].double()
-    v, err = act64(x, act), act_bound(x, act)
+    v, err = act64(x, act), act_bound(x, act, False)
     if gated:
         u = h[:, F:].double()
         v, err = v * u, err * u.abs() + (v * u).abs() * U

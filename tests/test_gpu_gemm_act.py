@@ -25,7 +25,7 @@ def expect(qa, st, qw, sc, bias, act, residual, dtype):
     if bias is not None:
         v = v + bias.double()
     err = err + v.abs() * U
-    ref, err = act64(v, act), err * 1.13 + act_bound(v, act)
+    ref, err = act64(v, act), err * 1.13 + act_bound(v, act, dtype is F32)
     if residual is not None:
         ref = ref + residual.double()
         err = err + (ref.abs() + err) * U
@@ -107,7 +107,7 @@ def test_activations_of_any_value():
             y = fp8.fp8_gemm_scaled_act(q0.expand(rows, 0).contiguous(), one.repeat(rows), w0, torch.ones_like(x), bias=x,
                                         act=act, y_dtype=F32)
             ref = act64(x.double(), act)
-            check(y, ref.expand(rows, -1), (act_bound(x.double(), act) + ref.abs() * U + 2.0 ** -126).expand(rows, -1), act)
+            check(y, ref.expand(rows, -1), (act_bound(x.double(), act, True) + ref.abs() * U + 2.0 ** -126).expand(rows, -1), act)
     for act in ACTS:  # NaN stays NaN
         y = fp8.fp8_gemm_scaled_act(q0, one, w0[:3], torch.ones(3, device=DEV), act=act, y_dtype=BF,
                                     bias=torch.tensor([float("nan"), 1.0, float("nan")], device=DEV))
