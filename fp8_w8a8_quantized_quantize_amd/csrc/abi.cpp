@@ -13,6 +13,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "act_plan.hpp"
 #include "attn_plan.hpp"
 #include "kernels.hpp"
 
@@ -231,9 +232,8 @@ fp8_status_t check_act(fp8_act_t act) {
     return act >= FP8_ACT_NONE && act <= FP8_ACT_GELU_TANH ? FP8_OK : FP8_ERR_INVALID_ARGUMENT;
 }
 
-// Output tiles of 128 x 128 of the products with an epilogue: one workgroup of 256
-// threads each, of which the runtime takes less than 2^32.
-bool act_tiles_ok(int64_t row_tiles, int64_t N) { return row_tiles * ((N + 127) / 128) < fp8k::kMaxGrid; }
+// Output tiles of 128 x 128 of the products with an epilogue.
+bool act_tiles_ok(int64_t row_tiles, int64_t N) { return row_tiles * ((N + 127) / 128) <= fp8k::kMaxActTiles; }
 
 // A vector of 32-bit words that is read one by one.
 fp8_status_t check_words(const void* p, int64_t n) {
@@ -654,7 +654,9 @@ fp8_status_t fp8_gemm_grouped_scaled(const uint8_t* qa, const float* s_tok, cons
 
 size_t fp8_gemm_act_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (check_dims(M, N, K) != FP8_OK || !act_tiles_ok((M + 127) / 128, N)) return SIZE_MAX;
-    return gemm_ws_bytes(M, N, K);
+    if (M <= fp8k::kSkinnyActMaxM) return gemm_ws_bytes(M, N, K);
+    return round_up(std::max(fp8k::act_plan_ws_bytes(fp8k::act_plan(M, N, K, false), M, N),
+                             fp8k::act_plan_ws_bytes(fp8k::act_plan(M, N, K, true), M, N)), kAlign);
 }
 
 fp8_status_t fp8_gemm_scaled_act(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw, int64_t ldw,
@@ -674,9 +676,9 @@ fp8_status_t fp8_gemm_scaled_act(const uint8_t* qa, int64_t lda, const float* s_
     if (need > 0 && ws == nullptr) return FP8_ERR_INVALID_ARGUMENT;
     if (need > 0 && !aligned16(ws)) return FP8_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return FP8_OK;
-    if (M <= fp8k::kSkinnyMaxM)
-        return from_hip(fp8k::launch_gemm_skinny_act(qa, lda, s_tok, qw, ldw, s_ch, epi, M, N, K, ws, stream));
-    return from_hip(fp8k::launch_gemm_mfma_act(qa, lda, s_tok, qw, ldw, s_ch, epi, M, N, K, stream));
+    if (M <= fp8k::kSkinnyActMaxM)
+        return from_hip(fp8k::launch_gemm_skinny_act(qa, lda, s_tok, qw, ldw, s_ch, epi, M, N, K, stream));
+    return from_hip(fp8k::launch_gemm_mfma_act(qa, lda, s_tok, qw, ldw, s_ch, epi, M, N, K, ws, stream));
 }
 
 fp8_status_t fp8_gemm_grouped_scaled_act(const uint8_t* qa, const float* s_tok, const int32_t* row_token,
@@ -688,7 +690,7 @@ fp8_status_t fp8_gemm_grouped_scaled_act(const uint8_t* qa, const float* s_tok, 
     FP8_TRY(check_dims(T, N, K));
     if (R < 0 || E < 0) return FP8_ERR_INVALID_ARGUMENT;
     if (R > kMaxDim || E > kMaxExperts) return FP8_ERR_UNSUPPORTED;
-    if (!act_tiles_ok((R + 127) / 128 + E + 1, N)) return FP8_ERR_UNSUPPORTED;
+    if (!act_tiles_ok((R + 127) / 128 + E, N)) return FP8_ERR_UNSUPPORTED;
     if (R > 0 && (E == 0 || T == 0)) return FP8_ERR_INVALID_ARGUMENT;
     FP8_TRY(check_matrix(qa, T, K, K, 1));
     FP8_TRY(check_vector(s_tok, T));

@@ -42,6 +42,7 @@
 #include <type_traits>
 
 #include "device_common.hpp"
+#include "act_plan.hpp"
 #include "kernels.hpp"
 #include "rows_common.hpp"
 
@@ -82,7 +83,7 @@ __device__ __forceinline__ int dswz(int row) { return (row ^ (row >> 3)) & 7; }
 
 __device__ __forceinline__ void compiler_fence() { asm volatile("" ::: "memory"); }
 
-// s_waitcnt vmcnt(n) for n = 8 * outstanding stages (n <= 63).
+// s_waitcnt vmcnt(n) for n = PER_STAGE * outstanding stages (n <= 63; at most 7 stages).
 template <int PER_STAGE>
 __device__ __forceinline__ void wait_dma(int outstanding_stages) {
     compiler_fence();
@@ -91,7 +92,10 @@ __device__ __forceinline__ void wait_dma(int outstanding_stages) {
         case 1: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PER_STAGE) : "memory"); break;
         case 2: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * PER_STAGE) : "memory"); break;
         case 3: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * PER_STAGE) : "memory"); break;
-        default: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * PER_STAGE) : "memory"); break;
+        case 4: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * PER_STAGE) : "memory"); break;
+        case 5: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(5 * PER_STAGE) : "memory"); break;
+        case 6: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(6 * PER_STAGE) : "memory"); break;
+        default: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(7 * PER_STAGE) : "memory"); break;
     }
     compiler_fence();
 }
@@ -162,6 +166,11 @@ struct MfmaArgs {
     int E;
     MxScales mx;  // block-scaled operands (MX kernels only)
     Epilogue epi;  // ACT kernels only
+    // Dense ACT kernels: workgroups of grid z take the k range [z split_k, (z + 1) split_k)
+    // (a multiple of 128) and, when part is set, write their fp32 sums to part[z][M][N]
+    // instead of the epilogue's output.
+    float* part;
+    int split_k;
 };
 
 // What a DMA lane past K reads (a K that is no whole number of stages).
@@ -241,8 +250,10 @@ __device__ void find_expert_tile(const MfmaArgs& p, int b, int* sh) {
 // type).  TAIL: K is no multiple of 128; the last stage's pieces past K are read
 // from a block of zeros, for both operands (a zero code times a NaN code is NaN).
 // HALF: products in fp16 (mfma_32x32x64_half).
+// NS: stages of the ring (a power of two).  The two of the pipeline above hide a
+// stage's load behind one step; small tiles, whose steps are short, take more.
 template <int BN, int BM, int WN, int WM, int GROUP_M, bool GROUPED, bool MX = false, bool SKIP = false, bool ACT = false,
-          bool TAIL = false, bool HALF = false>
+          bool TAIL = false, bool HALF = false, int NS = 2>
 __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) {
     static_assert(!(MX && GROUPED), "block scales: dense GEMM only");
     static_assert(!(MX && (ACT || TAIL)), "block scales: plain epilogue, whole stages");
@@ -255,17 +266,19 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
     constexpr int DS = MX ? (BN + BM) / (64 * NW) : 0;  // ... block-scale words (64 rows each)
     constexpr int PER_STAGE = DA + DB + DS;
     constexpr int STAGE = (BN + BM) * kBK;
-    constexpr int SRING = 2 * STAGE + 4 * (BN + BM);    // block-scale ring: 2 x (BN + BM) words
+    constexpr int SRING = NS * STAGE + 4 * (BN + BM);    // block-scale ring: 2 x (BN + BM) words
     static_assert(DA * 8 * NW == BN && DB * 8 * NW == BM, "whole DMA instructions per wave");
+    static_assert((NS & (NS - 1)) == 0 && NS <= 8 && (NS - 1) * PER_STAGE <= 63, "ring slots by mask, vmcnt field");
+    static_assert(!MX || NS == 2, "block scales have a ring of two");
     static_assert(!MX || DS * 64 * NW == BN + BM, "whole scale DMA instructions per wave");
     static_assert(BM * BN * 2 <= 2 * STAGE, "the BF16 output tile must fit in the ring");
-    int* sh = reinterpret_cast<int*>(smem + 2 * STAGE + 4 * (BN + BM));  // grouped tile lookup
+    int* sh = reinterpret_cast<int*>(smem + NS * STAGE + 4 * (BN + BM));  // grouped tile lookup
     // Grouped: the weight tile's lines of stage s + 3 are touched into L2
     // during step s (one 4-byte DMA per row into a dummy LDS slot), so the
     // stage's own DMA one step later finds them there: expert weights stream
     // from HBM, whose latency one step of MFMAs does not always cover.
-    constexpr bool PF = GROUPED && BN == 64 * NW;  // one prefetch row per lane
-    uint8_t* pf_lds = smem + 2 * STAGE + 4 * (BN + BM) + 16;
+    constexpr bool PF = GROUPED && BN == 64 * NW && NS == 2;  // one prefetch row per lane
+    uint8_t* pf_lds = smem + NS * STAGE + 4 * (BN + BM) + 16;
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -327,8 +340,17 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
         s_ch += (int64_t)expert * p.N;
     }
 
+    int K = p.K;
+    const uint8_t* qa = p.qa;
+    if constexpr (ACT && !GROUPED) {
+        const int k0 = blockIdx.z * p.split_k;
+        K = min(K - k0, p.split_k);
+        qw += k0;
+        qa += k0;
+    }
+
     // ---- tile scales -> LDS (used by the epilogue) ------------------------
-    constexpr int RING = 2 * STAGE;
+    constexpr int RING = NS * STAGE;
     float* s_ch_t = reinterpret_cast<float*>(smem + RING);
     float* s_tok_t = s_ch_t + BN;
     for (int i = tid; i < BN; i += NTH) s_ch_t[i] = MX ? 1.0f : s_ch[min(n0 + i, p.N - 1)];
@@ -363,7 +385,7 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
             src_row = p.row_token[row_begin + m0 + ml];
         else
             src_row = m0 + ml;
-        bsrc[j] = p.qa + src_row * lda + ((lpos ^ dswz(row)) << 4);
+        bsrc[j] = qa + src_row * lda + ((lpos ^ dswz(row)) << 4);
     }
     const int nlast = p.N - 1;
     const uint8_t* pf_src = qw + (int64_t)min(n0 + wave * 64 + lane, nlast) * ldw;
@@ -388,11 +410,11 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
                                          smem + SRING + slot * 4 * (BN + BM) + (wave * DS + j) * 256, 4, 0, 0);
     };
 
-    const int KT = p.K / kBK + (TAIL ? 1 : 0);
+    const int KT = K / kBK + (TAIL && K % kBK != 0 ? 1 : 0);
     // The lane's source in stage kt, piece c of its row's 128 bytes: src, or zeros past K.
     auto within = [&](const uint8_t* src, int kt, int c) {
         if constexpr (TAIL) {
-            if (kt == KT - 1 && kt * kBK + (c << 4) >= p.K) src = reinterpret_cast<const uint8_t*>(&kZero16);
+            if (kt == KT - 1 && kt * kBK + (c << 4) >= K) src = reinterpret_cast<const uint8_t*>(&kZero16);
         }
         return src;
     };
@@ -487,6 +509,9 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
     // the compiler pairs the reads into ds_read2_b32
     constexpr int SR = MX ? (FN + FM) / 2 : 0;
 
+    // the slot after stage s's (of a ring of two, the other one: cheaper in registers)
+    auto next_slot = [&](int s, int cur) { return NS == 2 ? cur ^ 1 : (s + 1) & (NS - 1); };
+
     // The K loop for FA active activation fragments per wave (FA <= FM).  A
     // wave whose last fragments cover only rows past the tile's real rows
     // (the last row tile of an expert, or of a short M) skips their MFMAs and LDS reads; its
@@ -499,7 +524,9 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
             // prologue: stages 0 and 1 in flight, stage 0 landed everywhere,
             // its first-half fragments in registers
             issue_stage(0, 0);
-            if (KT > 1) issue_stage(1, 1);
+#pragma unroll
+            for (int i = 1; i < NS; ++i)
+                if (KT > i) issue_stage(i, i);
             if (PF && KT > 2) prefetch_a(2);
             if (PF && KT > 2) {
                 static_assert(PER_STAGE + 1 <= 63, "vmcnt field");
@@ -507,7 +534,7 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
                 asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PER_STAGE + 1) : "memory");
                 compiler_fence();
             } else {
-                wait_dma<PER_STAGE>(KT > 1 ? 1 : 0);
+                wait_dma<PER_STAGE>(NS == 2 ? (KT > 1 ? 1 : 0) : min(KT - 1, NS - 1));
             }
             block_barrier();
             read_scales(0, sc_a, sc_b);
@@ -516,13 +543,13 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
 #pragma unroll
             for (int a = 0; a < FN; ++a) fa[a] = read_a(0, 0, a);
         }
-        // Steps with a stage s+2 to load: no branches in the body, the DMA
+        // Steps with a stage s+NS (s+2) to load: no branches in the body, the DMA
         // instructions of stage s+2 dealt round-robin to the second-half MFMAs
         // (in program order they must precede the LDS reads that follow them,
         // which keeps them spread out instead of in one burst after the barrier).
         int s = 0;
-        for (; s + 2 < KT; ++s) {
-            const int cur = s & 1;
+        for (; s + NS < KT; ++s) {
+            const int cur = s & (NS - 1), nxt = next_slot(s, cur);
 #pragma unroll
             for (int a = 0; a < FN; ++a) {
 #pragma unroll
@@ -540,29 +567,29 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
                 asm volatile("s_waitcnt vmcnt(1)" ::: "memory");
                 compiler_fence();
             } else {
-                wait_dma<PER_STAGE>(0);
+                wait_dma<PER_STAGE>(NS - 2);
             }
             wait_lds_reads();        // ... and its reads of stage s are done
             block_barrier();
-            read_scales(cur ^ 1, nx_a, nx_b);
+            read_scales(nxt, nx_a, nx_b);
 #pragma unroll
             for (int a = 0; a < FN; ++a) {
 #pragma unroll
                 for (int b = 0; b < FA; ++b) {
                     acc[a][b] = mma(fa[a], fb[b], acc[a][b], a, b, 1);
 #pragma unroll
-                    for (int j = a * FA + b; j < PER_STAGE; j += FN * FA) issue_one(s + 2, cur, j);
-                    if (a == FN - 1) fb[b] = read_b(cur ^ 1, 0, b);
+                    for (int j = a * FA + b; j < PER_STAGE; j += FN * FA) issue_one(s + NS, cur, j);
+                    if (a == FN - 1) fb[b] = read_b(nxt, 0, b);
                 }
-                fa[a] = read_a(cur ^ 1, 0, a);
+                fa[a] = read_a(nxt, 0, a);
             }
             interleave_mfma_reads<FN * FA, 2 * (FN + FA) + SR>();
             if (PF && s + 3 < KT) prefetch_a(s + 3);  // issued last: the next step waits for all but it
             next_scales();
         }
-        // The last two steps (nothing left to load).
+        // The last NS steps (nothing left to load).
         for (; s < KT; ++s) {
-            const int cur = s & 1;
+            const int cur = s & (NS - 1);
             const bool more = s + 1 < KT;
             // first K half of stage s; refill with the second half
 #pragma unroll
@@ -576,14 +603,14 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
             }
             interleave_mfma_reads<FN * FA, 2 * (FN + FA)>();
             if (more) {
-                wait_dma<PER_STAGE>(0);
+                wait_dma<PER_STAGE>(NS == 2 ? 0 : min(NS - 2, KT - 2 - s));
                 wait_lds_reads();
                 block_barrier();
-                read_scales(cur ^ 1, nx_a, nx_b);
+                read_scales(next_slot(s, cur), nx_a, nx_b);
             }
             // second K half of stage s; refill with the first half of stage s+1
             // (the last step re-reads its own slot, unused)
-            const int nxt = more ? cur ^ 1 : cur;
+            const int nxt = more ? next_slot(s, cur) : cur;
 #pragma unroll
             for (int a = 0; a < FN; ++a) {
 #pragma unroll
@@ -600,7 +627,7 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
     // Fragments holding at least one real row (at least 1, so that every wave
     // runs the loop body; a wave with none computes one discarded fragment).
     const int fa_live = min(FM, max(1, (rows_valid - wm * 32 + 32 * WM - 1) / (32 * WM)));
-    if constexpr ((GROUPED || SKIP) && FM == 4 && !MX) {
+    if constexpr ((GROUPED || SKIP) && FM == 4 && !MX && !ACT) {
         switch (fa_live) {
             case 1: k_loop(std::integral_constant<int, 1>{}); break;
             case 2: k_loop(std::integral_constant<int, 2>{}); break;
@@ -613,21 +640,25 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
     }
 
     if constexpr (ACT) {
-        // The accumulators leave through LDS as fp32, two fragments (64 WM rows)
+        // The accumulators leave through LDS as fp32, up to two fragments (64 WM rows)
         // at a time: there a thread takes 8 columns of its own, whose scales and
         // bias stay in its registers, and whole row pieces of the residual and of
         // the output, and the activation's code is there once, not once per
-        // accumulator.  16-byte pieces are XOR-swizzled by row.
-        constexpr int FP = 2, ROWS = FP * 32 * WM;
-        constexpr int CG = BN / 8;      // column groups of a row
-        constexpr int STEP = NTH / CG;  // rows the workgroup covers at once
-        constexpr int U = 4;            // of a thread's rows, residuals loaded ahead
+        // accumulator.  16-byte pieces are XOR-swizzled by row.  A thread whose 8
+        // columns run past N works on the last 8 of the row and stores its own.
+        constexpr int FP = FM < 2 ? FM : 2, ROWS = FP * 32 * WM;
+        constexpr int CG = BN / 8;                          // column groups of a row
+        constexpr int STEP = NTH / CG;                      // rows the workgroup covers at once
+        constexpr int U = ROWS / STEP < 4 ? ROWS / STEP : 4;  // of a thread's rows, residuals loaded ahead
+        constexpr int SW = BN / 4 < 32 ? BN / 4 - 1 : 31;   // swizzle within a row's pieces
         static_assert(FM % FP == 0 && NTH % CG == 0 && ROWS % (STEP * U) == 0, "whole passes");
         static_assert(ROWS * BN * 4 <= 2 * STAGE, "the fp32 rows of a pass must fit in the ring");
         float* ct = reinterpret_cast<float*>(smem);
         const int cg = tid % CG, row0 = tid / CG;
-        const int n = n0 + cg * 8;
-        const int left = p.N - n;
+        const int own = n0 + cg * 8;                // the thread's first column
+        const int n = max(min(own, p.N - 8), 0);    // the first one it works on
+        const int nt = n - n0;                      // its place in the tile, below 0 where that lies in the tile before
+        const int left = p.N - own;
         auto run_pass = [&](auto pass_number) {
             constexpr int pass = decltype(pass_number)::value;
             wait_lds_reads();
@@ -640,74 +671,102 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const int nl = wn * (BN / WN) + a * 32 + 8 * q + 4 * g;
-                        *reinterpret_cast<float4*>(ct + ml * BN + (((nl >> 2) ^ (ml & 31)) << 2)) = make_float4(
+                        *reinterpret_cast<float4*>(ct + ml * BN + (((nl >> 2) ^ (ml & SW)) << 2)) = make_float4(
                             acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]);
                     }
                 }
             }
             block_barrier();
+            const int rows = min(ROWS, rows_valid - pass * ROWS);
+            const int64_t m_first = (int64_t)row_begin + m0 + pass * ROWS;
+            // the sums of the thread's 8 columns in row r
+            auto sums = [&](int r, float (&x)[8]) {
+                if (n == own) {
+                    const float4 lo = *reinterpret_cast<const float4*>(ct + r * BN + (((2 * cg) ^ (r & SW)) << 2));
+                    const float4 hi = *reinterpret_cast<const float4*>(ct + r * BN + (((2 * cg + 1) ^ (r & SW)) << 2));
+                    x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int c = max(nt + i, 0);
+                        x[i] = ct[r * BN + (((c >> 2) ^ (r & SW)) << 2) + (c & 3)];
+                    }
+                }
+            };
+            // x to the columns of row `row` of a matrix that are the thread's own
+            auto store = [&](auto dt, void* base, int64_t row, int64_t ld, const float (&x)[8]) {
+                constexpr int DT = decltype(dt)::value;
+                if (left >= 8) {
+                    store_run<DT, 8>(base, row * ld + n, 8, x);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (n + i >= own && n + i < p.N) store_elem<DT>(base, row * ld + n + i, x[i]);
+                }
+            };
+            if constexpr (!GROUPED) {
+                if (p.part != nullptr) {
+                    for (int r = row0; r < rows && left > 0; r += STEP) {
+                        float x[8];
+                        sums(r, x);
+                        store(std::integral_constant<int, kKvF32>{}, p.part, (int64_t)blockIdx.z * p.M + m_first + r, p.N, x);
+                    }
+                    return;
+                }
+            }
             auto finish = [&](auto dt) {
                 constexpr int DT = decltype(dt)::value;
                 constexpr int ES = elem_size<DT>();
+                if (left <= 0) return;
                 float sc[8], bi[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sc[i] = s_ch_t[cg * 8 + i], bi[i] = bias_t[cg * 8 + i];
-                const int rows = min(ROWS, rows_valid - pass * ROWS);
-                const int64_t m_first = (int64_t)row_begin + m0 + pass * ROWS;
+                for (int i = 0; i < 8; ++i) {
+                    const int c = min(max(nt + i, 0), BN - 1);
+                    sc[i] = s_ch_t[c], bi[i] = bias_t[c];
+                }
                 const bool add = p.epi.residual != nullptr;
-                // act(v) of the thread's 8 columns of row r
-                auto value = [&](int r, float (&x)[8]) {
-                    const float st = s_tok_t[pass * ROWS + r];
-                    const float4 lo = *reinterpret_cast<const float4*>(ct + r * BN + (((2 * cg) ^ (r & 31)) << 2));
-                    const float4 hi = *reinterpret_cast<const float4*>(ct + r * BN + (((2 * cg + 1) ^ (r & 31)) << 2));
-                    const float acc8[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                const int width = min(8, p.N);  // of what a thread may read of a row
+                // the residuals of the next U rows are under way while these are worked on
+                uint32_t res[U][2 * ES], ahead[U][2 * ES];
+                auto load_rows = [&](int r0, uint32_t (&to)[U][2 * ES]) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(acc8[i], st * sc[i], bi[i]);
-                    activate<DT == kKvF32, 8>(x, p.epi.act);
-                };
-                if (left >= 8) {
-                    // the residuals of the next U rows are under way while these are worked on
-                    uint32_t res[U][2 * ES], ahead[U][2 * ES];
-                    auto load_rows = [&](int r0, uint32_t (&to)[U][2 * ES]) {
-#pragma unroll
-                        for (int u = 0; u < U; ++u)
-                            load_words(static_cast<const uint8_t*>(p.epi.residual) +
-                                           ((m_first + min(r0 + u * STEP, rows - 1)) * p.epi.ldr + n) * ES,
-                                       to[u]);
-                    };
-                    if (add) load_rows(row0, res);
-                    for (int r0 = row0; r0 < rows; r0 += STEP * U) {
-                        if (add) load_rows(r0 + STEP * U, ahead);
-#pragma unroll
-                        for (int u = 0; u < U; ++u) {
-                            const int r = r0 + u * STEP;
-                            float x[8];
-                            value(min(r, rows - 1), x);
-                            if (add) {
-                                float y[8];
-                                unpack<DT, 8>(res[u], y);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) x[i] += y[i];
-                            }
-                            if (r < rows) store_run<DT, 8>(p.epi.y, (m_first + r) * p.epi.ldy + n, 8, x);
-                        }
-                        if (add) {
-#pragma unroll
-                            for (int u = 0; u < U; ++u)
-#pragma unroll
-                                for (int i = 0; i < 2 * ES; ++i) res[u][i] = ahead[u][i];
+                    for (int u = 0; u < U; ++u) {
+                        const int64_t at = (m_first + min(r0 + u * STEP, rows - 1)) * p.epi.ldr + n;
+                        if (width == 8) {
+                            load_words(static_cast<const uint8_t*>(p.epi.residual) + at * ES, to[u]);
+                        } else {  // N < 8
+                            float y[8];
+                            load_run<DT, 8>(p.epi.residual, at, width, y);
+                            pack<DT, 8>(y, to[u]);
                         }
                     }
-                } else {  // the last columns, less than 8
-                    for (int r = row0; r < rows && left > 0; r += STEP) {
-                        float x[8];
-                        value(r, x);
+                };
+                if (add) load_rows(row0, res);
+                for (int r0 = row0; r0 < rows; r0 += STEP * U) {
+                    if (add) load_rows(r0 + STEP * U, ahead);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            if (i >= left) continue;
-                            if (add) x[i] += load_elem<DT>(p.epi.residual, (m_first + r) * p.epi.ldr + n + i);
-                            store_elem<DT>(p.epi.y, (m_first + r) * p.epi.ldy + n + i, x[i]);
+                    for (int u = 0; u < U; ++u) {
+                        const int r = r0 + u * STEP, at = min(r, rows - 1);
+                        const float st = s_tok_t[pass * ROWS + at];
+                        float x[8];
+                        sums(at, x);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(x[i], st * sc[i], bi[i]);
+                        activate<DT == kKvF32, 8>(x, p.epi.act);
+                        if (add) {
+                            float y[8];
+                            unpack<DT, 8>(res[u], y);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[i] += y[i];
                         }
+                        // rows past the last one repeat it and are not stored: it may be the residual's too
+                        if (r < rows) store(dt, p.epi.y, m_first + r, p.epi.ldy, x);
+                    }
+                    if (add) {
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+#pragma unroll
+                            for (int i = 0; i < 2 * ES; ++i) res[u][i] = ahead[u][i];
                     }
                 }
             };
@@ -839,54 +898,110 @@ hipError_t launch_gemm_mfma(const uint8_t* qa, int64_t lda, const float* s_tok, 
 }
 
 // Dense products with an epilogue.
-template <int BN, int BM, bool SKIP, bool TAIL, bool HALF>
-static hipError_t launch_dense_act(MfmaArgs p, hipStream_t stream) {
-    constexpr int LDS = 2 * (BN + BM) * kBK + 4 * (BN + BM) + 4 * BN;  // ring + tile scales + bias
+template <int BN, int BM, int NS, bool SKIP, bool TAIL, bool HALF>
+static hipError_t launch_dense_act(MfmaArgs p, int splits, hipStream_t stream) {
+    constexpr int LDS = NS * (BN + BM) * kBK + 4 * (BN + BM) + 4 * BN;  // ring + tile scales + bias
     p.tiles_m = (p.M - 1) / BM + 1;
     p.tiles_n = (p.N - 1) / BN + 1;
-    const hipError_t e = FP8K_SET_LDS((gemm_mfma_kernel<BN, BM, 2, 2, 4, false, false, SKIP, true, TAIL, HALF>), LDS);
+    const hipError_t e = FP8K_SET_LDS((gemm_mfma_kernel<BN, BM, 2, 2, 4, false, false, SKIP, true, TAIL, HALF, NS>), LDS);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((gemm_mfma_kernel<BN, BM, 2, 2, 4, false, false, SKIP, true, TAIL, HALF>),
-                       dim3((unsigned)p.tiles_m * (unsigned)p.tiles_n), dim3(256), LDS, stream, p);
+    hipLaunchKernelGGL((gemm_mfma_kernel<BN, BM, 2, 2, 4, false, false, SKIP, true, TAIL, HALF, NS>),
+                       dim3((unsigned)p.tiles_m * (unsigned)p.tiles_n, 1, (unsigned)splits), dim3(256), LDS, stream, p);
     return hipGetLastError();
 }
 
-// fp32 outputs take products in fp16, and tiles of 128 x 128 for them: twice the
-// operands' registers leave no room for a 256 x 256 tile's accumulators.
+// The sums of a split k, added in order, through the epilogue; four outputs a thread.
+__global__ __launch_bounds__(256) void act_splitk_reduce(const float* __restrict__ part, int splits, int M, int N,
+                                                         const float* __restrict__ s_tok, const float* __restrict__ s_ch,
+                                                         Epilogue epi) {
+    const int n4 = (N + 3) >> 2;
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (t >= (int64_t)M * n4) return;
+    const int m = (int)(t / n4);
+    const int nb = (int)(t - (int64_t)m * n4) * 4;
+    const int64_t plane = (int64_t)M * N;
+    const float* p = part + (int64_t)m * N + nb;
+    v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (nb + 4 <= N) {
+        constexpr int AHEAD = 4;
+        for (int z0 = 0; z0 < splits; z0 += AHEAD) {
+            uint32_t w[AHEAD][4];
+#pragma unroll
+            for (int a = 0; a < AHEAD; ++a) load_words(p + min(z0 + a, splits - 1) * plane, w[a]);
+#pragma unroll
+            for (int a = 0; a < AHEAD; ++a)
+                if (z0 + a < splits) {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) sum[v] += __uint_as_float(w[a][v]);
+                }
+        }
+    } else {
+        for (int v = 0; nb + v < N; ++v) {
+            float x = 0.0f;
+            for (int z = 0; z < splits; ++z) x += p[z * plane + v];
+            sum[v] = x;
+        }
+    }
+    finish4(epi, sum, s_tok[m], s_ch, m, nb, N);
+}
+
 template <bool TAIL>
-static hipError_t launch_dense_tail(const MfmaArgs& p, hipStream_t stream) {
-    if (p.epi.type == kKvF32) return launch_dense_act<128, 128, false, TAIL, true>(p, stream);
-    if (p.M <= 192) return launch_dense_act<256, 256, true, TAIL, false>(p, stream);
-    return launch_dense_act<256, 256, false, TAIL, false>(p, stream);
+static hipError_t launch_dense_tail(const MfmaArgs& p, const ActPlan& plan, hipStream_t stream) {
+    const int s = plan.splits;
+    if (p.epi.type == kKvF32) {
+        if (plan.tile == 128) return launch_dense_act<128, 128, 2, false, TAIL, true>(p, s, stream);
+        if (plan.stages == 4) return launch_dense_act<64, 64, 4, false, TAIL, true>(p, s, stream);
+        return launch_dense_act<64, 64, 2, false, TAIL, true>(p, s, stream);
+    }
+    if (plan.tile == 256) return launch_dense_act<256, 256, 2, false, TAIL, false>(p, s, stream);
+    if (plan.tile == 128 && plan.stages == 4) return launch_dense_act<128, 128, 4, false, TAIL, false>(p, s, stream);
+    if (plan.tile == 128) return launch_dense_act<128, 128, 2, false, TAIL, false>(p, s, stream);
+    if (plan.stages == 4) return launch_dense_act<64, 64, 4, false, TAIL, false>(p, s, stream);
+    return launch_dense_act<64, 64, 2, false, TAIL, false>(p, s, stream);
 }
 
 hipError_t launch_gemm_mfma_act(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw, int64_t ldw,
                                 const float* s_ch, const Epilogue& epi, int64_t M, int64_t N, int64_t K,
-                                hipStream_t stream) {
+                                void* ws, hipStream_t stream) {
     if (M <= 0 || N <= 0) return hipSuccess;
+    const ActPlan plan = act_plan(M, N, K, epi.type == kKvF32);
     MfmaArgs p{};
     p.qa = qa; p.lda = lda; p.s_tok = s_tok; p.qw = qw; p.ldw = ldw; p.s_ch = s_ch; p.epi = epi;
     p.M = (int)M; p.N = (int)N; p.K = (int)K;
-    return K % kBK == 0 ? launch_dense_tail<false>(p, stream) : launch_dense_tail<true>(p, stream);
+    p.part = plan.splits > 1 ? static_cast<float*>(ws) : nullptr;
+    p.split_k = plan.split_k;
+    const hipError_t e = K % kBK == 0 ? launch_dense_tail<false>(p, plan, stream) : launch_dense_tail<true>(p, plan, stream);
+    if (e != hipSuccess || plan.splits == 1) return e;
+    const int64_t threads = M * ((N + 3) / 4);
+    hipLaunchKernelGGL(act_splitk_reduce, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, p.part, plan.splits,
+                       p.M, p.N, s_tok, s_ch, epi);
+    return hipGetLastError();
 }
 
-template <int BN, int BM, bool TAIL, bool HALF>
+template <int BN, int BM, int NS, bool TAIL, bool HALF>
 static hipError_t launch_grouped_act(MfmaArgs p, int64_t R, int64_t E, hipStream_t stream) {
     // ring + tile scales + tile lookup + prefetch slot + bias
-    constexpr int LDS = 2 * (BN + BM) * kBK + 4 * (BN + BM) + 16 + 256 + 4 * BN;
+    constexpr int LDS = NS * (BN + BM) * kBK + 4 * (BN + BM) + 16 + 256 + 4 * BN;
     p.tiles_n = (p.N - 1) / BN + 1;
-    const hipError_t e = FP8K_SET_LDS((gemm_mfma_kernel<BN, BM, 2, 2, 4, true, false, false, true, TAIL, HALF>), LDS);
+    const hipError_t e = FP8K_SET_LDS((gemm_mfma_kernel<BN, BM, 2, 2, 4, true, false, false, true, TAIL, HALF, NS>), LDS);
     if (e != hipSuccess) return e;
     const int64_t tiles_max = ((R + BM - 1) / BM + E) * p.tiles_n;
-    hipLaunchKernelGGL((gemm_mfma_kernel<BN, BM, 2, 2, 4, true, false, false, true, TAIL, HALF>),
+    hipLaunchKernelGGL((gemm_mfma_kernel<BN, BM, 2, 2, 4, true, false, false, true, TAIL, HALF, NS>),
                        dim3((unsigned)(8 * ((tiles_max + 7) / 8))), dim3(256), LDS, stream, p);
     return hipGetLastError();
 }
 
 template <bool TAIL>
-static hipError_t launch_grouped_tail(const MfmaArgs& p, int64_t R, int64_t E, hipStream_t stream) {
-    if (p.epi.type == kKvF32) return launch_grouped_act<128, 128, TAIL, true>(p, R, E, stream);
-    return launch_grouped_act<256, 256, TAIL, false>(p, R, E, stream);
+static hipError_t launch_grouped_tail(const MfmaArgs& p, const ActPlan& plan, int64_t R, int64_t E, hipStream_t stream) {
+    if (p.epi.type == kKvF32) {
+        if (plan.tile == 128) return launch_grouped_act<128, 128, 2, TAIL, true>(p, R, E, stream);
+        if (plan.stages == 4) return launch_grouped_act<64, 64, 4, TAIL, true>(p, R, E, stream);
+        return launch_grouped_act<64, 64, 2, TAIL, true>(p, R, E, stream);
+    }
+    if (plan.tile == 256) return launch_grouped_act<256, 256, 2, TAIL, false>(p, R, E, stream);
+    if (plan.tile == 128) return launch_grouped_act<128, 128, 2, TAIL, false>(p, R, E, stream);
+    if (plan.stages == 4) return launch_grouped_act<64, 64, 4, TAIL, false>(p, R, E, stream);
+    return launch_grouped_act<64, 64, 2, TAIL, false>(p, R, E, stream);
 }
 
 hipError_t launch_gemm_grouped_mfma_act(const uint8_t* qa, const float* s_tok, const int32_t* row_token,
@@ -899,7 +1014,8 @@ hipError_t launch_gemm_grouped_mfma_act(const uint8_t* qa, const float* s_tok, c
     p.qa = qa; p.lda = K; p.s_tok = s_tok; p.qw = qw; p.ldw = K; p.s_ch = s_ch; p.epi = epi;
     p.M = (int)R; p.N = (int)N; p.K = (int)K;
     p.row_token = row_token; p.offsets = offsets; p.E = (int)E;
-    return K % kBK == 0 ? launch_grouped_tail<false>(p, R, E, stream) : launch_grouped_tail<true>(p, R, E, stream);
+    const ActPlan plan = grouped_act_plan(R, E, N, K, epi.type == kKvF32);
+    return K % kBK == 0 ? launch_grouped_tail<false>(p, plan, R, E, stream) : launch_grouped_tail<true>(p, plan, R, E, stream);
 }
 
 hipError_t launch_gemm_mfma_mx(const uint8_t* qa, int64_t lda, const uint8_t* sa, const uint8_t* qw, int64_t ldw,

@@ -28,42 +28,6 @@ namespace fp8k {
 // would wait for loads that are meant to stay in flight).
 __device__ __forceinline__ void issue_order_fence() { __builtin_amdgcn_sched_barrier(0); }
 
-// The epilogue of four neighbouring outputs from their sums.  A missing bias
-// enters as -0, which leaves every value as it is, signed zeros included.
-template <int DT>
-__device__ __forceinline__ void finish4_typed(const Epilogue& e, const v4f& sum, float st,
-                                              const float* __restrict__ s_ch, int m, int nb, int N) {
-    const int left = N - nb;
-    float sc[4], x[4];
-    load_run<kKvF32, 4>(s_ch, nb, left, sc);
-    if (e.bias != nullptr) {
-        load_run<kKvF32, 4>(e.bias, nb, left, x);
-    } else {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) x[v] = -0.0f;
-    }
-#pragma unroll
-    for (int v = 0; v < 4; ++v) x[v] = __builtin_fmaf(sum[v], st * sc[v], x[v]);
-    activate<DT == kKvF32, 4>(x, e.act);
-    if (e.residual != nullptr) {
-        float r[4];
-        load_run<DT, 4>(e.residual, (int64_t)m * e.ldr + nb, left, r);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) x[v] += r[v];
-    }
-    store_run<DT, 4>(e.y, (int64_t)m * e.ldy + nb, left, x);
-}
-
-__device__ __forceinline__ void finish4(const Epilogue& e, const v4f& sum, float st, const float* __restrict__ s_ch,
-                                        int m, int nb, int N) {
-    if (e.type == kKvBF16)
-        finish4_typed<kKvBF16>(e, sum, st, s_ch, m, nb, N);
-    else if (e.type == kKvF16)
-        finish4_typed<kKvF16>(e, sum, st, s_ch, m, nb, N);
-    else
-        finish4_typed<kKvF32>(e, sum, st, s_ch, m, nb, N);
-}
-
 // The 128-k product in fp16, for fp32 outputs: the FP8 instruction keeps about 14
 // bits below the largest of 8 neighbouring products (measured; sums off by 1e-5
 // of their norm), the fp16 ones fp32's.  The weights' stream hides the rest.
@@ -515,30 +479,6 @@ __global__ __launch_bounds__(256) void skinny_splitk_reduce(const float* __restr
     }
 }
 
-// The same sums through an epilogue.
-__global__ __launch_bounds__(256) void skinny_splitk_reduce_act(const float* __restrict__ part, int splits, int M, int N,
-                                                               const float* __restrict__ s_tok,
-                                                               const float* __restrict__ s_ch, Epilogue epi) {
-    const int n4 = (N + 3) >> 2;
-    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (t >= (int64_t)M * n4) return;
-    const int m = (int)(t / n4);
-    const int nb = (int)(t - (int64_t)m * n4) * 4;
-    const int64_t plane = (int64_t)M * N;
-    const float* p = part + (int64_t)m * N + nb;
-    v4f sum;
-    float x[4];
-    load_run<kKvF32, 4>(p, 0, N - nb, x);
-#pragma unroll
-    for (int v = 0; v < 4; ++v) sum[v] = x[v];
-    for (int z = 1; z < splits; ++z) {
-        load_run<kKvF32, 4>(p, z * plane, N - nb, x);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) sum[v] += x[v];
-    }
-    finish4(epi, sum, s_tok[m], s_ch, m, nb, N);
-}
-
 template <int MT, int NT, int KW, bool MX, bool ACT, bool HALF>
 static void launch_cfg(dim3 grid, hipStream_t stream, const uint8_t* qa, int64_t lda, const float* s_tok,
                        const uint8_t* qw, int64_t ldw, const float* s_ch, uint16_t* y, float* y32, int64_t ldy, int M,
@@ -628,37 +568,31 @@ size_t gemm_skinny_ws_bytes(int64_t M, int64_t N, int64_t K) {
     return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * sizeof(float) : 0;
 }
 
-template <bool MX, bool ACT, bool HALF>
+template <bool MX>
 static hipError_t launch_skinny_any(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw,
                                     int64_t ldw, const float* s_ch, uint16_t* y, float* y32, int64_t ldy, int64_t M,
-                                    int64_t N, int64_t K, void* ws, MxScales mx, const Epilogue& epi,
-                                    hipStream_t stream) {
+                                    int64_t N, int64_t K, void* ws, MxScales mx, hipStream_t stream) {
     if (M <= 0 || N <= 0) return hipSuccess;
     SkinnyPlan p = skinny_plan(M, N, K);
-    // MX and HALF: 4 activation tiles with nt = 4 (8 waves, 256 VGPRs each) would
+    // MX: 4 activation tiles with nt = 4 (8 waves, 256 VGPRs each) would
     // spill; take nt = 8 (4 waves) there (same splits: none on this branch).
     // The shallower MX prefetch also measured slower with nt = 5..7 than
     // with nt = 8 (70B gate/up: 62.8 vs 60.8 us), so MX keeps nt = 8.
-    if ((MX || HALF) && p.mt == 4 && p.nt == 4) p.nt = 8;
+    if (MX && p.mt == 4 && p.nt == 4) p.nt = 8;
     if (MX && p.nt >= 5 && p.nt <= 7) p.nt = 8;
     float* part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
     const dim3 grid((unsigned)((N + 16 * p.nt - 1) / (16 * p.nt)), 1, (unsigned)p.splits);
     const int m = (int)M, n = (int)N, k = (int)K;
     switch (p.mt) {
-        case 1: launch_mt<1, MX, ACT, HALF>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx, epi); break;
-        case 2: launch_mt<2, MX, ACT, HALF>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx, epi); break;
-        case 3: launch_mt<3, MX, ACT, HALF>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx, epi); break;
-        default: launch_mt<4, MX, ACT, HALF>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx, epi); break;
+        case 1: launch_mt<1, MX, false, false>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx, Epilogue{}); break;
+        case 2: launch_mt<2, MX, false, false>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx, Epilogue{}); break;
+        case 3: launch_mt<3, MX, false, false>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx, Epilogue{}); break;
+        default: launch_mt<4, MX, false, false>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx, Epilogue{}); break;
     }
     if (part != nullptr) {
         const int64_t threads = M * ((N + 3) / 4);
-        const dim3 blocks((unsigned)((threads + 255) / 256));
-        if constexpr (ACT)
-            hipLaunchKernelGGL(skinny_splitk_reduce_act, blocks, dim3(256), 0, stream, part, p.splits, m, n, s_tok, s_ch,
-                               epi);
-        else
-            hipLaunchKernelGGL(skinny_splitk_reduce, blocks, dim3(256), 0, stream, part, p.splits, m, n,
-                               MX ? nullptr : s_tok, MX ? nullptr : s_ch, y, y32, ldy);
+        hipLaunchKernelGGL(skinny_splitk_reduce, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, part,
+                           p.splits, m, n, MX ? nullptr : s_tok, MX ? nullptr : s_ch, y, y32, ldy);
     }
     return hipGetLastError();
 }
@@ -666,22 +600,27 @@ static hipError_t launch_skinny_any(const uint8_t* qa, int64_t lda, const float*
 hipError_t launch_gemm_skinny(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw,
                               int64_t ldw, const float* s_ch, uint16_t* y, float* y32, int64_t ldy, int64_t M, int64_t N,
                               int64_t K, void* ws, hipStream_t stream) {
-    return launch_skinny_any<false, false, false>(qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, ws, MxScales{},
-                                           Epilogue{}, stream);
+    return launch_skinny_any<false>(qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, ws, MxScales{}, stream);
 }
 
 hipError_t launch_gemm_skinny_act(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw, int64_t ldw,
-                                  const float* s_ch, const Epilogue& epi, int64_t M, int64_t N, int64_t K, void* ws,
+                                  const float* s_ch, const Epilogue& epi, int64_t M, int64_t N, int64_t K,
                                   hipStream_t stream) {
-    const auto launch = epi.type == kKvF32 ? launch_skinny_any<false, true, true> : launch_skinny_any<false, true, false>;
-    return launch(qa, lda, s_tok, qw, ldw, s_ch, nullptr, nullptr, 0, M, N, K, ws, MxScales{}, epi, stream);
+    if (M <= 0 || N <= 0) return hipSuccess;
+    if (M > kSkinnyActMaxM) return hipErrorInvalidValue;
+    const SkinnyPlan p = skinny_plan(M, N, K);  // one activation tile, K not split
+    const dim3 grid((unsigned)((N + 16 * p.nt - 1) / (16 * p.nt)));
+    const auto launch = epi.type == kKvF32 ? launch_mt<1, false, true, true> : launch_mt<1, false, true, false>;
+    launch(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, nullptr, nullptr, 0, (int)M, (int)N, (int)K, nullptr,
+           p.split_chunks, MxScales{}, epi);
+    return hipGetLastError();
 }
 
 hipError_t launch_gemm_skinny_mx(const uint8_t* qa, int64_t lda, const uint8_t* sa, const uint8_t* qw, int64_t ldw,
                                  const uint8_t* sw, uint16_t* y, int64_t ldy, int64_t M, int64_t N, int64_t K, void* ws,
                                  hipStream_t stream) {
-    return launch_skinny_any<true, false, false>(qa, lda, nullptr, qw, ldw, nullptr, y, nullptr, ldy, M, N, K, ws,
-                                          MxScales{sa, sw}, Epilogue{}, stream);
+    return launch_skinny_any<true>(qa, lda, nullptr, qw, ldw, nullptr, y, nullptr, ldy, M, N, K, ws,
+                                   MxScales{sa, sw}, stream);
 }
 
 // The one-kernel path pays for every workgroup reading all of x (fp32) from

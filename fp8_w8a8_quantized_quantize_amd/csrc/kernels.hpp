@@ -161,8 +161,12 @@ hipError_t launch_gemm_skinny(const uint8_t* qa, int64_t lda, const float* s_tok
                               int64_t ldw, const float* s_ch, uint16_t* y, float* y32, int64_t ldy, int64_t M, int64_t N,
                               int64_t K, void* ws, hipStream_t stream);
 
+// With an epilogue, M <= kSkinnyActMaxM: one activation tile, which the weights'
+// stream bounds (8 x 4096 x 4096: 6.3 us, by tiles of 64 10.5; 32 rows 12.7 against
+// 10.6, 64 x 16384 x 1024 12.2 against 6.9).  No workspace.
+constexpr int64_t kSkinnyActMaxM = 16;
 hipError_t launch_gemm_skinny_act(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw, int64_t ldw,
-                                  const float* s_ch, const Epilogue& epi, int64_t M, int64_t N, int64_t K, void* ws,
+                                  const float* s_ch, const Epilogue& epi, int64_t M, int64_t N, int64_t K,
                                   hipStream_t stream);
 
 // Block-scaled skinny GEMM (K % 128 == 0): y = bf16_rne(sum over blocks of
@@ -196,9 +200,10 @@ hipError_t launch_gemm_mfma(const uint8_t* qa, int64_t lda, const float* s_tok, 
                             const float* s_ch, uint16_t* y, float* y32, int64_t ldy, int64_t M, int64_t N, int64_t K,
                             hipStream_t stream);
 
-// The same kernel with an epilogue, any K % 16 == 0.
+// The same kernel with an epilogue, any K % 16 == 0, in the tiles and k splits of
+// act_plan.hpp; ws: act_plan_ws_bytes bytes.
 hipError_t launch_gemm_mfma_act(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw, int64_t ldw,
-                                const float* s_ch, const Epilogue& epi, int64_t M, int64_t N, int64_t K,
+                                const float* s_ch, const Epilogue& epi, int64_t M, int64_t N, int64_t K, void* ws,
                                 hipStream_t stream);
 hipError_t launch_gemm_grouped_mfma_act(const uint8_t* qa, const float* s_tok, const int32_t* row_token,
                                         const int32_t* offsets, const uint8_t* qw, const float* s_ch,

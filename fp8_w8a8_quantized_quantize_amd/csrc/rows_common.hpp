@@ -249,6 +249,42 @@ __device__ __forceinline__ void activate(float (&x)[V], int act) {
     }
 }
 
+// The epilogue of four neighbouring outputs from their sums.  A missing bias
+// enters as -0, which leaves every value as it is, signed zeros included.
+template <int DT>
+__device__ __forceinline__ void finish4_typed(const Epilogue& e, const v4f& sum, float st,
+                                              const float* __restrict__ s_ch, int m, int nb, int N) {
+    const int left = N - nb;
+    float sc[4], x[4];
+    load_run<kKvF32, 4>(s_ch, nb, left, sc);
+    if (e.bias != nullptr) {
+        load_run<kKvF32, 4>(e.bias, nb, left, x);
+    } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x[v] = -0.0f;
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) x[v] = __builtin_fmaf(sum[v], st * sc[v], x[v]);
+    activate<DT == kKvF32, 4>(x, e.act);
+    if (e.residual != nullptr) {
+        float r[4];
+        load_run<DT, 4>(e.residual, (int64_t)m * e.ldr + nb, left, r);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x[v] += r[v];
+    }
+    store_run<DT, 4>(e.y, (int64_t)m * e.ldy + nb, left, x);
+}
+
+__device__ __forceinline__ void finish4(const Epilogue& e, const v4f& sum, float st, const float* __restrict__ s_ch,
+                                        int m, int nb, int N) {
+    if (e.type == kKvBF16)
+        finish4_typed<kKvBF16>(e, sum, st, s_ch, m, nb, N);
+    else if (e.type == kKvF16)
+        finish4_typed<kKvF16>(e, sum, st, s_ch, m, nb, N);
+    else
+        finish4_typed<kKvF32>(e, sum, st, s_ch, m, nb, N);
+}
+
 // kernel<DT>(...) of a runtime element type: f(std::integral_constant<int, DT>).
 template <typename F>
 hipError_t with_type(int dtype, F&& f) {

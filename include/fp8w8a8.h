@@ -549,9 +549,13 @@ typedef enum {
  * fp32 y is what fp8_quantize_per_token takes next.  bias fp32 [N] and residual
  * [M, N] (row stride ldr >= N) may be NULL; residual may be y itself (same
  * pointer and stride), else it does not overlap y.  y [M, N], any row stride
- * ldy >= N.  Without bias, activation and residual a bf16 y holds the bits of
- * fp8_gemm_scaled wherever both take the same division of K.  ws: at least
- * fp8_gemm_act_workspace_bytes(M, N, K) bytes (may be NULL when that is 0).
+ * ldy >= N.  For an fp32 y the products are summed to fp32's own precision (fp16
+ * matrix instructions, at half the rate); for 16-bit ones as fp8_gemm_scaled does,
+ * whose instructions leave 1e-5 of a sum's norm, far below the rounding.  An output
+ * of more than 2^24 - 9 tiles of 128 x 128 (grouped: as for
+ * fp8_gemm_grouped_scaled) is FP8_ERR_UNSUPPORTED.  ws: at least
+ * fp8_gemm_act_workspace_bytes(M, N, K) bytes, 16-byte aligned (sums of a split K,
+ * added in a fixed order; may be NULL when that is 0).
  */
 fp8_status_t fp8_gemm_scaled_act(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw, int64_t ldw,
                                  const float* s_ch, const float* bias, fp8_act_t act, const void* residual, int64_t ldr,
