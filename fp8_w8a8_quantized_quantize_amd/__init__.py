@@ -883,18 +883,19 @@ def _act(act):
 
 def _mat(t, name, di, dtype=None, cols=None, rows=None):
     """A 2-D row-major tensor on device number di, of dtype, rows and cols when given -> (rows, cols, row stride, address)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or (dtype is not None and t.dtype is not dtype):
-        raise TypeError(f"{name}: expected a {dtype or 'CUDA'} CUDA tensor" if dtype else f"{name}: expected a CUDA tensor")
-    if t.get_device() != di:
-        raise ValueError(f"{name}: on {t.device}, expected device {di}")
-    if t.dim() != 2:
+    if not isinstance(t, _torch().Tensor) or (dtype is not None and t.dtype is not dtype) or t.get_device() != di or t.dim() != 2:
+        if dtype is not None:
+            _on_device(t, dtype, name)
+        elif not isinstance(t, _torch().Tensor) or not t.is_cuda:
+            raise TypeError(f"{name}: expected a CUDA tensor")
+        if t.get_device() != di:
+            raise ValueError(f"{name}: on {t.device}, expected device {di}")
         raise ValueError(f"{name}: expected a 2-D row-major tensor (unit stride along the last dim)")
     n, c = t.shape
     s0, s1 = t.stride()
     if s1 != 1 and c > 1 and n > 0:
         raise ValueError(f"{name}: expected a 2-D row-major tensor (unit stride along the last dim)")
-    if (rows is not None and n != rows) or (cols is not None and c != cols):
+    if rows is not None and n != rows or cols is not None and c != cols:
         raise ValueError(f"{name}: expected shape [{'*' if rows is None else rows}, {'*' if cols is None else cols}]")
     return n, c, (s0 if n > 1 else c), t.data_ptr()
 
@@ -913,6 +914,7 @@ def _dtype_code(dtype, name):
     return code
 
 
+@functools.lru_cache(maxsize=1024)
 def fp8_gemm_act_workspace_bytes(M, N, K):
     """Workspace bytes of fp8_gemm_scaled_act."""
     return int(lib().fp8_gemm_act_workspace_bytes(M, N, K))
@@ -944,7 +946,7 @@ def fp8_gemm_scaled_act(qa, s_tok, qw, s_ch, bias=None, act="none", residual=Non
     dtype = _y_type(y, y_dtype, residual)
     code = _dtype_code(dtype, "y")
     if y is None:
-        y = torch.empty((M, N), dtype=dtype, device=qa.device)
+        y = qa.new_empty((M, N), dtype=dtype)
     _, _, ldy, yp = _mat(y, "y", di, dtype, N, M)
     ldr = rp = 0
     if residual is not None:
@@ -984,7 +986,7 @@ def fp8_gemm_grouped_scaled_act(qa, s_tok, row_token, expert_offsets, qw, s_ch, 
     dtype = _y_type(y, y_dtype, None)
     code = _dtype_code(dtype, "y")
     if y is None:
-        y = torch.empty((R, N), dtype=dtype, device=qa.device)
+        y = qa.new_empty((R, N), dtype=dtype)
     _, _, ldy, yp = _mat(y, "y", di, dtype, N, R)
     ws, wsp, wsn = _attn_ws(ws, fp8_grouped_workspace_bytes(T, R, E, N, K), qa.device)
     _check("fp8_gemm_grouped_scaled_act",
@@ -1009,9 +1011,9 @@ def fp8_act_quantize(h, act="silu", gated=True, q=None, scales=None, live_rows=N
         raise ValueError("h: expected [M, 2 F] (gated)")
     F = C // 2 if gated else C
     if q is None:
-        q = torch.empty((M, F), dtype=torch.uint8, device=h.device)
+        q = h.new_empty((M, F), dtype=torch.uint8)
     if scales is None:
-        scales = torch.empty(M, dtype=torch.float32, device=h.device)
+        scales = h.new_empty(M, dtype=torch.float32)
     _, _, ldq, qp = _mat(q, "q", di, torch.uint8, F, M)
     lp = 0 if live_rows is None else _flat(live_rows, torch.int32, "live_rows", 1, di)
     _check("fp8_act_quantize",
@@ -1020,6 +1022,7 @@ def fp8_act_quantize(h, act="silu", gated=True, q=None, scales=None, live_rows=N
     return q, scales
 
 
+@functools.lru_cache(maxsize=1024)
 def fp8_moe_sort_workspace_bytes(T, topk, E):
     """Workspace bytes of fp8_moe_sort."""
     return int(lib().fp8_moe_sort_workspace_bytes(T, topk, E))
@@ -1041,11 +1044,11 @@ def fp8_moe_sort(expert_ids, num_experts, expert_offsets=None, row_token=None, r
     T, topk = expert_ids.shape
     R = T * topk
     if expert_offsets is None:
-        expert_offsets = torch.empty(max(num_experts, 0) + 1, dtype=i32, device=expert_ids.device)
+        expert_offsets = expert_ids.new_empty(max(num_experts, 0) + 1, dtype=i32)
     if row_token is None:
-        row_token = torch.empty(R, dtype=i32, device=expert_ids.device)
+        row_token = expert_ids.new_empty(R, dtype=i32)
     if row_of is None:
-        row_of = torch.empty((T, topk), dtype=i32, device=expert_ids.device)
+        row_of = expert_ids.new_empty((T, topk), dtype=i32)
     op = _flat(expert_offsets, i32, "expert_offsets", max(num_experts, 0) + 1, di)
     ws, wsp, wsn = _attn_ws(ws, fp8_moe_sort_workspace_bytes(T, topk, num_experts), expert_ids.device)
     _check("fp8_moe_sort",
@@ -1080,13 +1083,13 @@ def fp8_moe_permute(x, row_of, num_rows=None, s_tok=None, out=None, s_out=None):
     T, topk, rp = _choices(row_of, di)
     _, H, ldx, xp = _mat(x, "x", di, rows=T)
     if out is None:
-        out = torch.empty((T * topk if num_rows is None else num_rows, H), dtype=x.dtype, device=x.device)
+        out = x.new_empty((T * topk if num_rows is None else num_rows, H))
     R, _, ldo, op = _mat(out, "out", di, x.dtype, H, num_rows)
     tp = sp = 0
     if s_tok is not None:
         tp = _flat(s_tok, torch.float32, "s_tok", T, di)
         if s_out is None:
-            s_out = torch.empty(R, dtype=torch.float32, device=x.device)
+            s_out = x.new_empty(R, dtype=torch.float32)
         sp = _flat(s_out, torch.float32, "s_out", R, di)
     elif s_out is not None:
         raise ValueError("s_out: given without s_tok")
@@ -1111,7 +1114,7 @@ def fp8_moe_combine(y, row_of, weights=None, residual=None, out=None, out_dtype=
     dtype = out.dtype if out is not None else out_dtype or (y if residual is None else residual).dtype
     out_code = _dtype_code(dtype, "out")
     if out is None:
-        out = torch.empty((T, H), dtype=dtype, device=y.device)
+        out = y.new_empty((T, H), dtype=dtype)
     _, _, ldo, op = _mat(out, "out", di, dtype, H, T)
     ldr = sp = 0
     if residual is not None:
@@ -1139,11 +1142,11 @@ def fp8_moe_combine_grad(dout, y, row_of, weights=None, dy=None, dweights=None, 
     lddy = yg = wg = 0
     if dy is not None or need_dy:
         if dy is None:
-            dy = torch.empty((R, H), dtype=y.dtype, device=y.device)
+            dy = y.new_empty((R, H))
         _, _, lddy, yg = _mat(dy, "dy", di, y.dtype, H, R)
     if dweights is not None or need_dweights:
         if dweights is None:
-            dweights = torch.empty((T, topk), dtype=torch.float32, device=y.device)
+            dweights = y.new_empty((T, topk), dtype=torch.float32)
         wg = _flat(dweights, torch.float32, "dweights", T * topk, di)
     _check("fp8_moe_combine_grad",
            lib().fp8_moe_combine_grad(dp, ldd, code, yp, ldy, y_code, rp, wp, yg, lddy, wg, T, topk, R, H,

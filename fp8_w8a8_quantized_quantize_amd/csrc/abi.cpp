@@ -654,7 +654,7 @@ fp8_status_t fp8_gemm_grouped_scaled(const uint8_t* qa, const float* s_tok, cons
 
 size_t fp8_gemm_act_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (check_dims(M, N, K) != FP8_OK || !act_tiles_ok((M + 127) / 128, N)) return SIZE_MAX;
-    if (M <= fp8k::kSkinnyActMaxM) return gemm_ws_bytes(M, N, K);
+    if (fp8k::skinny_act(M, N)) return 0;
     return round_up(std::max(fp8k::act_plan_ws_bytes(fp8k::act_plan(M, N, K, false), M, N),
                              fp8k::act_plan_ws_bytes(fp8k::act_plan(M, N, K, true), M, N)), kAlign);
 }
@@ -676,7 +676,7 @@ fp8_status_t fp8_gemm_scaled_act(const uint8_t* qa, int64_t lda, const float* s_
     if (need > 0 && ws == nullptr) return FP8_ERR_INVALID_ARGUMENT;
     if (need > 0 && !aligned16(ws)) return FP8_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return FP8_OK;
-    if (M <= fp8k::kSkinnyActMaxM)
+    if (fp8k::skinny_act(M, N))
         return from_hip(fp8k::launch_gemm_skinny_act(qa, lda, s_tok, qw, ldw, s_ch, epi, M, N, K, stream));
     return from_hip(fp8k::launch_gemm_mfma_act(qa, lda, s_tok, qw, ldw, s_ch, epi, M, N, K, ws, stream));
 }

@@ -303,6 +303,11 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
             sub_n = p.tiles_n >> 2;
             off_m = (x >> 2) * sub_m;
             off_n = (x & 3) * sub_n;
+        } else if constexpr (ACT) {
+            // any other grid: XCD x takes a contiguous run of the tiles below, one longer
+            // for the first total % 8 of them
+            const int total = p.tiles_m * p.tiles_n, x = t & 7;
+            t = x * (total >> 3) + min(x, total & 7) + (t >> 3);
         }
         const int per_group = GROUP_M * sub_n;
         const int grp = t / per_group;

@@ -607,7 +607,7 @@ hipError_t launch_gemm_skinny_act(const uint8_t* qa, int64_t lda, const float* s
                                   const float* s_ch, const Epilogue& epi, int64_t M, int64_t N, int64_t K,
                                   hipStream_t stream) {
     if (M <= 0 || N <= 0) return hipSuccess;
-    if (M > kSkinnyActMaxM) return hipErrorInvalidValue;
+    if (!skinny_act(M, N)) return hipErrorInvalidValue;
     const SkinnyPlan p = skinny_plan(M, N, K);  // one activation tile, K not split
     const dim3 grid((unsigned)((N + 16 * p.nt - 1) / (16 * p.nt)));
     const auto launch = epi.type == kKvF32 ? launch_mt<1, false, true, true> : launch_mt<1, false, true, false>;

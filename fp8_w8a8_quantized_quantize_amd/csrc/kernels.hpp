@@ -164,7 +164,10 @@ hipError_t launch_gemm_skinny(const uint8_t* qa, int64_t lda, const float* s_tok
 // With an epilogue, M <= kSkinnyActMaxM: one activation tile, which the weights'
 // stream bounds (8 x 4096 x 4096: 6.3 us, by tiles of 64 10.5; 32 rows 12.7 against
 // 10.6, 64 x 16384 x 1024 12.2 against 6.9).  No workspace.
+// Past kSkinnyActMaxN its grid would have 2^32 threads or more.
 constexpr int64_t kSkinnyActMaxM = 16;
+constexpr int64_t kSkinnyActMaxN = int64_t(1) << 28;
+inline bool skinny_act(int64_t M, int64_t N) { return M <= kSkinnyActMaxM && N <= kSkinnyActMaxN; }
 hipError_t launch_gemm_skinny_act(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw, int64_t ldw,
                                   const float* s_ch, const Epilogue& epi, int64_t M, int64_t N, int64_t K,
                                   hipStream_t stream);
