@@ -516,10 +516,16 @@ def _on_stream(fn):
     return call
 
 
+_raw_stream_of = None
+
+
 def _raw_stream(di):
     """The current stream of device number di, as a pointer."""
-    get = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
-    return get(di) if get is not None else _torch().cuda.current_stream(di).cuda_stream
+    global _raw_stream_of
+    if _raw_stream_of is None:
+        _raw_stream_of = getattr(_torch()._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: _torch().cuda.current_stream(d).cuda_stream)
+    return _raw_stream_of(di)
 
 
 def _heads(t, name, di=None, dtype=None):

@@ -426,46 +426,60 @@ __global__ __launch_bounds__(kRowThreads) void moe_combine_grad(MoeCombineGrad p
             const int64_t t = c / p.topk;
             const float w = p.weights != nullptr ? p.weights[c] : 1.0f;
             const int64_t d0 = t * p.ldd, y0 = (int64_t)r * p.ldy, g0 = (int64_t)r * p.lddy;
-            // M pieces of the lane, `lanes` apart, from element n on; its own begin at `own`
-            auto pieces = [&](auto many, int64_t n, int64_t own) {
+            // M pieces of the lane, `lanes` apart, from element n0 on.  LAST: not all of them
+            // whole and in the row.  The row's last piece reaches back over the one before
+            // it, as in moe_combine, and one past it reads that too, so that all loads go out
+            // together; what is not the lane's own counts nowhere.
+            auto pieces = [&](auto many, auto last, int64_t n0) {
                 constexpr int M = decltype(many)::value;
+                constexpr bool LAST = decltype(last)::value;
                 uint32_t dr[M][V * elem_size<DT>() / 4], yr[M][4];
+                int64_t at[M];
 #pragma unroll
                 for (int m = 0; m < M; ++m) {
-                    const int64_t at = n + (int64_t)m * V * lanes;
-                    load_words(static_cast<const uint8_t*>(p.dout) + (d0 + at) * elem_size<DT>(), dr[m]);
+                    at[m] = n0 + (int64_t)m * V * lanes;
+                    if constexpr (LAST) at[m] = min(at[m], p.H - V);
+                    load_words(static_cast<const uint8_t*>(p.dout) + (d0 + at[m]) * elem_size<DT>(), dr[m]);
                     if (p.dweights != nullptr)
-                        load_words(static_cast<const uint8_t*>(p.y) + (y0 + at) * elem_size<YDT>(), yr[m]);
+                        load_words(static_cast<const uint8_t*>(p.y) + (y0 + at[m]) * elem_size<YDT>(), yr[m]);
                 }
 #pragma unroll
                 for (int m = 0; m < M; ++m) {
+                    const int64_t own = n0 + (int64_t)m * V * lanes;
                     float d[V], y[V];
                     unpack<DT, V>(dr[m], d);
                     if (p.dweights != nullptr) {
                         unpack<YDT, V>(yr[m], y);
 #pragma unroll
                         for (int i = 0; i < V; ++i)
-                            if (M > 1 || n + i >= own) dot = __builtin_fmaf(d[i], y[i], dot);
+                            if (!LAST || at[m] + i >= own) dot = __builtin_fmaf(d[i], y[i], dot);
                     }
                     if (p.dy != nullptr) {
 #pragma unroll
                         for (int i = 0; i < V; ++i) d[i] *= w;
-                        if (M > 1 || n == own) {
-                            store_run<YDT, V>(p.dy, g0 + n + (int64_t)m * V * lanes, V, d);
+                        if (!LAST || at[m] == own) {
+                            store_run<YDT, V>(p.dy, g0 + at[m], V, d);
                         } else {
 #pragma unroll
                             for (int i = 0; i < V; ++i)
-                                if (n + i >= own) store_elem<YDT>(p.dy, g0 + n + i, d[i]);
+                                if (at[m] + i >= own) store_elem<YDT>(p.dy, g0 + at[m] + i, d[i]);
                         }
                     }
                 }
             };
-            int64_t n = (int64_t)V * l;
-            for (; n + (int64_t)(U - 1) * V * lanes + V <= p.H; n += (int64_t)U * V * lanes)
-                pieces(std::integral_constant<int, U>{}, n, n);
+            const int64_t run = (int64_t)V * lanes;  // elements of the choice's lanes together
+            int64_t n0 = 0;
+            for (; n0 + U * run <= p.H; n0 += U * run)
+                pieces(std::integral_constant<int, U>{}, std::false_type{}, n0 + (int64_t)V * l);
             if (p.H >= V) {
-                // the row's last piece reaches back over the one before it, as in moe_combine
-                for (; n < p.H; n += (int64_t)V * lanes) pieces(std::integral_constant<int, 1>{}, min(n, p.H - V), n);
+                const int64_t n = n0 + (int64_t)V * l;
+                switch ((int)((p.H - n0 + run - 1) / run)) {
+                    case 0: break;
+                    case 1: pieces(std::integral_constant<int, 1>{}, std::true_type{}, n); break;
+                    case 2: pieces(std::integral_constant<int, 2>{}, std::true_type{}, n); break;
+                    case 3: pieces(std::integral_constant<int, 3>{}, std::true_type{}, n); break;
+                    default: pieces(std::integral_constant<int, U>{}, std::true_type{}, n); break;
+                }
             } else if (l == 0) {
                 for (int64_t i = 0; i < p.H; ++i) {
                     const float d = load_elem<DT>(p.dout, d0 + i);
@@ -598,7 +612,10 @@ hipError_t launch_moe_combine_grad(const MoeCombineGrad& p, int dtype, int y_dty
         return with_type(y_dtype, [&](auto ydt) {
             constexpr int DT = decltype(dt)::value, YDT = decltype(ydt)::value;
             const int64_t choices = (int64_t)p.T * p.topk;
-            const int bits = bits_for(ceil_div(p.H, 16 / elem_size<YDT>()), choices < 1024 ? 8 : 6);
+            // Few choices: a lane a piece, up to a workgroup each.  Many: two to four pieces a
+            // lane, up to a wave each (10000 choices of 333 fp16 elements: 14 us with a wave each, 6.4 with 16 lanes).
+            const int64_t each = ceil_div(p.H, 16 / elem_size<YDT>());
+            const int bits = choices < 1024 ? bits_for(each, 8) : bits_for(ceil_div(each, 4), 6);
             hipLaunchKernelGGL((moe_combine_grad<DT, YDT>), row_grid(ceil_div(choices, kRowThreads >> bits)),
                                dim3(kRowThreads), 0, stream, p, bits);
             return hipGetLastError();
