@@ -174,6 +174,17 @@ def _torch():
     return _torch_module
 
 
+_tensor_class = None
+
+
+def _tensor():
+    """torch.Tensor."""
+    global _tensor_class
+    if _tensor_class is None:
+        _tensor_class = _torch().Tensor
+    return _tensor_class
+
+
 def _stream(stream):
     torch = _torch()
     s = torch.cuda.current_stream() if stream is None else stream
@@ -499,21 +510,36 @@ def _on_stream(fn):
 
     @functools.wraps(fn)
     def call(*args, stream=None, **kwargs):
-        torch = _torch()
         t = args[0] if args else kwargs.get(first)
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        try:
+            di = t.get_device()
+        except AttributeError:
+            di = -1
+        if di < 0:
             raise TypeError(f"{fn.__name__}: expected CUDA tensors")
+        if stream is None and di == _current_device():
+            return fn(*args, **kwargs)
+        torch = _torch()
         if stream is not None:
             if stream.device != t.device:
                 raise ValueError(f"stream: on {stream.device}, expected {t.device}")
             with torch.cuda.stream(stream):
                 return fn(*args, **kwargs)
-        if t.get_device() != torch.cuda.current_device():
-            with torch.cuda.device(t.device):
-                return fn(*args, **kwargs)
-        return fn(*args, **kwargs)
+        with torch.cuda.device(t.device):
+            return fn(*args, **kwargs)
 
     return call
+
+
+_device_of = None
+
+
+def _current_device():
+    """The number of the current device (some tensor is on one: the runtime is up)."""
+    global _device_of
+    if _device_of is None:
+        _device_of = getattr(_torch()._C, "_cuda_getDevice", None) or _torch().cuda.current_device
+    return _device_of()
 
 
 _raw_stream_of = None
@@ -548,7 +574,7 @@ def _heads(t, name, di=None, dtype=None):
 
 def _flat(t, dtype, name, n, di):
     """Address of a contiguous tensor of n elements on device number di."""
-    if isinstance(t, _torch().Tensor) and t.dtype is dtype and t.get_device() == di and t.numel() == n and t.is_contiguous():
+    if isinstance(t, _tensor()) and t.dtype is dtype and t.get_device() == di and t.numel() == n and t.is_contiguous():
         return t.data_ptr()
     _vec(t, dtype, name, n)
     raise ValueError(f"{name}: on {t.device}, expected device {di}")
@@ -889,10 +915,10 @@ def _act(act):
 
 def _mat(t, name, di, dtype=None, cols=None, rows=None):
     """A 2-D row-major tensor on device number di, of dtype, rows and cols when given -> (rows, cols, row stride, address)."""
-    if not isinstance(t, _torch().Tensor) or (dtype is not None and t.dtype is not dtype) or t.get_device() != di or t.dim() != 2:
+    if not isinstance(t, _tensor()) or (dtype is not None and t.dtype is not dtype) or t.get_device() != di or t.dim() != 2:
         if dtype is not None:
             _on_device(t, dtype, name)
-        elif not isinstance(t, _torch().Tensor) or not t.is_cuda:
+        elif not isinstance(t, _tensor()) or not t.is_cuda:
             raise TypeError(f"{name}: expected a CUDA tensor")
         if t.get_device() != di:
             raise ValueError(f"{name}: on {t.device}, expected device {di}")
@@ -953,7 +979,9 @@ def fp8_gemm_scaled_act(qa, s_tok, qw, s_ch, bias=None, act="none", residual=Non
     code = _dtype_code(dtype, "y")
     if y is None:
         y = qa.new_empty((M, N), dtype=dtype)
-    _, _, ldy, yp = _mat(y, "y", di, dtype, N, M)
+        ldy, yp = N, y.data_ptr()
+    else:
+        _, _, ldy, yp = _mat(y, "y", di, dtype, N, M)
     ldr = rp = 0
     if residual is not None:
         _, _, ldr, rp = _mat(residual, "residual", di, dtype, N, M)
@@ -993,7 +1021,9 @@ def fp8_gemm_grouped_scaled_act(qa, s_tok, row_token, expert_offsets, qw, s_ch, 
     code = _dtype_code(dtype, "y")
     if y is None:
         y = qa.new_empty((R, N), dtype=dtype)
-    _, _, ldy, yp = _mat(y, "y", di, dtype, N, R)
+        ldy, yp = N, y.data_ptr()
+    else:
+        _, _, ldy, yp = _mat(y, "y", di, dtype, N, R)
     ws, wsp, wsn = _attn_ws(ws, fp8_grouped_workspace_bytes(T, R, E, N, K), qa.device)
     _check("fp8_gemm_grouped_scaled_act",
            lib().fp8_gemm_grouped_scaled_act(qp, tp, rp, op, qw.data_ptr(), cp, bp, _act(act), yp, code, ldy, T, R, E, N,
@@ -1051,16 +1081,23 @@ def fp8_moe_sort(expert_ids, num_experts, expert_offsets=None, row_token=None, r
     R = T * topk
     if expert_offsets is None:
         expert_offsets = expert_ids.new_empty(max(num_experts, 0) + 1, dtype=i32)
+        op = expert_offsets.data_ptr()
+    else:
+        op = _flat(expert_offsets, i32, "expert_offsets", max(num_experts, 0) + 1, di)
     if row_token is None:
         row_token = expert_ids.new_empty(R, dtype=i32)
+        tp = row_token.data_ptr()
+    else:
+        tp = _flat(row_token, i32, "row_token", R, di)
     if row_of is None:
         row_of = expert_ids.new_empty((T, topk), dtype=i32)
-    op = _flat(expert_offsets, i32, "expert_offsets", max(num_experts, 0) + 1, di)
+        rp = row_of.data_ptr()
+    else:
+        rp = _flat(row_of, i32, "row_of", R, di)
     ws, wsp, wsn = _attn_ws(ws, fp8_moe_sort_workspace_bytes(T, topk, num_experts), expert_ids.device)
     _check("fp8_moe_sort",
-           lib().fp8_moe_sort(expert_ids.data_ptr(), 0 if expert_ids.dtype is i32 else 1, T, topk, num_experts, op,
-                              _flat(row_token, i32, "row_token", R, di), _flat(row_of, i32, "row_of", R, di), wsp, wsn,
-                              _raw_stream(di)))
+           lib().fp8_moe_sort(expert_ids.data_ptr(), 0 if expert_ids.dtype is i32 else 1, T, topk, num_experts, op, tp, rp,
+                              wsp, wsn, _raw_stream(di)))
     return expert_offsets, row_token, row_of
 
 
@@ -1121,7 +1158,9 @@ def fp8_moe_combine(y, row_of, weights=None, residual=None, out=None, out_dtype=
     out_code = _dtype_code(dtype, "out")
     if out is None:
         out = y.new_empty((T, H), dtype=dtype)
-    _, _, ldo, op = _mat(out, "out", di, dtype, H, T)
+        ldo, op = H, out.data_ptr()
+    else:
+        _, _, ldo, op = _mat(out, "out", di, dtype, H, T)
     ldr = sp = 0
     if residual is not None:
         _, _, ldr, sp = _mat(residual, "residual", di, dtype, H, T)
