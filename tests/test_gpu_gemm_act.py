@@ -147,6 +147,94 @@ def test_grouped(T, topk, E, N, K, dropped, dtype):
         assert (whole[:, N:] == 7).all() and (y[int(off[-1]):] == 7).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(4000, 4090, 4112), (4090, 4001, 4096), (5000, 7000, 528), (4097, 4096, 512),
+                                   (1100, 2000, 2064), (300, 300, 8192), (20, 300, 16384), (17, 64, 32768)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gemm_of_each_division(M, N, K, dtype):
+    """Sizes that take the larger tiles and the longer splits, ragged on every side."""
+    log(f"gemm {M} {N} {K} {dtype}")
+    qa, qw, st, sc = codes(1, M, K), codes(2, N, K), scales(3, M), scales(4, N, K)
+    bias, res = randn(5, N) * 0.5, randn(6, M, N, dtype=dtype)
+    for act, r in (("gelu", res), ("none", None)):
+        y = fp8.fp8_gemm_scaled_act(qa, st, qw, sc, bias=bias, act=act, residual=r, y_dtype=dtype)
+        ref, bound = expect(qa, st, qw, sc, bias, act, r, dtype)
+        check(y, ref, bound, act)
+        near(y, ref, dtype, K, act)
+        if r is not None:
+            own = r.clone()
+            fp8.fp8_gemm_scaled_act(qa, st, qw, sc, bias=bias, act=act, residual=own, y=own)
+            assert torch.equal(own, y)
+
+
+@pytest.mark.parametrize("T,topk,E,N,K", [(4000, 1, 3, 3500, 2064), (4000, 1, 3, 3500, 2048), (3000, 3, 2, 3000, 528),
+                                          (9000, 1, 8, 2049, 1024)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_grouped_of_each_division(T, topk, E, N, K, dtype):
+    log(f"grouped {T} {topk} {E} {N} {K} {dtype}")
+    off, tok, _ = sorted_rows(choices(T + N, T, min(topk, E), E, 0.02, 50), E)
+    qa, qw, st = codes(1, T, K), codes(2, E * N, K).view(E, N, K), scales(3, T)
+    sc, bias = scales(4, E * N, K).view(E, N), randn(5, E, N) * 0.5
+    y = torch.full((tok.size, N), 7.0, dtype=dtype, device=DEV)
+    before = y.clone()
+    fp8.fp8_gemm_grouped_scaled_act(qa, st, torch.from_numpy(tok).to(DEV), torch.from_numpy(off).to(DEV), qw, sc, bias=bias,
+                                    act="silu", y=y)
+    ref, bound = grouped_expect(qa, st, tok, off, qw, sc, bias, "silu", before, dtype)
+    check(y, ref, bound, "grouped")
+    assert (y[int(off[-1]):] == 7).all()
+
+
+def test_replays_match_eager():
+    """Captured products, one of them with its sums in a workspace of its own, replayed with eager work in between."""
+    made = []
+    for M, N, K, dtype in ((5, 300, 512, BF), (20, 300, 16384, F32), (100, 700, 528, HF), (300, 1300, 1024, BF)):
+        qa, qw, st, sc = codes(1, M, K), codes(2, N, K), scales(3, M), scales(4, N, K)
+        res, y = randn(6, M, N, dtype=dtype), torch.empty((M, N), dtype=dtype, device=DEV)
+        ws = torch.empty(max(1, fp8.fp8_gemm_act_workspace_bytes(M, N, K)), dtype=U8, device=DEV)
+        made.append((qa, st, qw, sc, res, y, ws))
+    assert made[1][6].numel() > 1
+
+    def run():
+        for qa, st, qw, sc, res, y, ws in made:
+            fp8.fp8_gemm_scaled_act(qa, st, qw, sc, act="gelu", residual=res, y=y, ws=ws)
+
+    run()
+    torch.cuda.synchronize()
+    eager = [m[5].clone() for m in made]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for r in range(3):
+        for m in made:
+            m[5].zero_()
+            m[6].fill_(255)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for m, e in zip(made, eager):
+            assert torch.equal(m[5], e), f"replay {r}: {tuple(m[5].shape)}"
+        run()
+
+
+def test_two_streams_at_once():
+    M, N, K = 40, 600, 8192  # a split k: each call has a workspace of its own
+    qa, qw, st, sc = codes(1, M, K), codes(2, N, K), scales(3, M), scales(4, N, K)
+    want = fp8.fp8_gemm_scaled_act(qa, st, qw, sc, act="silu", y_dtype=F32)
+    assert fp8.fp8_gemm_act_workspace_bytes(M, N, K) > 0
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for s in streams:
+            got.append(fp8.fp8_gemm_scaled_act(qa, st, qw, sc, act="silu", y_dtype=F32, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in got)
+
+
 def test_refused_arguments():
     qa, qw, st, sc = codes(1, 8, 64), codes(2, 24, 64), scales(3, 8), scales(4, 24)
     for f in (lambda: fp8.fp8_gemm_scaled_act(qa, st, qw, sc, act="tanh"), lambda: fp8.fp8_gemm_scaled_act(qa, st, qw[:, :48], sc),
