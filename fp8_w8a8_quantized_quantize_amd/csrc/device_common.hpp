@@ -62,17 +62,6 @@ __device__ __forceinline__ v8i join(const v4i& lo, const v4i& hi) {
     return r;
 }
 
-// Eight E4M3 codes (two words) as the fp16 values they are, exactly.
-typedef _Float16 v8h __attribute__((ext_vector_type(8)));
-__device__ __forceinline__ v8h half8_of(int lo, int hi) {
-    typedef _Float16 v2h __attribute__((ext_vector_type(2)));
-    const v2h a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
-    const v2h b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
-    const v2h c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
-    const v2h d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
-    return v8h{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
 // Cross-lane max over a wave of 64.
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll

@@ -651,6 +651,8 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
         // the output, and the activation's code is there once, not once per
         // accumulator.  16-byte pieces are XOR-swizzled by row.  A thread whose 8
         // columns run past N works on the last 8 of the row and stores its own.
+        // 8192^3, bf16, with the matrix units waiting meanwhile: 422 us (the plain
+        // epilogue 410), with silu 433, gelu 452, gelu_tanh and a residual 452.
         constexpr int FP = FM < 2 ? FM : 2, ROWS = FP * 32 * WM;
         constexpr int CG = BN / 8;                          // column groups of a row
         constexpr int STEP = NTH / CG;                      // rows the workgroup covers at once

@@ -479,10 +479,10 @@ __global__ __launch_bounds__(256) void skinny_splitk_reduce(const float* __restr
     }
 }
 
-template <int MT, int NT, int KW, bool MX, bool ACT, bool HALF>
+template <int MT, int NT, int KW, bool MX, bool ACT = false, bool HALF = false>
 static void launch_cfg(dim3 grid, hipStream_t stream, const uint8_t* qa, int64_t lda, const float* s_tok,
                        const uint8_t* qw, int64_t ldw, const float* s_ch, uint16_t* y, float* y32, int64_t ldy, int M,
-                       int N, int K, float* part, int split_chunks, MxScales mx, const Epilogue& epi) {
+                       int N, int K, float* part, int split_chunks, MxScales mx, const Epilogue& epi = {}) {
     // The block-scaled MFMA keeps its operands in VGPRs (the plain one also
     // reads AGPRs), so the MX kernels keep fewer steps in flight to stay
     // within the register file without spills (checked in the compiler's
@@ -493,18 +493,18 @@ static void launch_cfg(dim3 grid, hipStream_t stream, const uint8_t* qa, int64_t
                        qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx, epi);
 }
 
-template <int MT, bool MX, bool ACT, bool HALF>
+template <int MT, bool MX>
 static void launch_mt(int nt, dim3 grid, hipStream_t stream, const uint8_t* qa, int64_t lda, const float* s_tok,
                       const uint8_t* qw, int64_t ldw, const float* s_ch, uint16_t* y, float* y32, int64_t ldy, int M,
-                      int N, int K, float* part, int split_chunks, MxScales mx, const Epilogue& epi) {
+                      int N, int K, float* part, int split_chunks, MxScales mx) {
     switch (nt) {
-        case 8: launch_cfg<MT, 8, 4, MX, ACT, HALF>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx, epi); break;
-        case 7: launch_cfg<MT, 7, 4, MX, ACT, HALF>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx, epi); break;
-        case 6: launch_cfg<MT, 6, 4, MX, ACT, HALF>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx, epi); break;
-        case 5: launch_cfg<MT, 5, 4, MX, ACT, HALF>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx, epi); break;
-        case 4: launch_cfg<MT, 4, 8, MX, ACT, HALF>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx, epi); break;
-        case 2: launch_cfg<MT, 2, 8, MX, ACT, HALF>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx, epi); break;
-        default: launch_cfg<MT, 1, 8, MX, ACT, HALF>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx, epi); break;
+        case 8: launch_cfg<MT, 8, 4, MX>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx); break;
+        case 7: launch_cfg<MT, 7, 4, MX>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx); break;
+        case 6: launch_cfg<MT, 6, 4, MX>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx); break;
+        case 5: launch_cfg<MT, 5, 4, MX>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx); break;
+        case 4: launch_cfg<MT, 4, 8, MX>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx); break;
+        case 2: launch_cfg<MT, 2, 8, MX>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx); break;
+        default: launch_cfg<MT, 1, 8, MX>(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx); break;
     }
 }
 
@@ -584,10 +584,10 @@ static hipError_t launch_skinny_any(const uint8_t* qa, int64_t lda, const float*
     const dim3 grid((unsigned)((N + 16 * p.nt - 1) / (16 * p.nt)), 1, (unsigned)p.splits);
     const int m = (int)M, n = (int)N, k = (int)K;
     switch (p.mt) {
-        case 1: launch_mt<1, MX, false, false>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx, Epilogue{}); break;
-        case 2: launch_mt<2, MX, false, false>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx, Epilogue{}); break;
-        case 3: launch_mt<3, MX, false, false>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx, Epilogue{}); break;
-        default: launch_mt<4, MX, false, false>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx, Epilogue{}); break;
+        case 1: launch_mt<1, MX>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx); break;
+        case 2: launch_mt<2, MX>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx); break;
+        case 3: launch_mt<3, MX>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx); break;
+        default: launch_mt<4, MX>(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, y, y32, ldy, m, n, k, part, p.split_chunks, mx); break;
     }
     if (part != nullptr) {
         const int64_t threads = M * ((N + 3) / 4);
@@ -610,9 +610,17 @@ hipError_t launch_gemm_skinny_act(const uint8_t* qa, int64_t lda, const float* s
     if (!skinny_act(M, N)) return hipErrorInvalidValue;
     const SkinnyPlan p = skinny_plan(M, N, K);  // one activation tile, K not split
     const dim3 grid((unsigned)((N + 16 * p.nt - 1) / (16 * p.nt)));
-    const auto launch = epi.type == kKvF32 ? launch_mt<1, false, true, true> : launch_mt<1, false, true, false>;
-    launch(p.nt, grid, stream, qa, lda, s_tok, qw, ldw, s_ch, nullptr, nullptr, 0, (int)M, (int)N, (int)K, nullptr,
-           p.split_chunks, MxScales{}, epi);
+    auto launch = [&](auto half) {
+        constexpr bool HALF = decltype(half)::value;
+        const auto kernel = p.nt == 4 ? launch_cfg<1, 4, 8, false, true, HALF>
+                            : p.nt == 2 ? launch_cfg<1, 2, 8, false, true, HALF> : launch_cfg<1, 1, 8, false, true, HALF>;
+        kernel(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, nullptr, nullptr, 0, (int)M, (int)N, (int)K, nullptr,
+               p.split_chunks, MxScales{}, epi);
+    };
+    if (epi.type == kKvF32)
+        launch(std::true_type{});
+    else
+        launch(std::false_type{});
     return hipGetLastError();
 }
 

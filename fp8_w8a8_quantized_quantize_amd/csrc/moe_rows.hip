@@ -5,7 +5,11 @@
 // Everything but the sort is a stream over rows, seen from the tokens: a token's
 // row is read once and written to its topk places (permute), or its topk rows
 // are read once and summed (combine).  No place is written twice and every sum
-// runs over j = 0, 1, .. in fp32, so results do not depend on timing.
+// runs over j = 0, 1, .. in fp32, so results do not depend on timing.  Memory
+// bounds them: 4096 x 8 rows of 7168, permute of codes 52 us (5.1 TB/s), combine of
+// bf16 rows onto a residual 110 us (5.3 TB/s, a plain copy's rate), its gradient
+// 197 us (5.1 TB/s); 1777 x 6 rows of 4999 fp16 elements, none of them aligned, 52 us
+// (4.1 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -514,9 +518,12 @@ dim3 row_grid(int64_t groups) { return dim3((unsigned)std::min<int64_t>(std::max
 
 }  // namespace
 
-// One launch up to here: every workgroup reads all choices.
-constexpr int64_t kSortOneWork = 4 << 20;
+// The single launch, whose every workgroup reads all choices, against the two, in us:
+//   choices x experts   512 x 64   8192 x 256   32768 x 64   32768 x 256   16384 x 1024   32768 x 1024   40000 x 256
+//   one                 2.4        4.3          7.7          9.7           12.2           23.3           16.8
+//   two                 8.5        11.5         11.9         12.8          14.8           14.8           12.8
 constexpr int64_t kSortOneMax = 32 * kSortOneThreads;
+constexpr int64_t kSortOneWork = 20 << 20;
 
 static bool sort_one(int64_t R, int64_t E) { return R <= kSortOneMax && R * (E + 1) <= kSortOneWork; }
 

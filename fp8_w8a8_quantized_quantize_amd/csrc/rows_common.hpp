@@ -1,7 +1,9 @@
 // Device helpers of the kernels around the products (expert rows, epilogues,
-// the activation quantizer): elements of rows at any alignment, and the
-// activation functions.
+// the activation quantizer): elements of rows at any alignment, codes as fp16,
+// the activation functions and the epilogue of four outputs.
 #pragma once
+
+#include <type_traits>
 
 #include "device_common.hpp"
 #include "kernels.hpp"
@@ -146,6 +148,17 @@ __device__ __forceinline__ void store_run(void* base, int64_t e, int n, const fl
         for (int i = 0; i < V; ++i)
             if (i < n) store_elem<DT>(base, e + i, x[i]);
     }
+}
+
+// Eight E4M3 codes (two words) as the fp16 values they are, exactly.
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ v8h half8_of(int lo, int hi) {
+    typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+    const v2h a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+    const v2h b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+    const v2h c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+    const v2h d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+    return v8h{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
 // Activation functions on fp32, each in a form that keeps its relative accuracy in
