@@ -246,6 +246,12 @@ fp8_status_t check_rows(const void* p, int64_t rows, int64_t cols, int64_t ld, i
     return check_matrix(p, rows, cols, ld, elem, true);
 }
 
+// A matrix written in place of one read: the same rows at the same stride, or no
+// element is where it was read.
+bool in_place_ok(const void* in, int64_t ld_in, const void* out, int64_t ld_out, int64_t rows, int64_t cols) {
+    return in != out || ld_in == ld_out || rows <= 1 || cols == 0;
+}
+
 // Extents of the expert-row calls: T tokens of topk choices, R expert rows of H elements.
 fp8_status_t check_choices(int64_t T, int64_t topk, int64_t R, int64_t H) {
     if (T < 0 || topk < 0 || R < 0 || H < 0) return FP8_ERR_INVALID_ARGUMENT;
@@ -260,7 +266,10 @@ fp8_status_t check_epilogue(const fp8k::Epilogue& e, fp8_act_t act, fp8_kv_dtype
     const int64_t eb = kv_elem_bytes(type);
     if (eb == 0) return FP8_ERR_INVALID_ARGUMENT;
     FP8_TRY(check_rows(e.y, M, N, e.ldy, eb));
-    if (e.residual != nullptr) FP8_TRY(check_rows(e.residual, M, N, e.ldr, eb));
+    if (e.residual != nullptr) {
+        FP8_TRY(check_rows(e.residual, M, N, e.ldr, eb));
+        if (!in_place_ok(e.residual, e.ldr, e.y, e.ldy, M, N)) return FP8_ERR_INVALID_ARGUMENT;
+    }
     return e.bias != nullptr ? check_vector(e.bias, bias) : FP8_OK;
 }
 
@@ -718,6 +727,7 @@ fp8_status_t fp8_act_quantize(const void* h, int64_t ldh, fp8_kv_dtype_t dtype, 
     FP8_TRY(check_vector(scales, rows));
     if (live_rows != nullptr) FP8_TRY(check_words(live_rows, 1));
     if (rows == 0) return FP8_OK;
+    if (F > 0 && h == q) return FP8_ERR_INVALID_ARGUMENT;
     return from_hip(fp8k::launch_act_quantize(h, ldh, (int)dtype, rows, F, (int)act, gated != 0, q, ldq, scales,
                                               live_rows, stream));
 }
@@ -760,6 +770,7 @@ fp8_status_t fp8_moe_permute(const void* x, int64_t ldx, const float* s_tok, con
         FP8_TRY(check_vector(s_out, R));
     }
     if (T == 0 || topk == 0 || R == 0 || (H == 0 && s_tok == nullptr)) return FP8_OK;
+    if ((H > 0 && x == out) || (s_tok != nullptr && s_tok == s_out)) return FP8_ERR_INVALID_ARGUMENT;
     return from_hip(fp8k::launch_moe_permute(x, ldx * elem_bytes, s_tok, row_of, T, topk, R, H * elem_bytes, out,
                                              ldo * elem_bytes, s_out, stream));
 }
@@ -777,6 +788,8 @@ fp8_status_t fp8_moe_combine(const void* y, int64_t ldy, fp8_kv_dtype_t y_dtype,
     FP8_TRY(check_vector(row_of, T * topk));
     if (weights != nullptr) FP8_TRY(check_vector(weights, T * topk));
     if (T == 0 || H == 0) return FP8_OK;
+    if ((R > 0 && y == out) || (residual != nullptr && !in_place_ok(residual, ldr, out, ldo, T, H)))
+        return FP8_ERR_INVALID_ARGUMENT;
     fp8k::MoeCombine p = {};
     p.y = y, p.row_of = row_of, p.weights = weights, p.residual = residual, p.out = out;
     p.ldy = ldy, p.ldr = ldr, p.ldo = ldo, p.H = H;
@@ -801,6 +814,9 @@ fp8_status_t fp8_moe_combine_grad(const void* dout, int64_t ldd, fp8_kv_dtype_t 
     FP8_TRY(check_vector(row_of, T * topk));
     if (weights != nullptr) FP8_TRY(check_vector(weights, T * topk));
     if (T == 0 || topk == 0 || (dy == nullptr && dweights == nullptr)) return FP8_OK;
+    if (dy != nullptr && R > 0 && H > 0 &&
+        (dy == dout || (dweights != nullptr && !in_place_ok(y, ldy, dy, lddy, R, H))))
+        return FP8_ERR_INVALID_ARGUMENT;
     fp8k::MoeCombineGrad p = {};
     p.dout = dout, p.y = y, p.row_of = row_of, p.weights = weights, p.dy = dy, p.dweights = dweights;
     p.ldd = ldd, p.ldy = ldy, p.lddy = lddy, p.H = H;

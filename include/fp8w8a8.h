@@ -461,7 +461,8 @@ size_t fp8_attn_prefill_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_
  * fp8_kv_dtype_t; sums are fp32, in the order of the choices, so results do not
  * depend on timing.  Matrices are row-major with any row stride >= the row
  * length; every pointer 16-byte aligned.  T, topk, R, H and T * topk up to
- * 2^31 - 1.
+ * 2^31 - 1.  An output at an input's own address, where that is not allowed below
+ * or has another stride, is FP8_ERR_INVALID_ARGUMENT; other overlaps are not found.
  *
  * fp8_moe_sort: the stable order of the choices by expert.  expert_ids [T, topk]
  * int32, or int64 when ids_64 != 0; an id outside [0, E) (dropped over capacity,
@@ -590,7 +591,8 @@ fp8_status_t fp8_gemm_grouped_scaled_act(const uint8_t* qa, const float* s_tok, 
  * (FP8_ACT_NONE, not gated: fp8_quantize_per_token of bf16, fp16 or fp32 rows).
  * live_rows: one int32 on the device, or NULL: rows from *live_rows on are left
  * as they were (e.g. &expert_offsets[E], past which rows have no expert).
- * F % 16 == 0, rows of h and q 16-byte aligned; h and v are assumed finite.
+ * F % 16 == 0, rows of h and q 16-byte aligned, q and h do not overlap; h and v
+ * are assumed finite.
  * No workspace.
  */
 fp8_status_t fp8_act_quantize(const void* h, int64_t ldh, fp8_kv_dtype_t dtype, int64_t rows, int64_t F, fp8_act_t act,

@@ -136,6 +136,16 @@ def test_act_quantize_refusals(kw, code):
     assert call(QUANT, fp8.lib().fp8_act_quantize, **kw) == code
 
 
+@pytest.mark.parametrize("base,fn,kw", [
+    (PERMUTE, "fp8_moe_permute", dict(out=P)), (PERMUTE, "fp8_moe_permute", dict(s_tok=P, s_out=P)),
+    (COMBINE, "fp8_moe_combine", dict(out=P)), (COMBINE, "fp8_moe_combine", dict(residual=Q, ldr=101)),
+    (GRAD, "fp8_moe_combine_grad", dict(dy=P, dout=P, y=Q)), (GRAD, "fp8_moe_combine_grad", dict(y=Q, ldy=101)),
+    (GEMM, "fp8_gemm_scaled_act", dict(residual=Q, ldr=16)), (QUANT, "fp8_act_quantize", dict(q=P, ldq=64)),
+], ids=str)
+def test_outputs_at_an_inputs_address_are_refused(base, fn, kw):
+    assert call(base, getattr(fp8.lib(), fn), **kw) == BAD
+
+
 def test_binding_takes_device_tensors_only():
     x, i = torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros((4, 2), dtype=torch.int32)
     c, s = torch.zeros((4, 64), dtype=torch.uint8), torch.ones(4)

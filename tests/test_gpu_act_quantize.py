@@ -107,3 +107,16 @@ def test_strides_and_refusals():
             f()
     with pytest.raises(TypeError):
         fp8.fp8_act_quantize(h.double())
+
+
+def test_rows_past_four_gigabytes():
+    rows, F, ld = 3, 1040, (1 << 31) + 48
+    for kind in (BF, F32):
+        log(f"rows 2^31 elements apart, {kind}")
+        h = torch.empty(2 * ld + 2 * F, dtype=kind, device=DEV).as_strided((rows, 2 * F), (ld, 1))
+        h.copy_(randn(1, rows, 2 * F, dtype=kind))
+        q = torch.empty(2 * ld + F, dtype=torch.uint8, device=DEV).as_strided((rows, F), (ld, 1))
+        _, s = fp8.fp8_act_quantize(h, "silu", True, q=q)
+        want_q, want_s = fp8.fp8_act_quantize(h.contiguous(), "silu", True)
+        quantize_ok(h.contiguous(), "silu", True, want_q, want_s, str(kind))
+        assert torch.equal(q, want_q) and torch.equal(s, want_s)

@@ -258,6 +258,18 @@ def test_grad_against_differences():
     assert abs(left - (x.double() * back.double()).sum()) <= bound
 
 
+def test_grad_of_rows_past_four_gigabytes():
+    T, topk, H, ld = 2, 2, 1003, (1 << 30) + 40
+    row_of = torch.tensor([[3, 0], [1, 2]], dtype=torch.int32, device=DEV)
+    dout, y, w = randn(1, T, H, dtype=HF), randn(2, T * topk, H, dtype=HF), randn(3, T, topk)
+    far = torch.empty(3 * ld + H, dtype=HF, device=DEV).as_strided((4, H), (ld, 1))
+    far.copy_(y)
+    log("rows 2^30 elements apart")
+    want_y, want_w = fp8.fp8_moe_combine_grad(dout, y, row_of, w)
+    dy, dw = fp8.fp8_moe_combine_grad(dout, far, row_of, w, dy=far)
+    assert torch.equal(dy, want_y) and torch.equal(dw, want_w)
+
+
 def test_refused_arguments():
     row_of = rows_of(1, 6, 2, 3)
     y, x = randn(1, 12, 32, dtype=BF), randn(2, 6, 32, dtype=BF)

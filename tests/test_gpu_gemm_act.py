@@ -252,3 +252,38 @@ def test_refused_arguments():
               lambda: fp8.fp8_gemm_scaled_act(qa[:, :48], st, qw[:, :48], sc, y=torch.empty((8, 26), device=DEV)[:, 1:25])):
         with pytest.raises(fp8.Fp8Error):
             f()
+
+
+def far(t):
+    """t's rows, 2^31 elements and some apart."""
+    ld = (1 << 31) + 48
+    out = torch.empty((t.shape[0] - 1) * ld + t.shape[1], dtype=t.dtype, device=DEV).as_strided(tuple(t.shape), (ld, 1))
+    return out.copy_(t)
+
+
+@pytest.mark.parametrize("M,N", [(3, 100), (20, 3), (300, 3)])
+def test_rows_past_four_gigabytes(M, N):
+    """Of the weights, and with few rows of the codes, the residual and the output too (which decode, tiles and a split k write)."""
+    K = 4112
+    qa, qw, st, sc, bias = codes(1, M, K), codes(2, N, K), scales(3, M), scales(4, N, K), randn(5, N)
+    for dtype in (BF, F32):
+        log(f"far rows {M} {N} {dtype}")
+        res = randn(6, M, N, dtype=dtype)
+        want = fp8.fp8_gemm_scaled_act(qa, st, qw, sc, bias=bias, act="gelu", residual=res)
+        if M == 3:
+            got = fp8.fp8_gemm_scaled_act(far(qa), st, qw, sc, bias=bias, act="gelu", residual=far(res), y=far(torch.zeros_like(res)))
+        else:
+            got = fp8.fp8_gemm_scaled_act(qa, st, far(qw), sc, bias=bias, act="gelu", residual=res)
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("M", [17, 30])
+def test_outputs_past_four_gigabytes(M):
+    N, K, ld = 40, 1040, (1 << 28) + 16
+    qa, qw, st, sc = codes(1, M, K), codes(2, N, K), scales(3, M), scales(4, N, K)
+    res = randn(6, M, N, dtype=BF)
+    log(f"rows 2^28 elements apart, {M}")
+    want = fp8.fp8_gemm_scaled_act(qa, st, qw, sc, act="silu", residual=res)
+    y = torch.empty((M - 1) * ld + N, dtype=BF, device=DEV).as_strided((M, N), (ld, 1))
+    y.copy_(res)
+    assert torch.equal(fp8.fp8_gemm_scaled_act(qa, st, qw, sc, act="silu", residual=y, y=y), want)
