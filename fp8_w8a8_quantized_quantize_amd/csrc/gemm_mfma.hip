@@ -106,11 +106,12 @@ __device__ __forceinline__ void dma16(const uint8_t* src, uint8_t* lds) {
     __builtin_amdgcn_global_load_lds(src, lds, 16, 0, 0);
 }
 
-// s_waitcnt lgkmcnt(0): this wave's LDS reads have completed.
-__device__ __forceinline__ void wait_lds_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-
+// The workgroup's barrier, this wave's LDS reads and writes having completed before it:
+// s_barrier itself waits for no memory operation and the compiler puts no wait before
+// the builtin, and the LDS requests of different waves have no order of their own.
+// DMA stays in flight across it (wait_dma).
 __device__ __forceinline__ void block_barrier() {
-    compiler_fence();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     compiler_fence();
 }
@@ -574,8 +575,7 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
             } else {
                 wait_dma<PER_STAGE>(NS - 2);
             }
-            wait_lds_reads();        // ... and its reads of stage s are done
-            block_barrier();
+            block_barrier();  // ... and its reads of stage s are done
             read_scales(nxt, nx_a, nx_b);
 #pragma unroll
             for (int a = 0; a < FN; ++a) {
@@ -609,7 +609,6 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
             interleave_mfma_reads<FN * FA, 2 * (FN + FA)>();
             if (more) {
                 wait_dma<PER_STAGE>(NS == 2 ? 0 : min(NS - 2, KT - 2 - s));
-                wait_lds_reads();
                 block_barrier();
                 read_scales(next_slot(s, cur), nx_a, nx_b);
             }
@@ -668,7 +667,6 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
         const int left = p.N - own;
         auto run_pass = [&](auto pass_number) {
             constexpr int pass = decltype(pass_number)::value;
-            wait_lds_reads();
             block_barrier();
 #pragma unroll
             for (int b = pass * FP; b < (pass + 1) * FP; ++b) {
@@ -832,7 +830,6 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
             return;
         }
     }
-    wait_lds_reads();
     block_barrier();
     uint8_t* ct = smem;
     constexpr int CH = BN / 8;  // 16-byte chunks per tile row
