@@ -795,6 +795,8 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
     // written out with 16-byte row-contiguous stores.
     // Accumulator layout of a 32x32 MFMA tile: lane l holds activation row
     // l % 32 and weight columns 8 * (v / 4) + 4 * (l / 32) + v % 4, v = 0..15.
+    // The K loop's barriers do not stand between the tile scales and here when there is no K.
+    block_barrier();
     if constexpr (!GROUPED) {
         if (p.y32 != nullptr) {
             // fp32 output straight from the accumulators: lane l holds 4
@@ -830,7 +832,6 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
             return;
         }
     }
-    block_barrier();
     uint8_t* ct = smem;
     constexpr int CH = BN / 8;  // 16-byte chunks per tile row
 #pragma unroll

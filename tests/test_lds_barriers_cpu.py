@@ -84,6 +84,29 @@ def barriers_with_writes(body):
     return barriers, bad
 
 
+def stores_before_a_barrier(body):
+    """Global stores that some path reaches without a barrier before them."""
+    index, base = {a: i for i, (a, _, _) in enumerate(body)}, body[0][0]
+    seen, bad, todo = set(), [], [0]
+    while todo:
+        i = todo.pop()
+        while i < len(body) and i not in seen:
+            seen.add(i)
+            addr, op, rest = body[i]
+            if op.startswith("global_store"):
+                bad.append(addr)
+            if op in ("s_barrier", "s_endpgm"):
+                break
+            if op.startswith(("s_cbranch", "s_branch")):
+                j = index[base + int(re.search(r"<\S+?(?:\+0x([0-9a-f]+))?>\s*$", rest).group(1) or "0", 16)]
+                if op == "s_branch":
+                    i = j
+                    continue
+                todo.append(j)
+            i += 1
+    return bad
+
+
 @pytest.fixture(scope="module")
 def functions():
     fp8.lib()
@@ -104,6 +127,15 @@ def test_no_lds_write_under_way_at_a_barrier(functions):
         if wrong:
             bad[name] = [hex(a) for a in sorted(wrong)]
     assert found > 100, "barriers in the disassembly"
+    assert not bad, f"{len(bad)} kernels: {dict(list(bad.items())[:4])}"
+
+
+def test_products_store_behind_a_barrier(functions):
+    """A product's outputs need scales that other waves put into LDS, so no path to a store is without a barrier -- that
+    of an empty K, which no step of the K loop lies on, included."""
+    products = [(name, body) for name, body in functions if "gemm_mfma_kernel" in name]
+    assert len(products) > 20
+    bad = {name: [hex(a) for a in at] for name, at in ((n, stores_before_a_barrier(b)) for n, b in products) if at}
     assert not bad, f"{len(bad)} kernels: {dict(list(bad.items())[:4])}"
 
 
