@@ -226,8 +226,9 @@ __device__ __forceinline__ float gelu(float x) {
         p = __builtin_fmaf(p, t, 0.12386069446802139f);
         e = __builtin_amdgcn_exp2f(s * (-0.5f * kLog2e));
     }
+    // the minimum: phi is 0 at +inf, and inf - inf 0 would be NaN
     const float phi = p * t * e;
-    return x < 0.0f ? x * phi : __builtin_fmaf(-x, phi, x);
+    return x < 0.0f ? x * phi : __builtin_fmaf(-fminf(x, 3.40282347e38f), phi, x);
 }
 
 template <bool FINE>
