@@ -8,9 +8,11 @@
 // rounded to 16 bits.  A row is read once: its values stay in registers between
 // the maximum and the cast.  WPR waves share a row; one wave per row needs no
 // LDS and no barrier, and takes over as soon as there are rows enough.  Memory bounds
-// many rows (32768 x 2048 gated bf16: 61 us, 5.3 TB/s, with the vector unit busy 55 %
-// of the cycles), the vector unit of the few compute units in use few long ones (64 x
-// 28672: 6.3 us for 9 MB).
+// many rows (32768 x 2048 gated bf16, silu: 60 us, 5.5 TB/s), the vector unit gelu on
+// 16-bit rows (74 us) and the few compute units in use few long ones (64 x 28672, silu:
+// 7.1 us for 9 MB).  The activation is that of fp32 outputs, for the scales are fp32 and
+// a value's error moves codes across their borders; with that of 16-bit outputs these
+// three took 61, 64 and 6.2 us, and gelu's scales were 4.7e-6 off.
 #include <type_traits>
 
 #include "rows_common.hpp"
@@ -40,7 +42,7 @@ template <int DT, bool GATED, int ACT>
 __device__ __forceinline__ void value_of(const Raw<GATED>& r, float (&v)[piece<DT>()]) {
     constexpr int V = piece<DT>();
     unpack<DT, V>(r.g, v);
-    activate<false, V>(v, ACT);
+    activate<true, V>(v, ACT);
     if constexpr (GATED) {
         float u[V];
         unpack<DT, V>(r.u, u);

@@ -167,11 +167,10 @@ __device__ __forceinline__ v8h half8_of(int lo, int hi) {
 //   gelu(x)      = x Phi(x), Phi(-a) = erfc(a / sqrt 2) / 2 and Phi(a) = 1 - Phi(-a) for a >= 0
 //   gelu_tanh(x) = x / (1 + e^-2u), u = sqrt(2 / pi) (x + 0.044715 x^3):
 //                  the same as x (1 + tanh u) / 2.
-// FINE, for fp32 outputs: within a few units of 2^-24 (gelu 5e-7).  Otherwise, for
-// outputs of 16 bits or 8, which round by 2^-12 or more themselves: an exponent's
-// argument t costs |t| 2^-23 and gelu's fit 4.7e-6, for half the instructions (the
-// activation quantizer is bound by them as much as by its bytes, and the products'
-// epilogues run while the matrix units wait).
+// FINE, for fp32 outputs (the activation quantizer's scales among them): within a few
+// units of 2^-24 (gelu 5e-7).  Otherwise, for the products' 16-bit outputs, which round
+// by 2^-12 or more themselves: an exponent's argument t costs |t| 2^-23 and gelu's fit
+// 4.7e-6, for half the instructions (the epilogues run while the matrix units wait).
 
 // 1 / x, to one step of fp32; 0 for inf.
 __device__ __forceinline__ float fast_recip(float x) { return __builtin_amdgcn_rcpf(x); }

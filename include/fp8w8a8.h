@@ -528,7 +528,8 @@ fp8_status_t fp8_moe_combine_grad(const void* dout, int64_t ldd, fp8_kv_dtype_t 
 
 /*
  * Activations, evaluated in fp32: to a few units of 2^-24 of their value for fp32
- * outputs, and for 16-bit and FP8 ones to 2^-17 and |x| 2^-22 (GELU_TANH: |u| 2^-21):
+ * outputs and by fp8_act_quantize, and for the products' 16-bit outputs to 2^-17 and
+ * |x| 2^-22 (GELU_TANH: |u| 2^-21):
  *   NONE x   RELU max(x, 0)   SILU x / (1 + e^-x)   GELU x Phi(x) = x (1 + erf(x / sqrt 2)) / 2
  *   GELU_TANH x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2
  * Infinite x as the formulas have it: +inf gives +inf; -inf gives 0 for RELU and
