@@ -162,7 +162,8 @@ __device__ __forceinline__ v8h half8_of(int lo, int hi) {
 }
 
 // Activation functions on fp32, each in a form that keeps its relative accuracy in
-// the tails (no 1 - x of nearly equal values):
+// the tails (no 1 - x of nearly equal values) down to 2^-126 (|x| + 1): there the
+// hardware's 2^t and reciprocal are past their range and give 0:
 //   silu(x)      = x / (1 + e^-x)
 //   gelu(x)      = x Phi(x), Phi(-a) = erfc(a / sqrt 2) / 2 and Phi(a) = 1 - Phi(-a) for a >= 0
 //   gelu_tanh(x) = x / (1 + e^-2u), u = sqrt(2 / pi) (x + 0.044715 x^3):

@@ -532,6 +532,7 @@ fp8_status_t fp8_moe_combine_grad(const void* dout, int64_t ldd, fp8_kv_dtype_t 
  * |x| 2^-22 (GELU_TANH: |u| 2^-21):
  *   NONE x   RELU max(x, 0)   SILU x / (1 + e^-x)   GELU x Phi(x) = x (1 + erf(x / sqrt 2)) / 2
  *   GELU_TANH x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2
+ * A value of less than 2^-126 (|x| + 1) may come out as 0 (silu(-88) is -5.3e-37).
  * Infinite x as the formulas have it: +inf gives +inf; -inf gives 0 for RELU and
  * NaN (-inf * 0) for the last three.  NaN gives NaN.
  */
