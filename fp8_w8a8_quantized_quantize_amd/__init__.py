@@ -952,11 +952,17 @@ def fp8_gemm_act_workspace_bytes(M, N, K):
     return int(lib().fp8_gemm_act_workspace_bytes(M, N, K))
 
 
-def _y_type(y, y_dtype, residual):
-    """The output's type: y's, else y_dtype, else the residual's, else bfloat16."""
-    if y is not None:
-        return y.dtype
-    return y_dtype or (residual.dtype if residual is not None else _torch().bfloat16)
+def _out_type(out, dtype, like, name):
+    """The type of an output: its own, which a dtype given beside it has to be, else dtype, else that of the tensor
+    `like`, else bfloat16."""
+    for t, n in ((out, name), (like, "residual")):
+        if t is not None and not isinstance(t, _tensor()):
+            raise TypeError(f"{n}: expected a CUDA tensor")
+    if out is None:
+        return dtype or (like.dtype if like is not None else _torch().bfloat16)
+    if dtype is not None and dtype is not out.dtype:
+        raise TypeError(f"{name}: of {out.dtype}, expected {name}_dtype {dtype}")
+    return out.dtype
 
 
 @_on_stream
@@ -966,7 +972,7 @@ def fp8_gemm_scaled_act(qa, s_tok, qw, s_ch, bias=None, act="none", residual=Non
     bias: fp32 [N] or None.  act: 'none', 'relu', 'silu', 'gelu' (erf) or 'gelu_tanh'.
     residual: [M, N] in y's type or None; it may be y itself.  y: [M, N] float32,
     bfloat16 or float16 with any row stride; allocated when not given, in y_dtype
-    (by default the residual's type, else bfloat16).  ws: uint8 workspace of at least
+    (by default the residual's type, else bfloat16; of a y given, its own type).  ws: uint8 workspace of at least
     fp8_gemm_act_workspace_bytes(M, N, K) bytes, allocated when not given.
     stream: the stream to run on."""
     torch = _torch()
@@ -975,7 +981,7 @@ def fp8_gemm_scaled_act(qa, s_tok, qw, s_ch, bias=None, act="none", residual=Non
     N, _, ldw, wp = _mat(qw, "qw", di, u8, cols=K)
     tp, cp = _flat(s_tok, f32, "s_tok", M, di), _flat(s_ch, f32, "s_ch", N, di)
     bp = 0 if bias is None else _flat(bias, f32, "bias", N, di)
-    dtype = _y_type(y, y_dtype, residual)
+    dtype = _out_type(y, y_dtype, residual, "y")
     code = _dtype_code(dtype, "y")
     if y is None:
         y = qa.new_empty((M, N), dtype=dtype)
@@ -1017,7 +1023,7 @@ def fp8_gemm_grouped_scaled_act(qa, s_tok, row_token, expert_offsets, qw, s_ch, 
     op = _flat(expert_offsets, i32, "expert_offsets", E + 1, di)
     cp = _flat(s_ch, f32, "s_ch", E * N, di)
     bp = 0 if bias is None else _flat(bias, f32, "bias", E * N, di)
-    dtype = _y_type(y, y_dtype, None)
+    dtype = _out_type(y, y_dtype, None, "y")
     code = _dtype_code(dtype, "y")
     if y is None:
         y = qa.new_empty((R, N), dtype=dtype)
@@ -1146,15 +1152,15 @@ def fp8_moe_combine(y, row_of, weights=None, residual=None, out=None, out_dtype=
     """out[t] = round(residual[t] + sum_j weights[t, j] * y[row_of[t, j]]): the experts' rows
     y [R, H] back to the tokens, weights fp32 [T, topk] (None: ones), residual [T, H] in
     out's type (None: nothing; it may be out itself) -> out [T, H].  Entries of row_of
-    int32 [T, topk] outside [0, R) add nothing.  out_dtype: the residual's type by
-    default, else y's."""
+    int32 [T, topk] outside [0, R) add nothing.  out_dtype: of an out given, its own;
+    else by default the residual's type, else y's."""
     torch = _torch()
     di = y.get_device()
     code = _dtype_code(y.dtype, "y")
     T, topk, rp = _choices(row_of, di)
     R, H, ldy, yp = _mat(y, "y", di)
     wp = 0 if weights is None else _flat(weights, torch.float32, "weights", T * topk, di)
-    dtype = out.dtype if out is not None else out_dtype or (y if residual is None else residual).dtype
+    dtype = _out_type(out, out_dtype, y if residual is None else residual, "out")
     out_code = _dtype_code(dtype, "out")
     if out is None:
         out = y.new_empty((T, H), dtype=dtype)
