@@ -12,6 +12,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "act_plan.hpp"
 #include "attn_plan.hpp"
@@ -250,6 +251,11 @@ fp8_status_t check_rows(const void* p, int64_t rows, int64_t cols, int64_t ld, i
 // element is where it was read.
 bool in_place_ok(const void* in, int64_t ld_in, const void* out, int64_t ld_out, int64_t rows, int64_t cols) {
     return in != out || ld_in == ld_out || rows <= 1 || cols == 0;
+}
+
+// Whether an output is at the address of one of these inputs (or outputs).
+bool at_any(const void* out, std::initializer_list<const void*> others) {
+    return out != nullptr && std::find(others.begin(), others.end(), out) != others.end();
 }
 
 // Extents of the expert-row calls: T tokens of topk choices, R expert rows of H elements.
@@ -685,6 +691,7 @@ fp8_status_t fp8_gemm_scaled_act(const uint8_t* qa, int64_t lda, const float* s_
     if (need > 0 && ws == nullptr) return FP8_ERR_INVALID_ARGUMENT;
     if (need > 0 && !aligned16(ws)) return FP8_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return FP8_OK;
+    if (at_any(y, {qa, s_tok, qw, s_ch, bias})) return FP8_ERR_INVALID_ARGUMENT;
     if (fp8k::skinny_act(M, N))
         return from_hip(fp8k::launch_gemm_skinny_act(qa, lda, s_tok, qw, ldw, s_ch, epi, M, N, K, stream));
     return from_hip(fp8k::launch_gemm_mfma_act(qa, lda, s_tok, qw, ldw, s_ch, epi, M, N, K, ws, stream));
@@ -711,6 +718,7 @@ fp8_status_t fp8_gemm_grouped_scaled_act(const uint8_t* qa, const float* s_tok, 
     FP8_TRY(check_epilogue(epi, act, y_dtype, E * N, R, N));
     if (ws_bytes < fp8_grouped_workspace_bytes(T, R, E, N, K)) return FP8_ERR_WORKSPACE;
     if (R == 0 || N == 0) return FP8_OK;
+    if (at_any(y, {qa, s_tok, row_token, expert_offsets, qw, s_ch, bias})) return FP8_ERR_INVALID_ARGUMENT;
     return from_hip(fp8k::launch_gemm_grouped_mfma_act(qa, s_tok, row_token, expert_offsets, qw, s_ch, epi, T, R, E, N, K,
                                                        stream));
 }
@@ -727,7 +735,8 @@ fp8_status_t fp8_act_quantize(const void* h, int64_t ldh, fp8_kv_dtype_t dtype, 
     FP8_TRY(check_vector(scales, rows));
     if (live_rows != nullptr) FP8_TRY(check_words(live_rows, 1));
     if (rows == 0) return FP8_OK;
-    if (F > 0 && h == q) return FP8_ERR_INVALID_ARGUMENT;
+    if ((F > 0 && at_any(q, {h, live_rows, scales})) || at_any(scales, {F > 0 ? h : nullptr, live_rows}))
+        return FP8_ERR_INVALID_ARGUMENT;
     return from_hip(fp8k::launch_act_quantize(h, ldh, (int)dtype, rows, F, (int)act, gated != 0, q, ldq, scales,
                                               live_rows, stream));
 }
@@ -752,6 +761,9 @@ fp8_status_t fp8_moe_sort(const void* expert_ids, int32_t ids_64, int64_t T, int
     if (ws_bytes < need) return FP8_ERR_WORKSPACE;
     if (need > 0 && ws == nullptr) return FP8_ERR_INVALID_ARGUMENT;
     if (need > 0 && !aligned16(ws)) return FP8_ERR_UNSUPPORTED;
+    if (R > 0 && (at_any(expert_offsets, {expert_ids, row_token, row_of}) || at_any(row_token, {expert_ids, row_of}) ||
+                  row_of == expert_ids))
+        return FP8_ERR_INVALID_ARGUMENT;
     return from_hip(fp8k::launch_moe_sort(expert_ids, ids_64 != 0, R, topk, E, expert_offsets, row_token, row_of, ws,
                                           stream));
 }
@@ -770,7 +782,8 @@ fp8_status_t fp8_moe_permute(const void* x, int64_t ldx, const float* s_tok, con
         FP8_TRY(check_vector(s_out, R));
     }
     if (T == 0 || topk == 0 || R == 0 || (H == 0 && s_tok == nullptr)) return FP8_OK;
-    if ((H > 0 && x == out) || (s_tok != nullptr && s_tok == s_out)) return FP8_ERR_INVALID_ARGUMENT;
+    if ((H > 0 && at_any(out, {x, row_of, s_tok, s_out})) || at_any(s_out, {H > 0 ? x : nullptr, row_of, s_tok}))
+        return FP8_ERR_INVALID_ARGUMENT;
     return from_hip(fp8k::launch_moe_permute(x, ldx * elem_bytes, s_tok, row_of, T, topk, R, H * elem_bytes, out,
                                              ldo * elem_bytes, s_out, stream));
 }
@@ -788,7 +801,8 @@ fp8_status_t fp8_moe_combine(const void* y, int64_t ldy, fp8_kv_dtype_t y_dtype,
     FP8_TRY(check_vector(row_of, T * topk));
     if (weights != nullptr) FP8_TRY(check_vector(weights, T * topk));
     if (T == 0 || H == 0) return FP8_OK;
-    if ((R > 0 && y == out) || (residual != nullptr && !in_place_ok(residual, ldr, out, ldo, T, H)))
+    if (at_any(out, {R > 0 ? y : nullptr, topk > 0 ? row_of : nullptr, topk > 0 ? weights : nullptr}) ||
+        (residual != nullptr && !in_place_ok(residual, ldr, out, ldo, T, H)))
         return FP8_ERR_INVALID_ARGUMENT;
     fp8k::MoeCombine p = {};
     p.y = y, p.row_of = row_of, p.weights = weights, p.residual = residual, p.out = out;
@@ -814,9 +828,10 @@ fp8_status_t fp8_moe_combine_grad(const void* dout, int64_t ldd, fp8_kv_dtype_t 
     FP8_TRY(check_vector(row_of, T * topk));
     if (weights != nullptr) FP8_TRY(check_vector(weights, T * topk));
     if (T == 0 || topk == 0 || (dy == nullptr && dweights == nullptr)) return FP8_OK;
-    if (dy != nullptr && R > 0 && H > 0 &&
-        (dy == dout || (dweights != nullptr && !in_place_ok(y, ldy, dy, lddy, R, H))))
+    if (R > 0 && H > 0 && (at_any(dy, {dout, row_of, weights, dweights}) || at_any(dweights, {dout, y}) ||
+                           (dy != nullptr && dweights != nullptr && !in_place_ok(y, ldy, dy, lddy, R, H))))
         return FP8_ERR_INVALID_ARGUMENT;
+    if (at_any(dweights, {row_of, weights})) return FP8_ERR_INVALID_ARGUMENT;
     fp8k::MoeCombineGrad p = {};
     p.dout = dout, p.y = y, p.row_of = row_of, p.weights = weights, p.dy = dy, p.dweights = dweights;
     p.ldd = ldd, p.ldy = ldy, p.lddy = lddy, p.H = H;

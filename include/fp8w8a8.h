@@ -461,8 +461,9 @@ size_t fp8_attn_prefill_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_
  * fp8_kv_dtype_t; sums are fp32, in the order of the choices, so results do not
  * depend on timing.  Matrices are row-major with any row stride >= the row
  * length; every pointer 16-byte aligned.  T, topk, R, H and T * topk up to
- * 2^31 - 1.  An output at an input's own address, where that is not allowed below
- * or has another stride, is FP8_ERR_INVALID_ARGUMENT; other overlaps are not found.
+ * 2^31 - 1.  An output at the address of an input, where that is not allowed below
+ * or has another stride, or of another output is FP8_ERR_INVALID_ARGUMENT; other
+ * overlaps are not found.
  *
  * fp8_moe_sort: the stable order of the choices by expert.  expert_ids [T, topk]
  * int32, or int64 when ids_64 != 0; an id outside [0, E) (dropped over capacity,
@@ -554,13 +555,14 @@ typedef enum {
  * fp32 y is what fp8_quantize_per_token takes next.  bias fp32 [N] and residual
  * [M, N] (row stride ldr >= N) may be NULL; residual may be y itself (same
  * pointer and stride), else it does not overlap y.  y [M, N], any row stride
- * ldy >= N.  For an fp32 y the products are summed to fp32's own precision (fp16
- * matrix instructions, at half the rate); for 16-bit ones as fp8_gemm_scaled does,
- * whose instructions leave 1e-5 of a sum's norm, far below the rounding.  An output
- * of more than 2^24 - 9 tiles of 128 x 128 (grouped: as for
- * fp8_gemm_grouped_scaled) is FP8_ERR_UNSUPPORTED.  ws: at least
- * fp8_gemm_act_workspace_bytes(M, N, K) bytes, 16-byte aligned (sums of a split K,
- * added in a fixed order; may be NULL when that is 0).
+ * ldy >= N; at the address of another input: FP8_ERR_INVALID_ARGUMENT.  For an fp32
+ * y the products are summed to fp32's own precision (fp16 matrix instructions, at
+ * half the rate); for 16-bit ones as fp8_gemm_scaled does, whose instructions leave
+ * 1e-5 of a sum's norm, far below the rounding.  An output of more than 2^24 - 9
+ * tiles of 128 x 128 (grouped: as for fp8_gemm_grouped_scaled) is
+ * FP8_ERR_UNSUPPORTED.  ws: at least fp8_gemm_act_workspace_bytes(M, N, K) bytes,
+ * 16-byte aligned (sums of a split K, added in a fixed order; may be NULL when that
+ * is 0).
  */
 fp8_status_t fp8_gemm_scaled_act(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw, int64_t ldw,
                                  const float* s_ch, const float* bias, fp8_act_t act, const void* residual, int64_t ldr,
@@ -595,8 +597,8 @@ fp8_status_t fp8_gemm_grouped_scaled_act(const uint8_t* qa, const float* s_tok, 
  * (FP8_ACT_NONE, not gated: fp8_quantize_per_token of bf16, fp16 or fp32 rows).
  * live_rows: one int32 on the device, or NULL: rows from *live_rows on are left
  * as they were (e.g. &expert_offsets[E], past which rows have no expert).
- * F % 16 == 0, rows of h and q 16-byte aligned, q and h do not overlap; h and v
- * are assumed finite.
+ * F % 16 == 0, rows of h and q 16-byte aligned; neither output overlaps an input
+ * (at the address of one: FP8_ERR_INVALID_ARGUMENT); h and v are assumed finite.
  * No workspace.
  */
 fp8_status_t fp8_act_quantize(const void* h, int64_t ldh, fp8_kv_dtype_t dtype, int64_t rows, int64_t F, fp8_act_t act,
