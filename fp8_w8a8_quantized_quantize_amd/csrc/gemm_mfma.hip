@@ -83,7 +83,7 @@ __device__ __forceinline__ int dswz(int row) { return (row ^ (row >> 3)) & 7; }
 
 __device__ __forceinline__ void compiler_fence() { asm volatile("" ::: "memory"); }
 
-// s_waitcnt vmcnt(n) for n = PER_STAGE * outstanding stages (n <= 63; at most 7 stages).
+// s_waitcnt vmcnt(n) for n = PER_STAGE * outstanding stages (n <= 63; at most 3 stages).
 template <int PER_STAGE>
 __device__ __forceinline__ void wait_dma(int outstanding_stages) {
     compiler_fence();
@@ -91,11 +91,7 @@ __device__ __forceinline__ void wait_dma(int outstanding_stages) {
         case 0: asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); break;
         case 1: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PER_STAGE) : "memory"); break;
         case 2: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * PER_STAGE) : "memory"); break;
-        case 3: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * PER_STAGE) : "memory"); break;
-        case 4: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * PER_STAGE) : "memory"); break;
-        case 5: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(5 * PER_STAGE) : "memory"); break;
-        case 6: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(6 * PER_STAGE) : "memory"); break;
-        default: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(7 * PER_STAGE) : "memory"); break;
+        default: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * PER_STAGE) : "memory"); break;
     }
     compiler_fence();
 }
@@ -244,7 +240,7 @@ __device__ void find_expert_tile(const MfmaArgs& p, int b, int* sh) {
 // lane of a scale DMA touch its own cache line (measured: 23 % slower on
 // 8192^3).
 // SKIP (dense): compile the K loop for 1-4 live activation fragments, as the
-// grouped kernel always does; the launcher takes it only when the whole grid
+// plain grouped kernel does; the launcher takes it only when the whole grid
 // is one row of tiles with at most 192 real rows (M in 65..192), because the
 // extra instantiations cost the full-tile loop about 1 % (measured on 8192^3).
 // ACT: the tile leaves through an Epilogue (bias, activation, residual, output
@@ -269,7 +265,7 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
     constexpr int STAGE = (BN + BM) * kBK;
     constexpr int SRING = NS * STAGE + 4 * (BN + BM);    // block-scale ring: 2 x (BN + BM) words
     static_assert(DA * 8 * NW == BN && DB * 8 * NW == BM, "whole DMA instructions per wave");
-    static_assert((NS & (NS - 1)) == 0 && NS <= 8 && (NS - 1) * PER_STAGE <= 63, "ring slots by mask, vmcnt field");
+    static_assert((NS & (NS - 1)) == 0 && NS <= 4 && (NS - 1) * PER_STAGE <= 63, "ring slots by mask, vmcnt field");
     static_assert(!MX || NS == 2, "block scales have a ring of two");
     static_assert(!MX || DS * 64 * NW == BN + BM, "whole scale DMA instructions per wave");
     static_assert(BM * BN * 2 <= 2 * STAGE, "the BF16 output tile must fit in the ring");
@@ -903,14 +899,14 @@ hipError_t launch_gemm_mfma(const uint8_t* qa, int64_t lda, const float* s_tok, 
 }
 
 // Dense products with an epilogue.
-template <int BN, int BM, int NS, bool SKIP, bool TAIL, bool HALF>
+template <int BN, int BM, int NS, bool TAIL, bool HALF>
 static hipError_t launch_dense_act(MfmaArgs p, int splits, hipStream_t stream) {
     constexpr int LDS = NS * (BN + BM) * kBK + 4 * (BN + BM) + 4 * BN;  // ring + tile scales + bias
     p.tiles_m = (p.M - 1) / BM + 1;
     p.tiles_n = (p.N - 1) / BN + 1;
-    const hipError_t e = FP8K_SET_LDS((gemm_mfma_kernel<BN, BM, 2, 2, 4, false, false, SKIP, true, TAIL, HALF, NS>), LDS);
+    const hipError_t e = FP8K_SET_LDS((gemm_mfma_kernel<BN, BM, 2, 2, 4, false, false, false, true, TAIL, HALF, NS>), LDS);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((gemm_mfma_kernel<BN, BM, 2, 2, 4, false, false, SKIP, true, TAIL, HALF, NS>),
+    hipLaunchKernelGGL((gemm_mfma_kernel<BN, BM, 2, 2, 4, false, false, false, true, TAIL, HALF, NS>),
                        dim3((unsigned)p.tiles_m * (unsigned)p.tiles_n, 1, (unsigned)splits), dim3(256), LDS, stream, p);
     return hipGetLastError();
 }
@@ -954,15 +950,15 @@ template <bool TAIL>
 static hipError_t launch_dense_tail(const MfmaArgs& p, const ActPlan& plan, hipStream_t stream) {
     const int s = plan.splits;
     if (p.epi.type == kKvF32) {
-        if (plan.tile == 128) return launch_dense_act<128, 128, 2, false, TAIL, true>(p, s, stream);
-        if (plan.stages == 4) return launch_dense_act<64, 64, 4, false, TAIL, true>(p, s, stream);
-        return launch_dense_act<64, 64, 2, false, TAIL, true>(p, s, stream);
+        if (plan.tile == 128) return launch_dense_act<128, 128, 2, TAIL, true>(p, s, stream);
+        if (plan.stages == 4) return launch_dense_act<64, 64, 4, TAIL, true>(p, s, stream);
+        return launch_dense_act<64, 64, 2, TAIL, true>(p, s, stream);
     }
-    if (plan.tile == 256) return launch_dense_act<256, 256, 2, false, TAIL, false>(p, s, stream);
-    if (plan.tile == 128 && plan.stages == 4) return launch_dense_act<128, 128, 4, false, TAIL, false>(p, s, stream);
-    if (plan.tile == 128) return launch_dense_act<128, 128, 2, false, TAIL, false>(p, s, stream);
-    if (plan.stages == 4) return launch_dense_act<64, 64, 4, false, TAIL, false>(p, s, stream);
-    return launch_dense_act<64, 64, 2, false, TAIL, false>(p, s, stream);
+    if (plan.tile == 256) return launch_dense_act<256, 256, 2, TAIL, false>(p, s, stream);
+    if (plan.tile == 128 && plan.stages == 4) return launch_dense_act<128, 128, 4, TAIL, false>(p, s, stream);
+    if (plan.tile == 128) return launch_dense_act<128, 128, 2, TAIL, false>(p, s, stream);
+    if (plan.stages == 4) return launch_dense_act<64, 64, 4, TAIL, false>(p, s, stream);
+    return launch_dense_act<64, 64, 2, TAIL, false>(p, s, stream);
 }
 
 hipError_t launch_gemm_mfma_act(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw, int64_t ldw,
