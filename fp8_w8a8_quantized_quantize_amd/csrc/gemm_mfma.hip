@@ -70,7 +70,8 @@ __device__ __forceinline__ v16f mfma_32x32x64_e4m3_mx(const v8i& a, const v8i& b
 // and keep about 14 bits below its leading one, whatever the accumulator holds
 // (measured), which leaves sums of normal data off by 1e-5 of their norm; the
 // fp16 ones keep fp32's.  Half the rate, for fp32 outputs alone: 16-bit ones
-// round by 2^-9 or 2^-12 themselves.
+// round by 2^-9 or 2^-12 themselves, which is more wherever the sum is at least 1/200
+// (bf16) or 1/25 (fp16) of the norm.
 __device__ __forceinline__ v16f mfma_32x32x64_half(const v8i& a, const v8i& b, v16f c) {
 #pragma unroll
     for (int t = 0; t < 4; ++t)

@@ -28,9 +28,13 @@ namespace fp8k {
 // would wait for loads that are meant to stay in flight).
 __device__ __forceinline__ void issue_order_fence() { __builtin_amdgcn_sched_barrier(0); }
 
-// The 128-k product in fp16, for fp32 outputs: the FP8 instruction keeps about 14
-// bits below the largest of 8 neighbouring products (measured; sums off by 1e-5
-// of their norm), the fp16 ones fp32's.  The weights' stream hides the rest.
+// The 128-k product in fp16, for products with an epilogue: the FP8 instruction keeps
+// about 14 bits below the largest of 8 neighbouring products (measured; sums off by
+// 1e-5 of their norm), the fp16 ones fp32's.  The weights' stream hides nearly all of
+// the conversions and the half rate: bf16 outputs, us, FP8 against fp16 with the
+// activation of fp32 outputs, 8 x 14336 x 4096 15.5 and 15.9 (weights in cache 12.4 and
+// 12.9), 16 x 14336 x 4096 15.7 and 16.1, 8 x 28672 x 8192 48.7 and 49.6, 8 x 8192 x
+// 28672 45.9 and 46.5.
 __device__ __forceinline__ v4f mfma_16x16x128_half(const v8i& a, const v8i& b, v4f c) {
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -55,9 +59,9 @@ __device__ __forceinline__ v4f mfma_16x16x128_half(const v8i& a, const v8i& b, v
 // (measured on gfx950), so each lane passes byte g of its row's chunk word.
 // K must be a multiple of 128.
 //
-// ACT: the sums leave through an Epilogue (bias, activation, residual, output
-// type) instead of y; HALF: products in fp16.
-template <int MT, int NT, int KW, int DEPTH, bool MX, bool ACT = false, bool HALF = false>
+// ACT: products in fp16, whose sums leave through an Epilogue (bias, activation,
+// residual, output type) instead of y.
+template <int MT, int NT, int KW, int DEPTH, bool MX, bool ACT = false>
 __global__ __launch_bounds__(KW * 64) void gemm_skinny_kernel(
     const uint8_t* __restrict__ qa, int64_t lda, const float* __restrict__ s_tok,
     const uint8_t* __restrict__ qw, int64_t ldw, const float* __restrict__ s_ch,
@@ -179,7 +183,7 @@ __global__ __launch_bounds__(KW * 64) void gemm_skinny_kernel(
                             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                                 a, xf[i], acc[i][j], 0, 0, 0, (int)((wsc[d % SD][j] >> (8 * g)) & 0xFFu), 0,
                                 (int)((xsc[d % SD][i] >> (8 * g)) & 0xFFu));
-                        else if constexpr (HALF)
+                        else if constexpr (ACT)
                             acc[i][j] = mfma_16x16x128_half(a, xf[i], acc[i][j]);
                         else
                             acc[i][j] = mfma_16x16x128_e4m3(a, xf[i], acc[i][j]);
@@ -479,7 +483,7 @@ __global__ __launch_bounds__(256) void skinny_splitk_reduce(const float* __restr
     }
 }
 
-template <int MT, int NT, int KW, bool MX, bool ACT = false, bool HALF = false>
+template <int MT, int NT, int KW, bool MX, bool ACT = false>
 static void launch_cfg(dim3 grid, hipStream_t stream, const uint8_t* qa, int64_t lda, const float* s_tok,
                        const uint8_t* qw, int64_t ldw, const float* s_ch, uint16_t* y, float* y32, int64_t ldy, int M,
                        int N, int K, float* part, int split_chunks, MxScales mx, const Epilogue& epi = {}) {
@@ -489,7 +493,7 @@ static void launch_cfg(dim3 grid, hipStream_t stream, const uint8_t* qa, int64_t
     // register report for every instantiation).
     constexpr int DEPTH = MX ? (MT * NT == 1 ? 4 : ((NT == 8 ? MT == 1 : MT * NT <= 6) ? 2 : 1))
                              : ((MT * NT <= 2) ? 4 : 2);
-    hipLaunchKernelGGL((gemm_skinny_kernel<MT, NT, KW, DEPTH, MX, ACT, HALF>), grid, dim3(KW * 64), 0, stream, qa, lda, s_tok,
+    hipLaunchKernelGGL((gemm_skinny_kernel<MT, NT, KW, DEPTH, MX, ACT>), grid, dim3(KW * 64), 0, stream, qa, lda, s_tok,
                        qw, ldw, s_ch, y, y32, ldy, M, N, K, part, split_chunks, mx, epi);
 }
 
@@ -610,17 +614,10 @@ hipError_t launch_gemm_skinny_act(const uint8_t* qa, int64_t lda, const float* s
     if (!skinny_act(M, N)) return hipErrorInvalidValue;
     const SkinnyPlan p = skinny_plan(M, N, K);  // one activation tile, K not split
     const dim3 grid((unsigned)((N + 16 * p.nt - 1) / (16 * p.nt)));
-    auto launch = [&](auto half) {
-        constexpr bool HALF = decltype(half)::value;
-        const auto kernel = p.nt == 4 ? launch_cfg<1, 4, 8, false, true, HALF>
-                            : p.nt == 2 ? launch_cfg<1, 2, 8, false, true, HALF> : launch_cfg<1, 1, 8, false, true, HALF>;
-        kernel(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, nullptr, nullptr, 0, (int)M, (int)N, (int)K, nullptr,
-               p.split_chunks, MxScales{}, epi);
-    };
-    if (epi.type == kKvF32)
-        launch(std::true_type{});
-    else
-        launch(std::false_type{});
+    const auto kernel = p.nt == 4 ? launch_cfg<1, 4, 8, false, true>
+                        : p.nt == 2 ? launch_cfg<1, 2, 8, false, true> : launch_cfg<1, 1, 8, false, true>;
+    kernel(grid, stream, qa, lda, s_tok, qw, ldw, s_ch, nullptr, nullptr, 0, (int)M, (int)N, (int)K, nullptr, p.split_chunks,
+           MxScales{}, epi);
     return hipGetLastError();
 }
 

@@ -168,10 +168,11 @@ __device__ __forceinline__ v8h half8_of(int lo, int hi) {
 //   gelu(x)      = x Phi(x), Phi(-a) = erfc(a / sqrt 2) / 2 and Phi(a) = 1 - Phi(-a) for a >= 0
 //   gelu_tanh(x) = x / (1 + e^-2u), u = sqrt(2 / pi) (x + 0.044715 x^3):
 //                  the same as x (1 + tanh u) / 2.
-// FINE, for fp32 outputs (the activation quantizer's scales among them): within a few
-// units of 2^-24 (gelu 5e-7).  Otherwise, for the products' 16-bit outputs, which round
-// by 2^-12 or more themselves: an exponent's argument t costs |t| 2^-23 and gelu's fit
-// 4.7e-6, for half the instructions (the epilogues run while the matrix units wait).
+// FINE, for fp32 outputs (the activation quantizer's scales among them) and where other
+// work hides it: within a few units of 2^-24 (gelu 5e-7).  Otherwise, for the tiled
+// products' 16-bit outputs, which round by 2^-12 or more themselves: an exponent's
+// argument t costs |t| 2^-23 and gelu's fit 4.7e-6, for half the instructions (these
+// epilogues run while the matrix units wait).
 
 // 1 / x, to one step of fp32; 0 for inf.
 __device__ __forceinline__ float fast_recip(float x) { return __builtin_amdgcn_rcpf(x); }
@@ -263,8 +264,9 @@ __device__ __forceinline__ void activate(float (&x)[V], int act) {
     }
 }
 
-// The epilogue of four neighbouring outputs from their sums.  A missing bias
-// enters as -0, which leaves every value as it is, signed zeros included.
+// The epilogue of four neighbouring outputs from their sums (decode and split k, whose
+// memory traffic hides the activation).  A missing bias enters as -0, which leaves every
+// value as it is, signed zeros included.
 template <int DT>
 __device__ __forceinline__ void finish4_typed(const Epilogue& e, const v4f& sum, float st,
                                               const float* __restrict__ s_ch, int m, int nb, int N) {
@@ -279,7 +281,7 @@ __device__ __forceinline__ void finish4_typed(const Epilogue& e, const v4f& sum,
     }
 #pragma unroll
     for (int v = 0; v < 4; ++v) x[v] = __builtin_fmaf(sum[v], st * sc[v], x[v]);
-    activate<DT == kKvF32, 4>(x, e.act);
+    activate<true, 4>(x, e.act);
     if (e.residual != nullptr) {
         float r[4];
         load_run<DT, 4>(e.residual, (int64_t)m * e.ldr + nb, left, r);

@@ -529,8 +529,8 @@ fp8_status_t fp8_moe_combine_grad(const void* dout, int64_t ldd, fp8_kv_dtype_t 
 
 /*
  * Activations, evaluated in fp32: to a few units of 2^-24 of their value for fp32
- * outputs and by fp8_act_quantize, and for the products' 16-bit outputs to 2^-17 and
- * |x| 2^-22 (GELU_TANH: |u| 2^-21):
+ * outputs and by fp8_act_quantize, and for 16-bit outputs of products of more than 16
+ * rows to 2^-17 and |x| 2^-22 (GELU_TANH: |u| 2^-21):
  *   NONE x   RELU max(x, 0)   SILU x / (1 + e^-x)   GELU x Phi(x) = x (1 + erf(x / sqrt 2)) / 2
  *   GELU_TANH x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2
  * A value of less than 2^-126 (|x| + 1) may come out as 0 (silu(-88) is -5.3e-37).
@@ -556,13 +556,15 @@ typedef enum {
  * [M, N] (row stride ldr >= N) may be NULL; residual may be y itself (same
  * pointer and stride), else it does not overlap y.  y [M, N], any row stride
  * ldy >= N; at the address of another input: FP8_ERR_INVALID_ARGUMENT.  For an fp32
- * y the products are summed to fp32's own precision (fp16 matrix instructions, at
- * half the rate); for 16-bit ones as fp8_gemm_scaled does, whose instructions leave
- * 1e-5 of a sum's norm, far below the rounding.  An output of more than 2^24 - 9
- * tiles of 128 x 128 (grouped: as for fp8_gemm_grouped_scaled) is
- * FP8_ERR_UNSUPPORTED.  ws: at least fp8_gemm_act_workspace_bytes(M, N, K) bytes,
- * 16-byte aligned (sums of a split K, added in a fixed order; may be NULL when that
- * is 0).
+ * y, and for up to 16 rows (N up to 2^28), the products are summed to fp32's own precision (fp16
+ * matrix instructions, at half the rate); otherwise as fp8_gemm_scaled does, whose
+ * instructions leave sums of normal data off by 1e-5 of their norm: below the
+ * rounding of a bf16 output of at least 1/200 of that norm and of an fp16 one of at
+ * least 1/25, above it where a sum cancels to less.
+ * An output of more than 2^24 - 9 tiles of 128 x 128 (grouped: as for
+ * fp8_gemm_grouped_scaled) is FP8_ERR_UNSUPPORTED.  ws: at least
+ * fp8_gemm_act_workspace_bytes(M, N, K) bytes, 16-byte aligned (sums of a split K,
+ * added in a fixed order; may be NULL when that is 0).
  */
 fp8_status_t fp8_gemm_scaled_act(const uint8_t* qa, int64_t lda, const float* s_tok, const uint8_t* qw, int64_t ldw,
                                  const float* s_ch, const float* bias, fp8_act_t act, const void* residual, int64_t ldr,
