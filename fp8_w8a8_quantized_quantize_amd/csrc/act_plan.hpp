@@ -13,6 +13,8 @@
 //   2048 x 4096 x 4096  57        38        55
 //   4096 x 4096 x 4096  109       72        65
 //   fp32 output         162       127       -      (4096 x 4096 x 4096)
+// With weights from HBM, 17 to 64 rows of 28672 x 8192 and 8192 x 28672 take 46 to 57 us
+// by these plans, 235 MB at 4.2 to 5.1 TB/s, and 60 to 66 with an fp32 output.
 // A k range is split when there are too few tiles of 64 for the card: 100 x 512 x
 // 16384 takes 28.6 us in 16 workgroups and 12.4 us in 128, the addition included.
 #pragma once
@@ -95,7 +97,9 @@ inline size_t act_plan_ws_bytes(const ActPlan& p, int64_t M, int64_t N) {
 // taken to leave half a tile empty.  With few of them the weights' stream from memory
 // is what counts, and small tiles with deep rings keep most of it under way (64
 // experts of 2048 x 7168, 16 tokens of 8 choices: tiles of 64 122 us, of 128 150, of
-// 256 182; 4096 tokens: 905, 610 and 505).
+// 256 182; 4096 tokens: 905, 610 and 505).  As planned, 16, 64, 256, 1000 and 4096
+// tokens take 122, 159, 193, 274 and 520 us, with an fp32 output 133, 184, 221, 360 and
+// 935.
 inline ActPlan grouped_act_plan(int64_t R, int64_t E, int64_t N, int64_t K, bool half) {
     auto most = [&](int tile) { return ((R + tile - 1) / tile + E) * ((N + tile - 1) / tile); };  // tiles
     if (R <= (half ? 64 : 32) * E && most(64) <= kMaxActTiles) return ActPlan{64, 4, 1, 0};

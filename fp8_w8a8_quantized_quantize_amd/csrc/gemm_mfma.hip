@@ -627,6 +627,9 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
     };
     // Fragments holding at least one real row (at least 1, so that every wave
     // runs the loop body; a wave with none computes one discarded fragment).
+    // With an epilogue every fragment is computed: 4096 tokens x 8 of 64 experts of
+    // 2048 x 7168 514 us, 499 with the loops of fewer (silu 522 and 510), 1000 tokens
+    // 274 and 277, and each of its kernels would hold four K loops.
     const int fa_live = min(FM, max(1, (rows_valid - wm * 32 + 32 * WM - 1) / (32 * WM)));
     if constexpr ((GROUPED || SKIP) && FM == 4 && !MX && !ACT) {
         switch (fa_live) {
@@ -647,8 +650,8 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void gemm_mfma_kernel(MfmaArgs p) 
         // the output, and the activation's code is there once, not once per
         // accumulator.  16-byte pieces are XOR-swizzled by row.  A thread whose 8
         // columns run past N works on the last 8 of the row and stores its own.
-        // 8192^3, bf16, with the matrix units waiting meanwhile: 422 us (the plain
-        // epilogue 410), with silu 433, gelu 452, gelu_tanh and a residual 452.
+        // 8192^3, bf16, with the matrix units waiting meanwhile: 441 us (the plain
+        // epilogue 422), with silu 447, gelu 465, gelu_tanh and a residual 465.
         constexpr int FP = FM < 2 ? FM : 2, ROWS = FP * 32 * WM;
         constexpr int CG = BN / 8;                          // column groups of a row
         constexpr int STEP = NTH / CG;                      // rows the workgroup covers at once

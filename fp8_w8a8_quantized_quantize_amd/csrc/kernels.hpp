@@ -162,8 +162,15 @@ hipError_t launch_gemm_skinny(const uint8_t* qa, int64_t lda, const float* s_tok
                               int64_t K, void* ws, hipStream_t stream);
 
 // With an epilogue, M <= kSkinnyActMaxM: one activation tile, which the weights'
-// stream bounds (8 x 4096 x 4096: 6.3 us, by tiles of 64 10.5; 32 rows 12.7 against
-// 10.6, 64 x 16384 x 1024 12.2 against 6.9).  No workspace.
+// stream bounds (weights in cache, 8 x 4096 x 4096: 6.3 us, by tiles of 64 10.5; 32 rows
+// 12.7 against 10.6, 64 x 16384 x 1024 12.2 against 6.9).  With weights from HBM the
+// tiles of the rows above it keep up with this kernel's further activation tiles too, in
+// us, tiles with bias and silu against the plain product of this file:
+//   rows                 17            32            64
+//   N 28672, K 8192      46.4  47.6    47.7  48.8    53.7  54.6
+//   N 8192, K 28672      47.9  48.9    49.2  50.8    57.1  55.8
+//   N 14336, K 4096      17.2  19.0    17.4  20.0    19.0  23.9
+// (fp32 outputs 61, 63 and 65 in the first of them).  No workspace.
 // Past kSkinnyActMaxN its grid would have 2^32 threads or more.
 constexpr int64_t kSkinnyActMaxM = 16;
 constexpr int64_t kSkinnyActMaxN = int64_t(1) << 28;
