@@ -170,7 +170,7 @@ hipError_t launch_gemm_skinny(const uint8_t* qa, int64_t lda, const float* s_tok
 //   N 28672, K 8192      46.4  47.6    47.7  48.8    53.7  54.6
 //   N 8192, K 28672      47.9  48.9    49.2  50.8    57.1  55.8
 //   N 14336, K 4096      17.2  19.0    17.4  20.0    19.0  23.9
-// (fp32 outputs 61, 63 and 65 in the first of them).  No workspace.
+// (fp32 outputs 60 to 66 in the first two).  No workspace.
 // Past kSkinnyActMaxN its grid would have 2^32 threads or more.
 constexpr int64_t kSkinnyActMaxM = 16;
 constexpr int64_t kSkinnyActMaxN = int64_t(1) << 28;
